@@ -130,7 +130,7 @@ def prepare(case, seed):
         s["v_descale"] = torch.tensor([4.0 / 448.0 * 1.25], device=_DEV)
     for n in ("k", "v"):
         x = torch.empty(shape, dtype=torch.bfloat16, device=_DEV).normal_(generator=g)
-        s[n + "_cache"] = (x / s[n + "_descale"].to(torch.bfloat16)).to(torch.float8_e4m3fn).view(torch.uint8) if e4m3 else x
+        s[n + "_cache"] = (x / s[n + "_descale"].to(torch.bfloat16)).clamp_(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8) if e4m3 else x
     if case["op"] == "append":
         # One projection's output holds the keys and the values: rows of 2 Hkv heads.
         kv = torch.empty(T, 2 * Hkv, d, dtype=torch.bfloat16, device=_DEV).normal_(generator=g)
