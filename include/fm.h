@@ -58,11 +58,13 @@ typedef enum {
     FM_ERR_WORKSPACE = 6,        /* workspace missing or too small                       */
     FM_ERR_CUDA = 7,             /* a CUDA runtime / driver call failed                  */
     FM_ERR_TIMEOUT = 8,          /* a bounded device-side wait ran out (kernel returned) */
-    FM_ERR_DEBUG_CHECK = 9       /* a device-side check of an FM_DEBUG build failed      */
+    FM_ERR_DEBUG_CHECK = 9,      /* a device-side check of an FM_DEBUG build failed      */
+    FM_ERR_LENGTHS = 10,         /* request lengths outside the sizes of the step        */
+    FM_ERR_PAGES = 11            /* too few free pages, or a page or slot out of range   */
 } fm_status;
 
 enum { FM_TILE_SKIP = 0, FM_TILE_FULL = 1, FM_TILE_PARTIAL = 2 };
-enum { FM_DT_BF16 = 0, FM_DT_F32 = 1 };
+enum { FM_DT_BF16 = 0, FM_DT_F32 = 1, FM_DT_E4M3 = 2 /* paged caches only */ };
 
 /* Flags of fm_attn_fwd / fm_attn_bwd.
  * FM_FLAG_PRECISE: the softmax probabilities P (forward and backward) and dS
@@ -319,6 +321,97 @@ FM_API fm_status fm_attn_fwd_fp8(const uint8_t *q8, const uint8_t *k8, const uin
                           fm_stream_t stream);
 
 /*
+ * Attention over a paged cache — DEVICE, async (fm_paged_plan_bytes: HOST).
+ * The serving form of the forward: requests of ragged lengths whose keys and
+ * values lie in fixed-size pages of one pool, each request with a row of page
+ * numbers (its block table), and per step a chunk of new tokens per request,
+ * from a single one (decoding) to thousands (a prompt).
+ *
+ * A step has `requests` requests; request r has ctx_lens[r] tokens in the cache
+ * and q_lens[r] new ones (0 or more).  The new tokens' rows (of q, of k and v to
+ * append, of o and lse) stand one behind the other in the order of the requests: rows
+ * [cu_q[r], cu_q[r + 1]).  New token i of request r has position ctx_lens[r] + i
+ * and attends, of its request's ctx_lens[r] + q_lens[r] keys (the new ones
+ * included, which therefore are appended first), key j if
+ *     j <= position  and  (window = 0  or  j > position - window  or  j < sink):
+ * causal, or a causal window with the first `sink` keys kept (blog §5,
+ * window_size and sink_tokens).  Query head h reads KV head h / (Hq / Hkv).
+ *
+ * fm_paged_plan: the step's bookkeeping, from lengths on the device.
+ *   Pages: a request needs ceil(len / page_size) of them.  With free_pages (int32
+ *   [n_free], device) the pages that the new tokens need are taken from it, from
+ *   index *free_head on, in the order of the requests and of their positions, and
+ *   entered into block_table (int32 [requests, max_pages]); *free_next becomes
+ *   the index behind the last one taken.  Without (NULL; n_free, free_head and
+ *   free_next unused) block_table has to hold every page already.  Entries of pages
+ *   already held are read, all others are left as they were.
+ *   Writes seq_lens[r] = ctx_lens[r] + q_lens[r]; cu_q (int32 [requests + 1]); per
+ *   row t < cu_q[requests] slots[t] = page * page_size + offset (int64
+ *   [max_tokens]) and positions[t] (int32 [max_tokens], may be NULL), -1 in both
+ *   behind; and the plan that fm_attn_paged walks.
+ *   seq_lens may be ctx_lens and free_next may be free_head: they are advanced in
+ *   place (a captured step can be replayed); no other two arrays may overlap.
+ *   Lengths that do not fit the step's sizes (negative, a chunk over max_q, more than
+ *   max_tokens rows, more than max_pages pages) give FM_ERR_LENGTHS, too few free
+ *   pages FM_ERR_PAGES, in dev_status; the plan is then empty: no page is taken,
+ *   cu_q is 0, every slot -1, seq_lens = ctx_lens, and fm_attn_paged does
+ *   nothing.  A page number outside [0, num_pages) gives FM_ERR_PAGES and slot -1 for
+ *   its rows alone.
+ * fm_paged_append: writes row t of k and v (bf16, [T, Hkv, d], strides of tokens and
+ *   heads in elements) to the cache's slot slots[t]; slots below 0 are skipped,
+ *   slots at or behind num_pages * page_size are skipped with FM_ERR_PAGES.  e4m3
+ *   caches get e4m3(x / descale) as fm_quantize_fp8 rounds.  Two rows with the same
+ *   slot: which one's values are left there, or parts of both, is not defined.
+ * fm_attn_paged: q bf16 [rows, Hq, d] (strides of tokens and heads in elements, the
+ *   last dimension contiguous), o [rows, Hq, d] and lse fp32 [rows, Hq] contiguous,
+ *   with rows at least cu_q[requests] (else FM_ERR_LENGTHS in dev_status and nothing
+ *   is written); rows at or behind cu_q[requests] are left as they were.  `step` has to be the plan's (else FM_ERR_PLAN_MISMATCH in dev_status),
+ *   block_table the one it was built from.  Keys that no row of a request
+ *   attends are never part of a product, whatever their pages hold: entries of
+ *   pages wholly outside the window may be stale, and what lies behind the last
+ *   token may be NaN.  A page number outside [0, num_pages) among the others
+ *   gives FM_ERR_PAGES and its keys read as zeros.  Outputs are rounded once; P
+ *   keeps 16 bits or more in the second product when o is fp32 or the rows are few
+ *   (see the kernels).
+ *   The plan holds the workspace as well: calls that share a plan (any number of layers
+ *   per step) have to follow one another on the GPU, and so have replays of graphs
+ *   that share one.  After a status other than 0, plan again.
+ *
+ * Sizes: d = 64 or 128; page_size a multiple of 16; Hq / Hkv whole and at most 32;
+ * at most 8192 requests and 2^24 rows; max_pages * page_size below 2^31 - 256;
+ * a sink needs a window.  Caches: page (p, h, t) of k begins at element p * k_page
+ * + h * k_head + t * k_tok, its d elements contiguous; strides and pointers are
+ * multiples of 16 bytes.  Values are code * descale for e4m3 (device
+ * float each; ignored for bf16).
+ */
+typedef struct {
+    int32_t requests, max_tokens, max_q, max_pages;
+    int32_t num_pages, page_size;
+    int32_t Hq, Hkv, d;
+    int32_t window, sink;           /* 0: none */
+} fm_paged_step;
+typedef struct {
+    void *k, *v;
+    int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;   /* strides, elements */
+    const float *k_descale, *v_descale;
+    int32_t num_pages, page_size, Hkv, d;
+    int32_t dtype;                  /* FM_DT_BF16 or FM_DT_E4M3 */
+} fm_paged_cache;
+FM_API size_t fm_paged_plan_bytes(const fm_paged_step *step);
+FM_API fm_status fm_paged_plan(const fm_paged_step *step, const int32_t *ctx_lens, const int32_t *q_lens,
+                               int32_t *block_table, const int32_t *free_pages, int n_free,
+                               const int32_t *free_head, int32_t *free_next, int32_t *seq_lens,
+                               int32_t *cu_q, int64_t *slots, int32_t *positions, void *plan,
+                               size_t plan_bytes, int32_t *dev_status, fm_stream_t stream);
+FM_API fm_status fm_paged_append(const void *k, int64_t k_tok, int64_t k_head, const void *v,
+                                 int64_t v_tok, int64_t v_head, const int64_t *slots, int T,
+                                 const fm_paged_cache *cache, int32_t *dev_status, fm_stream_t stream);
+FM_API fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok, int64_t q_head,
+                               int rows, const fm_paged_cache *cache, const int32_t *block_table,
+                               void *plan, size_t plan_bytes, float scale, void *o, int o_dtype,
+                               float *lse, int32_t *dev_status, fm_stream_t stream);
+
+/*
  * Step graphs — create / destroy HOST, synchronous; launch DEVICE, async.
  * One step of the path (fm_tile_classify, fm_attn_fwd and, when dO is given,
  * fm_attn_bwd; 128 x 128 tiles) captured once into a CUDA graph for a fixed
@@ -367,7 +460,8 @@ FM_API fm_status fm_step_graph_destroy(fm_step_graph graph);
  */
 enum { FM_K_CLASSIFY_MINMAX = 0, FM_K_CLASSIFY_LISTS = 1, FM_K_FWD = 2, FM_K_BWD_PRE = 3,
        FM_K_BWD = 4, FM_K_BWD_POST = 5, FM_K_CLASSIFY_ORDER = 6, FM_K_FP8_AMAX = 7,
-       FM_K_FP8_CONVERT = 8, FM_K_COUNT = 9 };
+       FM_K_FP8_CONVERT = 8, FM_K_PAGED_PLAN = 9, FM_K_PAGED_APPEND = 10, FM_K_PAGED_DECODE = 11,
+       FM_K_COUNT = 12 };
 typedef struct {
     int32_t kernel;
     float ms;

@@ -263,6 +263,8 @@ const char *fm_status_string(fm_status st)
     case FM_ERR_CUDA: return "CUDA error";
     case FM_ERR_TIMEOUT: return "device-side wait timed out";
     case FM_ERR_DEBUG_CHECK: return "device-side check of a debug build failed";
+    case FM_ERR_LENGTHS: return "request lengths outside the sizes of the step";
+    case FM_ERR_PAGES: return "too few free pages, or a page or slot out of range";
     }
     return "unknown status";
 }

@@ -182,6 +182,9 @@ enum KernelId {
     kKClassifyOrder = FM_K_CLASSIFY_ORDER,
     kKFp8Amax = FM_K_FP8_AMAX,
     kKFp8Convert = FM_K_FP8_CONVERT,
+    kKPagedPlan = FM_K_PAGED_PLAN,
+    kKPagedAppend = FM_K_PAGED_APPEND,
+    kKPagedDecode = FM_K_PAGED_DECODE,
 };
 
 // Devices a process may use (per-device caches of kernel attributes).

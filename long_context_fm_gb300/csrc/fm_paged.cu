@@ -1,0 +1,485 @@
+// Paged key/value cache: the step's planner (block tables, slot map, positions
+// and the attention's work list from request lengths), the append of new keys
+// and values, and the C entry points of both and of the attention.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "fm_paged.h"
+#include "fm_ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace fm {
+
+// ---- planner -------------------------------------------------------------------
+// One cluster: every CTA scans the request lengths for itself (they are few
+// next to the tokens) and writes its share of the tokens' slots and of the
+// new table entries; CTA 0 also writes what there is once per request.  The
+// cluster barrier at the end lets the lengths and the free-list head be
+// advanced in place.  Latency-bound: two dependent reads (lengths, then a table
+// entry or a free page) around one block scan.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanCluster = 8;         // portable cluster size
+constexpr int kPlanTokensPerCta = 4096; // above this many rows of q the planner runs as a cluster
+
+struct PlanArgs {
+    PagedShape s;
+    PagedLayout L;
+    const int32_t *ctx, *n_new, *free_pages, *free_head;
+    int32_t n_free;
+    int32_t *table, *free_next, *seq, *cu, *pos;
+    int64_t *slots;
+    uint8_t *plan;
+    int32_t *status;
+};
+
+
+// Exclusive scan over the block (every thread calls); *total gets the sums.
+template <int N>
+__device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t (*sh)[N])
+{
+    const int lane = lane_id(), warp = threadIdx.x >> 5;
+    int64_t x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = v[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x[i], o);
+            if (lane >= o) x[i] += y;
+        }
+        if (lane == 31) sh[warp][i] = x[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        int64_t before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int64_t y = sh[w][i];
+            if (w < warp) before += y;
+            all += y;
+        }
+        v[i] = before + x[i] - v[i];
+        total[i] = all;
+    }
+    __syncthreads();
+}
+
+// Index of the last of n non-decreasing values that is <= x (a[0] = 0 <= x).
+template <class T>
+__device__ __forceinline__ int last_at_most(const T *a, int n, T x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs a)
+{
+    extern __shared__ __align__(16) uint8_t plan_smem[];
+    __shared__ int64_t sh[kPlanWarps][4];
+    const PagedShape &s = a.s;
+    const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;
+    int64_t *s_tiles = reinterpret_cast<int64_t *>(plan_smem);             // [R + 1] tiles before few-rows entry i
+    int32_t *s_cu = reinterpret_cast<int32_t *>(s_tiles + s.R + 1);        // [R] tokens before request r
+    int32_t *s_off = s_cu + s.R;                                           // [R] pages handed out before request r
+    const int G = s.Hq / s.Hkv;
+    const int64_t max_keys = (int64_t)s.max_pages * s.page_size;
+    PagedEntry *few = reinterpret_cast<PagedEntry *>(a.plan + a.L.off_few);
+    int64_t *few_cum = reinterpret_cast<int64_t *>(a.plan + a.L.off_few_cum);
+    const int32_t head = a.free_pages ? *a.free_head : 0;
+
+    int64_t run[4] = {0, 0, 0, 0};
+    bool bad = false;
+    for (int r0 = 0; r0 < s.R; r0 += kPlanThreads) {
+        const int r = r0 + tid;
+        int ctx = 0, n = 0;
+        if (r < s.R) {
+            ctx = a.ctx[r];
+            n = a.n_new[r];
+            if (ctx < 0 || n < 0 || n > s.max_q || (int64_t)ctx + n > max_keys) {
+                bad = true;
+                ctx = n = 0;
+            }
+        }
+        const bool is_few = n > 0 && (int64_t)n * G <= kFewRows;
+        KeyRange kr{};
+        if (is_few) kr = key_range(ctx, ctx + n - 1, s.window, s.sink);
+        int64_t v[4], total[4];
+        v[0] = n;
+        v[1] = (ctx + n + s.page_size - 1) / s.page_size - (ctx + s.page_size - 1) / s.page_size;
+        v[2] = is_few;
+        v[3] = is_few ? (int64_t)kr.n * s.Hkv : 0;
+        block_scan(v, total, sh);
+        if (r < s.R) {
+            s_cu[r] = (int32_t)(run[0] + v[0]);     // meaningful when the total fits (checked below)
+            s_off[r] = (int32_t)(run[1] + v[1]);
+            if (is_few) {
+                const int e = (int)(run[2] + v[2]);
+                s_tiles[e] = run[3] + v[3];
+                if (cta == 0) {
+                    few[e] = PagedEntry{r, (int32_t)(run[0] + v[0]), n, ctx};
+                    few_cum[e] = run[3] + v[3];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) run[i] += total[i];
+    }
+    // Every CTA comes to the same verdict.  A plan that fails hands out nothing
+    // and is empty: no slot, no row of attention.
+    int32_t err = FM_OK;
+    if (__syncthreads_or(bad) || run[0] > s.T) err = FM_ERR_LENGTHS;
+    else if (a.free_pages && (head < 0 || head > a.n_free || run[1] > a.n_free - head)) err = FM_ERR_PAGES;
+    if (err != FM_OK && cta == 0 && tid == 0) set_status(a.status, err);
+    const int total = err == FM_OK ? (int)run[0] : 0;
+    const int handed = err == FM_OK && a.free_pages ? (int)run[1] : 0;
+    const int n_few = err == FM_OK ? (int)run[2] : 0;
+    const int64_t W = err == FM_OK ? run[3] : 0;
+
+    // Page b of request r, as the step leaves the table.
+    auto page_at = [&](int r, int b, int ctx) -> int {
+        const int have = (ctx + s.page_size - 1) / s.page_size;
+        if (a.free_pages && b >= have) return a.free_pages[head + s_off[r] + b - have];
+        return a.table[(int64_t)r * s.max_pages + b];
+    };
+    const int stride = ctas * kPlanThreads;
+    for (int t = cta * kPlanThreads + tid; t < s.T; t += stride) {
+        int64_t slot = -1;
+        int p = -1;
+        if (t < total) {
+            const int r = last_at_most(s_cu, s.R, t);
+            const int ctx = a.ctx[r];
+            p = ctx + t - s_cu[r];
+            const int b = p / s.page_size;
+            const int page = page_at(r, b, ctx);
+            if (page >= 0 && page < s.num_pages)
+                slot = (int64_t)page * s.page_size + (p - b * s.page_size);
+            else
+                set_status(a.status, FM_ERR_PAGES);
+        }
+        a.slots[t] = slot;
+        if (a.pos) a.pos[t] = p;
+    }
+    for (int x = cta * kPlanThreads + tid; x < handed; x += stride) {
+        const int r = last_at_most(s_off, s.R, x);
+        const int have = (a.ctx[r] + s.page_size - 1) / s.page_size;
+        a.table[(int64_t)r * s.max_pages + have + x - s_off[r]] = a.free_pages[head + x];
+    }
+    if (cta == 0) {
+        const int ctas_few = (int)(W < kPagedCtas ? W : kPagedCtas);
+        if (tid == 0) {
+            PagedHeader h{};
+            h.magic = kPagedMagic;
+            h.s = s;
+            h.n_few = n_few;
+            h.ctas_few = ctas_few;
+            h.tiles_few = W;
+            h.rows = total;
+            *reinterpret_cast<PagedHeader *>(a.plan) = h;
+            few_cum[n_few] = W;
+            a.cu[s.R] = total;
+        }
+        for (int r = tid; r < s.R; r += kPlanThreads) a.cu[r] = err == FM_OK ? s_cu[r] : 0;
+        for (int i = tid; i < kPagedCtas; i += kPlanThreads) {
+            int4 st = make_int4(0, 0, 0, 0);
+            if (i < ctas_few) {
+                const int64_t x = share_begin(W, ctas_few, i);
+                const int e = last_at_most(s_tiles, n_few, x);
+                const int64_t next = e + 1 < n_few ? s_tiles[e + 1] : W;
+                const int n = (int)((next - s_tiles[e]) / s.Hkv), y = (int)(x - s_tiles[e]);
+                st = make_int4(e, y / n, y % n, 0);
+            }
+            reinterpret_cast<int4 *>(a.plan + a.L.off_start)[i] = st;
+            reinterpret_cast<uint32_t *>(a.plan + a.L.off_count)[i] = 0u;
+        }
+    }
+    // Every CTA has read the lengths and the head: they may be advanced in place.
+    if (ctas > 1) cg::this_cluster().sync();
+    else __syncthreads();
+    if (cta == 0) {
+        for (int r = tid; r < s.R; r += kPlanThreads) {
+            const int ctx = a.ctx[r];
+            a.seq[r] = err == FM_OK ? ctx + a.n_new[r] : ctx;
+        }
+        if (tid == 0 && a.free_next) *a.free_next = head + handed;
+    }
+}
+
+// ---- append -----------------------------------------------------------------------
+// cache[slot] = x, 8 elements (16 bytes of bf16) of K and of V per thread and
+// step: bound by the bytes.  e4m3: code = e4m3(x / descale), the division in
+// fp32, nearest even, saturating: the quantizer's rule.
+struct AppendArgs {
+    const uint8_t *k, *v;                        // bf16; strides in bytes
+    int64_t k_tok, k_head, v_tok, v_head;
+    uint8_t *kc, *vc;
+    int64_t kc_page, kc_head, kc_tok, vc_page, vc_head, vc_tok;
+    const int64_t *slots;
+    const float *k_descale, *v_descale;
+    int64_t n_slots;                             // num_pages * page_size
+    int32_t page_size, Hkv, per_row;             // per_row: 16-byte pieces of a row of x
+    int64_t total;                               // T * Hkv * per_row
+    int32_t *status;
+};
+
+template <bool FP8>
+__global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a)
+{
+    const float kd = FP8 ? *a.k_descale : 1.f, vd = FP8 ? *a.v_descale : 1.f;
+    const int per_tok = a.Hkv * a.per_row;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < a.total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = i / per_tok;
+        const int rest = (int)(i - t * per_tok), h = rest / a.per_row, ch = rest - h * a.per_row;
+        const int64_t slot = a.slots[t];
+        if (slot < 0) continue;
+        if (slot >= a.n_slots) {
+            set_status(a.status, FM_ERR_PAGES);
+            continue;
+        }
+        const int64_t page = slot / a.page_size, in = slot - page * a.page_size;
+        const uint4 k = *reinterpret_cast<const uint4 *>(a.k + t * a.k_tok + h * a.k_head + ch * 16);
+        const uint4 v = *reinterpret_cast<const uint4 *>(a.v + t * a.v_tok + h * a.v_head + ch * 16);
+        uint8_t *kd_ = a.kc + page * a.kc_page + h * a.kc_head + in * a.kc_tok + ch * (FP8 ? 8 : 16);
+        uint8_t *vd_ = a.vc + page * a.vc_page + h * a.vc_head + in * a.vc_tok + ch * (FP8 ? 8 : 16);
+        if (!FP8) {
+            *reinterpret_cast<uint4 *>(kd_) = k;
+            *reinterpret_cast<uint4 *>(vd_) = v;
+        } else {
+            auto codes = [](uint32_t w, float ds) {
+                return pack_e4m3x2(__uint_as_float(w << 16) / ds, __uint_as_float(w & 0xffff0000u) / ds);
+            };
+            *reinterpret_cast<uint2 *>(kd_) = make_uint2(codes(k.x, kd) | codes(k.y, kd) << 16, codes(k.z, kd) | codes(k.w, kd) << 16);
+            *reinterpret_cast<uint2 *>(vd_) = make_uint2(codes(v.x, vd) | codes(v.y, vd) << 16, codes(v.z, vd) | codes(v.w, vd) << 16);
+        }
+    }
+}
+
+}  // namespace fm
+
+using namespace fm;
+
+namespace {
+
+bool aligned16(const void *p) { return p && ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
+
+// Sizes of a step; *out gets them in the library's own form.
+fm_status check_step(const fm_paged_step *p, PagedShape *out)
+{
+    if (!p) return FM_ERR_INVALID_ARG;
+    if (p->requests <= 0 || p->max_tokens <= 0 || p->max_q <= 0 || p->max_pages <= 0 || p->num_pages <= 0 || p->page_size <= 0 ||
+        p->Hq <= 0 || p->Hkv <= 0 || p->window < 0 || p->sink < 0)
+        return FM_ERR_INVALID_ARG;
+    if (p->max_q > p->max_tokens || p->Hq % p->Hkv != 0 || (p->sink > 0 && p->window == 0)) return FM_ERR_INVALID_ARG;
+    if (p->d != 64 && p->d != 128) return FM_ERR_UNSUPPORTED;
+    if (p->requests > kMaxRequests || p->max_tokens > (1 << 24) || p->page_size % kPageGranule != 0 || p->Hq > 4096 ||
+        p->Hq / p->Hkv > kFewRows)
+        return FM_ERR_UNSUPPORTED;
+    // Positions are int32, and a tile's last key must be one too.
+    if ((int64_t)p->max_pages * p->page_size > (int64_t)0x7fffffff - 2 * kKeyTile) return FM_ERR_UNSUPPORTED;
+    if (p->window > (1 << 30) || p->sink > (1 << 30)) return FM_ERR_UNSUPPORTED;
+    *out = PagedShape{p->requests, p->max_tokens, p->max_q, p->max_pages, p->num_pages, p->page_size, p->Hq, p->Hkv, p->d,
+                      p->window, p->sink};
+    return FM_OK;
+}
+
+// Pages, strides and descales of a cache; alignment of 16 bytes everywhere.
+fm_status check_cache(const fm_paged_cache *c)
+{
+    if (!c || !aligned16(c->k) || !aligned16(c->v)) return FM_ERR_INVALID_ARG;
+    if (c->num_pages <= 0 || c->page_size <= 0 || c->Hkv <= 0) return FM_ERR_INVALID_ARG;
+    if (c->dtype != FM_DT_BF16 && c->dtype != FM_DT_E4M3) return FM_ERR_INVALID_ARG;
+    if (c->d != 64 && c->d != 128) return FM_ERR_UNSUPPORTED;
+    if (c->page_size % kPageGranule != 0) return FM_ERR_UNSUPPORTED;
+    const int esz = c->dtype == FM_DT_E4M3 ? 1 : 2;
+    const int64_t st[6] = {c->k_page, c->k_head, c->k_tok, c->v_page, c->v_head, c->v_tok};
+    for (int64_t x : st)
+        if (x <= 0 || (x * esz) % 16 != 0 || x > ((int64_t)1 << 38)) return FM_ERR_INVALID_ARG;
+    if (c->k_tok < c->d || c->v_tok < c->d) return FM_ERR_INVALID_ARG;
+    if (esz == 1 && (!aligned4(c->k_descale) || !aligned4(c->v_descale))) return FM_ERR_INVALID_ARG;
+    return FM_OK;
+}
+
+// Rows of bf16 read 16 bytes at a time: token and head strides in elements.
+bool rows_ok(const void *p, int64_t tok, int64_t head)
+{
+    return aligned16(p) && tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0 && tok <= ((int64_t)1 << 38) &&
+           head <= ((int64_t)1 << 38);
+}
+
+fm_status device_ok()
+{
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return FM_ERR_CUDA;
+    static std::atomic<int8_t> known[kMaxDevices];
+    if (dev >= kMaxDevices) return FM_ERR_UNSUPPORTED;
+    int8_t k = known[dev].load(std::memory_order_acquire);
+    if (k == 0) {
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+            return FM_ERR_CUDA;
+        k = (major == 10 && minor == 3) ? 1 : 2;
+        if (k == 1 && cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kMaxRequests * 16 + 16) != cudaSuccess)
+            return FM_ERR_CUDA;
+        known[dev].store(k, std::memory_order_release);
+    }
+    return k == 1 ? FM_OK : FM_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fm_paged_plan_bytes(const fm_paged_step *step)
+{
+    PagedShape s;
+    return check_step(step, &s) == FM_OK ? (size_t)paged_layout(s).total : 0;
+}
+
+fm_status fm_paged_plan(const fm_paged_step *step, const int32_t *ctx_lens, const int32_t *q_lens, int32_t *block_table,
+                        const int32_t *free_pages, int n_free, const int32_t *free_head, int32_t *free_next,
+                        int32_t *seq_lens, int32_t *cu_q, int64_t *slots, int32_t *positions, void *plan, size_t plan_bytes,
+                        int32_t *dev_status, fm_stream_t stream)
+{
+    PlanArgs a{};
+    const fm_status st = check_step(step, &a.s);
+    if (st != FM_OK) return st;
+    if (!aligned4(ctx_lens) || !aligned4(q_lens) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_q) ||
+        !slots || ((uintptr_t)slots & 7u) || ((uintptr_t)positions & 3u) || !aligned4(dev_status))
+        return FM_ERR_INVALID_ARG;
+    if (free_pages && (((uintptr_t)free_pages & 3u) || n_free < 0 || !aligned4(free_head) || !aligned4(free_next)))
+        return FM_ERR_INVALID_ARG;
+    a.L = paged_layout(a.s);
+    if (!plan || ((uintptr_t)plan & 255u) || plan_bytes < (size_t)a.L.total) return FM_ERR_WORKSPACE;
+    const fm_status dv = device_ok();
+    if (dv != FM_OK) return dv;
+    a.ctx = ctx_lens;
+    a.n_new = q_lens;
+    a.table = block_table;
+    a.free_pages = free_pages;
+    a.n_free = n_free;
+    a.free_head = free_head;
+    a.free_next = free_pages ? free_next : nullptr;
+    a.seq = seq_lens;
+    a.cu = cu_q;
+    a.slots = slots;
+    a.pos = positions;
+    a.plan = (uint8_t *)plan;
+    a.status = dev_status;
+    const int ctas = a.s.T > kPlanTokensPerCta ? kPlanCluster : 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = (size_t)a.s.R * 16 + 16;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    ProfScope ps(kKPagedPlan, stream);
+    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, (const PlanArgs)a) == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+}
+
+fm_status fm_paged_append(const void *k, int64_t k_tok, int64_t k_head, const void *v, int64_t v_tok, int64_t v_head,
+                          const int64_t *slots, int T, const fm_paged_cache *cache, int32_t *dev_status, fm_stream_t stream)
+{
+    const fm_status st = check_cache(cache);
+    if (st != FM_OK) return st;
+    if (T < 0 || T > (1 << 24) || !rows_ok(k, k_tok, k_head) || !rows_ok(v, v_tok, v_head) || !slots ||
+        ((uintptr_t)slots & 7u) || !aligned4(dev_status))
+        return FM_ERR_INVALID_ARG;
+    const fm_status dv = device_ok();
+    if (dv != FM_OK) return dv;
+    if (T == 0) return FM_OK;
+    const bool fp8 = cache->dtype == FM_DT_E4M3;
+    const int64_t esz = fp8 ? 1 : 2;
+    AppendArgs a{};
+    a.k = (const uint8_t *)k;
+    a.v = (const uint8_t *)v;
+    a.k_tok = k_tok * 2;
+    a.k_head = k_head * 2;
+    a.v_tok = v_tok * 2;
+    a.v_head = v_head * 2;
+    a.kc = (uint8_t *)cache->k;
+    a.vc = (uint8_t *)cache->v;
+    a.kc_page = cache->k_page * esz;
+    a.kc_head = cache->k_head * esz;
+    a.kc_tok = cache->k_tok * esz;
+    a.vc_page = cache->v_page * esz;
+    a.vc_head = cache->v_head * esz;
+    a.vc_tok = cache->v_tok * esz;
+    a.slots = slots;
+    a.k_descale = cache->k_descale;
+    a.v_descale = cache->v_descale;
+    a.n_slots = (int64_t)cache->num_pages * cache->page_size;
+    a.page_size = cache->page_size;
+    a.Hkv = cache->Hkv;
+    a.per_row = cache->d / 8;
+    a.total = (int64_t)T * cache->Hkv * a.per_row;
+    a.status = dev_status;
+    const int64_t want = (a.total + 255) / 256;
+    const int blocks = (int)(want < 152 * 8 ? want : 152 * 8);
+    ProfScope ps(kKPagedAppend, stream);
+    if (fp8) paged_append_kernel<true><<<blocks, 256, 0, (cudaStream_t)stream>>>(a);
+    else paged_append_kernel<false><<<blocks, 256, 0, (cudaStream_t)stream>>>(a);
+    return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+}
+
+fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok, int64_t q_head, int rows,
+                        const fm_paged_cache *cache, const int32_t *block_table, void *plan, size_t plan_bytes, float scale, void *o, int o_dtype,
+                        float *lse, int32_t *dev_status, fm_stream_t stream)
+{
+    PagedArgs a{};
+    fm_status st = check_step(step, &a.s);
+    if (st != FM_OK) return st;
+    if ((st = check_cache(cache)) != FM_OK) return st;
+    if (cache->num_pages != a.s.num_pages || cache->page_size != a.s.page_size || cache->Hkv != a.s.Hkv || cache->d != a.s.d)
+        return FM_ERR_INVALID_ARG;
+    if (rows < 0 || !rows_ok(q, q_tok, q_head) || !aligned16(o) || !aligned4(lse) || !aligned4(block_table) || !aligned4(dev_status))
+        return FM_ERR_INVALID_ARG;
+    if (o_dtype != FM_DT_BF16 && o_dtype != FM_DT_F32) return FM_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return FM_ERR_INVALID_ARG;
+    a.L = paged_layout(a.s);
+    if (!plan || ((uintptr_t)plan & 255u) || plan_bytes < (size_t)a.L.total) return FM_ERR_WORKSPACE;
+    if ((st = device_ok()) != FM_OK) return st;
+    const bool fp8 = cache->dtype == FM_DT_E4M3;
+    const int64_t esz = fp8 ? 1 : 2;
+    a.plan = (uint8_t *)plan;
+    a.table = block_table;
+    a.q = (const uint8_t *)q;
+    a.q_tok = q_tok * 2;
+    a.q_head = q_head * 2;
+    a.k = (const uint8_t *)cache->k;
+    a.v = (const uint8_t *)cache->v;
+    a.k_page = cache->k_page * esz;
+    a.k_head = cache->k_head * esz;
+    a.k_tok = cache->k_tok * esz;
+    a.v_page = cache->v_page * esz;
+    a.v_head = cache->v_head * esz;
+    a.v_tok = cache->v_tok * esz;
+    a.k_descale = cache->k_descale;
+    a.v_descale = cache->v_descale;
+    a.o = o;
+    a.lse = lse;
+    a.status = dev_status;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.o_f32 = o_dtype == FM_DT_F32;
+    a.rows = rows;
+    if ((int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv) > kFewRows) return FM_ERR_UNSUPPORTED;
+    return fm_paged_decode_launch(a, fp8, (cudaStream_t)stream);
+}
+
+}  // extern "C"

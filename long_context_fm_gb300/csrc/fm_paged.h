@@ -1,0 +1,111 @@
+// Internal definitions of the paged-cache operators: the layout of a step's
+// plan buffer and the key ranges that the planner and the kernels share.
+#pragma once
+
+#include "fm_internal.h"
+
+namespace fm {
+
+constexpr uint32_t kPagedMagic = 0x464D5047u;   // "FMPG"
+constexpr int kKeyTile = 128;                   // keys per tile of work, a multiple of every page granule
+constexpr int kPageGranule = 16;                // page sizes are multiples of this: 16 aligned keys share a page
+constexpr int kFewRows = 32;                    // (new tokens x query heads per KV head) up to which a request is "few rows"
+constexpr int kPagedCtas = 152;                 // CTAs of the persistent attention kernels (no CTA waits for another)
+constexpr int kMaxRequests = 8192;
+
+struct PagedShape {
+    int32_t R, T, max_q, max_pages, num_pages, page_size, Hq, Hkv, d, window, sink;
+};
+
+// First 256 bytes of a plan, written by the planner.
+struct PagedHeader {
+    uint32_t magic;
+    PagedShape s;
+    int32_t n_few;        // entries of the few-rows list
+    int32_t ctas_few;     // CTAs that share its tiles (0: none)
+    int64_t tiles_few;    // key tiles of the list, over all KV heads
+    int32_t rows;         // rows of q: new tokens of all requests
+    int32_t pad[47];
+};
+static_assert(sizeof(PagedHeader) == 256, "plan header size");
+
+// One request of an attention work list.
+struct PagedEntry {
+    int32_t r, tok0, n, ctx;   // request, its first row of q, new tokens, tokens cached before them
+};
+
+struct PagedLayout {
+    int64_t off_few;       // PagedEntry [R]
+    int64_t off_few_cum;   // int64 [R + 1]  tiles before entry i, over all KV heads
+    int64_t off_start;     // int4 [kPagedCtas]  entry, head, tile of a CTA's first tile
+    int64_t off_count;     // uint32 [kPagedCtas]  arrivals at the split unit that begins in CTA c
+    int64_t off_few_o;     // fp32 [2 kPagedCtas][kFewRows][d]  unnormalised partial outputs
+    int64_t off_few_ml;    // fp32 [2 kPagedCtas][2][kFewRows]  their row maxima (base 2) and sums
+    int64_t total;
+};
+
+inline PagedLayout paged_layout(const PagedShape &s)
+{
+    PagedLayout L;
+    int64_t off = 256;
+    L.off_few = off;      off = align256(off + (int64_t)s.R * 16);
+    L.off_few_cum = off;  off = align256(off + ((int64_t)s.R + 1) * 8);
+    L.off_start = off;    off = align256(off + kPagedCtas * 16);
+    L.off_count = off;    off = align256(off + kPagedCtas * 4);
+    L.off_few_o = off;    off = align256(off + (int64_t)2 * kPagedCtas * kFewRows * s.d * 4);
+    L.off_few_ml = off;   off = align256(off + (int64_t)2 * kPagedCtas * 2 * kFewRows * 4);
+    L.total = off;
+    return L;
+}
+
+// Keys that the rows at positions [p0, p1] of a request attend: j < hi and
+// (j >= lo or j < sink), with j <= p for the row at p, and j > p - window or
+// j < sink when there is a window.  As key tiles: tile x of n stands for key
+// tile x while x < ns (the sink), else for first + x - ns.
+struct KeyRange {
+    int lo, hi;
+    int ns, first, n;
+    FM_HD int tile(int x) const { return x < ns ? x : first + x - ns; }
+};
+
+FM_HD KeyRange key_range(int p0, int p1, int window, int sink)
+{
+    KeyRange k;
+    k.hi = p1 + 1;
+    k.lo = (window > 0 && p0 >= window) ? p0 - window + 1 : 0;
+    if (sink >= k.lo) k.lo = 0;
+    k.first = k.lo / kKeyTile;
+    const int s = (sink + kKeyTile - 1) / kKeyTile;
+    k.ns = k.lo > 0 ? (s < k.first ? s : k.first) : 0;
+    k.n = k.ns + (k.hi + kKeyTile - 1) / kKeyTile - k.first;
+    return k;
+}
+
+// Tiles [share_begin(c), share_begin(c + 1)) of n belong to CTA c of ctas;
+// tile x belongs to CTA share_owner(x).
+FM_HD int64_t share_begin(int64_t n, int ctas, int64_t c) { return c * n / ctas; }
+FM_HD int share_owner(int64_t n, int ctas, int64_t x) { return (int)(((x + 1) * ctas - 1) / n); }
+
+// Arguments of the attention kernels (everything but TMA descriptors).
+struct PagedArgs {
+    PagedShape s;
+    PagedLayout L;
+    uint8_t *plan;
+    const int32_t *table;
+    const uint8_t *q;               // bf16
+    int64_t q_tok, q_head;          // strides in bytes, as all of these
+    const uint8_t *k, *v;
+    int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;
+    const float *k_descale, *v_descale;   // e4m3 cache: one float each
+    void *o;                        // [rows, Hq, d]
+    float *lse;                     // [rows, Hq]
+    int32_t *status;
+    float scale_log2;
+    int o_f32;
+    int rows;                       // rows that q, o and lse have
+};
+
+}  // namespace fm
+
+// Launcher of the few-rows kernel (fm_paged_decode.cu).
+fm_status fm_paged_decode_launch(const fm::PagedArgs &a, bool e4m3, cudaStream_t stream);

@@ -1,0 +1,754 @@
+// Attention of few new tokens over a paged cache (decoding steps): requests
+// whose new tokens times the query heads per KV head make at most kFewRows
+// rows.
+//
+//   o_row = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  s_j = scale q_row . k_j
+//
+// over the keys j that the row attends, one pass over K and V with the running
+// maximum and sum per row.  Bound by reading K and V once from HBM: at 8 rows
+// the work is 8 FLOPs per byte, so the products run on warp-level matrix
+// instructions straight from registers (a 16-row operand; a 128-row tcgen05
+// operand would be padding), and everything is arranged around the loads.
+//
+// Work: the key tiles (128 keys) of every (request, KV head) in a row, cut
+// into equal shares for the persistent CTAs, so ragged lengths and few
+// requests balance alike.  A unit (request, KV head) that crosses a border is
+// finished by the CTA that arrives last at it, which adds the partial results
+// in the order of the CTAs: the result does not depend on who is last.
+//
+// A warp takes 16 keys of every tile and works alone until its unit ends: it
+// loads them through a ring of its own (cp.async, no barrier), 16 aligned keys
+// always lying in one page.  Fragment layouts: the head-dim order of the score
+// product is free as long as Q and K agree, and the order of output columns is
+// free altogether, so both K and V fragments are read with 16-byte
+// shared loads (chunks XOR-swizzled by row: conflict-free) and V is transposed
+// by byte permutes of two keys' registers.
+//
+// P enters the second product as two 16-bit terms (hi + lo, about 16
+// significant bits) where that is free, which leaves the rounding of the output
+// alone; e4m3 caches with 16-bit outputs use one fp16 term (11 bits): e4m3
+// values are exact in fp16, and so is Q after a power-of-two factor per row
+// that puts its largest element in [2^14, 2^15).
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "fm_paged.h"
+#include "fm_ptx.cuh"
+
+namespace fm {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr float kBand = 8.f;   // lazy rescale: P stays <= 2^8, sums are rescaled when a maximum grows by more
+
+template <int D, bool FP8>
+struct DecodeCfg {
+    static constexpr int kRow = D * (FP8 ? 1 : 2);          // bytes of a key's row
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kSlot = 2 * 16 * kRow;             // a warp's 16 keys: K rows, then V rows
+    static constexpr int kStages = 192 * 1024 / (kWarps * kSlot) < 8 ? 192 * 1024 / (kWarps * kSlot) : 8;
+    static constexpr int kRing = 0;
+    static constexpr int kRed = kWarps * kStages * kSlot;   // float4 [8 warps][8][32 lanes]; Q of 32 rows between units
+    static constexpr int kMl = kRed + kWarps * 8 * 32 * 16; // float [8 warps][2][kFewRows]
+    static constexpr int kMisc = kMl + kWarps * 2 * kFewRows * 4;
+    static constexpr int kBytes = kMisc + 16;
+    static_assert(kBytes <= 227 * 1024, "shared memory of the few-rows kernel");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    // bytes < 16: the rest of the 16 destination bytes is zero
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// Two e4m3 bytes (low half of x) as two fp16, exactly.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t x)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// c (16 x 8 fp32) += a (16 x 16) b (16 x 8)
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk ch of key row `row` (0-15): the chunk moves so
+// that the eight lanes of a shared-load phase hit eight different bank groups.
+// K is read as (rows 2 x, 2 x + 1; four chunks), V as (rows 2 c, c = 0..3; two
+// chunks).
+template <int CH>
+__device__ __forceinline__ uint32_t swz_k(int row, int ch)
+{
+    return CH >= 8 ? (uint32_t)((row * CH + (ch ^ ((row & 1) << 2))) * 16) : (uint32_t)((row * CH + ch) * 16);
+}
+template <int CH>
+__device__ __forceinline__ uint32_t swz_v(int row, int ch)
+{
+    if (CH >= 8) return (uint32_t)((row * CH + (ch ^ (((row >> 1) & 3) << 1))) * 16);
+    return (uint32_t)(((row >> 1) * 8 + ((((row & 1) << 2) + ch) ^ (((row >> 1) & 3) << 1))) * 16);   // 64-byte rows
+}
+
+// A walk over the CTA's share of the list.
+struct Cursor {
+    int e, h, x;          // entry, KV head, tile of the entry's range
+    PagedEntry ent;
+    KeyRange kr;
+};
+
+}  // namespace
+
+template <int D, bool FP8, int MT, bool TWO>
+__global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const PagedArgs a)
+{
+    using C = DecodeCfg<D, FP8>;
+    constexpr int CH = C::kChunks, ST = C::kStages;
+    constexpr int KS = D / 16;              // score product: k-steps
+    constexpr int NT = D / 8;               // output product: 8-column tiles
+    constexpr int NP = NT / 8;              // groups of 8 tiles
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = warp_id(), lane = lane_id();
+    const int g = lane >> 2, c = lane & 3;
+    const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
+    const PagedShape &s = a.s;
+    if (hd->magic != kPagedMagic || hd->s.R != s.R || hd->s.T != s.T || hd->s.max_q != s.max_q || hd->s.max_pages != s.max_pages ||
+        hd->s.num_pages != s.num_pages || hd->s.page_size != s.page_size || hd->s.Hq != s.Hq || hd->s.Hkv != s.Hkv ||
+        hd->s.d != s.d || hd->s.window != s.window || hd->s.sink != s.sink) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_PLAN_MISMATCH);
+        return;
+    }
+    if (hd->rows > a.rows) {            // more rows than the caller's tensors have
+        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_LENGTHS);
+        return;
+    }
+    const int ctas = hd->ctas_few;
+    const int64_t W = hd->tiles_few;
+    if ((int)blockIdx.x >= ctas) return;
+    const int64_t x0 = share_begin(W, ctas, blockIdx.x);
+    int left = (int)(share_begin(W, ctas, blockIdx.x + 1) - x0);   // tiles to compute
+    if (left == 0) return;
+    int to_load = left;
+
+    const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_few);
+    const int64_t *cum = reinterpret_cast<const int64_t *>(a.plan + a.L.off_few_cum);
+    const int G = s.Hq / s.Hkv;
+    auto enter = [&](Cursor &u) {
+        const int4 v = *reinterpret_cast<const int4 *>(list + u.e);
+        u.ent = PagedEntry{v.x, v.y, v.z, v.w};
+        u.kr = key_range(v.w, v.w + v.z - 1, s.window, s.sink);
+    };
+    // Next tile of the walk; true when it begins another unit.
+    auto advance = [&](Cursor &u, bool more) -> bool {
+        if (++u.x < u.kr.n) return false;
+        u.x = 0;
+        if (++u.h == s.Hkv) {
+            u.h = 0;
+            ++u.e;
+            if (more) enter(u);
+        }
+        return true;
+    };
+
+    Cursor ld;
+    {
+        const int4 v = *reinterpret_cast<const int4 *>(a.plan + a.L.off_start + (int64_t)blockIdx.x * 16);
+        ld.e = v.x;
+        ld.h = v.y;
+        ld.x = v.z;
+        enter(ld);
+    }
+    Cursor cu = ld;
+
+    const uint32_t ring = smem_u32(smem) + C::kRing + warp * ST * C::kSlot;
+    // The page of this warp's keys of the tile that `u` stands at, or -1: none
+    // of them is attended, or the number is outside the pool.
+    auto page_of = [&](const Cursor &u) -> int {
+        const int k0 = u.kr.tile(u.x) * kKeyTile + warp * 16;
+        if (k0 >= u.kr.hi || (k0 + 16 <= u.kr.lo && k0 >= s.sink)) return -1;
+        const int p = __ldg(a.table + (int64_t)u.ent.r * s.max_pages + k0 / s.page_size);
+        if (p < 0 || p >= s.num_pages) {
+            if (lane == 0) set_status(a.status, FM_ERR_PAGES);
+            return -1;
+        }
+        return p;
+    };
+    int page = page_of(ld);
+    int slot_ld = 0;
+    // Starts the copies of the tile that the load walk stands at, and looks up
+    // the next tile's page meanwhile.
+    auto load_tile = [&]() {
+        if (to_load > 0) {
+            const int k0 = ld.kr.tile(ld.x) * kKeyTile + warp * 16;
+            const uint32_t dst = ring + slot_ld * C::kSlot;
+            const int hi = ld.kr.hi, lo = ld.kr.lo;
+            const bool some = k0 < hi && !(k0 + 16 <= lo && k0 >= s.sink);
+            const int in_page = k0 % s.page_size;
+            const uint8_t *kp = a.k + (int64_t)max(page, 0) * a.k_page + (int64_t)ld.h * a.k_head + (int64_t)in_page * a.k_tok;
+            const uint8_t *vp = a.v + (int64_t)max(page, 0) * a.v_page + (int64_t)ld.h * a.v_head + (int64_t)in_page * a.v_tok;
+            const int pg = page;
+            --to_load;
+            advance(ld, to_load > 0);
+            if (to_load > 0) page = page_of(ld);
+            if (some) {
+                // Rows that no row of the request attends arrive as zeros: what
+                // a page holds behind the last token reaches no product.
+#pragma unroll
+                for (int i = 0; i < CH / 2; ++i) {
+                    const int row = i * (32 / CH) + lane / CH, ch = lane % CH;
+                    const int j = k0 + row;
+                    const uint32_t n = (pg >= 0 && j < hi && (j >= lo || j < s.sink)) ? 16u : 0u;
+                    cp_async16(dst + swz_k<CH>(row, ch), kp + row * a.k_tok + ch * 16, n);
+                    cp_async16(dst + 16 * C::kRow + swz_v<CH>(row, ch), vp + row * a.v_tok + ch * 16, n);
+                }
+            }
+        }
+        cp_async_commit();
+        slot_ld = slot_ld + 1 == ST ? 0 : slot_ld + 1;
+    };
+
+    uint32_t qf[MT == 1 ? KS : 1][4];       // one 16-row block: Q fragments in registers
+    float qs[MT][2];                        // score factor of rows g, g + 8 (softmax scale, log2 e, descale, Q's own factor)
+    int pos[MT][2];                         // position of rows g, g + 8 of each block
+    float m[MT][2], l[MT][2];
+    float oa[MT][NT][4];
+    uint8_t *sq = smem + C::kRed;           // two blocks: Q in shared memory between units
+    const float kds = FP8 ? *a.k_descale : 1.f, vds = FP8 ? *a.v_descale : 1.f;
+
+    // Factor that puts a row's largest element in [2^14, 2^15) (e4m3 caches: Q
+    // as fp16), 1 when the row is zero or not finite.
+    auto row_factor = [](float amax) -> float {
+        if (!(amax > 0.f) || amax == INFINITY) return 1.f;
+        const int ex = (int)(__float_as_uint(amax) >> 23) - 127;      // bf16 subnormals: ex = -127, still in range below
+        return exp2f((float)min(14 - ex, 100));
+    };
+    auto begin_unit = [&]() {
+        const int nrows = cu.ent.n * G;
+#pragma unroll
+        for (int b = 0; b < MT; ++b)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int row = b * 16 + hf * 8 + g;
+                const bool in = row < nrows;
+                const int tk = in ? row / G : 0;
+                pos[b][hf] = in ? cu.ent.ctx + tk : -1;
+                m[b][hf] = -INFINITY;
+                l[b][hf] = 0.f;
+                const uint8_t *qp = a.q + (int64_t)(cu.ent.tok0 + tk) * a.q_tok + (int64_t)(cu.h * G + (in ? row - tk * G : 0)) * a.q_head;
+                if (MT == 1) {
+                    // Thread c holds the dims that it reads of K (see the product below).
+                    float amax = 0.f;
+                    uint32_t w[KS][2];
+#pragma unroll
+                    for (int i = 0; i < KS * 8 / 16; ++i) {      // 16 bytes of Q each
+                        const int ch = FP8 ? (c + 4 * (i >> 1)) * 2 + (i & 1) : c + 4 * i;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (in) v = *reinterpret_cast<const uint4 *>(qp + ch * 16);
+                        w[2 * i][0] = v.x;
+                        w[2 * i][1] = v.y;
+                        w[2 * i + 1][0] = v.z;
+                        w[2 * i + 1][1] = v.w;
+                    }
+                    float f = 1.f;
+                    if (FP8) {
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                amax = fmax3(amax, fabsf(__uint_as_float(w[i][y] << 16)), fabsf(__uint_as_float(w[i][y] & 0xffff0000u)));
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                        f = row_factor(amax);
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                w[i][y] = pack_f16x2(__uint_as_float(w[i][y] << 16) * f, __uint_as_float(w[i][y] & 0xffff0000u) * f);
+                    }
+                    qs[b][hf] = a.scale_log2 * kds / f;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        qf[MT == 1 ? i : 0][hf] = w[i][0];
+                        qf[MT == 1 ? i : 0][2 + hf] = w[i][1];
+                    }
+                }
+            }
+#pragma unroll
+        for (int b = 0; b < MT; ++b)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) oa[b][t][y] = 0.f;
+        if (MT == 2) {
+            // Q of up to 32 rows to shared memory: eight threads a row, as bf16
+            // or as scaled fp16 (the factor kept behind the rows).
+            const int row = threadIdx.x >> 3, part = threadIdx.x & 7;
+            const bool in = row < nrows;
+            const int tk = in ? row / G : 0;
+            const uint8_t *qp = a.q + (int64_t)(cu.ent.tok0 + tk) * a.q_tok + (int64_t)(cu.h * G + (in ? row - tk * G : 0)) * a.q_head;
+            uint32_t w[D / 16];
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (in) v = *reinterpret_cast<const uint4 *>(qp + (part * (D / 64) + i) * 16);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+            float f = 1.f;
+            if (FP8) {
+                float amax = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    amax = fmax3(amax, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
+#pragma unroll
+                for (int y = 1; y < 8; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
+                f = row_factor(amax);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+            }
+            __syncthreads();                    // the previous unit's use of the space is over
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const int ch = part * (D / 64) + i;
+                *reinterpret_cast<uint4 *>(sq + row * D * 2 + ((ch ^ (FP8 ? (row & 1) : ((row & 1) << 2))) << 4)) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
+            if (part == 0) *reinterpret_cast<float *>(sq + kFewRows * D * 2 + row * 4) = f;
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < MT; ++b)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+                    qs[b][hf] = a.scale_log2 * kds / *reinterpret_cast<const float *>(sq + kFewRows * D * 2 + (b * 16 + hf * 8 + g) * 4);
+        }
+    };
+
+    // Sums the unit over the warps, in groups of eight output tiles through
+    // shared memory, and writes the rows or this CTA's partial result of them.
+    const uint32_t bid = blockIdx.x;
+    float4 *red = reinterpret_cast<float4 *>(smem + C::kRed);
+    float *sml = reinterpret_cast<float *>(smem + C::kMl);
+    volatile int *flag = reinterpret_cast<volatile int *>(smem + C::kMisc);
+    float *ws_o = reinterpret_cast<float *>(a.plan + a.L.off_few_o);
+    float *ws_ml = reinterpret_cast<float *>(a.plan + a.L.off_few_ml);
+
+    auto store4 = [&](const PagedEntry &en, int h, int row, int dim, float4 v, float inv) {
+        const int tk = row / G;
+        const int64_t at = ((int64_t)(en.tok0 + tk) * s.Hq + h * G + (row - tk * G)) * D + dim;
+        if (a.o_f32)
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + at) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        else
+            *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.o) + at) =
+                make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    };
+    auto store_lse = [&](const PagedEntry &en, int h, int row, float mx, float sum) {
+        const int tk = row / G;
+        a.lse[(int64_t)(en.tok0 + tk) * s.Hq + h * G + (row - tk * G)] =
+            sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : (sum == 0.f ? -INFINITY : sum);
+    };
+    // Pieces of the unit's output that a thread handles in the sums below: rows
+    // 8 (z >> 2) + g, columns of 4 in the order of the fragments.
+    auto dim_of = [&](int np, int z) {
+        const int cc = 2 * c + ((z >> 1) & 1), jq = (z & 1) * 4;
+        return (FP8 && D == 128) ? 16 * cc + 8 * np + jq : 64 * np + 8 * cc + jq;
+    };
+    auto end_unit = [&]() {
+        const PagedEntry en = cu.ent;
+        const int h = cu.h, nrows = en.n * G;
+        const int64_t ub = cum[cu.e] + (int64_t)cu.h * cu.kr.n;   // the unit's tiles are [ub, ub + n) of the list
+        const int c_first = share_owner(W, ctas, ub), c_last = share_owner(W, ctas, ub + cu.kr.n - 1);
+        const int parts = c_last - c_first + 1;
+#pragma unroll
+        for (int b = 0; b < MT; ++b)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float sum = l[b][hf];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (c == 0) {
+                    sml[(warp * 2) * kFewRows + b * 16 + hf * 8 + g] = m[b][hf];
+                    sml[(warp * 2 + 1) * kFewRows + b * 16 + hf * 8 + g] = sum;
+                }
+            }
+        __syncthreads();
+        // Slot of a partial result: 2 c + 1 when the unit begins in this CTA's share, 2 c when it comes in from the left.
+        const int slot = 2 * (int)bid + ((int)bid == c_first ? 1 : 0);
+#pragma unroll
+        for (int b = 0; b < MT; ++b) {
+            float f[2], inv[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int row = b * 16 + hf * 8 + g;
+                float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sml[(w * 2) * kFewRows + row]);
+                const float mu = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) sum += sml[(w * 2 + 1) * kFewRows + row] * ex2(sml[(w * 2) * kFewRows + row] - mu);
+                f[hf] = ex2(m[b][hf] - mu);
+                inv[hf] = sum != 0.f ? vds / sum : 0.f;
+                if (warp == 0 && c == 0 && row < nrows) {
+                    if (parts == 1) {
+                        store_lse(en, h, row, mx, sum);
+                    } else {
+                        __stcg(ws_ml + (int64_t)slot * 2 * kFewRows + row, mx);
+                        __stcg(ws_ml + (int64_t)slot * 2 * kFewRows + kFewRows + row, sum);
+                    }
+                }
+            }
+#pragma unroll
+            for (int np = 0; np < NP; ++np) {
+                if (b > 0 || np > 0) __syncthreads();
+                // piece z = (row half, column half, 4 of 8 tiles)
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    const int hf = z >> 2, y = 2 * hf + ((z >> 1) & 1), t = np * 8 + (z & 1) * 4;
+                    if (b * 16 + hf * 8 < nrows)
+                        red[(warp * 8 + z) * 32 + lane] = make_float4(oa[b][t][y] * f[hf], oa[b][t + 1][y] * f[hf],
+                                                                      oa[b][t + 2][y] * f[hf], oa[b][t + 3][y] * f[hf]);
+                }
+                __syncthreads();
+                const int z = warp, row = b * 16 + (z >> 2) * 8 + g;
+                if (row < nrows) {
+                    float4 v = red[z * 32 + lane];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) {
+                        const float4 u = red[(w * 8 + z) * 32 + lane];
+                        v.x += u.x;
+                        v.y += u.y;
+                        v.z += u.z;
+                        v.w += u.w;
+                    }
+                    if (parts == 1)
+                        store4(en, h, row, dim_of(np, z), v, inv[z >> 2]);
+                    else
+                        __stcg(reinterpret_cast<float4 *>(ws_o + ((int64_t)slot * kFewRows + row) * D + dim_of(np, z)), v);
+                }
+            }
+        }
+        if (parts == 1) return;
+        // A split unit: the last of its CTAs adds the partial results up, in the CTAs' order.
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            unsigned *cnt = reinterpret_cast<unsigned *>(a.plan + a.L.off_count) + c_first;
+            *flag = atomicInc(cnt, (unsigned)(parts - 1)) == (unsigned)(parts - 1);   // returns to 0 by itself
+            __threadfence();
+        }
+        __syncthreads();
+        if (!*flag) return;
+        float *wt = reinterpret_cast<float *>(red);             // [part][row] weights, then [row] 1 / sum
+        for (int row = warp; row < nrows; row += kWarps) {
+            float mx = -INFINITY;
+            for (int p = lane; p < parts; p += 32)
+                mx = fmaxf(mx, __ldcg(ws_ml + (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)) * 2 * kFewRows + row));
+#pragma unroll
+            for (int y = 1; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
+            const float mu = mx == -INFINITY ? 0.f : mx;
+            float sum = 0.f;
+            for (int p = lane; p < parts; p += 32) {
+                const float *pm = ws_ml + (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)) * 2 * kFewRows + row;
+                const float w = ex2(__ldcg(pm) - mu);
+                wt[p * kFewRows + row] = w;
+                sum += w * __ldcg(pm + kFewRows);
+            }
+#pragma unroll
+            for (int y = 1; y < 32; y <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+            if (lane == 0) {
+                store_lse(en, h, row, mx, sum);
+                sml[row] = sum != 0.f ? vds / sum : 0.f;
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
+            const int row = i / (D / 4), dim = (i % (D / 4)) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int p = 0; p < parts; ++p) {
+                const float w = wt[p * kFewRows + row];
+                const float4 u = __ldcg(reinterpret_cast<const float4 *>(
+                    ws_o + ((int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)) * kFewRows + row) * D + dim));
+                v.x += u.x * w;
+                v.y += u.y * w;
+                v.z += u.z * w;
+                v.w += u.w * w;
+            }
+            store4(en, h, row, dim, v, sml[row]);
+        }
+        __syncthreads();
+    };
+
+    // ---- the walk -------------------------------------------------------------
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) load_tile();
+    begin_unit();
+    int slot = 0;
+    while (left > 0) {
+        load_tile();                    // into the slot that the previous round has read
+        cp_async_wait<ST - 1>();
+        __syncwarp();
+        const int k0 = cu.kr.tile(cu.x) * kKeyTile + warp * 16;
+        const bool some = k0 < cu.kr.hi && !(k0 + 16 <= cu.kr.lo && k0 >= s.sink);
+        if (some) {
+            const uint32_t kb = ring + slot * C::kSlot, vb = kb + 16 * C::kRow;
+            float sc[MT][2][4];
+#pragma unroll
+            for (int b = 0; b < MT; ++b)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) sc[b][nt][y] = 0.f;
+            // Scores: 16 bytes of a key per thread and load are two k-steps of
+            // bf16 (words 0, 1 and 2, 3) or four of e4m3 (one word each).
+#pragma unroll
+            for (int i = 0; i < CH / 4; ++i) {
+                constexpr int PER = FP8 ? 4 : 2;
+                uint32_t qa[MT][PER][4];
+#pragma unroll
+                for (int b = 0; b < MT; ++b) {
+                    if (MT == 1) {
+#pragma unroll
+                        for (int y = 0; y < PER; ++y)
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) qa[b][y][z] = qf[MT == 1 ? i * PER + y : 0][z];
+                    } else {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int row = b * 16 + hf * 8 + g;
+                            const uint32_t base = smem_u32(sq) + row * D * 2;
+#pragma unroll
+                            for (int y = 0; y < PER / 2; ++y) {
+                                const int ch = FP8 ? (c + 4 * i) * 2 + y : c + 4 * i;
+                                const uint4 v = lds128(base + ((ch ^ (FP8 ? (row & 1) : ((row & 1) << 2))) << 4));
+                                qa[b][2 * y][hf] = v.x;
+                                qa[b][2 * y][2 + hf] = v.y;
+                                qa[b][2 * y + 1][hf] = v.z;
+                                qa[b][2 * y + 1][2 + hf] = v.w;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const uint4 kv = lds128(kb + swz_k<CH>(nt * 8 + g, c + 4 * i));
+                    const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+                    for (int y = 0; y < PER; ++y) {
+                        const uint32_t b0 = FP8 ? f16x2_of_e4m3(w[y]) : w[(2 * y) & 3];
+                        const uint32_t b1 = FP8 ? f16x2_of_e4m3(w[y] >> 16) : w[(2 * y + 1) & 3];
+#pragma unroll
+                        for (int b = 0; b < MT; ++b)
+                            mma16816<FP8>(sc[b][nt], qa[b][y][0], qa[b][y][1], qa[b][y][2], qa[b][y][3], b0, b1);
+                    }
+                }
+            }
+            // Scaled, masked where some row does not attend some of the 16 keys.
+            const bool edge = s.window > 0 || k0 + 15 > cu.ent.ctx;
+#pragma unroll
+            for (int b = 0; b < MT; ++b)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        float x = sc[b][nt][y] * qs[b][y >> 1];
+                        if (edge) {
+                            const int j = k0 + nt * 8 + 2 * c + (y & 1), p = pos[b][y >> 1];
+                            if (!(j <= p && (s.window == 0 || j > p - s.window || j < s.sink))) x = -INFINITY;
+                        }
+                        sc[b][nt][y] = x;
+                    }
+            // Running maxima (raised lazily), P and its sums.
+            uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+            for (int b = 0; b < MT; ++b) {
+                bool raise = false;
+                float mn[2];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float x = fmaxf(fmaxf(sc[b][0][2 * hf], sc[b][0][2 * hf + 1]), fmaxf(sc[b][1][2 * hf], sc[b][1][2 * hf + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    mn[hf] = x > m[b][hf] + kBand ? x : m[b][hf];
+                    raise = raise || mn[hf] != m[b][hf];
+                }
+                if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const float f = m[b][hf] == mn[hf] ? 1.f : ex2(m[b][hf] - mn[hf]);
+                        m[b][hf] = mn[hf];
+                        l[b][hf] *= f;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            oa[b][t][2 * hf] *= f;
+                            oa[b][t][2 * hf + 1] *= f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float mu = m[b][hf] == -INFINITY ? 0.f : m[b][hf];
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const float p0 = ex2(sc[b][nt][2 * hf] - mu), p1 = ex2(sc[b][nt][2 * hf + 1] - mu);
+                        l[b][hf] += p0 + p1;
+                        const uint32_t hi = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                        ph[b][2 * nt + hf] = hi;
+                        if (TWO) {
+                            if (FP8) {
+                                const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                                pl[b][2 * nt + hf] = pack_f16x2(p0 - u.x, p1 - u.y);
+                            } else {
+                                pl[b][2 * nt + hf] = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+                            }
+                        }
+                    }
+                }
+            }
+            // O += P V: the thread's two key pairs, columns as dim_of() says.
+            auto pv = [&](int t, uint32_t b0, uint32_t b1) {
+#pragma unroll
+                for (int b = 0; b < MT; ++b) {
+                    mma16816<FP8>(oa[b][t], ph[b][0], ph[b][1], ph[b][2], ph[b][3], b0, b1);
+                    if (TWO) mma16816<FP8>(oa[b][t], pl[b][0], pl[b][1], pl[b][2], pl[b][3], b0, b1);
+                }
+            };
+            const int rows[4] = {2 * c, 2 * c + 1, 2 * c + 8, 2 * c + 9};
+            if (!FP8) {
+#pragma unroll
+                for (int np = 0; np < NP; ++np) {
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint4 v = lds128(vb + swz_v<CH>(rows[r], np * 8 + g));
+                        w[r][0] = v.x;
+                        w[r][1] = v.y;
+                        w[r][2] = v.z;
+                        w[r][3] = v.w;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        pv(np * 8 + 2 * x, __byte_perm(w[0][x], w[1][x], 0x5410), __byte_perm(w[2][x], w[3][x], 0x5410));
+                        pv(np * 8 + 2 * x + 1, __byte_perm(w[0][x], w[1][x], 0x7632), __byte_perm(w[2][x], w[3][x], 0x7632));
+                    }
+                }
+            } else {
+                constexpr int WD = D / 32;      // words of e4m3 per key and thread
+                uint32_t w[4][WD];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if (WD == 4) {
+                        const uint4 v = lds128(vb + swz_v<CH>(rows[r], g));
+                        w[r][0] = v.x;
+                        w[r][1] = v.y;
+                        w[r][2 % WD] = v.z;
+                        w[r][3 % WD] = v.w;
+                    } else {
+                        const uint2 v = lds64(vb + swz_v<CH>(rows[r], g >> 1) + (g & 1) * 8);
+                        w[r][0] = v.x;
+                        w[r][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < WD; ++x)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t e[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) e[r] = f16x2_of_e4m3(w[r][x] >> (16 * half));
+                        pv(4 * x + 2 * half, __byte_perm(e[0], e[1], 0x5410), __byte_perm(e[2], e[3], 0x5410));
+                        pv(4 * x + 2 * half + 1, __byte_perm(e[0], e[1], 0x7632), __byte_perm(e[2], e[3], 0x7632));
+                    }
+            }
+        }
+        __syncwarp();                   // every lane has read the slot before it is filled again
+        slot = slot + 1 == ST ? 0 : slot + 1;
+        --left;
+        const bool last_of_unit = cu.x + 1 == cu.kr.n || left == 0;
+        if (last_of_unit) end_unit();
+        advance(cu, left > 0);
+        if (last_of_unit && left > 0) begin_unit();
+    }
+    cp_async_wait<0>();
+}
+
+}  // namespace fm
+
+using namespace fm;
+
+namespace {
+
+template <int D, bool FP8, int MT, bool TWO>
+fm_status launch(const PagedArgs &a, cudaStream_t stream)
+{
+    constexpr int smem = DecodeCfg<D, FP8>::kBytes;
+    static std::atomic<uint8_t> done[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FM_ERR_CUDA;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(fm_paged_decode_kernel<D, FP8, MT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess)
+            return FM_ERR_CUDA;
+        done[dev].store(1, std::memory_order_release);
+    }
+    ProfScope ps(kKPagedDecode, stream);
+    fm_paged_decode_kernel<D, FP8, MT, TWO><<<kPagedCtas, kWarps * 32, smem, stream>>>(a);
+    return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+}
+
+template <int D, bool FP8>
+fm_status launch_rows(const PagedArgs &a, cudaStream_t stream)
+{
+    // One block of 16 rows where no request can have more, else two.
+    const bool one = (int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv) <= 16;
+    if constexpr (FP8)
+        if (!a.o_f32) return one ? launch<D, FP8, 1, false>(a, stream) : launch<D, FP8, 2, false>(a, stream);
+    return one ? launch<D, FP8, 1, true>(a, stream) : launch<D, FP8, 2, true>(a, stream);
+}
+
+}  // namespace
+
+fm_status fm_paged_decode_launch(const PagedArgs &a, bool e4m3, cudaStream_t stream)
+{
+    if (a.s.d == 128) return e4m3 ? launch_rows<128, true>(a, stream) : launch_rows<128, false>(a, stream);
+    return e4m3 ? launch_rows<64, true>(a, stream) : launch_rows<64, false>(a, stream);
+}

@@ -22,12 +22,12 @@ _lib = ctypes.CDLL(_LIB_PATH)
 
 FM_OK, FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_UNREPRESENTABLE = 0, 1, 2, 3
 FM_ERR_BAD_BOUNDS, FM_ERR_PLAN_MISMATCH, FM_ERR_WORKSPACE, FM_ERR_CUDA, FM_ERR_TIMEOUT = 4, 5, 6, 7, 8
-FM_ERR_DEBUG_CHECK = 9
+FM_ERR_DEBUG_CHECK, FM_ERR_LENGTHS, FM_ERR_PAGES = 9, 10, 11
 FM_TILE_SKIP, FM_TILE_FULL, FM_TILE_PARTIAL = 0, 1, 2
-FM_DT_BF16, FM_DT_F32 = 0, 1
+FM_DT_BF16, FM_DT_F32, FM_DT_E4M3 = 0, 1, 2
 FM_FLAG_PRECISE = 1
 KERNEL_NAMES = ["classify_minmax", "classify_lists", "fwd", "bwd_pre", "bwd", "bwd_post",
-                "classify_order", "fp8_amax", "fp8_convert"]
+                "classify_order", "fp8_amax", "fp8_convert", "paged_plan", "paged_append", "paged_decode"]
 
 EXPORTED = ["fm_status_string", "fm_abi_version", "fm_mask_from_rows", "fm_mask_from_row_intervals",
             "fm_plan_bytes", "fm_tile_classify", "fm_fwd_workspace_bytes", "fm_attn_fwd", "fm_bwd_workspace_bytes",
@@ -35,7 +35,8 @@ EXPORTED = ["fm_status_string", "fm_abi_version", "fm_mask_from_rows", "fm_mask_
             "fm_attn_bwd_noalloc", "fm_step_graph_create", "fm_step_graph_launch", "fm_step_graph_destroy",
             "fm_plan_bytes_rows", "fm_tile_classify_rows", "fm_attn_fwd_rows", "fm_attn_bwd_rows",
             "fm_quantize_fp8", "fm_attn_fwd_fp8", "fm_debug_wait_test", "fm_bounds_compressed_bytes",
-            "fm_bounds_compress", "fm_bounds_decompress"]
+            "fm_bounds_compress", "fm_bounds_decompress", "fm_paged_plan_bytes", "fm_paged_plan", "fm_paged_append",
+            "fm_attn_paged"]
 # Size of the library's built-in backward workspace (FM_NOALLOC_SCRATCH_BYTES in fm.h).
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
@@ -62,6 +63,20 @@ class StepArgs(ctypes.Structure):
                 ("ws_bytes", ctypes.c_size_t), ("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int),
                 ("d", ctypes.c_int), ("scale", ctypes.c_float), ("flags", ctypes.c_int),
                 ("dev_status", ctypes.c_void_p)]
+
+
+class PagedStep(ctypes.Structure):
+    """fm_paged_step of include/fm.h: the sizes that a step's plan is built for."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("requests", "max_tokens", "max_q", "max_pages", "num_pages", "page_size",
+                                              "Hq", "Hkv", "d", "window", "sink")]
+
+
+class PagedCache(ctypes.Structure):
+    """fm_paged_cache of include/fm.h."""
+    _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] +
+                [(n, ctypes.c_int64) for n in ("k_page", "k_head", "k_tok", "v_page", "v_head", "v_tok")] +
+                [("k_descale", ctypes.c_void_p), ("v_descale", ctypes.c_void_p)] +
+                [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "Hkv", "d", "dtype")])
 
 
 class KernelTime(ctypes.Structure):
@@ -104,6 +119,13 @@ _lib.fm_attn_bwd_rows.argtypes = [_P, _P, _P, _P, _I, _P, _P, Bounds, _P, _I, _I
                                   _P, _I, _I, _P, _SZ, _P, _P]
 _lib.fm_quantize_fp8.argtypes = [_P, _I, _I, _I, _I, _I, _P, _P, _P]
 _lib.fm_attn_fwd_fp8.argtypes = [_P, _P, _P, _P, Bounds, _P, _I, _I, _I, _I, _F, _P, _I, _P, _P, _P]
+_lib.fm_paged_plan_bytes.restype = _SZ
+_lib.fm_paged_plan_bytes.argtypes = [ctypes.POINTER(PagedStep)]
+_lib.fm_paged_plan.argtypes = [ctypes.POINTER(PagedStep), _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]
+_lib.fm_paged_append.argtypes = [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int64, _P, _I,
+                                 ctypes.POINTER(PagedCache), _P, _P]
+_lib.fm_attn_paged.argtypes = [ctypes.POINTER(PagedStep), _P, ctypes.c_int64, ctypes.c_int64, _I,
+                               ctypes.POINTER(PagedCache), _P, _P, _SZ, _F, _P, _I, _P, _P, _P]
 _lib.fm_step_graph_create.argtypes = [ctypes.POINTER(StepArgs), ctypes.POINTER(ctypes.c_void_p)]
 _lib.fm_step_graph_launch.argtypes = [_P, _P]
 _lib.fm_step_graph_destroy.argtypes = [_P]
@@ -412,6 +434,139 @@ def fm_attn_fwd_fp8(q8, k8, vt8, descale, bounds: Bounds, plan, scale, o, lse, d
     _check(code, "fm_attn_fwd_fp8")
 
 
+def _same_device(first, **tensors):
+    """All tensors on the first one's device, which has to be the current one (kernels launch there)."""
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    for n, t in tensors.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{n} is on {t.device}, not on {first.device}")
+
+
+def _rows(t, name, d=None):
+    """bf16 [T, H, d] rows with any token and head strides: (token stride, head stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1) or (d is not None and t.shape[2] != d):
+        raise ValueError(f"{name} must be [T, H, {d or 'd'}] with a contiguous last dimension")
+    T, H, _ = t.shape
+    st, sh, _ = t.stride()
+    return st if T > 1 else 0, sh if H > 1 else 0
+
+
+def paged_cache(k_cache, v_cache, k_descale=None, v_descale=None) -> PagedCache:
+    """fm_paged_cache of two page pools [num_pages, Hkv, page_size, d]: bf16, or
+    e4m3 (uint8 codes or torch.float8_e4m3fn) with device float32 [1] descales.
+    Views with other strides (tokens before heads, K and V interleaved) serve
+    as they are, so long as the last dimension is contiguous."""
+    c = PagedCache()
+    for n, t in (("k", k_cache), ("v", v_cache)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{n}_cache must be a CUDA tensor")
+        if t.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn) or t.dtype != k_cache.dtype:
+            raise TypeError("caches must both be bfloat16, or both hold e4m3 codes (uint8 or float8_e4m3fn)")
+        if t.dim() != 4 or t.shape != k_cache.shape or t.stride(3) != 1:
+            raise ValueError("caches must be [num_pages, Hkv, page_size, d], of one shape, with a contiguous last dimension")
+    shape = k_cache.shape
+    d = shape[3]
+    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
+    # The stride of a dimension of size one is never used.
+    c.k_page, c.k_head, c.k_tok = (s if n > 1 else d for s, n in zip(k_cache.stride(), shape[:3]))
+    c.v_page, c.v_head, c.v_tok = (s if n > 1 else d for s, n in zip(v_cache.stride(), shape[:3]))
+    c.num_pages, c.Hkv, c.page_size, c.d = shape
+    c.dtype = FM_DT_BF16
+    if k_cache.dtype != torch.bfloat16:
+        c.dtype = FM_DT_E4M3
+        if k_descale is None or v_descale is None:
+            raise ValueError("an e4m3 cache needs k_descale and v_descale")
+        c.k_descale = _dev(k_descale, torch.float32, "k_descale").data_ptr()
+        c.v_descale = _dev(v_descale, torch.float32, "v_descale").data_ptr()
+    _same_device(k_cache, v_cache=v_cache, k_descale=k_descale, v_descale=v_descale)
+    return c
+
+
+def fm_paged_plan_bytes(step: PagedStep) -> int:
+    return int(_lib.fm_paged_plan_bytes(ctypes.byref(step)))
+
+
+def fm_paged_plan(step: PagedStep, ctx_lens, q_lens, block_table, seq_lens, cu_q, slots, positions, plan, dev_status,
+                  free_pages=None, free_head=None, free_next=None, stream=None):
+    """Block tables, slot map, positions and attention plan of a step (see fm.h).
+    ctx_lens, q_lens, seq_lens: int32 [requests]; block_table: int32 [requests,
+    max_pages]; cu_q: int32 [requests + 1]; slots: int64, positions: int32 or
+    None [max_tokens]; free_pages: int32 [n] with free_head and free_next int32 [1]."""
+    R = step.requests
+    for n, t, dt, shape in (("ctx_lens", ctx_lens, torch.int32, (R,)), ("q_lens", q_lens, torch.int32, (R,)),
+                            ("block_table", block_table, torch.int32, (R, step.max_pages)),
+                            ("seq_lens", seq_lens, torch.int32, (R,)), ("cu_q", cu_q, torch.int32, (R + 1,)),
+                            ("slots", slots, torch.int64, (step.max_tokens,)), ("plan", plan, torch.uint8, None),
+                            ("dev_status", dev_status, torch.int32, (1,))):
+        if _dev(t, dt, n).shape != shape and shape is not None:
+            raise ValueError(f"{n} must have the shape {list(shape)}")
+    if positions is not None and _dev(positions, torch.int32, "positions").shape != slots.shape:
+        raise ValueError("positions must have the shape of slots")
+    if free_pages is not None:
+        if free_head is None or free_next is None:
+            raise ValueError("free_pages comes with free_head and free_next")
+        for n, t in (("free_pages", free_pages), ("free_head", free_head), ("free_next", free_next)):
+            if _dev(t, torch.int32, n).dim() != 1 or (t is not free_pages and t.numel() != 1):
+                raise ValueError("free_pages is int32 [n], free_head and free_next are int32 [1]")
+    _same_device(ctx_lens, q_lens=q_lens, block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, slots=slots,
+                 positions=positions, plan=plan, dev_status=dev_status, free_pages=free_pages, free_head=free_head,
+                 free_next=free_next)
+    code = _lib.fm_paged_plan(ctypes.byref(step), _ptr(ctx_lens), _ptr(q_lens), _ptr(block_table), _ptr(free_pages),
+                              0 if free_pages is None else free_pages.numel(), _ptr(free_head), _ptr(free_next),
+                              _ptr(seq_lens), _ptr(cu_q), _ptr(slots), _ptr(positions), _ptr(plan), plan.numel(),
+                              _ptr(dev_status), _stream(stream))
+    _check(code, "fm_paged_plan")
+
+
+def fm_paged_append(k, v, slots, k_cache, v_cache, dev_status, k_descale=None, v_descale=None, stream=None):
+    """Rows of k and v (bf16 [T, Hkv, d], any token and head strides) to the cache's
+    slots (int64, T of them at least; negative ones are skipped)."""
+    cache = paged_cache(k_cache, v_cache, k_descale, v_descale)
+    kt, kh = _rows(k, "k", cache.d)
+    vt, vh = _rows(v, "v", cache.d)
+    T = k.shape[0]
+    if v.shape != k.shape or k.shape[1] != cache.Hkv:
+        raise ValueError("k and v must be [T, Hkv, d] of the cache")
+    if _dev(slots, torch.int64, "slots").dim() != 1 or slots.shape[0] < T:
+        raise ValueError("slots must be int64 with an entry for every row of k")
+    _dev(dev_status, torch.int32, "dev_status")
+    _same_device(k_cache, k=k, v=v, slots=slots, dev_status=dev_status)
+    if T == 0:
+        return
+    code = _lib.fm_paged_append(_ptr(k), kt, kh, _ptr(v), vt, vh, _ptr(slots), T, ctypes.byref(cache), _ptr(dev_status),
+                                _stream(stream))
+    _check(code, "fm_paged_append")
+
+
+def fm_attn_paged(step: PagedStep, q, k_cache, v_cache, block_table, plan, scale, o, lse, dev_status, k_descale=None,
+                  v_descale=None, stream=None):
+    """Attention of a step's new tokens (q: bf16 [rows, Hq, d]) over the paged cache;
+    o: bf16 or fp32 [rows, Hq, d], lse: fp32 [rows, Hq] (see fm.h)."""
+    cache = paged_cache(k_cache, v_cache, k_descale, v_descale)
+    qt, qh = _rows(q, "q", step.d)
+    if q.shape[1] != step.Hq:
+        raise ValueError("q must be [rows, Hq, d] of the step")
+    _dev(o, o.dtype, "o")
+    if o.shape != q.shape or _dev(lse, torch.float32, "lse").shape != q.shape[:2]:
+        raise ValueError("o must have the shape of q, and lse [rows, Hq]")
+    if _dev(block_table, torch.int32, "block_table").shape != (step.requests, step.max_pages):
+        raise ValueError("block_table must be [requests, max_pages]")
+    _dev(plan, torch.uint8, "plan")
+    _dev(dev_status, torch.int32, "dev_status")
+    _same_device(q, k_cache=k_cache, o=o, lse=lse, block_table=block_table, plan=plan, dev_status=dev_status)
+    if q.shape[0] == 0:
+        return
+    code = _lib.fm_attn_paged(ctypes.byref(step), _ptr(q), qt, qh, q.shape[0], ctypes.byref(cache), _ptr(block_table),
+                              _ptr(plan), plan.numel(), float(scale), _ptr(o), _dt(o), _ptr(lse), _ptr(dev_status),
+                              _stream(stream))
+    _check(code, "fm_attn_paged")
+
+
 def fm_step_graph_create(q, k, v, dO, bounds: Bounds, plan, scale, o, lse, dev_status, dq=None, dk=None,
                          dv=None, ws=None, flags=0):
     """Capture classify + forward (+ backward when dO is given) for these
@@ -514,6 +669,51 @@ class MaskedAttention:
         fm_attn_bwd(q, k, v, o, lse, dO, self.bounds, self.plan, scale, dq, dk, dv, ws, self.status,
                     stream=self.stream, flags=flags)
         return dq, dk, dv
+
+    def check_status(self):
+        code = int(self.status.item())
+        if code != 0:
+            raise FmError(code, "device")
+
+
+class PagedAttention:
+    """A batch of requests over a paged cache: the step's sizes, plan, slot map and
+    status word.  Per step one plan() (lengths and block table on the device), then
+    per layer an append() and an attend() with that layer's cache."""
+
+    def __init__(self, requests, Hq, Hkv, d, page_size, num_pages, max_pages, max_tokens, max_q, window=0, sink=0,
+                 device="cuda"):
+        self.step = PagedStep(requests, max_tokens, max_q, max_pages, num_pages, page_size, Hq, Hkv, d, window, sink)
+        n = fm_paged_plan_bytes(self.step)
+        if n == 0:
+            raise ValueError("sizes of the step outside what fm.h allows")
+        i32 = dict(dtype=torch.int32, device=device)
+        self.plan_buffer = torch.empty(n, dtype=torch.uint8, device=device)
+        self.cu_q = torch.empty(requests + 1, **i32)
+        self.seq_lens = torch.empty(requests, **i32)
+        self.slots = torch.empty(max_tokens, dtype=torch.int64, device=device)
+        self.positions = torch.empty(max_tokens, **i32)
+        self.free_next = torch.empty(1, **i32)
+        self.status = torch.zeros(1, **i32)
+
+    def plan(self, ctx_lens, q_lens, block_table, free_pages=None, free_head=None, in_place=False):
+        """Plans a step; with in_place, ctx_lens and free_head are advanced too
+        (a captured step can then be replayed)."""
+        fm_paged_plan(self.step, ctx_lens, q_lens, block_table, ctx_lens if in_place else self.seq_lens, self.cu_q,
+                      self.slots, self.positions, self.plan_buffer, self.status, free_pages, free_head,
+                      None if free_pages is None else free_head if in_place else self.free_next)
+
+    def append(self, k, v, k_cache, v_cache, k_descale=None, v_descale=None):
+        fm_paged_append(k, v, self.slots, k_cache, v_cache, self.status, k_descale, v_descale)
+
+    def attend(self, q, k_cache, v_cache, block_table, scale=None, o_dtype=torch.bfloat16, k_descale=None,
+               v_descale=None):
+        scale = 1.0 / self.step.d ** 0.5 if scale is None else scale
+        o = torch.empty(q.shape, dtype=o_dtype, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        fm_attn_paged(self.step, q, k_cache, v_cache, block_table, self.plan_buffer, scale, o, lse, self.status,
+                      k_descale, v_descale)
+        return o, lse
 
     def check_status(self):
         code = int(self.status.item())
