@@ -366,11 +366,12 @@ FM_API fm_status fm_attn_fwd_fp8(const uint8_t *q8, const uint8_t *k8, const uin
  *   last dimension contiguous), o [rows, Hq, d] and lse fp32 [rows, Hq] contiguous,
  *   with rows at least cu_q[requests] (else FM_ERR_LENGTHS in dev_status and nothing
  *   is written); rows at or behind cu_q[requests] are left as they were.  `step` has to be the plan's (else FM_ERR_PLAN_MISMATCH in dev_status),
- *   block_table the one it was built from.  Keys that no row of a request
- *   attends are never part of a product, whatever their pages hold: entries of
- *   pages wholly outside the window may be stale, and what lies behind the last
- *   token may be NaN.  A page number outside [0, num_pages) among the others
- *   gives FM_ERR_PAGES and its keys read as zeros.  Outputs are rounded once; P
+ *   block_table the one it was built from.  Pages that no row of their request
+ *   attends are not read, so their table entries may be stale (behind a window),
+ *   and what a page holds behind the request's last token may be NaN.  The
+ *   request's own tokens are expected to be finite: a value that is not may reach
+ *   rows of the same request whose mask excludes it.  A page number outside
+ *   [0, num_pages) among the attended gives FM_ERR_PAGES and its keys read as zeros.  Outputs are rounded once; P
  *   keeps 16 bits or more in the second product when o is fp32 or the rows are few
  *   (see the kernels).
  *   The plan holds the workspace as well: calls that share a plan (any number of layers
@@ -461,7 +462,7 @@ FM_API fm_status fm_step_graph_destroy(fm_step_graph graph);
 enum { FM_K_CLASSIFY_MINMAX = 0, FM_K_CLASSIFY_LISTS = 1, FM_K_FWD = 2, FM_K_BWD_PRE = 3,
        FM_K_BWD = 4, FM_K_BWD_POST = 5, FM_K_CLASSIFY_ORDER = 6, FM_K_FP8_AMAX = 7,
        FM_K_FP8_CONVERT = 8, FM_K_PAGED_PLAN = 9, FM_K_PAGED_APPEND = 10, FM_K_PAGED_DECODE = 11,
-       FM_K_COUNT = 12 };
+       FM_K_PAGED_CHUNK = 12, FM_K_COUNT = 13 };
 typedef struct {
     int32_t kernel;
     float ms;

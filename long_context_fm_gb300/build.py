@@ -23,7 +23,7 @@ LIB = os.path.join(OUT_DIR, "libfm.so")
 DEBUG_DIR = os.path.join(OUT_DIR, "debug")
 DEBUG_LIB = os.path.join(DEBUG_DIR, "libfm_debug.so")
 SOURCES = ["fm_api.cu", "fm_classify.cu", "fm_fwd.cu", "fm_bwd.cu", "fm_fp8.cu", "fm_compress.cu", "fm_noalloc.cu",
-           "fm_paged.cu", "fm_paged_decode.cu", "fm_mask.cpp"]
+           "fm_paged.cu", "fm_paged_decode.cu", "fm_paged_chunk.cu", "fm_mask.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

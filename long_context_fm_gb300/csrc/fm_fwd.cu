@@ -94,17 +94,6 @@ struct FwdSmem {
     static constexpr int kBytes = (kMisc + 64 > 120 * 1024) ? kMisc + 64 : 120 * 1024;
 };
 
-
-// Bits x of a 32-row group with lo <= x < hi (bounds clamped to [0, 32]): the
-// bits at or above lo and below hi, as two clamping funnel shifts (a shift by
-// 32 gives 0); empty when hi <= lo.
-__device__ __forceinline__ uint32_t row_bits32(int lo, int hi)
-{
-    lo = min(max(lo, 0), 32);
-    hi = min(max(hi, 0), 32);
-    return __funnelshift_lc(0u, 0xffffffffu, (uint32_t)lo) & __funnelshift_rc(0xffffffffu, 0u, (uint32_t)(32 - hi));
-}
-
 constexpr int kSB = 3;              // score buffers in TMEM
 constexpr int kUnitRing = 4;        // claimed units buffered between the K producer and the other roles
 constexpr int kUnitReaders = 11;    // V producer, two MMA issuers, eight softmax warps

@@ -185,6 +185,7 @@ enum KernelId {
     kKPagedPlan = FM_K_PAGED_PLAN,
     kKPagedAppend = FM_K_PAGED_APPEND,
     kKPagedDecode = FM_K_PAGED_DECODE,
+    kKPagedChunk = FM_K_PAGED_CHUNK,
 };
 
 // Devices a process may use (per-device caches of kernel attributes).

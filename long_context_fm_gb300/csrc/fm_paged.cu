@@ -83,10 +83,23 @@ __device__ __forceinline__ int last_at_most(const T *a, int n, T x)
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs a)
+// Pieces per many-rows unit: whole units once they fill the GPU twice over; else
+// about three pieces per CTA, of at least eight tiles on average (a piece costs its
+// partial sums and the pipeline's start, together about four tiles).
+__device__ __forceinline__ int split_of(int64_t units, int64_t tiles)
+{
+    if (units == 0 || units > kMaxSplitUnits) return 1;
+    const int64_t want = (3 * kPagedCtas + units - 1) / units, most = kMaxPieces / units, by_len = tiles / units / 8;
+    int64_t x = want < most ? want : most;
+    x = x < by_len ? x : by_len;
+    return x > 1 ? (int)x : 1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanArgs a)
 {
     extern __shared__ __align__(16) uint8_t plan_smem[];
-    __shared__ int64_t sh[kPlanWarps][4];
+    constexpr int NV = 7;   // tokens, pages; few: entries, tiles; many: entries, units, tiles (about)
+    __shared__ int64_t sh[kPlanWarps][NV];
     const PagedShape &s = a.s;
     const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;
     int64_t *s_tiles = reinterpret_cast<int64_t *>(plan_smem);             // [R + 1] tiles before few-rows entry i
@@ -98,7 +111,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
     int64_t *few_cum = reinterpret_cast<int64_t *>(a.plan + a.L.off_few_cum);
     const int32_t head = a.free_pages ? *a.free_head : 0;
 
-    int64_t run[4] = {0, 0, 0, 0};
+    PagedEntry *many = reinterpret_cast<PagedEntry *>(a.plan + a.L.off_many);
+    int32_t *many_cum = reinterpret_cast<int32_t *>(a.plan + a.L.off_many_cum);
+    const int tpt = 128 / G;                 // tokens of a many-rows unit
+    int64_t run[NV] = {};
     bool bad = false;
     for (int r0 = 0; r0 < s.R; r0 += kPlanThreads) {
         const int r = r0 + tid;
@@ -112,13 +128,21 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
             }
         }
         const bool is_few = n > 0 && (int64_t)n * G <= kFewRows;
+        const bool is_many = n > 0 && !is_few;
         KeyRange kr{};
         if (is_few) kr = key_range(ctx, ctx + n - 1, s.window, s.sink);
-        int64_t v[4], total[4];
+        const int64_t units = is_many ? (int64_t)((n + tpt - 1) / tpt) * s.Hkv : 0;
+        int64_t v[NV], total[NV];
         v[0] = n;
         v[1] = (ctx + n + s.page_size - 1) / s.page_size - (ctx + s.page_size - 1) / s.page_size;
         v[2] = is_few;
         v[3] = is_few ? (int64_t)kr.n * s.Hkv : 0;
+        v[4] = is_many;
+        v[5] = units;
+        v[6] = 0;
+        if (is_many)        // the units' mean length lies between the first one's and the last one's
+            v[6] = units * (key_range(ctx, ctx + min(n, tpt) - 1, s.window, s.sink).n +
+                            key_range(ctx + (n - 1) / tpt * tpt, ctx + n - 1, s.window, s.sink).n) / 2;
         block_scan(v, total, sh);
         if (r < s.R) {
             s_cu[r] = (int32_t)(run[0] + v[0]);     // meaningful when the total fits (checked below)
@@ -131,14 +155,19 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
                     few_cum[e] = run[3] + v[3];
                 }
             }
+            if (is_many && cta == 0) {
+                const int e = (int)(run[4] + v[4]);
+                many[e] = PagedEntry{r, (int32_t)(run[0] + v[0]), n, ctx};
+                many_cum[e] = (int32_t)(run[5] + v[5]);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) run[i] += total[i];
+        for (int i = 0; i < NV; ++i) run[i] += total[i];
     }
     // Every CTA comes to the same verdict.  A plan that fails hands out nothing
     // and is empty: no slot, no row of attention.
     int32_t err = FM_OK;
-    if (__syncthreads_or(bad) || run[0] > s.T) err = FM_ERR_LENGTHS;
+    if (__syncthreads_or(bad) || run[0] > s.T || run[5] >= ((int64_t)1 << 31) - kPagedCtas) err = FM_ERR_LENGTHS;
     else if (a.free_pages && (head < 0 || head > a.n_free || run[1] > a.n_free - head)) err = FM_ERR_PAGES;
     if (err != FM_OK && cta == 0 && tid == 0) set_status(a.status, err);
     const int total = err == FM_OK ? (int)run[0] : 0;
@@ -185,8 +214,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
             h.ctas_few = ctas_few;
             h.tiles_few = W;
             h.rows = total;
+            h.n_many = err == FM_OK ? (int)run[4] : 0;
+            h.units_many = err == FM_OK ? (int)run[5] : 0;
+            h.splits_many = split_of(run[5], run[6]);
             *reinterpret_cast<PagedHeader *>(a.plan) = h;
             few_cum[n_few] = W;
+            if (h.n_many > 0) many_cum[h.n_many] = h.units_many;
+            *reinterpret_cast<uint32_t *>(a.plan + a.L.off_claim) = 0u;
             a.cu[s.R] = total;
         }
         for (int r = tid; r < s.R; r += kPlanThreads) a.cu[r] = err == FM_OK ? s_cu[r] : 0;
@@ -202,6 +236,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanArgs
             reinterpret_cast<int4 *>(a.plan + a.L.off_start)[i] = st;
             reinterpret_cast<uint32_t *>(a.plan + a.L.off_count)[i] = 0u;
         }
+        for (int i = tid; i < kMaxSplitUnits; i += kPlanThreads)
+            reinterpret_cast<uint32_t *>(a.plan + a.L.off_many_count)[i] = 0u;
     }
     // Every CTA has read the lengths and the head: they may be advanced in place.
     if (ctas > 1) cg::this_cluster().sync();
@@ -313,7 +349,7 @@ fm_status check_cache(const fm_paged_cache *c)
 // Rows of bf16 read 16 bytes at a time: token and head strides in elements.
 bool rows_ok(const void *p, int64_t tok, int64_t head)
 {
-    return aligned16(p) && tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0 && tok <= ((int64_t)1 << 38) &&
+    return aligned16(p) && tok > 0 && head > 0 && tok % 8 == 0 && head % 8 == 0 && tok <= ((int64_t)1 << 38) &&
            head <= ((int64_t)1 << 38);
 }
 
@@ -478,7 +514,26 @@ fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok,
     a.scale_log2 = scale * 1.4426950408889634f;
     a.o_f32 = o_dtype == FM_DT_F32;
     a.rows = rows;
-    if ((int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv) > kFewRows) return FM_ERR_UNSUPPORTED;
+    const int G = a.s.Hq / a.s.Hkv;
+    if ((int64_t)a.s.max_q * G > kFewRows) {
+        // Some request may have many rows.  Boxes: the query heads of a KV head times
+        // as many tokens as make 128 rows; consecutive keys of one page, a power of two.
+        int box_keys = kPageGranule;
+        while (box_keys < kKeyTile && a.s.page_size % (2 * box_keys) == 0) box_keys *= 2;
+        const uint64_t d = a.s.d;
+        CUtensorMap tq, tk, tv;
+        const uint64_t qd[3] = {d, (uint64_t)a.s.Hq, (uint64_t)(rows > 0 ? rows : 1)};
+        const uint64_t qs[2] = {(uint64_t)a.q_head, (uint64_t)a.q_tok};
+        const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)(128 / G)};
+        const uint64_t cd[4] = {d, (uint64_t)a.s.page_size, (uint64_t)a.s.Hkv, (uint64_t)a.s.num_pages};
+        const uint64_t ks[3] = {(uint64_t)a.k_tok, (uint64_t)a.k_head, (uint64_t)a.k_page};
+        const uint64_t vs[3] = {(uint64_t)a.v_tok, (uint64_t)a.v_head, (uint64_t)a.v_page};
+        const uint32_t cb[4] = {fp8 ? (uint32_t)a.s.d : 64u, (uint32_t)box_keys, 1, 1};
+        if (!make_tmap_strided(&tq, q, false, 3, qd, qs, qb, true) || !make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, !fp8) ||
+            !make_tmap_strided(&tv, cache->v, fp8, 4, cd, vs, cb, !fp8))
+            return FM_ERR_CUDA;
+        if ((st = fm_paged_chunk_launch(tq, tk, tv, a, box_keys, fp8, (cudaStream_t)stream)) != FM_OK) return st;
+    }
     return fm_paged_decode_launch(a, fp8, (cudaStream_t)stream);
 }
 

@@ -2,6 +2,10 @@
 // plan buffer and the key ranges that the planner and the kernels share.
 #pragma once
 
+#include <cuda.h>
+
+#include <cmath>
+
 #include "fm_internal.h"
 
 namespace fm {
@@ -12,6 +16,8 @@ constexpr int kPageGranule = 16;                // page sizes are multiples of t
 constexpr int kFewRows = 32;                    // (new tokens x query heads per KV head) up to which a request is "few rows"
 constexpr int kPagedCtas = 152;                 // CTAs of the persistent attention kernels (no CTA waits for another)
 constexpr int kMaxRequests = 8192;
+constexpr int kMaxSplitUnits = 2 * kPagedCtas;  // many-rows units that are still split along the keys
+constexpr int kMaxPieces = 4 * kPagedCtas;      // pieces they are split into at most
 
 struct PagedShape {
     int32_t R, T, max_q, max_pages, num_pages, page_size, Hq, Hkv, d, window, sink;
@@ -25,7 +31,10 @@ struct PagedHeader {
     int32_t ctas_few;     // CTAs that share its tiles (0: none)
     int64_t tiles_few;    // key tiles of the list, over all KV heads
     int32_t rows;         // rows of q: new tokens of all requests
-    int32_t pad[47];
+    int32_t n_many;       // entries of the many-rows list
+    int32_t units_many;   // its units (request, KV head, query tile)
+    int32_t splits_many;  // pieces per unit along the keys (1: whole units)
+    int32_t pad[44];
 };
 static_assert(sizeof(PagedHeader) == 256, "plan header size");
 
@@ -41,6 +50,12 @@ struct PagedLayout {
     int64_t off_count;     // uint32 [kPagedCtas]  arrivals at the split unit that begins in CTA c
     int64_t off_few_o;     // fp32 [2 kPagedCtas][kFewRows][d]  unnormalised partial outputs
     int64_t off_few_ml;    // fp32 [2 kPagedCtas][2][kFewRows]  their row maxima (base 2) and sums
+    int64_t off_many;      // PagedEntry [R]
+    int64_t off_many_cum;  // int32 [R + 1]  units before entry i
+    int64_t off_claim;     // uint32  next piece to claim
+    int64_t off_many_count;// uint32 [kMaxSplitUnits]  arrivals at a split unit
+    int64_t off_many_o;    // fp32 [kMaxPieces][d / 4][128][4]  unnormalised partial outputs
+    int64_t off_many_ml;   // fp32 [kMaxPieces][2][128]
     int64_t total;
 };
 
@@ -54,6 +69,13 @@ inline PagedLayout paged_layout(const PagedShape &s)
     L.off_count = off;    off = align256(off + kPagedCtas * 4);
     L.off_few_o = off;    off = align256(off + (int64_t)2 * kPagedCtas * kFewRows * s.d * 4);
     L.off_few_ml = off;   off = align256(off + (int64_t)2 * kPagedCtas * 2 * kFewRows * 4);
+    const bool many = (int64_t)s.max_q * (s.Hq / s.Hkv) > kFewRows;   // else no request can have many rows
+    L.off_many = off;       off = align256(off + (many ? (int64_t)s.R * 16 : 0));
+    L.off_many_cum = off;   off = align256(off + (many ? ((int64_t)s.R + 1) * 4 : 0));
+    L.off_claim = off;      off = align256(off + 4);
+    L.off_many_count = off; off = align256(off + kMaxSplitUnits * 4);
+    L.off_many_o = off;     off = align256(off + (many ? (int64_t)kMaxPieces * 128 * s.d * 4 : 0));
+    L.off_many_ml = off;    off = align256(off + (many ? (int64_t)kMaxPieces * 2 * 128 * 4 : 0));
     L.total = off;
     return L;
 }
@@ -86,6 +108,26 @@ FM_HD KeyRange key_range(int p0, int p1, int window, int sink)
 FM_HD int64_t share_begin(int64_t n, int ctas, int64_t c) { return c * n / ctas; }
 FM_HD int share_owner(int64_t n, int ctas, int64_t x) { return (int)(((x + 1) * ctas - 1) / n); }
 
+#if defined(__CUDACC__)
+__device__ __forceinline__ bool paged_plan_fits(const PagedHeader *h, const PagedShape &s)
+{
+    const PagedShape &p = h->s;
+    return h->magic == kPagedMagic && p.R == s.R && p.T == s.T && p.max_q == s.max_q && p.max_pages == s.max_pages &&
+           p.num_pages == s.num_pages && p.page_size == s.page_size && p.Hq == s.Hq && p.Hkv == s.Hkv && p.d == s.d &&
+           p.window == s.window && p.sink == s.sink;
+}
+
+// e4m3 caches take Q as fp16: the power of two that puts a row's largest
+// element in [2^14, 2^15), so that bf16 values down to 2^-29 of it keep all
+// their bits; 1 when the row is zero or not finite.
+__device__ __forceinline__ float f16_row_factor(float amax)
+{
+    if (!(amax > 0.f) || amax == INFINITY) return 1.f;
+    const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+    return exp2f((float)min(14 - ex, 100));
+}
+#endif
+
 // Arguments of the attention kernels (everything but TMA descriptors).
 struct PagedArgs {
     PagedShape s;
@@ -105,7 +147,15 @@ struct PagedArgs {
     int rows;                       // rows that q, o and lse have
 };
 
+// Tensor map of bf16 or 8-bit data with any strides (bytes, of dimensions 1 and
+// up), zero fill outside, 128-byte swizzle or none (fm_api.cu).
+bool make_tmap_strided(CUtensorMap *map, const void *base, bool u8, int rank, const uint64_t *dims, const uint64_t *strides,
+                       const uint32_t *box, bool swizzle);
+
 }  // namespace fm
 
-// Launcher of the few-rows kernel (fm_paged_decode.cu).
+// Launchers of the few-rows kernel (fm_paged_decode.cu) and of the many-rows
+// kernel (fm_paged_chunk.cu; box_keys: keys of one TMA box).
 fm_status fm_paged_decode_launch(const fm::PagedArgs &a, bool e4m3, cudaStream_t stream);
+fm_status fm_paged_chunk_launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const fm::PagedArgs &a,
+                                int box_keys, bool e4m3, cudaStream_t stream);

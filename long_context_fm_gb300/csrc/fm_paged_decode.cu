@@ -29,7 +29,6 @@
 // alone; e4m3 caches with 16-bit outputs use one fp16 term (11 bits): e4m3
 // values are exact in fp16, and so is Q after a power-of-two factor per row
 // that puts its largest element in [2^14, 2^15).
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -80,20 +79,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
     uint2 v;
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
-}
-
-// Two e4m3 bytes (low half of x) as two fp16, exactly.
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t x)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 // c (16 x 8 fp32) += a (16 x 16) b (16 x 8)
@@ -149,9 +134,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
     const int g = lane >> 2, c = lane & 3;
     const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
     const PagedShape &s = a.s;
-    if (hd->magic != kPagedMagic || hd->s.R != s.R || hd->s.T != s.T || hd->s.max_q != s.max_q || hd->s.max_pages != s.max_pages ||
-        hd->s.num_pages != s.num_pages || hd->s.page_size != s.page_size || hd->s.Hq != s.Hq || hd->s.Hkv != s.Hkv ||
-        hd->s.d != s.d || hd->s.window != s.window || hd->s.sink != s.sink) {
+    if (!paged_plan_fits(hd, s)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_PLAN_MISMATCH);
         return;
     }
@@ -252,13 +235,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
     uint8_t *sq = smem + C::kRed;           // two blocks: Q in shared memory between units
     const float kds = FP8 ? *a.k_descale : 1.f, vds = FP8 ? *a.v_descale : 1.f;
 
-    // Factor that puts a row's largest element in [2^14, 2^15) (e4m3 caches: Q
-    // as fp16), 1 when the row is zero or not finite.
-    auto row_factor = [](float amax) -> float {
-        if (!(amax > 0.f) || amax == INFINITY) return 1.f;
-        const int ex = (int)(__float_as_uint(amax) >> 23) - 127;      // bf16 subnormals: ex = -127, still in range below
-        return exp2f((float)min(14 - ex, 100));
-    };
     auto begin_unit = [&]() {
         const int nrows = cu.ent.n * G;
 #pragma unroll
@@ -295,7 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                                 amax = fmax3(amax, fabsf(__uint_as_float(w[i][y] << 16)), fabsf(__uint_as_float(w[i][y] & 0xffff0000u)));
                         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                        f = row_factor(amax);
+                        f = f16_row_factor(amax);
 #pragma unroll
                         for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -341,7 +317,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                     amax = fmax3(amax, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
 #pragma unroll
                 for (int y = 1; y < 8; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
-                f = row_factor(amax);
+                f = f16_row_factor(amax);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
@@ -635,8 +611,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                         ph[b][2 * nt + hf] = hi;
                         if (TWO) {
                             if (FP8) {
-                                const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                                pl[b][2 * nt + hf] = pack_f16x2(p0 - u.x, p1 - u.y);
+                                float u0, u1;
+                                unpack_f16x2(hi, u0, u1);
+                                pl[b][2 * nt + hf] = pack_f16x2(p0 - u0, p1 - u1);
                             } else {
                                 pl[b][2 * nt + hf] = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
                             }

@@ -209,6 +209,16 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// 4-D tiled load, as above.
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 // 3-D tiled store from shared memory (bulk async group of the issuing thread).
 // Elements of the box outside the tensor are not written.  Callers keep
 // x * element size a multiple of 16 bytes and every coordinate >= 0.
@@ -317,6 +327,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
            ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same with fp16 A and B (format code 0), A K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
+{
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem] . B[smem]^T   (one instruction: K = 16)
@@ -485,6 +501,16 @@ __device__ __forceinline__ void red_add_f32(float *addr, float v)
     asm volatile("red.global.add.f32 [%0], %1;" ::"l"(addr), "f"(v) : "memory");
 }
 
+// Bits x of a 32-bit group with lo <= x < hi (bounds clamped to [0, 32]): the
+// bits at or above lo and below hi, as two clamping funnel shifts (a shift by
+// 32 gives 0); empty when hi <= lo.
+__device__ __forceinline__ uint32_t row_bits32(int lo, int hi)
+{
+    lo = min(max(lo, 0), 32);
+    hi = min(max(hi, 0), 32);
+    return __funnelshift_lc(0u, 0xffffffffu, (uint32_t)lo) & __funnelshift_rc(0xffffffffu, 0u, (uint32_t)(32 - hi));
+}
+
 // ---- FP8 (e4m3) ---------------------------------------------------------------
 // Instruction descriptor, kind::f8f6f4 with e4m3 A and B (format code 0 in
 // both fields), fp32 accumulate, both operands K-major: the kind::f16 layout
@@ -526,6 +552,27 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi)
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Two e4m3 values (bits 0-7 and 8-15 of x) as two fp16, exactly.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t x)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void unpack_f16x2(uint32_t v, float &lo, float &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(v));
 }
 
 }  // namespace fm

@@ -27,7 +27,8 @@ FM_TILE_SKIP, FM_TILE_FULL, FM_TILE_PARTIAL = 0, 1, 2
 FM_DT_BF16, FM_DT_F32, FM_DT_E4M3 = 0, 1, 2
 FM_FLAG_PRECISE = 1
 KERNEL_NAMES = ["classify_minmax", "classify_lists", "fwd", "bwd_pre", "bwd", "bwd_post",
-                "classify_order", "fp8_amax", "fp8_convert", "paged_plan", "paged_append", "paged_decode"]
+                "classify_order", "fp8_amax", "fp8_convert", "paged_plan", "paged_append", "paged_decode",
+                "paged_chunk"]
 
 EXPORTED = ["fm_status_string", "fm_abi_version", "fm_mask_from_rows", "fm_mask_from_row_intervals",
             "fm_plan_bytes", "fm_tile_classify", "fm_fwd_workspace_bytes", "fm_attn_fwd", "fm_bwd_workspace_bytes",
@@ -451,9 +452,9 @@ def _rows(t, name, d=None):
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1) or (d is not None and t.shape[2] != d):
         raise ValueError(f"{name} must be [T, H, {d or 'd'}] with a contiguous last dimension")
-    T, H, _ = t.shape
+    T, H, n = t.shape
     st, sh, _ = t.stride()
-    return st if T > 1 else 0, sh if H > 1 else 0
+    return st if T > 1 else n, sh if H > 1 else n       # the stride of a dimension of size one is never used
 
 
 def paged_cache(k_cache, v_cache, k_descale=None, v_descale=None) -> PagedCache:

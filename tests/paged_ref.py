@@ -52,9 +52,16 @@ def attend(q, k_cache, v_cache, table, ctx, new, scale, window=0, sink=0):
     S = torch.zeros(T, Hq, dtype=torch.float64)
     cnt = torch.zeros(T, 1, dtype=torch.float64)
     vmax = torch.zeros_like(o)
+    loose = torch.zeros(T, Hq, d, dtype=torch.bool)
     t0 = 0
     for r, (c, n) in enumerate(zip(ctx, new)):
         L = c + n
+        if n:       # columns of the request that hold a value that is not finite in some held page's token
+            own = [(int(table[r][j // page]), j % page) for j in range(L) if int(table[r][j // page]) >= 0]
+            pg, off = torch.tensor(own).T
+            bad_k = (~torch.isfinite(k_cache[pg, :, off])).any(2).any(0)
+            bad = (~torch.isfinite(v_cache[pg, :, off])).any(0) | bad_k[:, None]
+            loose[t0:t0 + n] = bad.repeat_interleave(G, 0)
         for i in range(n):
             p = c + i
             j = np.arange(L)
@@ -75,16 +82,18 @@ def attend(q, k_cache, v_cache, table, ctx, new, scale, window=0, sink=0):
                 vmax[t0 + i, sl] = v.abs().amax(0)
             cnt[t0 + i] = len(keep)
         t0 += n
-    return dict(o=o, lse=lse, A=A, S=S, n=cnt, vmax=vmax)
+    return dict(o=o, lse=lse, A=A, S=S, n=cnt, vmax=vmax, loose=loose)
 
 
 def check_attention(ref, o, lse, d, p_err, fp16):
     """Every element of o and lse (device tensors, rows of the step) within the bounds above."""
     got = o.double().cpu()
-    # A value that is not finite where it is attended (an e4m3 cast of torch's
-    # gives NaN above 464) reaches the same outputs here and there.
-    fin = torch.isfinite(ref["o"])
-    assert torch.equal(torch.isfinite(got), fin)
+    # A value that is not finite (an e4m3 cast of torch's gives NaN above 464)
+    # reaches every row that attends it; rows of the same request that do not may
+    # have it too (the contract), so nothing is asked of those columns there.
+    fin, loose = torch.isfinite(ref["o"]), ref["loose"]
+    assert (torch.isfinite(got) == fin)[~loose].all() and not torch.isfinite(got)[~fin].any()
+    fin = fin & torch.isfinite(got)
     w = (2 * d + 8) * 2.0 ** -24 * (ref["S"] + 1) + 2.0 ** -21
     out = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}[o.dtype]
     tol = (2 * w + p_err + ref["n"] * 2.0 ** -24)[..., None] * ref["A"]

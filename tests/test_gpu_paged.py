@@ -23,6 +23,7 @@ class Batch:
 
     def __init__(self, fm, ctx, new, Hq, Hkv, d, page, window=0, sink=0, e4m3=False, seed=0, layout="heads", q_max=None, spare=2,
                  q_scale=1.5, poison=True):
+        many = max(new) * (Hq // Hkv) > 32
         g = torch.Generator().manual_seed(seed)
         self.fm, self.ctx, self.new, self.scale = fm, ctx, new, 1.0 / d ** 0.5
         self.Hq, self.Hkv, self.d, self.page, self.window, self.sink, self.e4m3 = Hq, Hkv, d, page, window, sink, e4m3
@@ -38,8 +39,10 @@ class Batch:
         v = k.clone()
         for r, (c, n) in enumerate(zip(ctx, new)):
             for j in range(c + n):
-                if window and n and poison and j <= c - window and j >= sink:
-                    continue            # behind the window of every row
+                b0 = j // page * page
+                gone = b0 + page - 1 <= c - window and b0 >= sink if many else j <= c - window and j >= sink
+                if window and n and poison and gone:
+                    continue            # behind the window of every row (many rows: with its whole page)
                 k[self.table[r][j // page], :, j % page] = torch.randn(Hkv, d, generator=g)
                 v[self.table[r][j // page], :, j % page] = torch.randn(Hkv, d, generator=g)
         if window and poison:           # pages wholly behind the window may be gone
@@ -256,3 +259,47 @@ def test_a_long_request_is_split_over_all_ctas(fm, e4m3):
     again = b.run(torch.float32)
     for x, y in zip((o, lse), again):                   # the same bits, whichever CTA comes last
         assert torch.equal(x.view(torch.int32), y.view(torch.int32))
+
+
+# ---- attention of many rows ----------------------------------------------------------------
+MANY = [
+    # ctx, new, Hq, Hkv, page, window, sink
+    ([0], [33], 1, 1, 16, 0, 0),
+    ([0], [128], 2, 2, 16, 0, 0),
+    ([0, 0, 0], [127, 129, 256], 2, 1, 32, 0, 0),
+    ([500, 3, 0, 1000], [40, 1, 0, 130], 8, 2, 16, 0, 0),
+    ([77], [61], 28, 4, 64, 0, 0),
+    ([300, 128, 9], [70, 2, 65], 6, 2, 48, 0, 0),
+    ([1000], [64], 4, 4, 128, 200, 0),
+    ([900, 20], [150, 100], 2, 2, 32, 64, 10),
+    ([900, 400], [100, 37], 4, 2, 16, 300, 140),
+    ([2500], [45], 2, 2, 256, 0, 0),
+    ([640, 255], [3, 5], 32, 1, 16, 0, 0),
+    ([100], [90], 5, 5, 16, 1, 0),
+]
+
+
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_rows(fm, case, d, e4m3, o_dtype):
+    ctx, new, Hq, Hkv, page, window, sink = MANY[case]
+    b = Batch(fm, ctx, new, Hq, Hkv, d, page, window, sink, e4m3, seed=100 + case, layout=["heads", "tokens", "pairs"][case % 3])
+    b.check(o_dtype, few=False)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_short_chunk_over_a_long_cache_is_split(fm, e4m3):
+    b = Batch(fm, [9000, 700], [20, 17], 4, 2, 128, 32, e4m3=e4m3, seed=6)
+    b.check(torch.float32, few=False)
+    first, again = b.run(torch.float32), b.run(torch.float32)
+    for x, y in zip(first, again):
+        assert torch.equal(x.view(torch.int32), y.view(torch.int32))
+
+
+def test_many_units_of_every_length(fm):
+    """More units than CTAs, whole and uneven."""
+    rng = np.random.default_rng(3)
+    ctx, new = rng.integers(0, 300, 40).tolist(), rng.integers(0, 90, 40).tolist()
+    Batch(fm, ctx, new, 8, 8, 64, 16, seed=7).check(torch.bfloat16, few=False)
