@@ -185,7 +185,7 @@ constexpr size_t kProfMax = 4096;
 
 namespace fm {
 bool make_tmap_strided(CUtensorMap *map, const void *base, bool u8, int rank, const uint64_t *dims, const uint64_t *strides,
-                       const uint32_t *box, bool swizzle)
+                       const uint32_t *box, int swizzle)
 {
     auto fn = encode_fn();
     if (!fn || rank < 2 || rank > 5) return false;
@@ -198,7 +198,8 @@ bool make_tmap_strided(CUtensorMap *map, const void *base, bool u8, int rank, co
         if (i > 0) st[i - 1] = strides[i - 1];
     }
     return fn(map, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, st, b, e,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

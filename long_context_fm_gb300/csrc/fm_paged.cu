@@ -498,14 +498,6 @@ fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok,
     a.q = (const uint8_t *)q;
     a.q_tok = q_tok * 2;
     a.q_head = q_head * 2;
-    a.k = (const uint8_t *)cache->k;
-    a.v = (const uint8_t *)cache->v;
-    a.k_page = cache->k_page * esz;
-    a.k_head = cache->k_head * esz;
-    a.k_tok = cache->k_tok * esz;
-    a.v_page = cache->v_page * esz;
-    a.v_head = cache->v_head * esz;
-    a.v_tok = cache->v_tok * esz;
     a.k_descale = cache->k_descale;
     a.v_descale = cache->v_descale;
     a.o = o;
@@ -514,27 +506,42 @@ fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok,
     a.scale_log2 = scale * 1.4426950408889634f;
     a.o_f32 = o_dtype == FM_DT_F32;
     a.rows = rows;
+    a.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (a.s.page_size == 1 << i) a.page_shift = i;
     const int G = a.s.Hq / a.s.Hkv;
+    const uint64_t d = a.s.d, kt = cache->k_tok * esz, kh = cache->k_head * esz, kp = cache->k_page * esz, vt = cache->v_tok * esz,
+                   vh = cache->v_head * esz, vp = cache->v_page * esz;
+    const uint64_t pages = a.s.num_pages, page = a.s.page_size, heads = a.s.Hkv;
     if ((int64_t)a.s.max_q * G > kFewRows) {
         // Some request may have many rows.  Boxes: the query heads of a KV head times
         // as many tokens as make 128 rows; consecutive keys of one page, a power of two.
         int box_keys = kPageGranule;
         while (box_keys < kKeyTile && a.s.page_size % (2 * box_keys) == 0) box_keys *= 2;
-        const uint64_t d = a.s.d;
         CUtensorMap tq, tk, tv;
         const uint64_t qd[3] = {d, (uint64_t)a.s.Hq, (uint64_t)(rows > 0 ? rows : 1)};
         const uint64_t qs[2] = {(uint64_t)a.q_head, (uint64_t)a.q_tok};
         const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)(128 / G)};
-        const uint64_t cd[4] = {d, (uint64_t)a.s.page_size, (uint64_t)a.s.Hkv, (uint64_t)a.s.num_pages};
-        const uint64_t ks[3] = {(uint64_t)a.k_tok, (uint64_t)a.k_head, (uint64_t)a.k_page};
-        const uint64_t vs[3] = {(uint64_t)a.v_tok, (uint64_t)a.v_head, (uint64_t)a.v_page};
+        const uint64_t cd[4] = {d, page, heads, pages};
+        const uint64_t ks[3] = {kt, kh, kp}, vs[3] = {vt, vh, vp};
         const uint32_t cb[4] = {fp8 ? (uint32_t)a.s.d : 64u, (uint32_t)box_keys, 1, 1};
-        if (!make_tmap_strided(&tq, q, false, 3, qd, qs, qb, true) || !make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, !fp8) ||
-            !make_tmap_strided(&tv, cache->v, fp8, 4, cd, vs, cb, !fp8))
+        if (!make_tmap_strided(&tq, q, false, 3, qd, qs, qb, 128) || !make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, fp8 ? 0 : 128) ||
+            !make_tmap_strided(&tv, cache->v, fp8, 4, cd, vs, cb, fp8 ? 0 : 128))
             return FM_ERR_CUDA;
         if ((st = fm_paged_chunk_launch(tq, tk, tv, a, box_keys, fp8, (cudaStream_t)stream)) != FM_OK) return st;
     }
-    return fm_paged_decode_launch(a, fp8, (cudaStream_t)stream);
+    // Boxes of 16 keys: rows of 128 bytes (bf16, d = 128: two of them, as a
+    // dimension of its own) or of 64 bytes (e4m3, d = 64).
+    const uint64_t wide = fp8 ? d : 64;
+    const uint32_t halves = (uint32_t)(d / wide);
+    CUtensorMap tk, tv;
+    const uint64_t cd[5] = {wide, page, halves, heads, pages};
+    const uint64_t ks[4] = {kt, 128, kh, kp}, vs[4] = {vt, 128, vh, vp};
+    const uint32_t cb[5] = {(uint32_t)wide, kPageGranule, halves, 1, 1};
+    const int swizzle = (int)(wide * esz);
+    if (!make_tmap_strided(&tk, cache->k, fp8, 5, cd, ks, cb, swizzle) || !make_tmap_strided(&tv, cache->v, fp8, 5, cd, vs, cb, swizzle))
+        return FM_ERR_CUDA;
+    return fm_paged_decode_launch(tk, tv, a, fp8, (cudaStream_t)stream);
 }
 
 }  // extern "C"

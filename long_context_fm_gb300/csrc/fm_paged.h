@@ -136,8 +136,6 @@ struct PagedArgs {
     const int32_t *table;
     const uint8_t *q;               // bf16
     int64_t q_tok, q_head;          // strides in bytes, as all of these
-    const uint8_t *k, *v;
-    int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;
     const float *k_descale, *v_descale;   // e4m3 cache: one float each
     void *o;                        // [rows, Hq, d]
     float *lse;                     // [rows, Hq]
@@ -145,17 +143,19 @@ struct PagedArgs {
     float scale_log2;
     int o_f32;
     int rows;                       // rows that q, o and lse have
+    int page_shift;                 // log2 of the page size, -1 if it is no power of two
 };
 
 // Tensor map of bf16 or 8-bit data with any strides (bytes, of dimensions 1 and
-// up), zero fill outside, 128-byte swizzle or none (fm_api.cu).
+// up), zero fill outside, swizzle of 128, 64 or 0 bytes (fm_api.cu).
 bool make_tmap_strided(CUtensorMap *map, const void *base, bool u8, int rank, const uint64_t *dims, const uint64_t *strides,
-                       const uint32_t *box, bool swizzle);
+                       const uint32_t *box, int swizzle);
 
 }  // namespace fm
 
 // Launchers of the few-rows kernel (fm_paged_decode.cu) and of the many-rows
 // kernel (fm_paged_chunk.cu; box_keys: keys of one TMA box).
-fm_status fm_paged_decode_launch(const fm::PagedArgs &a, bool e4m3, cudaStream_t stream);
+fm_status fm_paged_decode_launch(const CUtensorMap &tk, const CUtensorMap &tv, const fm::PagedArgs &a, bool e4m3,
+                                 cudaStream_t stream);
 fm_status fm_paged_chunk_launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const fm::PagedArgs &a,
                                 int box_keys, bool e4m3, cudaStream_t stream);

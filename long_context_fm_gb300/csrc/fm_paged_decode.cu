@@ -16,19 +16,23 @@
 // finished by the CTA that arrives last at it, which adds the partial results
 // in the order of the CTAs: the result does not depend on who is last.
 //
-// A warp takes 16 keys of every tile and works alone until its unit ends: it
-// loads them through a ring of its own (cp.async, no barrier), 16 aligned keys
-// always lying in one page.  Fragment layouts: the head-dim order of the score
-// product is free as long as Q and K agree, and the order of output columns is
-// free altogether, so both K and V fragments are read with 16-byte
-// shared loads (chunks XOR-swizzled by row: conflict-free) and V is transposed
-// by byte permutes of two keys' registers.
+// A warp takes 16 keys of every tile and works alone until its unit ends: one
+// lane loads them by TMA through a ring of the warp's own (an mbarrier per slot,
+// no barrier between warps), 16 aligned keys always lying in one page.  Fragment
+// layouts: the head-dim order of the score product is free as long as Q and K
+// agree, the order of keys as long as P and V do, and the order of output columns
+// altogether, so K and V fragments are read with 16-byte shared loads in an
+// order that meets no bank conflict under TMA's swizzle, and V is transposed by
+// byte permutes of two keys' registers.
 //
 // P enters the second product as two 16-bit terms (hi + lo, about 16
-// significant bits) where that is free, which leaves the rounding of the output
-// alone; e4m3 caches with 16-bit outputs use one fp16 term (11 bits): e4m3
+// significant bits), so that the rounding of a 16-bit output is the only one
+// that counts, and as three when the output is fp32.  With at most 8 rows the low
+// terms use the 8 idle rows of the 16-row operand, and are free.  e4m3 caches
+// take P as fp16 (11 bits a term; one term for 16-bit outputs of more rows): e4m3
 // values are exact in fp16, and so is Q after a power-of-two factor per row
 // that puts its largest element in [2^14, 2^15).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -45,28 +49,16 @@ constexpr float kBand = 8.f;   // lazy rescale: P stays <= 2^8, sums are rescale
 template <int D, bool FP8>
 struct DecodeCfg {
     static constexpr int kRow = D * (FP8 ? 1 : 2);          // bytes of a key's row
-    static constexpr int kChunks = kRow / 16;
     static constexpr int kSlot = 2 * 16 * kRow;             // a warp's 16 keys: K rows, then V rows
     static constexpr int kStages = 192 * 1024 / (kWarps * kSlot) < 8 ? 192 * 1024 / (kWarps * kSlot) : 8;
     static constexpr int kRing = 0;
     static constexpr int kRed = kWarps * kStages * kSlot;   // float4 [8 warps][8][32 lanes]; Q of 32 rows between units
     static constexpr int kMl = kRed + kWarps * 8 * 32 * 16; // float [8 warps][2][kFewRows]
-    static constexpr int kMisc = kMl + kWarps * 2 * kFewRows * 4;
+    static constexpr int kBar = kMl + kWarps * 2 * kFewRows * 4;   // mbarrier [8 warps][stages]
+    static constexpr int kMisc = kBar + kWarps * kStages * 8;
     static constexpr int kBytes = kMisc + 16;
     static_assert(kBytes <= 227 * 1024, "shared memory of the few-rows kernel");
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes)
-{
-    // bytes < 16: the rest of the 16 destination bytes is zero
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
@@ -96,20 +88,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Byte offset of 16-byte chunk ch of key row `row` (0-15): the chunk moves so
-// that the eight lanes of a shared-load phase hit eight different bank groups.
-// K is read as (rows 2 x, 2 x + 1; four chunks), V as (rows 2 c, c = 0..3; two
-// chunks).
-template <int CH>
-__device__ __forceinline__ uint32_t swz_k(int row, int ch)
+// Order of keys and columns.  Column n of the score fragment is key
+// key_of(n) of its group of eight, and column n of the output fragment is piece
+// piece_of(n) of the head dim: the lanes of a shared-load phase then hit eight
+// different bank groups under the 128-byte swizzle (chunk ^ row & 7).  Rows of 64
+// bytes (e4m3, d = 64; 64-byte swizzle) keep V free of conflicts and K at two ways.
+template <bool NARROW>
+__host__ __device__ constexpr int key_of(int n)
 {
-    return CH >= 8 ? (uint32_t)((row * CH + (ch ^ ((row & 1) << 2))) * 16) : (uint32_t)((row * CH + ch) * 16);
+    return NARROW ? ((n >> 1) & 1) | ((n >> 2) << 2) | ((n & 1) << 1) : (n >> 1) | ((n & 1) << 2);
 }
-template <int CH>
-__device__ __forceinline__ uint32_t swz_v(int row, int ch)
+template <bool NARROW>
+__host__ __device__ constexpr int piece_of(int n)
 {
-    if (CH >= 8) return (uint32_t)((row * CH + (ch ^ (((row >> 1) & 3) << 1))) * 16);
-    return (uint32_t)(((row >> 1) * 8 + ((((row & 1) << 2) + ch) ^ (((row >> 1) & 3) << 1))) * 16);   // 64-byte rows
+    return NARROW ? n : (n >> 1) | ((n & 1) << 2);
+}
+// Byte offset of 16-byte chunk ch of key row `row` (0-15) in a 16-row box.
+template <bool NARROW>
+__device__ __forceinline__ uint32_t chunk_at(int row, int ch)
+{
+    return NARROW ? (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4)) : (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4));
 }
 
 // A walk over the CTA's share of the list.
@@ -121,17 +119,23 @@ struct Cursor {
 
 }  // namespace
 
-template <int D, bool FP8, int MT, bool TWO>
-__global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const PagedArgs a)
+// ROWS: 8, 16 or 32 rows of a unit at most; TERMS: 16-bit terms of P.
+template <int D, bool FP8, int ROWS, int TERMS>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    fm_paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PagedArgs a)
 {
     using C = DecodeCfg<D, FP8>;
-    constexpr int CH = C::kChunks, ST = C::kStages;
+    constexpr int ST = C::kStages;
+    constexpr bool NARROW = C::kRow == 64;
+    constexpr int MT = ROWS == 32 ? 2 : 1;  // 16-row blocks
+    constexpr int NR = ROWS == 8 ? 1 : 2;   // rows of a block per thread
     constexpr int KS = D / 16;              // score product: k-steps
     constexpr int NT = D / 8;               // output product: 8-column tiles
     constexpr int NP = NT / 8;              // groups of 8 tiles
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = warp_id(), lane = lane_id();
     const int g = lane >> 2, c = lane & 3;
+    const int kg = key_of<NARROW>(g), ka = key_of<NARROW>(2 * c), kb2 = key_of<NARROW>(2 * c + 1);
     const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
     const PagedShape &s = a.s;
     if (!paged_plan_fits(hd, s)) {
@@ -149,6 +153,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
     int left = (int)(share_begin(W, ctas, blockIdx.x + 1) - x0);   // tiles to compute
     if (left == 0) return;
     int to_load = left;
+    const int loaded = left;
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBar) + warp * ST;
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
+    if (lane == 0) {
+        for (int i = 0; i < ST; ++i) mbar_init(&bars[i], 1);
+        if (warp == 0) *abort = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
 
     const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_few);
     const int64_t *cum = reinterpret_cast<const int64_t *>(a.plan + a.L.off_few_cum);
@@ -180,57 +194,50 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
     }
     Cursor cu = ld;
 
-    const uint32_t ring = smem_u32(smem) + C::kRing + warp * ST * C::kSlot;
-    // The page of this warp's keys of the tile that `u` stands at, or -1: none
-    // of them is attended, or the number is outside the pool.
+    uint8_t *ring = smem + C::kRing + warp * ST * C::kSlot;
+    // This warp's 16 keys of the tile that `u` stands at; some: a row attends one of them.
+    auto first_key = [&](const Cursor &u) { return u.kr.tile(u.x) * kKeyTile + warp * 16; };
+    auto some = [&](const Cursor &u, int k0) { return k0 < u.kr.hi && !(k0 + 16 <= u.kr.lo && k0 >= s.sink); };
+    // Their page: num_pages (outside the pool: arrives as zeros) when its number is.
     auto page_of = [&](const Cursor &u) -> int {
-        const int k0 = u.kr.tile(u.x) * kKeyTile + warp * 16;
-        if (k0 >= u.kr.hi || (k0 + 16 <= u.kr.lo && k0 >= s.sink)) return -1;
-        const int p = __ldg(a.table + (int64_t)u.ent.r * s.max_pages + k0 / s.page_size);
+        const int k0 = first_key(u);
+        if (!some(u, k0)) return -1;
+        const int p = __ldg(a.table + (int64_t)u.ent.r * s.max_pages + (a.page_shift >= 0 ? k0 >> a.page_shift : k0 / s.page_size));
         if (p < 0 || p >= s.num_pages) {
             if (lane == 0) set_status(a.status, FM_ERR_PAGES);
-            return -1;
+            return s.num_pages;
         }
         return p;
     };
     int page = page_of(ld);
     int slot_ld = 0;
     // Starts the copies of the tile that the load walk stands at, and looks up
-    // the next tile's page meanwhile.
+    // the next tile's page meanwhile.  A tile without keys for this warp
+    // completes its slot's phase with no bytes.
     auto load_tile = [&]() {
-        if (to_load > 0) {
-            const int k0 = ld.kr.tile(ld.x) * kKeyTile + warp * 16;
-            const uint32_t dst = ring + slot_ld * C::kSlot;
-            const int hi = ld.kr.hi, lo = ld.kr.lo;
-            const bool some = k0 < hi && !(k0 + 16 <= lo && k0 >= s.sink);
-            const int in_page = k0 % s.page_size;
-            const uint8_t *kp = a.k + (int64_t)max(page, 0) * a.k_page + (int64_t)ld.h * a.k_head + (int64_t)in_page * a.k_tok;
-            const uint8_t *vp = a.v + (int64_t)max(page, 0) * a.v_page + (int64_t)ld.h * a.v_head + (int64_t)in_page * a.v_tok;
-            const int pg = page;
-            --to_load;
-            advance(ld, to_load > 0);
-            if (to_load > 0) page = page_of(ld);
-            if (some) {
-                // Rows that no row of the request attends arrive as zeros: what
-                // a page holds behind the last token reaches no product.
-#pragma unroll
-                for (int i = 0; i < CH / 2; ++i) {
-                    const int row = i * (32 / CH) + lane / CH, ch = lane % CH;
-                    const int j = k0 + row;
-                    const uint32_t n = (pg >= 0 && j < hi && (j >= lo || j < s.sink)) ? 16u : 0u;
-                    cp_async16(dst + swz_k<CH>(row, ch), kp + row * a.k_tok + ch * 16, n);
-                    cp_async16(dst + 16 * C::kRow + swz_v<CH>(row, ch), vp + row * a.v_tok + ch * 16, n);
-                }
+        if (to_load == 0) return;
+        if (lane == 0) {
+            if (page >= 0) {
+                const int k0 = first_key(ld);
+                const int in = a.page_shift >= 0 ? k0 & (s.page_size - 1) : k0 % s.page_size;
+                uint8_t *dst = ring + slot_ld * C::kSlot;
+                mbar_arrive_expect_tx(&bars[slot_ld], C::kSlot);
+                tma_load_5d(dst, &tk, &bars[slot_ld], 0, in, 0, ld.h, page);
+                tma_load_5d(dst + 16 * C::kRow, &tv, &bars[slot_ld], 0, in, 0, ld.h, page);
+            } else {
+                mbar_arrive(&bars[slot_ld]);
             }
         }
-        cp_async_commit();
+        --to_load;
+        advance(ld, to_load > 0);
+        if (to_load > 0) page = page_of(ld);
         slot_ld = slot_ld + 1 == ST ? 0 : slot_ld + 1;
     };
 
     uint32_t qf[MT == 1 ? KS : 1][4];       // one 16-row block: Q fragments in registers
-    float qs[MT][2];                        // score factor of rows g, g + 8 (softmax scale, log2 e, descale, Q's own factor)
-    int pos[MT][2];                         // position of rows g, g + 8 of each block
-    float m[MT][2], l[MT][2];
+    float qs[MT][NR];                       // score factor of rows g, g + 8 (softmax scale, log2 e, descale, Q's own factor)
+    int pos[MT][NR];                        // position of rows g, g + 8 of each block
+    float m[MT][NR], l[MT][NR];
     float oa[MT][NT][4];
     uint8_t *sq = smem + C::kRed;           // two blocks: Q in shared memory between units
     const float kds = FP8 ? *a.k_descale : 1.f, vds = FP8 ? *a.v_descale : 1.f;
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
 #pragma unroll
         for (int b = 0; b < MT; ++b)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < NR; ++hf) {
                 const int row = b * 16 + hf * 8 + g;
                 const bool in = row < nrows;
                 const int tk = in ? row / G : 0;
@@ -283,6 +290,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                     for (int i = 0; i < KS; ++i) {
                         qf[MT == 1 ? i : 0][hf] = w[i][0];
                         qf[MT == 1 ? i : 0][2 + hf] = w[i][1];
+                        if (NR == 1) qf[MT == 1 ? i : 0][1] = qf[MT == 1 ? i : 0][3] = 0u;
                     }
                 }
             }
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
 #pragma unroll
             for (int b = 0; b < MT; ++b)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
+                for (int hf = 0; hf < NR; ++hf)
                     qs[b][hf] = a.scale_log2 * kds / *reinterpret_cast<const float *>(sq + kFewRows * D * 2 + (b * 16 + hf * 8 + g) * 4);
         }
     };
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
     // Pieces of the unit's output that a thread handles in the sums below: rows
     // 8 (z >> 2) + g, columns of 4 in the order of the fragments.
     auto dim_of = [&](int np, int z) {
-        const int cc = 2 * c + ((z >> 1) & 1), jq = (z & 1) * 4;
+        const int cc = piece_of<NARROW>(2 * c + ((z >> 1) & 1)), jq = (z & 1) * 4;
         return (FP8 && D == 128) ? 16 * cc + 8 * np + jq : 64 * np + 8 * cc + jq;
     };
     auto end_unit = [&]() {
@@ -374,10 +382,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
         const int64_t ub = cum[cu.e] + (int64_t)cu.h * cu.kr.n;   // the unit's tiles are [ub, ub + n) of the list
         const int c_first = share_owner(W, ctas, ub), c_last = share_owner(W, ctas, ub + cu.kr.n - 1);
         const int parts = c_last - c_first + 1;
+        if (NR == 1) {                  // the low terms' products stand in the idle rows
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                oa[0][t][0] += oa[0][t][2];
+                oa[0][t][1] += oa[0][t][3];
+            }
+        }
 #pragma unroll
         for (int b = 0; b < MT; ++b)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < NR; ++hf) {
                 float sum = l[b][hf];
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -391,9 +406,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
         const int slot = 2 * (int)bid + ((int)bid == c_first ? 1 : 0);
 #pragma unroll
         for (int b = 0; b < MT; ++b) {
-            float f[2], inv[2];
+            float f[NR], inv[NR];
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int hf = 0; hf < NR; ++hf) {
                 const int row = b * 16 + hf * 8 + g;
                 float mx = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -417,7 +432,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                 if (b > 0 || np > 0) __syncthreads();
                 // piece z = (row half, column half, 4 of 8 tiles)
 #pragma unroll
-                for (int z = 0; z < 8; ++z) {
+                for (int z = 0; z < 4 * NR; ++z) {
                     const int hf = z >> 2, y = 2 * hf + ((z >> 1) & 1), t = np * 8 + (z & 1) * 4;
                     if (b * 16 + hf * 8 < nrows)
                         red[(warp * 8 + z) * 32 + lane] = make_float4(oa[b][t][y] * f[hf], oa[b][t + 1][y] * f[hf],
@@ -425,7 +440,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                 }
                 __syncthreads();
                 const int z = warp, row = b * 16 + (z >> 2) * 8 + g;
-                if (row < nrows) {
+                if (z < 4 * NR && row < nrows) {
                     float4 v = red[z * 32 + lane];
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) {
@@ -436,7 +451,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                         v.w += u.w;
                     }
                     if (parts == 1)
-                        store4(en, h, row, dim_of(np, z), v, inv[z >> 2]);
+                        store4(en, h, row, dim_of(np, z), v, inv[NR == 1 ? 0 : z >> 2]);
                     else
                         __stcg(reinterpret_cast<float4 *>(ws_o + ((int64_t)slot * kFewRows + row) * D + dim_of(np, z)), v);
                 }
@@ -498,15 +513,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) load_tile();
     begin_unit();
+    // Byte offsets of this thread's fragments in a slot.
+    uint32_t k_at[2], v_at[2];          // K: even and odd load of a box; V: keys ka and kb2
+    k_at[0] = chunk_at<NARROW>(kg, c);
+    k_at[1] = NARROW ? 0 : chunk_at<NARROW>(kg, c + 4);
+    v_at[0] = 16 * C::kRow + (NARROW ? chunk_at<NARROW>(ka, g >> 1) + (g & 1) * 8 : chunk_at<NARROW>(ka, piece_of<NARROW>(g)));
+    v_at[1] = 16 * C::kRow + (NARROW ? chunk_at<NARROW>(kb2, g >> 1) + (g & 1) * 8 : chunk_at<NARROW>(kb2, piece_of<NARROW>(g)));
+    constexpr uint32_t ROW8 = NARROW ? 512 : 1024;          // eight rows further
     int slot = 0;
+    uint32_t phase = 0;
     while (left > 0) {
         load_tile();                    // into the slot that the previous round has read
-        cp_async_wait<ST - 1>();
-        __syncwarp();
-        const int k0 = cu.kr.tile(cu.x) * kKeyTile + warp * 16;
-        const bool some = k0 < cu.kr.hi && !(k0 + 16 <= cu.kr.lo && k0 >= s.sink);
-        if (some) {
-            const uint32_t kb = ring + slot * C::kSlot, vb = kb + 16 * C::kRow;
+        // A wait that ran out has set the status: the walk goes on, so that every
+        // barrier is reached, and what it writes does not count.
+        warp_wait(&bars[slot], phase, abort, a.status);
+        const int k0 = first_key(cu);
+        if (some(cu, k0)) {
+            uint8_t *sp = ring + slot * C::kSlot;
+            const uint32_t base = smem_u32(sp);
+            const bool whole = k0 + 16 <= cu.kr.hi && (k0 >= cu.kr.lo || k0 + 16 <= s.sink);
+            if (!whole) {
+                // V of keys that no row attends becomes zero: what a page holds behind
+                // the last token reaches no product (0 x NaN).
+                constexpr int CH = C::kRow / 16;
+                for (int i = lane; i < 16 * CH; i += 32) {
+                    const int row = i / CH, ch = i % CH, j = k0 + row;
+                    if (j >= cu.kr.hi || (j < cu.kr.lo && j >= s.sink))
+                        st_shared_v4(sp + 16 * C::kRow + (ch >> 3) * 2048 + chunk_at<NARROW>(row, ch & 7), make_uint4(0, 0, 0, 0));
+                }
+                __syncwarp();
+            }
             float sc[MT][2][4];
 #pragma unroll
             for (int b = 0; b < MT; ++b)
@@ -517,7 +553,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
             // Scores: 16 bytes of a key per thread and load are two k-steps of
             // bf16 (words 0, 1 and 2, 3) or four of e4m3 (one word each).
 #pragma unroll
-            for (int i = 0; i < CH / 4; ++i) {
+            for (int i = 0; i < C::kRow / 64; ++i) {
                 constexpr int PER = FP8 ? 4 : 2;
                 uint32_t qa[MT][PER][4];
 #pragma unroll
@@ -531,11 +567,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             const int row = b * 16 + hf * 8 + g;
-                            const uint32_t base = smem_u32(sq) + row * D * 2;
+                            const uint32_t qb = smem_u32(sq) + row * D * 2;
 #pragma unroll
                             for (int y = 0; y < PER / 2; ++y) {
                                 const int ch = FP8 ? (c + 4 * i) * 2 + y : c + 4 * i;
-                                const uint4 v = lds128(base + ((ch ^ (FP8 ? (row & 1) : ((row & 1) << 2))) << 4));
+                                const uint4 v = lds128(qb + ((ch ^ (FP8 ? (row & 1) : ((row & 1) << 2))) << 4));
                                 qa[b][2 * y][hf] = v.x;
                                 qa[b][2 * y][2 + hf] = v.y;
                                 qa[b][2 * y + 1][hf] = v.z;
@@ -546,7 +582,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                 }
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
-                    const uint4 kv = lds128(kb + swz_k<CH>(nt * 8 + g, c + 4 * i));
+                    const uint4 kv = lds128(base + k_at[i & 1] + (i >> 1) * 2048 + nt * ROW8);
                     const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
 #pragma unroll
                     for (int y = 0; y < PER; ++y) {
@@ -558,85 +594,105 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                     }
                 }
             }
-            // Scaled, masked where some row does not attend some of the 16 keys.
-            const bool edge = s.window > 0 || k0 + 15 > cu.ent.ctx;
+            // Scaled, and masked where some row does not attend some of the 16 keys.
+            const bool edge = k0 + 15 > cu.ent.ctx ||
+                              (s.window > 0 && k0 <= cu.ent.ctx + cu.ent.n - 1 - s.window && k0 + 16 > s.sink);
 #pragma unroll
             for (int b = 0; b < MT; ++b)
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        float x = sc[b][nt][y] * qs[b][y >> 1];
-                        if (edge) {
-                            const int j = k0 + nt * 8 + 2 * c + (y & 1), p = pos[b][y >> 1];
-                            if (!(j <= p && (s.window == 0 || j > p - s.window || j < s.sink))) x = -INFINITY;
+                    for (int y = 0; y < 2 * NR; ++y) sc[b][nt][y] *= qs[b][y >> 1];
+            if (edge) {
+#pragma unroll
+                for (int b = 0; b < MT; ++b)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int y = 0; y < 2 * NR; ++y) {
+                            const int j = k0 + nt * 8 + ((y & 1) ? kb2 : ka), p = pos[b][y >> 1];
+                            if (!(j <= p && (s.window == 0 || j > p - s.window || j < s.sink))) sc[b][nt][y] = -INFINITY;
                         }
-                        sc[b][nt][y] = x;
-                    }
-            // Running maxima (raised lazily), P and its sums.
-            uint32_t ph[MT][4], pl[MT][4];
+            }
+            // Running maxima, raised lazily: only when a score exceeds one by more
+            // than the band do the lanes of a row agree on a new one.
+            bool raise = false;
 #pragma unroll
-            for (int b = 0; b < MT; ++b) {
-                bool raise = false;
-                float mn[2];
+            for (int b = 0; b < MT; ++b)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float x = fmaxf(fmaxf(sc[b][0][2 * hf], sc[b][0][2 * hf + 1]), fmaxf(sc[b][1][2 * hf], sc[b][1][2 * hf + 1]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    mn[hf] = x > m[b][hf] + kBand ? x : m[b][hf];
-                    raise = raise || mn[hf] != m[b][hf];
-                }
-                if (__any_sync(0xffffffffu, raise)) {
+                for (int hf = 0; hf < NR; ++hf)
+                    raise = raise || fmaxf(fmax3(sc[b][0][2 * hf], sc[b][0][2 * hf + 1], sc[b][1][2 * hf]), sc[b][1][2 * hf + 1]) >
+                                         m[b][hf] + kBand;
+            if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const float f = m[b][hf] == mn[hf] ? 1.f : ex2(m[b][hf] - mn[hf]);
-                        m[b][hf] = mn[hf];
-                        l[b][hf] *= f;
+                for (int b = 0; b < MT; ++b)
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            oa[b][t][2 * hf] *= f;
-                            oa[b][t][2 * hf + 1] *= f;
+                    for (int hf = 0; hf < NR; ++hf) {
+                        float x = fmaxf(fmax3(sc[b][0][2 * hf], sc[b][0][2 * hf + 1], sc[b][1][2 * hf]), sc[b][1][2 * hf + 1]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        if (x > m[b][hf]) {
+                            const float f = ex2(m[b][hf] - x);
+                            m[b][hf] = x;
+                            l[b][hf] *= f;
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                oa[b][t][2 * hf] *= f;
+                                oa[b][t][2 * hf + 1] *= f;
+                                if (NR == 1) {
+                                    oa[b][t][2] *= f;
+                                    oa[b][t][3] *= f;
+                                }
+                            }
                         }
                     }
-                }
+            }
+            // P and its sums, as fragments: pt[term][key half][row half].
+            uint32_t pt[MT][3][2][2];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+            for (int b = 0; b < MT; ++b)
+#pragma unroll
+                for (int hf = 0; hf < NR; ++hf) {
                     const float mu = m[b][hf] == -INFINITY ? 0.f : m[b][hf];
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
-                        const float p0 = ex2(sc[b][nt][2 * hf] - mu), p1 = ex2(sc[b][nt][2 * hf + 1] - mu);
+                        float p0 = ex2(sc[b][nt][2 * hf] - mu), p1 = ex2(sc[b][nt][2 * hf + 1] - mu);
                         l[b][hf] += p0 + p1;
-                        const uint32_t hi = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-                        ph[b][2 * nt + hf] = hi;
-                        if (TWO) {
-                            if (FP8) {
-                                float u0, u1;
-                                unpack_f16x2(hi, u0, u1);
-                                pl[b][2 * nt + hf] = pack_f16x2(p0 - u0, p1 - u1);
-                            } else {
-                                pl[b][2 * nt + hf] = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+#pragma unroll
+                        for (int y = 0; y < TERMS; ++y) {
+                            const uint32_t hi = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                            pt[b][y][nt][hf] = hi;
+                            if (y + 1 < TERMS) {
+                                float u0 = __uint_as_float(hi << 16), u1 = __uint_as_float(hi & 0xffff0000u);
+                                if (FP8) unpack_f16x2(hi, u0, u1);
+                                p0 -= u0;
+                                p1 -= u1;
                             }
                         }
                     }
                 }
-            }
             // O += P V: the thread's two key pairs, columns as dim_of() says.
             auto pv = [&](int t, uint32_t b0, uint32_t b1) {
 #pragma unroll
                 for (int b = 0; b < MT; ++b) {
-                    mma16816<FP8>(oa[b][t], ph[b][0], ph[b][1], ph[b][2], ph[b][3], b0, b1);
-                    if (TWO) mma16816<FP8>(oa[b][t], pl[b][0], pl[b][1], pl[b][2], pl[b][3], b0, b1);
+                    if (NR == 1) {
+                        // Rows 0-7 the first term, rows 8-15 the second; then the third.
+                        mma16816<FP8>(oa[b][t], pt[b][0][0][0], TERMS > 1 ? pt[b][1][0][0] : 0u, pt[b][0][1][0], TERMS > 1 ? pt[b][1][1][0] : 0u, b0, b1);
+                        if (TERMS > 2) mma16816<FP8>(oa[b][t], 0u, pt[b][2][0][0], 0u, pt[b][2][1][0], b0, b1);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < TERMS; ++y)
+                            mma16816<FP8>(oa[b][t], pt[b][y][0][0], pt[b][y][0][NR - 1], pt[b][y][1][0], pt[b][y][1][NR - 1], b0, b1);
+                    }
                 }
             };
-            const int rows[4] = {2 * c, 2 * c + 1, 2 * c + 8, 2 * c + 9};
             if (!FP8) {
 #pragma unroll
                 for (int np = 0; np < NP; ++np) {
                     uint32_t w[4][4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const uint4 v = lds128(vb + swz_v<CH>(rows[r], np * 8 + g));
+                        const uint4 v = lds128(base + v_at[r & 1] + np * 2048 + (r >> 1) * ROW8);
                         w[r][0] = v.x;
                         w[r][1] = v.y;
                         w[r][2] = v.z;
@@ -653,39 +709,45 @@ __global__ void __launch_bounds__(kWarps * 32, 1) fm_paged_decode_kernel(const P
                 uint32_t w[4][WD];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
+                    const uint32_t at = base + v_at[r & 1] + (r >> 1) * ROW8;
                     if (WD == 4) {
-                        const uint4 v = lds128(vb + swz_v<CH>(rows[r], g));
+                        const uint4 v = lds128(at);
                         w[r][0] = v.x;
                         w[r][1] = v.y;
                         w[r][2 % WD] = v.z;
                         w[r][3 % WD] = v.w;
                     } else {
-                        const uint2 v = lds64(vb + swz_v<CH>(rows[r], g >> 1) + (g & 1) * 8);
+                        const uint2 v = lds64(at);
                         w[r][0] = v.x;
                         w[r][1] = v.y;
                     }
                 }
+                // The bytes of two keys are paired before they are expanded.
 #pragma unroll
-                for (int x = 0; x < WD; ++x)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t e[4];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) e[r] = f16x2_of_e4m3(w[r][x] >> (16 * half));
-                        pv(4 * x + 2 * half, __byte_perm(e[0], e[1], 0x5410), __byte_perm(e[2], e[3], 0x5410));
-                        pv(4 * x + 2 * half + 1, __byte_perm(e[0], e[1], 0x7632), __byte_perm(e[2], e[3], 0x7632));
-                    }
+                for (int x = 0; x < WD; ++x) {
+                    const uint32_t lo01 = __byte_perm(w[0][x], w[1][x], 0x5140), hi01 = __byte_perm(w[0][x], w[1][x], 0x7362);
+                    const uint32_t lo23 = __byte_perm(w[2][x], w[3][x], 0x5140), hi23 = __byte_perm(w[2][x], w[3][x], 0x7362);
+                    pv(4 * x, f16x2_of_e4m3(lo01), f16x2_of_e4m3(lo23));
+                    pv(4 * x + 1, f16x2_of_e4m3(lo01 >> 16), f16x2_of_e4m3(lo23 >> 16));
+                    pv(4 * x + 2, f16x2_of_e4m3(hi01), f16x2_of_e4m3(hi23));
+                    pv(4 * x + 3, f16x2_of_e4m3(hi01 >> 16), f16x2_of_e4m3(hi23 >> 16));
+                }
             }
         }
         __syncwarp();                   // every lane has read the slot before it is filled again
-        slot = slot + 1 == ST ? 0 : slot + 1;
+        if (++slot == ST) {
+            slot = 0;
+            phase ^= 1;
+        }
         --left;
         const bool last_of_unit = cu.x + 1 == cu.kr.n || left == 0;
         if (last_of_unit) end_unit();
         advance(cu, left > 0);
         if (last_of_unit && left > 0) begin_unit();
     }
-    cp_async_wait<0>();
+    // After a wait that ran out: the copies end before the CTA leaves.
+    if (*abort && lane == 0)
+        for (int i = max(loaded - ST, 0); i < loaded; ++i) mbar_wait_drain(&bars[i % ST], (i / ST) & 1, a.status);
 }
 
 }  // namespace fm
@@ -694,38 +756,46 @@ using namespace fm;
 
 namespace {
 
-template <int D, bool FP8, int MT, bool TWO>
-fm_status launch(const PagedArgs &a, cudaStream_t stream)
+template <int D, bool FP8, int ROWS, int TERMS>
+fm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, cudaStream_t stream)
 {
     constexpr int smem = DecodeCfg<D, FP8>::kBytes;
     static std::atomic<uint8_t> done[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FM_ERR_CUDA;
     if (!done[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(fm_paged_decode_kernel<D, FP8, MT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        if (cudaFuncSetAttribute(fm_paged_decode_kernel<D, FP8, ROWS, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
             cudaSuccess)
             return FM_ERR_CUDA;
         done[dev].store(1, std::memory_order_release);
     }
     ProfScope ps(kKPagedDecode, stream);
-    fm_paged_decode_kernel<D, FP8, MT, TWO><<<kPagedCtas, kWarps * 32, smem, stream>>>(a);
+    fm_paged_decode_kernel<D, FP8, ROWS, TERMS><<<kPagedCtas, kWarps * 32, smem, stream>>>(tk, tv, a);
     return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
+// By the rows that a request of the step can have at most.
 template <int D, bool FP8>
-fm_status launch_rows(const PagedArgs &a, cudaStream_t stream)
+fm_status launch_rows(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, cudaStream_t stream)
 {
-    // One block of 16 rows where no request can have more, else two.
-    const bool one = (int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv) <= 16;
-    if constexpr (FP8)
-        if (!a.o_f32) return one ? launch<D, FP8, 1, false>(a, stream) : launch<D, FP8, 2, false>(a, stream);
-    return one ? launch<D, FP8, 1, true>(a, stream) : launch<D, FP8, 2, true>(a, stream);
+    const int64_t rows = (int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv);
+    if constexpr (FP8) {
+        if (rows <= 8) return launch<D, FP8, 8, 2>(tk, tv, a, stream);
+        if (a.o_f32) return rows <= 16 ? launch<D, FP8, 16, 2>(tk, tv, a, stream) : launch<D, FP8, 32, 2>(tk, tv, a, stream);
+        return rows <= 16 ? launch<D, FP8, 16, 1>(tk, tv, a, stream) : launch<D, FP8, 32, 1>(tk, tv, a, stream);
+    } else {
+        if (a.o_f32)
+            return rows <= 8 ? launch<D, FP8, 8, 3>(tk, tv, a, stream)
+                             : rows <= 16 ? launch<D, FP8, 16, 3>(tk, tv, a, stream) : launch<D, FP8, 32, 3>(tk, tv, a, stream);
+        return rows <= 8 ? launch<D, FP8, 8, 2>(tk, tv, a, stream)
+                         : rows <= 16 ? launch<D, FP8, 16, 2>(tk, tv, a, stream) : launch<D, FP8, 32, 2>(tk, tv, a, stream);
+    }
 }
 
 }  // namespace
 
-fm_status fm_paged_decode_launch(const PagedArgs &a, bool e4m3, cudaStream_t stream)
+fm_status fm_paged_decode_launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, bool e4m3, cudaStream_t stream)
 {
-    if (a.s.d == 128) return e4m3 ? launch_rows<128, true>(a, stream) : launch_rows<128, false>(a, stream);
-    return e4m3 ? launch_rows<64, true>(a, stream) : launch_rows<64, false>(a, stream);
+    if (a.s.d == 128) return e4m3 ? launch_rows<128, true>(tk, tv, a, stream) : launch_rows<128, false>(tk, tv, a, stream);
+    return e4m3 ? launch_rows<64, true>(tk, tv, a, stream) : launch_rows<64, false>(tk, tv, a, stream);
 }

@@ -435,26 +435,49 @@ def fm_attn_fwd_fp8(q8, k8, vt8, descale, bounds: Bounds, plan, scale, o, lse, d
     _check(code, "fm_attn_fwd_fp8")
 
 
-def _same_device(first, **tensors):
-    """All tensors on the first one's device, which has to be the current one (kernels launch there)."""
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {first.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    for n, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{n} is on {t.device}, not on {first.device}")
+# The paged calls are made once per layer and decoding step, where the host's time
+# counts: their checks are written for few attribute reads and no wrappers.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _rows(t, name, d=None):
-    """bf16 [T, H, d] rows with any token and head strides: (token stride, head stride)."""
+def _on(t, name):
+    """Index of the CUDA device of t, which has to be the current one (kernels launch there)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    dev = t.get_device()
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _flat(t, dtype, dev, name, shape=None):
+    """Address of a contiguous tensor of that type (and shape) on device dev."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, dev, name, d):
+    """bf16 [T, H, d] rows with any token and head strides: (T, H, token stride, head stride)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1) or (d is not None and t.shape[2] != d):
-        raise ValueError(f"{name} must be [T, H, {d or 'd'}] with a contiguous last dimension")
-    T, H, n = t.shape
-    st, sh, _ = t.stride()
-    return st if T > 1 else n, sh if H > 1 else n       # the stride of a dimension of size one is never used
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"{name} must be [T, H, {d}], got {list(shape)}")
+    st, sh, se = t.stride()
+    if se != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    T, H, _ = shape
+    return T, H, st if T > 1 else d, sh if H > 1 else d     # the stride of a dimension of size one is never used
 
 
 def paged_cache(k_cache, v_cache, k_descale=None, v_descale=None) -> PagedCache:
@@ -462,34 +485,38 @@ def paged_cache(k_cache, v_cache, k_descale=None, v_descale=None) -> PagedCache:
     e4m3 (uint8 codes or torch.float8_e4m3fn) with device float32 [1] descales.
     Views with other strides (tokens before heads, K and V interleaved) serve
     as they are, so long as the last dimension is contiguous."""
-    c = PagedCache()
-    for n, t in (("k", k_cache), ("v", v_cache)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{n}_cache must be a CUDA tensor")
-        if t.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn) or t.dtype != k_cache.dtype:
-            raise TypeError("caches must both be bfloat16, or both hold e4m3 codes (uint8 or float8_e4m3fn)")
-        if t.dim() != 4 or t.shape != k_cache.shape or t.stride(3) != 1:
-            raise ValueError("caches must be [num_pages, Hkv, page_size, d], of one shape, with a contiguous last dimension")
-    shape = k_cache.shape
-    d = shape[3]
-    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
-    # The stride of a dimension of size one is never used.
-    c.k_page, c.k_head, c.k_tok = (s if n > 1 else d for s, n in zip(k_cache.stride(), shape[:3]))
-    c.v_page, c.v_head, c.v_tok = (s if n > 1 else d for s, n in zip(v_cache.stride(), shape[:3]))
-    c.num_pages, c.Hkv, c.page_size, c.d = shape
-    c.dtype = FM_DT_BF16
-    if k_cache.dtype != torch.bfloat16:
-        c.dtype = FM_DT_E4M3
+    dev = _on(k_cache, "k_cache")
+    if not isinstance(v_cache, torch.Tensor) or v_cache.get_device() != dev:
+        raise TypeError(f"v_cache must be a CUDA tensor on cuda:{dev}")
+    dtype, shape = k_cache.dtype, k_cache.shape
+    kd = vd = None
+    if v_cache.dtype is not dtype or dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+        raise TypeError("caches must both be bfloat16, or both hold e4m3 codes (uint8 or float8_e4m3fn)")
+    code = FM_DT_BF16
+    if dtype is not torch.bfloat16:
+        code = FM_DT_E4M3
         if k_descale is None or v_descale is None:
             raise ValueError("an e4m3 cache needs k_descale and v_descale")
-        c.k_descale = _dev(k_descale, torch.float32, "k_descale").data_ptr()
-        c.v_descale = _dev(v_descale, torch.float32, "v_descale").data_ptr()
-    _same_device(k_cache, v_cache=v_cache, k_descale=k_descale, v_descale=v_descale)
-    return c
+        kd = _flat(k_descale, torch.float32, dev, "k_descale")
+        vd = _flat(v_descale, torch.float32, dev, "v_descale")
+        if k_descale.numel() != 1 or v_descale.numel() != 1:
+            raise ValueError("k_descale and v_descale hold one value each")
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("caches must be [num_pages, Hkv, page_size, d], of one shape")
+    kp, kh, kt, ke = k_cache.stride()
+    vp, vh, vt, ve = v_cache.stride()
+    if ke != 1 or ve != 1:
+        raise ValueError("the last dimension of the caches must be contiguous")
+    P, Hkv, page, d = shape
+    if P == 1 or Hkv == 1 or page == 1:                     # the stride of a dimension of size one is never used
+        kp, vp = (kp, vp) if P > 1 else (d, d)
+        kh, vh = (kh, vh) if Hkv > 1 else (d, d)
+        kt, vt = (kt, vt) if page > 1 else (d, d)
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), kp, kh, kt, vp, vh, vt, kd, vd, P, page, Hkv, d, code)
 
 
 def fm_paged_plan_bytes(step: PagedStep) -> int:
-    return int(_lib.fm_paged_plan_bytes(ctypes.byref(step)))
+    return int(_lib.fm_paged_plan_bytes(step))
 
 
 def fm_paged_plan(step: PagedStep, ctx_lens, q_lens, block_table, seq_lens, cu_q, slots, positions, plan, dev_status,
@@ -498,74 +525,74 @@ def fm_paged_plan(step: PagedStep, ctx_lens, q_lens, block_table, seq_lens, cu_q
     ctx_lens, q_lens, seq_lens: int32 [requests]; block_table: int32 [requests,
     max_pages]; cu_q: int32 [requests + 1]; slots: int64, positions: int32 or
     None [max_tokens]; free_pages: int32 [n] with free_head and free_next int32 [1]."""
-    R = step.requests
-    for n, t, dt, shape in (("ctx_lens", ctx_lens, torch.int32, (R,)), ("q_lens", q_lens, torch.int32, (R,)),
-                            ("block_table", block_table, torch.int32, (R, step.max_pages)),
-                            ("seq_lens", seq_lens, torch.int32, (R,)), ("cu_q", cu_q, torch.int32, (R + 1,)),
-                            ("slots", slots, torch.int64, (step.max_tokens,)), ("plan", plan, torch.uint8, None),
-                            ("dev_status", dev_status, torch.int32, (1,))):
-        if _dev(t, dt, n).shape != shape and shape is not None:
-            raise ValueError(f"{n} must have the shape {list(shape)}")
-    if positions is not None and _dev(positions, torch.int32, "positions").shape != slots.shape:
-        raise ValueError("positions must have the shape of slots")
+    dev, i32 = _on(ctx_lens, "ctx_lens"), torch.int32
+    R, T = step.requests, step.max_tokens
+    free = head = after = None
+    n_free = 0
     if free_pages is not None:
         if free_head is None or free_next is None:
             raise ValueError("free_pages comes with free_head and free_next")
-        for n, t in (("free_pages", free_pages), ("free_head", free_head), ("free_next", free_next)):
-            if _dev(t, torch.int32, n).dim() != 1 or (t is not free_pages and t.numel() != 1):
-                raise ValueError("free_pages is int32 [n], free_head and free_next are int32 [1]")
-    _same_device(ctx_lens, q_lens=q_lens, block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, slots=slots,
-                 positions=positions, plan=plan, dev_status=dev_status, free_pages=free_pages, free_head=free_head,
-                 free_next=free_next)
-    code = _lib.fm_paged_plan(ctypes.byref(step), _ptr(ctx_lens), _ptr(q_lens), _ptr(block_table), _ptr(free_pages),
-                              0 if free_pages is None else free_pages.numel(), _ptr(free_head), _ptr(free_next),
-                              _ptr(seq_lens), _ptr(cu_q), _ptr(slots), _ptr(positions), _ptr(plan), plan.numel(),
-                              _ptr(dev_status), _stream(stream))
-    _check(code, "fm_paged_plan")
+        n_free = free_pages.numel()
+        free = _flat(free_pages, i32, dev, "free_pages", (n_free,))
+        head = _flat(free_head, i32, dev, "free_head", (1,))
+        after = _flat(free_next, i32, dev, "free_next", (1,))
+    code = _lib.fm_paged_plan(
+        step, _flat(ctx_lens, i32, dev, "ctx_lens", (R,)), _flat(q_lens, i32, dev, "q_lens", (R,)),
+        _flat(block_table, i32, dev, "block_table", (R, step.max_pages)), free, n_free, head, after,
+        _flat(seq_lens, i32, dev, "seq_lens", (R,)), _flat(cu_q, i32, dev, "cu_q", (R + 1,)),
+        _flat(slots, torch.int64, dev, "slots", (T,)),
+        None if positions is None else _flat(positions, i32, dev, "positions", (T,)),
+        _flat(plan, torch.uint8, dev, "plan"), plan.numel(), _flat(dev_status, i32, dev, "dev_status", (1,)),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_paged_plan")
 
 
 def fm_paged_append(k, v, slots, k_cache, v_cache, dev_status, k_descale=None, v_descale=None, stream=None):
     """Rows of k and v (bf16 [T, Hkv, d], any token and head strides) to the cache's
     slots (int64, T of them at least; negative ones are skipped)."""
     cache = paged_cache(k_cache, v_cache, k_descale, v_descale)
-    kt, kh = _rows(k, "k", cache.d)
-    vt, vh = _rows(v, "v", cache.d)
-    T = k.shape[0]
-    if v.shape != k.shape or k.shape[1] != cache.Hkv:
+    dev = k_cache.get_device()
+    T, H, kt, kh = _rows(k, dev, "k", cache.d)
+    Tv, Hv, vt, vh = _rows(v, dev, "v", cache.d)
+    if T != Tv or H != Hv or H != cache.Hkv:
         raise ValueError("k and v must be [T, Hkv, d] of the cache")
-    if _dev(slots, torch.int64, "slots").dim() != 1 or slots.shape[0] < T:
+    if slots.dim() != 1 or slots.shape[0] < T:
         raise ValueError("slots must be int64 with an entry for every row of k")
-    _dev(dev_status, torch.int32, "dev_status")
-    _same_device(k_cache, k=k, v=v, slots=slots, dev_status=dev_status)
+    at, status = _flat(slots, torch.int64, dev, "slots"), _flat(dev_status, torch.int32, dev, "dev_status", (1,))
     if T == 0:
         return
-    code = _lib.fm_paged_append(_ptr(k), kt, kh, _ptr(v), vt, vh, _ptr(slots), T, ctypes.byref(cache), _ptr(dev_status),
-                                _stream(stream))
-    _check(code, "fm_paged_append")
+    code = _lib.fm_paged_append(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, at, T, cache, status,
+                                _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_paged_append")
 
 
 def fm_attn_paged(step: PagedStep, q, k_cache, v_cache, block_table, plan, scale, o, lse, dev_status, k_descale=None,
                   v_descale=None, stream=None):
     """Attention of a step's new tokens (q: bf16 [rows, Hq, d]) over the paged cache;
     o: bf16 or fp32 [rows, Hq, d], lse: fp32 [rows, Hq] (see fm.h)."""
+    dev = _on(q, "q")
+    _flat(o, o.dtype, dev, "o", q.shape)
+    _flat(lse, torch.float32, dev, "lse", q.shape[:2])
+    _attn_paged(step, q, k_cache, v_cache, block_table, plan, scale, o, lse, dev_status, k_descale, v_descale, stream)
+
+
+def _attn_paged(step, q, k_cache, v_cache, block_table, plan, scale, o, lse, dev_status, k_descale, v_descale, stream):
+    """fm_attn_paged with o and lse known to fit q."""
     cache = paged_cache(k_cache, v_cache, k_descale, v_descale)
-    qt, qh = _rows(q, "q", step.d)
-    if q.shape[1] != step.Hq:
+    dev = k_cache.get_device()
+    T, H, qt, qh = _rows(q, dev, "q", step.d)
+    if H != step.Hq:
         raise ValueError("q must be [rows, Hq, d] of the step")
-    _dev(o, o.dtype, "o")
-    if o.shape != q.shape or _dev(lse, torch.float32, "lse").shape != q.shape[:2]:
-        raise ValueError("o must have the shape of q, and lse [rows, Hq]")
-    if _dev(block_table, torch.int32, "block_table").shape != (step.requests, step.max_pages):
-        raise ValueError("block_table must be [requests, max_pages]")
-    _dev(plan, torch.uint8, "plan")
-    _dev(dev_status, torch.int32, "dev_status")
-    _same_device(q, k_cache=k_cache, o=o, lse=lse, block_table=block_table, plan=plan, dev_status=dev_status)
-    if q.shape[0] == 0:
+    table = _flat(block_table, torch.int32, dev, "block_table", (step.requests, step.max_pages))
+    buf, status = _flat(plan, torch.uint8, dev, "plan"), _flat(dev_status, torch.int32, dev, "dev_status", (1,))
+    if T == 0:
         return
-    code = _lib.fm_attn_paged(ctypes.byref(step), _ptr(q), qt, qh, q.shape[0], ctypes.byref(cache), _ptr(block_table),
-                              _ptr(plan), plan.numel(), float(scale), _ptr(o), _dt(o), _ptr(lse), _ptr(dev_status),
-                              _stream(stream))
-    _check(code, "fm_attn_paged")
+    code = _lib.fm_attn_paged(step, q.data_ptr(), qt, qh, T, cache, table, buf, plan.numel(), scale, o.data_ptr(), _dt(o),
+                              lse.data_ptr(), status, _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_attn_paged")
 
 
 def fm_step_graph_create(q, k, v, dO, bounds: Bounds, plan, scale, o, lse, dev_status, dq=None, dk=None,
@@ -710,10 +737,11 @@ class PagedAttention:
     def attend(self, q, k_cache, v_cache, block_table, scale=None, o_dtype=torch.bfloat16, k_descale=None,
                v_descale=None):
         scale = 1.0 / self.step.d ** 0.5 if scale is None else scale
-        o = torch.empty(q.shape, dtype=o_dtype, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        fm_attn_paged(self.step, q, k_cache, v_cache, block_table, self.plan_buffer, scale, o, lse, self.status,
-                      k_descale, v_descale)
+        shape = q.shape
+        o = torch.empty(shape, dtype=o_dtype, device=q.device)
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        _attn_paged(self.step, q, k_cache, v_cache, block_table, self.plan_buffer, scale, o, lse, self.status, k_descale,
+                    v_descale, None)
         return o, lse
 
     def check_status(self):
