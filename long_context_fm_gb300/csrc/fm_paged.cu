@@ -513,11 +513,12 @@ fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok,
     const uint64_t d = a.s.d, kt = cache->k_tok * esz, kh = cache->k_head * esz, kp = cache->k_page * esz, vt = cache->v_tok * esz,
                    vh = cache->v_head * esz, vp = cache->v_page * esz;
     const uint64_t pages = a.s.num_pages, page = a.s.page_size, heads = a.s.Hkv;
+    // Boxes of consecutive keys of one page, a power of two of them.
+    int box_keys = kPageGranule;
+    while (box_keys < kKeyTile && a.s.page_size % (2 * box_keys) == 0) box_keys *= 2;
     if ((int64_t)a.s.max_q * G > kFewRows) {
-        // Some request may have many rows.  Boxes: the query heads of a KV head times
-        // as many tokens as make 128 rows; consecutive keys of one page, a power of two.
-        int box_keys = kPageGranule;
-        while (box_keys < kKeyTile && a.s.page_size % (2 * box_keys) == 0) box_keys *= 2;
+        // Some request may have many rows.  Q boxes: the query heads of a KV head times
+        // as many tokens as make 128 rows.
         CUtensorMap tq, tk, tv;
         const uint64_t qd[3] = {d, (uint64_t)a.s.Hq, (uint64_t)(rows > 0 ? rows : 1)};
         const uint64_t qs[2] = {(uint64_t)a.q_head, (uint64_t)a.q_tok};
@@ -530,18 +531,18 @@ fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok,
             return FM_ERR_CUDA;
         if ((st = fm_paged_chunk_launch(tq, tk, tv, a, box_keys, fp8, (cudaStream_t)stream)) != FM_OK) return st;
     }
-    // Boxes of 16 keys: rows of 128 bytes (bf16, d = 128: two of them, as a
+    // Rows of 128 bytes (bf16, d = 128: two of them, as a
     // dimension of its own) or of 64 bytes (e4m3, d = 64).
     const uint64_t wide = fp8 ? d : 64;
     const uint32_t halves = (uint32_t)(d / wide);
     CUtensorMap tk, tv;
     const uint64_t cd[5] = {wide, page, halves, heads, pages};
     const uint64_t ks[4] = {kt, 128, kh, kp}, vs[4] = {vt, 128, vh, vp};
-    const uint32_t cb[5] = {(uint32_t)wide, kPageGranule, halves, 1, 1};
+    const uint32_t cb[5] = {(uint32_t)wide, (uint32_t)box_keys, halves, 1, 1};
     const int swizzle = (int)(wide * esz);
     if (!make_tmap_strided(&tk, cache->k, fp8, 5, cd, ks, cb, swizzle) || !make_tmap_strided(&tv, cache->v, fp8, 5, cd, vs, cb, swizzle))
         return FM_ERR_CUDA;
-    return fm_paged_decode_launch(tk, tv, a, fp8, (cudaStream_t)stream);
+    return fm_paged_decode_launch(tk, tv, a, box_keys, fp8, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -154,8 +154,8 @@ bool make_tmap_strided(CUtensorMap *map, const void *base, bool u8, int rank, co
 }  // namespace fm
 
 // Launchers of the few-rows kernel (fm_paged_decode.cu) and of the many-rows
-// kernel (fm_paged_chunk.cu; box_keys: keys of one TMA box).
-fm_status fm_paged_decode_launch(const CUtensorMap &tk, const CUtensorMap &tv, const fm::PagedArgs &a, bool e4m3,
-                                 cudaStream_t stream);
+// kernel (fm_paged_chunk.cu); box_keys: consecutive keys of one TMA box.
+fm_status fm_paged_decode_launch(const CUtensorMap &tk, const CUtensorMap &tv, const fm::PagedArgs &a, int box_keys,
+                                 bool e4m3, cudaStream_t stream);
 fm_status fm_paged_chunk_launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const fm::PagedArgs &a,
                                 int box_keys, bool e4m3, cudaStream_t stream);

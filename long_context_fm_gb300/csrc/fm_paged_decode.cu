@@ -43,21 +43,33 @@
 namespace fm {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr float kBand = 8.f;   // lazy rescale: P stays <= 2^8, sums are rescaled when a maximum grows by more
 
-template <int D, bool FP8>
+constexpr int kWarps = 8;              // that compute; a warpgroup behind them has the one that loads
+constexpr int kThreads = (kWarps + 4) * 32;
+// Registers: the loading warpgroup gives its share to the others.
+constexpr int kLaunchRegs = 168, kRegsCompute = 232, kRegsLoad = 40;
+static_assert(kWarps * 32 * kRegsCompute + 128 * kRegsLoad <= kThreads * kLaunchRegs, "register split");
+constexpr int kSumBar = 1;             // named barrier of the computing warps
+
+template <int D, bool FP8, int ROWS>
 struct DecodeCfg {
     static constexpr int kRow = D * (FP8 ? 1 : 2);          // bytes of a key's row
-    static constexpr int kSlot = 2 * 16 * kRow;             // a warp's 16 keys: K rows, then V rows
-    static constexpr int kStages = 192 * 1024 / (kWarps * kSlot) < 8 ? 192 * 1024 / (kWarps * kSlot) : 8;
-    static constexpr int kRing = 0;
-    static constexpr int kRed = kWarps * kStages * kSlot;   // float4 [8 warps][8][32 lanes]; Q of 32 rows between units
-    static constexpr int kMl = kRed + kWarps * 8 * 32 * 16; // float [8 warps][2][kFewRows]
-    static constexpr int kBar = kMl + kWarps * 2 * kFewRows * 4;   // mbarrier [8 warps][stages]
-    static constexpr int kMisc = kBar + kWarps * kStages * 8;
+    // 16-key groups that a warp takes at a time.  Two where a row has 128 bytes or
+    // fewer and the registers allow it: more independent products per step; every
+    // other tile then belongs to one half of the warps.
+    static constexpr int kSub = (kRow == 256 || ROWS == 32) ? 1 : 2;
+    static constexpr int kStage = 2 * kKeyTile * kRow;      // a tile: K boxes, then V boxes
+    static constexpr int kStages = 192 * 1024 / kStage < 8 ? 192 * 1024 / kStage : 8;
+    static constexpr int kPieces = ROWS == 8 ? 4 : 8;
+    static constexpr int kRed = kStages * kStage;           // float4 [warps][pieces][32 lanes]; Q of 32 rows between units
+    static constexpr int kMl = kRed + kWarps * kPieces * 32 * 16;   // float [warps][2][kFewRows]
+    static constexpr int kBar = kMl + kWarps * 2 * kFewRows * 4;    // mbarrier [2][stages]: loaded, read
+    static constexpr int kMisc = kBar + 2 * kStages * 8;
     static constexpr int kBytes = kMisc + 16;
     static_assert(kBytes <= 227 * 1024, "shared memory of the few-rows kernel");
+    static_assert(kPagedCtas * ROWS * 4 <= kMl - kRed, "weights of a split unit's parts");
+    static_assert(ROWS != 32 || kFewRows * (D * 2 + 4) <= kMl - kRed, "Q of 32 rows");
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t a)
@@ -121,11 +133,13 @@ struct Cursor {
 
 // ROWS: 8, 16 or 32 rows of a unit at most; TERMS: 16-bit terms of P.
 template <int D, bool FP8, int ROWS, int TERMS>
-__global__ void __launch_bounds__(kWarps * 32, 1)
-    fm_paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PagedArgs a)
+__global__ void __launch_bounds__(kThreads, 1)
+    fm_paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PagedArgs a,
+                           const int box_keys)
 {
-    using C = DecodeCfg<D, FP8>;
-    constexpr int ST = C::kStages;
+    using C = DecodeCfg<D, FP8, ROWS>;
+    constexpr int ST = C::kStages, SUB = C::kSub;
+    constexpr int WPT = kWarps / SUB;       // warps of a tile
     constexpr bool NARROW = C::kRow == 64;
     constexpr int MT = ROWS == 32 ? 2 : 1;  // 16-row blocks
     constexpr int NR = ROWS == 8 ? 1 : 2;   // rows of a block per thread
@@ -152,14 +166,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int64_t x0 = share_begin(W, ctas, blockIdx.x);
     int left = (int)(share_begin(W, ctas, blockIdx.x + 1) - x0);   // tiles to compute
     if (left == 0) return;
-    int to_load = left;
-    const int loaded = left;
 
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBar) + warp * ST;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBar), *empty = full + ST;
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
-    if (lane == 0) {
-        for (int i = 0; i < ST; ++i) mbar_init(&bars[i], 1);
-        if (warp == 0) *abort = 0;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 4);         // the loading warps
+            mbar_init(&empty[i], WPT);
+        }
+        *abort = 0;
         fence_barrier_init();
     }
     __syncthreads();
@@ -184,55 +199,69 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         return true;
     };
 
-    Cursor ld;
+    Cursor cu;
     {
         const int4 v = *reinterpret_cast<const int4 *>(a.plan + a.L.off_start + (int64_t)blockIdx.x * 16);
-        ld.e = v.x;
-        ld.h = v.y;
-        ld.x = v.z;
-        enter(ld);
+        cu.e = v.x;
+        cu.h = v.y;
+        cu.x = v.z;
+        enter(cu);
     }
-    Cursor cu = ld;
+    // A tile's boxes of box_keys consecutive keys of one page: [128-byte box of a
+    // row][key][128 bytes] each.  Some: a row attends one of the n keys from j on.
+    const int n_box = kKeyTile / box_keys;
+    auto some = [&](int j, int n) { return j < cu.kr.hi && !(j + n <= cu.kr.lo && j >= s.sink); };
 
-    uint8_t *ring = smem + C::kRing + warp * ST * C::kSlot;
-    // This warp's 16 keys of the tile that `u` stands at; some: a row attends one of them.
-    auto first_key = [&](const Cursor &u) { return u.kr.tile(u.x) * kKeyTile + warp * 16; };
-    auto some = [&](const Cursor &u, int k0) { return k0 < u.kr.hi && !(k0 + 16 <= u.kr.lo && k0 >= s.sink); };
-    // Their page: num_pages (outside the pool: arrives as zeros) when its number is.
-    auto page_of = [&](const Cursor &u) -> int {
-        const int k0 = first_key(u);
-        if (!some(u, k0)) return -1;
-        const int p = __ldg(a.table + (int64_t)u.ent.r * s.max_pages + (a.page_shift >= 0 ? k0 >> a.page_shift : k0 / s.page_size));
-        if (p < 0 || p >= s.num_pages) {
-            if (lane == 0) set_status(a.status, FM_ERR_PAGES);
-            return s.num_pages;
-        }
-        return p;
-    };
-    int page = page_of(ld);
-    int slot_ld = 0;
-    // Starts the copies of the tile that the load walk stands at, and looks up
-    // the next tile's page meanwhile.  A tile without keys for this warp
-    // completes its slot's phase with no bytes.
-    auto load_tile = [&]() {
-        if (to_load == 0) return;
-        if (lane == 0) {
-            if (page >= 0) {
-                const int k0 = first_key(ld);
-                const int in = a.page_shift >= 0 ? k0 & (s.page_size - 1) : k0 % s.page_size;
-                uint8_t *dst = ring + slot_ld * C::kSlot;
-                mbar_arrive_expect_tx(&bars[slot_ld], C::kSlot);
-                tma_load_5d(dst, &tk, &bars[slot_ld], 0, in, 0, ld.h, page);
-                tma_load_5d(dst + 16 * C::kRow, &tv, &bars[slot_ld], 0, in, 0, ld.h, page);
-            } else {
-                mbar_arrive(&bars[slot_ld]);
+    if (warp >= kWarps) {
+        warp_regs_dec<kRegsLoad>();
+        // ------------------------------------------------ loads
+        // Warps 0 and 1 of the group load the even and the odd boxes of K, 2 and 3
+        // those of V, a lane each with its own page, looked up a tile ahead.  (One
+        // warp alone takes about 130 cycles per box one after the other: 16-token
+        // pages of e4m3, 0.160 ms where four warps need ... see below.)
+        const int part = warp - kWarps, bx = (part & 1) + 2 * lane;
+        const bool mine = bx < n_box;
+        const CUtensorMap *map = part < 2 ? &tk : &tv;
+        const uint32_t box_bytes = (uint32_t)box_keys * C::kRow;
+        const int none = -1 - s.num_pages;      // no page number of a box without attended keys
+        auto look_up = [&]() -> int {
+            const int j = cu.kr.tile(cu.x) * kKeyTile + bx * box_keys;
+            if (!mine || !some(j, box_keys)) return none;
+            return __ldg(a.table + (int64_t)cu.ent.r * s.max_pages + (a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size));
+        };
+        int next = look_up(), t = 0;
+        for (; t < left; ++t) {
+            const int st = t % ST;
+            int page = next;
+            const int j = cu.kr.tile(cu.x) * kKeyTile + bx * box_keys, h = cu.h;
+            advance(cu, t + 1 < left);
+            if (t + 1 < left) next = look_up();
+            if (t >= ST && !warp_wait(&empty[st], ((t / ST) - 1) & 1, abort, a.status)) break;
+            const unsigned used = __ballot_sync(0xffffffffu, page != none);
+            if (lane == 0) {
+                if (used) mbar_arrive_expect_tx(&full[st], __popc(used) * box_bytes);
+                else mbar_arrive(&full[st]);
+            }
+            __syncwarp();
+            if (page != none) {
+                if (page < 0 || page >= s.num_pages) {
+                    set_status(a.status, FM_ERR_PAGES);
+                    page = s.num_pages;         // outside the pool: arrives as zeros
+                }
+                const int in = a.page_shift >= 0 ? j & (s.page_size - 1) : j % s.page_size;
+                tma_load_5d(smem + st * C::kStage + ((part >> 1) * n_box + bx) * box_bytes, map, &full[st], 0, in, 0, h, page);
             }
         }
-        --to_load;
-        advance(ld, to_load > 0);
-        if (to_load > 0) page = page_of(ld);
-        slot_ld = slot_ld + 1 == ST ? 0 : slot_ld + 1;
-    };
+        // After a wait that ran out: the copies end before the CTA leaves.
+        if (*abort && lane == 0)
+            for (int i = max(t - ST, 0); i < t; ++i) mbar_wait_drain(&full[i % ST], (i / ST) & 1, a.status);
+        return;
+    }
+    warp_regs_inc<kRegsCompute>();
+    // This warp's keys of a tile, 16 SUB of them, and where they lie in a stage.
+    const int turn = warp / WPT;            // with SUB = 2: takes the even or the odd tiles of the walk
+    const int key0 = (warp % WPT) * (16 * SUB);
+    const uint32_t half_box = (uint32_t)box_keys * 128;     // from a row's first 128 bytes to its second
 
     uint32_t qf[MT == 1 ? KS : 1][4];       // one 16-row block: Q fragments in registers
     float qs[MT][NR];                       // score factor of rows g, g + 8 (softmax scale, log2 e, descale, Q's own factor)
@@ -330,7 +359,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int i = 0; i < D / 16; ++i)
                     w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
             }
-            __syncthreads();                    // the previous unit's use of the space is over
+            named_bar_sync(kSumBar, kWarps * 32);                    // the previous unit's use of the space is over
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 const int ch = part * (D / 64) + i;
@@ -338,7 +367,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             }
             if (part == 0) *reinterpret_cast<float *>(sq + kFewRows * D * 2 + row * 4) = f;
-            __syncthreads();
+            named_bar_sync(kSumBar, kWarps * 32);
 #pragma unroll
             for (int b = 0; b < MT; ++b)
 #pragma unroll
@@ -401,7 +430,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     sml[(warp * 2 + 1) * kFewRows + b * 16 + hf * 8 + g] = sum;
                 }
             }
-        __syncthreads();
+        named_bar_sync(kSumBar, kWarps * 32);
         // Slot of a partial result: 2 c + 1 when the unit begins in this CTA's share, 2 c when it comes in from the left.
         const int slot = 2 * (int)bid + ((int)bid == c_first ? 1 : 0);
 #pragma unroll
@@ -429,22 +458,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
 #pragma unroll
             for (int np = 0; np < NP; ++np) {
-                if (b > 0 || np > 0) __syncthreads();
+                if (b > 0 || np > 0) named_bar_sync(kSumBar, kWarps * 32);
                 // piece z = (row half, column half, 4 of 8 tiles)
 #pragma unroll
                 for (int z = 0; z < 4 * NR; ++z) {
                     const int hf = z >> 2, y = 2 * hf + ((z >> 1) & 1), t = np * 8 + (z & 1) * 4;
                     if (b * 16 + hf * 8 < nrows)
-                        red[(warp * 8 + z) * 32 + lane] = make_float4(oa[b][t][y] * f[hf], oa[b][t + 1][y] * f[hf],
+                        red[(warp * 4 * NR + z) * 32 + lane] = make_float4(oa[b][t][y] * f[hf], oa[b][t + 1][y] * f[hf],
                                                                       oa[b][t + 2][y] * f[hf], oa[b][t + 3][y] * f[hf]);
                 }
-                __syncthreads();
+                named_bar_sync(kSumBar, kWarps * 32);
                 const int z = warp, row = b * 16 + (z >> 2) * 8 + g;
                 if (z < 4 * NR && row < nrows) {
                     float4 v = red[z * 32 + lane];
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) {
-                        const float4 u = red[(w * 8 + z) * 32 + lane];
+                        const float4 u = red[(w * 4 * NR + z) * 32 + lane];
                         v.x += u.x;
                         v.y += u.y;
                         v.z += u.z;
@@ -460,15 +489,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (parts == 1) return;
         // A split unit: the last of its CTAs adds the partial results up, in the CTAs' order.
         __threadfence();
-        __syncthreads();
+        named_bar_sync(kSumBar, kWarps * 32);
         if (threadIdx.x == 0) {
             unsigned *cnt = reinterpret_cast<unsigned *>(a.plan + a.L.off_count) + c_first;
             *flag = atomicInc(cnt, (unsigned)(parts - 1)) == (unsigned)(parts - 1);   // returns to 0 by itself
             __threadfence();
         }
-        __syncthreads();
+        named_bar_sync(kSumBar, kWarps * 32);
         if (!*flag) return;
-        float *wt = reinterpret_cast<float *>(red);             // [part][row] weights, then [row] 1 / sum
+        float *wt = reinterpret_cast<float *>(red);             // [part][row] weights
         for (int row = warp; row < nrows; row += kWarps) {
             float mx = -INFINITY;
             for (int p = lane; p < parts; p += 32)
@@ -480,7 +509,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int p = lane; p < parts; p += 32) {
                 const float *pm = ws_ml + (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)) * 2 * kFewRows + row;
                 const float w = ex2(__ldcg(pm) - mu);
-                wt[p * kFewRows + row] = w;
+                wt[p * ROWS + row] = w;
                 sum += w * __ldcg(pm + kFewRows);
             }
 #pragma unroll
@@ -490,13 +519,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 sml[row] = sum != 0.f ? vds / sum : 0.f;
             }
         }
-        __syncthreads();
+        named_bar_sync(kSumBar, kWarps * 32);
         for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
             const int row = i / (D / 4), dim = (i % (D / 4)) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
             for (int p = 0; p < parts; ++p) {
-                const float w = wt[p * kFewRows + row];
+                const float w = wt[p * ROWS + row];
                 const float4 u = __ldcg(reinterpret_cast<const float4 *>(
                     ws_o + ((int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)) * kFewRows + row) * D + dim));
                 v.x += u.x * w;
@@ -506,48 +535,53 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
             store4(en, h, row, dim, v, sml[row]);
         }
-        __syncthreads();
+        named_bar_sync(kSumBar, kWarps * 32);
     };
 
     // ---- the walk -------------------------------------------------------------
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) load_tile();
     begin_unit();
-    // Byte offsets of this thread's fragments in a slot.
-    uint32_t k_at[2], v_at[2];          // K: even and odd load of a box; V: keys ka and kb2
+    // Byte offsets of this thread's fragments in a stage.
+    uint32_t group[SUB], k_at[2], v_at[2];  // groups of 16 keys; K: even and odd load of a box; V: keys ka and kb2
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) {
+        const int j = key0 + 16 * i;
+        group[i] = (uint32_t)(j / box_keys * box_keys * C::kRow + j % box_keys * (NARROW ? 64 : 128));
+    }
     k_at[0] = chunk_at<NARROW>(kg, c);
     k_at[1] = NARROW ? 0 : chunk_at<NARROW>(kg, c + 4);
-    v_at[0] = 16 * C::kRow + (NARROW ? chunk_at<NARROW>(ka, g >> 1) + (g & 1) * 8 : chunk_at<NARROW>(ka, piece_of<NARROW>(g)));
-    v_at[1] = 16 * C::kRow + (NARROW ? chunk_at<NARROW>(kb2, g >> 1) + (g & 1) * 8 : chunk_at<NARROW>(kb2, piece_of<NARROW>(g)));
+    constexpr uint32_t V0 = kKeyTile * C::kRow;             // V behind K
+    v_at[0] = V0 + (NARROW ? chunk_at<NARROW>(ka, g >> 1) + (g & 1) * 8 : chunk_at<NARROW>(ka, piece_of<NARROW>(g)));
+    v_at[1] = V0 + (NARROW ? chunk_at<NARROW>(kb2, g >> 1) + (g & 1) * 8 : chunk_at<NARROW>(kb2, piece_of<NARROW>(g)));
     constexpr uint32_t ROW8 = NARROW ? 512 : 1024;          // eight rows further
-    int slot = 0;
+    int st = 0, step = 0;
     uint32_t phase = 0;
     while (left > 0) {
-        load_tile();                    // into the slot that the previous round has read
+        const int kw = cu.kr.tile(cu.x) * kKeyTile + key0;
         // A wait that ran out has set the status: the walk goes on, so that every
         // barrier is reached, and what it writes does not count.
-        warp_wait(&bars[slot], phase, abort, a.status);
-        const int k0 = first_key(cu);
-        if (some(cu, k0)) {
-            uint8_t *sp = ring + slot * C::kSlot;
-            const uint32_t base = smem_u32(sp);
-            const bool whole = k0 + 16 <= cu.kr.hi && (k0 >= cu.kr.lo || k0 + 16 <= s.sink);
+        if (step % SUB == turn) warp_wait(&full[st], phase, abort, a.status);
+        if (step % SUB == turn && some(kw, 16 * SUB)) {
+            const uint32_t base = smem_u32(smem) + st * C::kStage;
+            const bool whole = kw + 16 * SUB <= cu.kr.hi && (kw >= cu.kr.lo || kw + 16 * SUB <= s.sink);
             if (!whole) {
                 // V of keys that no row attends becomes zero: what a page holds behind
-                // the last token reaches no product (0 x NaN).
+                // the last token (or the stage from before) reaches no product (0 x NaN).
                 constexpr int CH = C::kRow / 16;
-                for (int i = lane; i < 16 * CH; i += 32) {
-                    const int row = i / CH, ch = i % CH, j = k0 + row;
-                    if (j >= cu.kr.hi || (j < cu.kr.lo && j >= s.sink))
-                        st_shared_v4(sp + 16 * C::kRow + (ch >> 3) * 2048 + chunk_at<NARROW>(row, ch & 7), make_uint4(0, 0, 0, 0));
-                }
+#pragma unroll
+                for (int q = 0; q < SUB; ++q)
+                    for (int i = lane; i < 16 * CH; i += 32) {
+                        const int row = i / CH, ch = i % CH, j = kw + 16 * q + row;
+                        if (j >= cu.kr.hi || (j < cu.kr.lo && j >= s.sink))
+                            st_shared_v4(smem + st * C::kStage + V0 + group[q] + (ch >> 3) * half_box + chunk_at<NARROW>(row, ch & 7),
+                                         make_uint4(0, 0, 0, 0));
+                    }
                 __syncwarp();
             }
-            float sc[MT][2][4];
+            float sc[MT][2 * SUB][4];
 #pragma unroll
             for (int b = 0; b < MT; ++b)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < 2 * SUB; ++nt)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) sc[b][nt][y] = 0.f;
             // Scores: 16 bytes of a key per thread and load are two k-steps of
@@ -581,8 +615,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     }
                 }
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const uint4 kv = lds128(base + k_at[i & 1] + (i >> 1) * 2048 + nt * ROW8);
+                for (int nt = 0; nt < 2 * SUB; ++nt) {
+                    const uint4 kv = lds128(base + group[nt >> 1] + k_at[i & 1] + (i >> 1) * half_box + (nt & 1) * ROW8);
                     const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
 #pragma unroll
                     for (int y = 0; y < PER; ++y) {
@@ -594,41 +628,46 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     }
                 }
             }
-            // Scaled, and masked where some row does not attend some of the 16 keys.
-            const bool edge = k0 + 15 > cu.ent.ctx ||
-                              (s.window > 0 && k0 <= cu.ent.ctx + cu.ent.n - 1 - s.window && k0 + 16 > s.sink);
+            // Scaled, and masked where some row does not attend some of the keys.
+            const bool edge = kw + 16 * SUB - 1 > cu.ent.ctx ||
+                              (s.window > 0 && kw <= cu.ent.ctx + cu.ent.n - 1 - s.window && kw + 16 * SUB > s.sink);
 #pragma unroll
             for (int b = 0; b < MT; ++b)
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < 2 * SUB; ++nt)
 #pragma unroll
                     for (int y = 0; y < 2 * NR; ++y) sc[b][nt][y] *= qs[b][y >> 1];
             if (edge) {
 #pragma unroll
                 for (int b = 0; b < MT; ++b)
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
+                    for (int nt = 0; nt < 2 * SUB; ++nt)
 #pragma unroll
                         for (int y = 0; y < 2 * NR; ++y) {
-                            const int j = k0 + nt * 8 + ((y & 1) ? kb2 : ka), p = pos[b][y >> 1];
+                            const int j = kw + nt * 8 + ((y & 1) ? kb2 : ka), p = pos[b][y >> 1];
                             if (!(j <= p && (s.window == 0 || j > p - s.window || j < s.sink))) sc[b][nt][y] = -INFINITY;
                         }
             }
             // Running maxima, raised lazily: only when a score exceeds one by more
             // than the band do the lanes of a row agree on a new one.
+            auto row_max = [&](int b, int hf) {
+                float x = fmaxf(sc[b][0][2 * hf], sc[b][0][2 * hf + 1]);
+#pragma unroll
+                for (int nt = 1; nt < 2 * SUB; ++nt) x = fmax3(x, sc[b][nt][2 * hf], sc[b][nt][2 * hf + 1]);
+                return x;
+            };
             bool raise = false;
 #pragma unroll
             for (int b = 0; b < MT; ++b)
 #pragma unroll
                 for (int hf = 0; hf < NR; ++hf)
-                    raise = raise || fmaxf(fmax3(sc[b][0][2 * hf], sc[b][0][2 * hf + 1], sc[b][1][2 * hf]), sc[b][1][2 * hf + 1]) >
-                                         m[b][hf] + kBand;
+                    raise = raise || row_max(b, hf) > m[b][hf] + kBand;
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int b = 0; b < MT; ++b)
 #pragma unroll
                     for (int hf = 0; hf < NR; ++hf) {
-                        float x = fmaxf(fmax3(sc[b][0][2 * hf], sc[b][0][2 * hf + 1], sc[b][1][2 * hf]), sc[b][1][2 * hf + 1]);
+                        float x = row_max(b, hf);
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                         if (x > m[b][hf]) {
@@ -648,14 +687,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     }
             }
             // P and its sums, as fragments: pt[term][key half][row half].
-            uint32_t pt[MT][3][2][2];
+            uint32_t pt[MT][TERMS][2 * SUB][NR];
 #pragma unroll
             for (int b = 0; b < MT; ++b)
 #pragma unroll
                 for (int hf = 0; hf < NR; ++hf) {
                     const float mu = m[b][hf] == -INFINITY ? 0.f : m[b][hf];
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
+                    for (int nt = 0; nt < 2 * SUB; ++nt) {
                         float p0 = ex2(sc[b][nt][2 * hf] - mu), p1 = ex2(sc[b][nt][2 * hf + 1] - mu);
                         l[b][hf] += p0 + p1;
 #pragma unroll
@@ -672,27 +711,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     }
                 }
             // O += P V: the thread's two key pairs, columns as dim_of() says.
-            auto pv = [&](int t, uint32_t b0, uint32_t b1) {
+            auto pv = [&](int q, int t, uint32_t b0, uint32_t b1) {
 #pragma unroll
                 for (int b = 0; b < MT; ++b) {
                     if (NR == 1) {
                         // Rows 0-7 the first term, rows 8-15 the second; then the third.
-                        mma16816<FP8>(oa[b][t], pt[b][0][0][0], TERMS > 1 ? pt[b][1][0][0] : 0u, pt[b][0][1][0], TERMS > 1 ? pt[b][1][1][0] : 0u, b0, b1);
-                        if (TERMS > 2) mma16816<FP8>(oa[b][t], 0u, pt[b][2][0][0], 0u, pt[b][2][1][0], b0, b1);
+                        mma16816<FP8>(oa[b][t], pt[b][0][2 * q][0], TERMS > 1 ? pt[b][1 % TERMS][2 * q][0] : 0u, pt[b][0][2 * q + 1][0],
+                                      TERMS > 1 ? pt[b][1 % TERMS][2 * q + 1][0] : 0u, b0, b1);
+                        if (TERMS > 2)
+                            mma16816<FP8>(oa[b][t], 0u, pt[b][2 % TERMS][2 * q][0], 0u, pt[b][2 % TERMS][2 * q + 1][0], b0, b1);
                     } else {
 #pragma unroll
                         for (int y = 0; y < TERMS; ++y)
-                            mma16816<FP8>(oa[b][t], pt[b][y][0][0], pt[b][y][0][NR - 1], pt[b][y][1][0], pt[b][y][1][NR - 1], b0, b1);
+                            mma16816<FP8>(oa[b][t], pt[b][y][2 * q][0], pt[b][y][2 * q][NR - 1], pt[b][y][2 * q + 1][0],
+                                          pt[b][y][2 * q + 1][NR - 1], b0, b1);
                     }
                 }
             };
+#pragma unroll
+            for (int q = 0; q < SUB; ++q) {
+            const uint32_t vq = base + group[q];
             if (!FP8) {
 #pragma unroll
                 for (int np = 0; np < NP; ++np) {
                     uint32_t w[4][4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const uint4 v = lds128(base + v_at[r & 1] + np * 2048 + (r >> 1) * ROW8);
+                        const uint4 v = lds128(vq + v_at[r & 1] + np * half_box + (r >> 1) * ROW8);
                         w[r][0] = v.x;
                         w[r][1] = v.y;
                         w[r][2] = v.z;
@@ -700,8 +745,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                     }
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        pv(np * 8 + 2 * x, __byte_perm(w[0][x], w[1][x], 0x5410), __byte_perm(w[2][x], w[3][x], 0x5410));
-                        pv(np * 8 + 2 * x + 1, __byte_perm(w[0][x], w[1][x], 0x7632), __byte_perm(w[2][x], w[3][x], 0x7632));
+                        pv(q, np * 8 + 2 * x, __byte_perm(w[0][x], w[1][x], 0x5410), __byte_perm(w[2][x], w[3][x], 0x5410));
+                        pv(q, np * 8 + 2 * x + 1, __byte_perm(w[0][x], w[1][x], 0x7632), __byte_perm(w[2][x], w[3][x], 0x7632));
                     }
                 }
             } else {
@@ -709,7 +754,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 uint32_t w[4][WD];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const uint32_t at = base + v_at[r & 1] + (r >> 1) * ROW8;
+                    const uint32_t at = vq + v_at[r & 1] + (r >> 1) * ROW8;
                     if (WD == 4) {
                         const uint4 v = lds128(at);
                         w[r][0] = v.x;
@@ -727,27 +772,29 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 for (int x = 0; x < WD; ++x) {
                     const uint32_t lo01 = __byte_perm(w[0][x], w[1][x], 0x5140), hi01 = __byte_perm(w[0][x], w[1][x], 0x7362);
                     const uint32_t lo23 = __byte_perm(w[2][x], w[3][x], 0x5140), hi23 = __byte_perm(w[2][x], w[3][x], 0x7362);
-                    pv(4 * x, f16x2_of_e4m3(lo01), f16x2_of_e4m3(lo23));
-                    pv(4 * x + 1, f16x2_of_e4m3(lo01 >> 16), f16x2_of_e4m3(lo23 >> 16));
-                    pv(4 * x + 2, f16x2_of_e4m3(hi01), f16x2_of_e4m3(hi23));
-                    pv(4 * x + 3, f16x2_of_e4m3(hi01 >> 16), f16x2_of_e4m3(hi23 >> 16));
+                    pv(q, 4 * x, f16x2_of_e4m3(lo01), f16x2_of_e4m3(lo23));
+                    pv(q, 4 * x + 1, f16x2_of_e4m3(lo01 >> 16), f16x2_of_e4m3(lo23 >> 16));
+                    pv(q, 4 * x + 2, f16x2_of_e4m3(hi01), f16x2_of_e4m3(hi23));
+                    pv(q, 4 * x + 3, f16x2_of_e4m3(hi01 >> 16), f16x2_of_e4m3(hi23 >> 16));
                 }
             }
+            }
         }
-        __syncwarp();                   // every lane has read the slot before it is filled again
-        if (++slot == ST) {
-            slot = 0;
+        if (step % SUB == turn) {
+            __syncwarp();               // every lane has read the stage
+            if (lane == 0) mbar_arrive(&empty[st]);
+        }
+        if (++st == ST) {
+            st = 0;
             phase ^= 1;
         }
+        ++step;
         --left;
         const bool last_of_unit = cu.x + 1 == cu.kr.n || left == 0;
         if (last_of_unit) end_unit();
         advance(cu, left > 0);
         if (last_of_unit && left > 0) begin_unit();
     }
-    // After a wait that ran out: the copies end before the CTA leaves.
-    if (*abort && lane == 0)
-        for (int i = max(loaded - ST, 0); i < loaded; ++i) mbar_wait_drain(&bars[i % ST], (i / ST) & 1, a.status);
 }
 
 }  // namespace fm
@@ -757,45 +804,51 @@ using namespace fm;
 namespace {
 
 template <int D, bool FP8, int ROWS, int TERMS>
-fm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, cudaStream_t stream)
+fm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int box_keys, cudaStream_t stream)
 {
-    constexpr int smem = DecodeCfg<D, FP8>::kBytes;
+    constexpr int smem = DecodeCfg<D, FP8, ROWS>::kBytes;
     static std::atomic<uint8_t> done[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FM_ERR_CUDA;
     if (!done[dev].load(std::memory_order_acquire)) {
+        // The register split adds up to the launch's registers only if the
+        // kernel was compiled to that many per thread.
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, fm_paged_decode_kernel<D, FP8, ROWS, TERMS>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+            return FM_ERR_CUDA;
         if (cudaFuncSetAttribute(fm_paged_decode_kernel<D, FP8, ROWS, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
             cudaSuccess)
             return FM_ERR_CUDA;
         done[dev].store(1, std::memory_order_release);
     }
     ProfScope ps(kKPagedDecode, stream);
-    fm_paged_decode_kernel<D, FP8, ROWS, TERMS><<<kPagedCtas, kWarps * 32, smem, stream>>>(tk, tv, a);
+    fm_paged_decode_kernel<D, FP8, ROWS, TERMS><<<kPagedCtas, kThreads, smem, stream>>>(tk, tv, a, box_keys);
     return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 // By the rows that a request of the step can have at most.
 template <int D, bool FP8>
-fm_status launch_rows(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, cudaStream_t stream)
+fm_status launch_rows(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int box_keys, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv);
     if constexpr (FP8) {
-        if (rows <= 8) return launch<D, FP8, 8, 2>(tk, tv, a, stream);
-        if (a.o_f32) return rows <= 16 ? launch<D, FP8, 16, 2>(tk, tv, a, stream) : launch<D, FP8, 32, 2>(tk, tv, a, stream);
-        return rows <= 16 ? launch<D, FP8, 16, 1>(tk, tv, a, stream) : launch<D, FP8, 32, 1>(tk, tv, a, stream);
+        if (rows <= 8) return launch<D, FP8, 8, 2>(tk, tv, a, box_keys, stream);
+        if (a.o_f32) return rows <= 16 ? launch<D, FP8, 16, 2>(tk, tv, a, box_keys, stream) : launch<D, FP8, 32, 2>(tk, tv, a, box_keys, stream);
+        return rows <= 16 ? launch<D, FP8, 16, 1>(tk, tv, a, box_keys, stream) : launch<D, FP8, 32, 1>(tk, tv, a, box_keys, stream);
     } else {
         if (a.o_f32)
-            return rows <= 8 ? launch<D, FP8, 8, 3>(tk, tv, a, stream)
-                             : rows <= 16 ? launch<D, FP8, 16, 3>(tk, tv, a, stream) : launch<D, FP8, 32, 3>(tk, tv, a, stream);
-        return rows <= 8 ? launch<D, FP8, 8, 2>(tk, tv, a, stream)
-                         : rows <= 16 ? launch<D, FP8, 16, 2>(tk, tv, a, stream) : launch<D, FP8, 32, 2>(tk, tv, a, stream);
+            return rows <= 8 ? launch<D, FP8, 8, 3>(tk, tv, a, box_keys, stream)
+                             : rows <= 16 ? launch<D, FP8, 16, 3>(tk, tv, a, box_keys, stream) : launch<D, FP8, 32, 3>(tk, tv, a, box_keys, stream);
+        return rows <= 8 ? launch<D, FP8, 8, 2>(tk, tv, a, box_keys, stream)
+                         : rows <= 16 ? launch<D, FP8, 16, 2>(tk, tv, a, box_keys, stream) : launch<D, FP8, 32, 2>(tk, tv, a, box_keys, stream);
     }
 }
 
 }  // namespace
 
-fm_status fm_paged_decode_launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, bool e4m3, cudaStream_t stream)
+fm_status fm_paged_decode_launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int box_keys, bool e4m3,
+                                 cudaStream_t stream)
 {
-    if (a.s.d == 128) return e4m3 ? launch_rows<128, true>(tk, tv, a, stream) : launch_rows<128, false>(tk, tv, a, stream);
-    return e4m3 ? launch_rows<64, true>(tk, tv, a, stream) : launch_rows<64, false>(tk, tv, a, stream);
+    if (a.s.d == 128) return e4m3 ? launch_rows<128, true>(tk, tv, a, box_keys, stream) : launch_rows<128, false>(tk, tv, a, box_keys, stream);
+    return e4m3 ? launch_rows<64, true>(tk, tv, a, box_keys, stream) : launch_rows<64, false>(tk, tv, a, box_keys, stream);
 }
