@@ -526,7 +526,7 @@ fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok,
         const uint64_t cd[4] = {d, page, heads, pages};
         const uint64_t ks[3] = {kt, kh, kp}, vs[3] = {vt, vh, vp};
         const uint32_t cb[4] = {fp8 ? (uint32_t)a.s.d : 64u, (uint32_t)box_keys, 1, 1};
-        if (!make_tmap_strided(&tq, q, false, 3, qd, qs, qb, 128) || !make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, fp8 ? 0 : 128) ||
+        if (!make_tmap_strided(&tq, q, false, 3, qd, qs, qb, 128) || !make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, fp8 ? a.s.d : 128) ||
             !make_tmap_strided(&tv, cache->v, fp8, 4, cd, vs, cb, fp8 ? 0 : 128))
             return FM_ERR_CUDA;
         if ((st = fm_paged_chunk_launch(tq, tk, tv, a, box_keys, fp8, (cudaStream_t)stream)) != FM_OK) return st;

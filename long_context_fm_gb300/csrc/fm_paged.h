@@ -117,14 +117,15 @@ __device__ __forceinline__ bool paged_plan_fits(const PagedHeader *h, const Page
            p.window == s.window && p.sink == s.sink;
 }
 
-// e4m3 caches take Q as fp16: the power of two that puts a row's largest
-// element in [2^14, 2^15), so that bf16 values down to 2^-29 of it keep all
-// their bits; 1 when the row is zero or not finite.
-__device__ __forceinline__ float f16_row_factor(float amax)
+// Power of two that puts a row's largest element amax in [2^top, 2^(top + 1));
+// 1 when the row is zero or not finite.  Q beside e4m3 keys: exact in fewer
+// exponents than bf16 has once the row is scaled, and taken back in the score
+// factor.
+__device__ __forceinline__ float row_factor(float amax, int top)
 {
     if (!(amax > 0.f) || amax == INFINITY) return 1.f;
     const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-    return exp2f((float)min(14 - ex, 100));
+    return exp2f((float)min(top - ex, 100));
 }
 #endif
 

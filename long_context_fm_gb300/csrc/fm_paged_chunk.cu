@@ -17,10 +17,13 @@
 //   warps 6-9   softmax of odd tiles
 //   warp 10     TMA of V
 //   warp 11     one thread issues P V
-//   warps 12-15 e4m3 caches only: 12, 13 expand K (and rescale Q), 14, 15 V, to fp16 in
-//               shared memory.  e4m3 is exact in fp16; Q is too after a power of two per
-//               row that puts its largest element in [2^14, 2^15), which the score
-//               factor takes back.
+//   warps 12-15 e4m3 caches only: Q to e4m3 terms, V to fp16, in shared memory
+// e4m3 caches: K is multiplied as it is (kind::f8f6f4, twice the rate of 16 bits) by Q as
+// two e4m3 terms of four bits each, which together hold bf16's eight: after a
+// power of two per row that puts its largest element in [128, 256), and which the
+// score factor takes back, elements down to 2^-9 of it are exact and smaller
+// ones are off by at most 2^-17 of it.  V becomes fp16, exactly, because P needs
+// more bits than e4m3 has.
 // P: bf16 caches one bf16 term for 16-bit outputs, two (hi + lo) for fp32
 // outputs; e4m3 caches fp16 terms likewise.
 //
@@ -43,13 +46,13 @@
 namespace fm {
 namespace {
 
-constexpr int kSBuf = 3, kKSt = 3, kVSt = 2, kRing = 4, kUnitInts = 16;
+constexpr int kSBuf = 3, kMaxSt = 4, kRing = 4, kUnitInts = 16;
 
 enum {
     B_Q = 0, B_QR,                                   // Q ready; Q landed (e4m3: before its conversion)
-    B_KF, B_KE = B_KF + kKSt, B_KR = B_KE + kKSt,    // K stage ready / free / landed
-    B_VF = B_KR + kKSt, B_VE = B_VF + kVSt, B_VR = B_VE + kVSt,
-    B_S = B_VR + kVSt, B_P = B_S + kSBuf, B_PB = B_P + kSBuf, B_O = B_PB + kSBuf,
+    B_KF, B_KE = B_KF + kMaxSt,                      // K stage ready / free
+    B_VF = B_KE + kMaxSt, B_VE = B_VF + kMaxSt, B_VR = B_VE + kMaxSt,   // V stage ready / free / landed, but not ready
+    B_S = B_VR + kMaxSt, B_P = B_S + kSBuf, B_PB = B_P + kSBuf, B_O = B_PB + kSBuf,
     B_QE = B_O + kSBuf, B_OE, B_UF, B_UE = B_UF + kRing, B_DRAIN = B_UE + kRing,
     B_COUNT
 };
@@ -61,16 +64,21 @@ struct ChunkCfg {
     static constexpr int kRegsLaunch = FP8 ? 128 : 168, kRegsSoftmax = FP8 ? 216 : 224, kRegsOther = FP8 ? 40 : 56;
     static_assert(8 * 32 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register split");
     static constexpr int kBox = 128 * 128;                     // 128 rows of 128 bytes (64 values of 16 bits)
-    static constexpr int kTile = 128 * D * 2;
-    static constexpr int kRaw = 128 * D;                       // an e4m3 tile as it lands
-    // d = 128: a raw row of 128 bytes lands where the row's second half will be, so it is
-    // overwritten by its own expansion alone.  d = 64: beside the stages.
-    static constexpr bool kRawInside = D == 128;
+    static constexpr int kTile = 128 * D * 2;                  // 16-bit Q or V
+    static constexpr int kRaw = 128 * D;                       // 8-bit K or V
+    static constexpr int kKTile = FP8 ? kRaw : kTile;
+    static constexpr int kKSt = FP8 ? 4 : 3, kVSt = FP8 ? 3 : 2;
+    static constexpr uint32_t kTerm = FP8 ? kRaw : 0;          // from Q's first e4m3 term to its second
+    // e4m3, d = 128: a raw row of 128 bytes lands where the V row's second half will be
+    // (and Q's terms replace Q), so it is overwritten by its own expansion alone.
+    // d = 64: beside the stages.
+    static constexpr bool kInside = D == 128;
     static constexpr int kQ = 0;
     static constexpr int kK = kTile;
-    static constexpr int kV = kK + kKSt * kTile;
-    static constexpr int kRawArea = kV + kVSt * kTile;
-    static constexpr int kOst = kRawArea + (FP8 && !kRawInside ? (kKSt + kVSt) * kRaw : 0);   // [8 warps][32 rows][64 bytes]
+    static constexpr int kV = kK + kKSt * kKTile;
+    static constexpr int kRawV = kV + kVSt * kTile;
+    static constexpr int kRawQ = kRawV + (FP8 && !kInside ? kVSt * kRaw : 0);
+    static constexpr int kOst = kRawQ + (FP8 && !kInside ? kTile : 0);   // [8 warps][32 rows][64 bytes]
     static constexpr int kMax = kOst + 8 * 2048;               // float [2][2][128]
     static constexpr int kSum = kMax + 2 * 2 * 128 * 4;        // float [2][2][128]
     static constexpr int kChain = kSum + 2 * 2 * 128 * 4;      // float [128]
@@ -107,6 +115,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
     using C = ChunkCfg<D, FP8>;
     constexpr float kLazy = FP8 ? 8.f : 32.f;     // fp16 P stays <= 2^8; bf16 P may grow to 2^32
     constexpr int NBOX = D / 64;                  // 128-byte boxes of a 16-bit row
+    constexpr int kKSt = C::kKSt, kVSt = C::kVSt;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *sMax = reinterpret_cast<float *>(smem + C::kMax);
     float *sSum = reinterpret_cast<float *>(smem + C::kSum);
@@ -134,15 +143,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
 
     if (warp == 0 && lane == 0) {
         *abort = 0;
-        mbar_init(&bars[B_Q], FP8 ? 2 : 1);
+        mbar_init(&bars[B_Q], FP8 ? 4 : 1);
         mbar_init(&bars[B_QR], 1);
         for (int i = 0; i < kKSt; ++i) {
-            mbar_init(&bars[B_KF + i], FP8 ? 2 : 1);
-            mbar_init(&bars[B_KR + i], 1);
+            mbar_init(&bars[B_KF + i], 1);
             mbar_init(&bars[B_KE + i], 1);
         }
         for (int i = 0; i < kVSt; ++i) {
-            mbar_init(&bars[B_VF + i], FP8 ? 2 : 1);
+            mbar_init(&bars[B_VF + i], FP8 ? 4 : 1);
             mbar_init(&bars[B_VR + i], 1);
             mbar_init(&bars[B_VE + i], 1);
         }
@@ -195,21 +203,40 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
         const int x = u.x0 + t;
         return (x < u.ns ? x : u.first + x - u.ns) * kKeyTile;
     };
-    // Page that holds the keys [j, j + box) of a unit's request, or num_pages
-    // (out of the pool: arrives as zeros) when no row of the unit needs them.
-    auto page_of = [&](const Unit &u, int j) -> int {
-        const int b = j / s.page_size, b0 = b * s.page_size;
-        // The page as a whole decides: one that is partly attended is held.
-        if (j >= u.hi || (b0 + s.page_size <= u.lo && b0 >= s.sink)) return s.num_pages;
-        const int p = __ldg(a.table + (int64_t)u.r * s.max_pages + b);
-        if (p < 0 || p >= s.num_pages) {
-            set_status(a.status, FM_ERR_PAGES);
-            return s.num_pages;
-        }
-        return p;
+    const int nb = kKeyTile / box_keys;         // boxes of a tile; lane i looks up the page of box i
+    // Number of the page that holds the lane's box of the unit's tile at kb, as the
+    // table has it; `none` when no row of the unit needs the page (it arrives as
+    // zeros).  The page as a whole decides: one that is partly attended is held.
+    const int none = -1 - s.num_pages;
+    auto look_up = [&](const Unit &u, int kb) -> int {
+        const int j = kb + lane * box_keys;
+        if (lane >= nb) return none;
+        const int b = a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size, b0 = b * s.page_size;
+        if (j >= u.hi || (b0 + s.page_size <= u.lo && b0 >= s.sink)) return none;
+        return __ldg(a.table + (int64_t)u.r * s.max_pages + b);
     };
-    // Lane i loads box i % nb of half i / nb of a tile (128 / box_keys boxes).
-    const int nb = kKeyTile / box_keys;
+    // Starts a tile's boxes, one per lane (all lanes call).
+    auto load_boxes = [&](const CUtensorMap *map, uint8_t *tile, uint64_t *bar, const Unit &u, int kb, int page) {
+        if (page < 0 || page >= s.num_pages) {
+            if (page != none) set_status(a.status, FM_ERR_PAGES);
+            page = s.num_pages;                 // outside the pool: zeros
+        }
+        const int in0 = a.page_shift >= 0 ? kb & (s.page_size - 1) : kb % s.page_size;
+        if (lane >= nb) return;
+        int in = in0 + lane * box_keys;         // past a page's end in the following ones
+        in = a.page_shift >= 0 ? in & (s.page_size - 1) : in % s.page_size;
+        if (FP8) {
+            tma_load_4d(tile + lane * box_keys * D, map, bar, 0, in, u.h, page);
+        } else {
+#pragma unroll
+            for (int half = 0; half < NBOX; ++half)
+                tma_load_4d(tile + half * C::kBox + lane * box_keys * 128, map, bar, half * 64, in, u.h, page);
+        }
+    };
+    auto k_tile = [&](int st) { return smem + C::kK + st * C::kKTile; };
+    auto v_tile = [&](int st) { return smem + C::kV + st * C::kTile; };
+    auto v_raw = [&](int st) { return C::kInside ? v_tile(st) + C::kBox : smem + C::kRawV + st * C::kRaw; };
+    uint8_t *q_raw = smem + (FP8 && !C::kInside ? C::kRawQ : C::kQ);
 
     if (warp == 0) {
         warp_regs_dec<C::kRegsOther>();
@@ -217,16 +244,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
         const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_many);
         const int32_t *cum = reinterpret_cast<const int32_t *>(a.plan + a.L.off_many_cum);
         unsigned *claim = reinterpret_cast<unsigned *>(a.plan + a.L.off_claim);
-        int g = 0, nq = 0, e = 0, k = 0;
-        bool run = true;
-        while (run) {
-            unsigned c = 0;
-            // Every CTA claims once past the end: the counter comes back to 0 by itself.
-            if (lane == 0) c = atomicInc(claim, n_claims + gridDim.x - 1);
-            c = __shfl_sync(0xffffffffu, c, 0);
+        int e = 0;
+        // Claims the next piece into ring entry k.  The entry of the unit after the
+        // one in work is filled early, so that the claim's trips to memory are over
+        // when its loads are due.
+        auto publish = [&](int k) -> bool {
             Unit u{};
-            u.n = -1;
-            if (c < n_claims) {
+            while (true) {
+                unsigned c = 0;
+                // Every CTA claims once past the end: the counter comes back to 0 by itself.
+                if (lane == 0) c = atomicInc(claim, n_claims + gridDim.x - 1);
+                c = __shfl_sync(0xffffffffu, c, 0);
+                u.n = -1;
+                if (c >= n_claims) break;
                 u.u = (int)(c / (unsigned)splits);
                 u.part = (int)(c - (unsigned)u.u * (unsigned)splits);
                 // Claims only grow, so the entry is at or behind the last one.
@@ -254,52 +284,55 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                 if (u.part >= u.parts) continue;                  // fewer tiles than pieces
                 u.x0 = (int)((int64_t)kr.n * u.part / u.parts);
                 u.n = (int)((int64_t)kr.n * (u.part + 1) / u.parts) - u.x0;
+                break;
             }
             const int slot = k % kRing;
-            if (k >= kRing && !warp_wait(&bars[B_UE + slot], ((k / kRing) - 1) & 1, abort, a.status, lim)) break;
+            if (k >= kRing && !warp_wait(&bars[B_UE + slot], ((k / kRing) - 1) & 1, abort, a.status, lim)) return false;
             if (lane == 0) {
                 const int w[15] = {u.n, u.r, u.h, u.tok0, u.ntok, u.pos0, u.seq, u.x0, u.ns, u.first, u.lo, u.hi, u.u, u.part, u.parts};
 #pragma unroll
                 for (int i = 0; i < 15; ++i) sUnit[slot * kUnitInts + i] = w[i];
                 mbar_arrive(&bars[B_UF + slot]);
             }
-            ++k;
+            __syncwarp();
+            return true;
+        };
+        int g = 0, nq = 0;
+        bool run = publish(0);
+        for (int k = 0; run; ++k) {
+            const volatile int *p = sUnit + (k % kRing) * kUnitInts;
+            const Unit u{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], p[10], p[11], p[12], p[13], p[14]};
             if (u.n < 0) break;
+            int page = look_up(u, key_base(u, 0));
             if (nq > 0 && !warp_wait(&bars[B_QE], (nq - 1) & 1, abort, a.status, lim)) break;
             if (lane == 0) {
                 uint64_t *qb = &bars[FP8 ? B_QR : B_Q];
                 mbar_arrive_expect_tx(qb, (uint32_t)(G * tpt * D * 2));
 #pragma unroll
-                for (int x = 0; x < NBOX; ++x) tma_load_3d(smem + C::kQ + x * C::kBox, &tq, qb, x * 64, u.h * G, u.tok0);
+                for (int x = 0; x < NBOX; ++x) tma_load_3d(q_raw + x * C::kBox, &tq, qb, x * 64, u.h * G, u.tok0);
             }
             ++nq;
-            int page = 0;
-            const int bx = lane % nb, half = lane / nb;
-            const bool mine = half < (FP8 ? 1 : NBOX);
-            if (mine) page = page_of(u, key_base(u, 0) + bx * box_keys);
             for (int t = 0; t < u.n; ++t, ++g) {
                 const int st = g % kKSt;
-                const int j = key_base(u, t) + bx * box_keys, pg = page;
-                if (mine && t + 1 < u.n) page = page_of(u, key_base(u, t + 1) + bx * box_keys);
+                const int kb = key_base(u, t), pg = page;
+                if (t + 1 < u.n) page = look_up(u, key_base(u, t + 1));
                 if (g >= kKSt && !warp_wait(&bars[B_KE + st], ((g / kKSt) - 1) & 1, abort, a.status, lim)) {
                     run = false;
                     break;
                 }
-                uint64_t *bar = &bars[(FP8 ? B_KR : B_KF) + st];
-                if (lane == 0) mbar_arrive_expect_tx(bar, FP8 ? C::kRaw : C::kTile);
+                uint64_t *bar = &bars[B_KF + st];
+                if (lane == 0) mbar_arrive_expect_tx(bar, C::kKTile);
                 __syncwarp();
-                if (mine) {
-                    uint8_t *dst = FP8 ? (C::kRawInside ? smem + C::kK + st * C::kTile + C::kBox : smem + C::kRawArea + st * C::kRaw) + bx * box_keys * D
-                                       : smem + C::kK + st * C::kTile + half * C::kBox + bx * box_keys * 128;
-                    tma_load_4d(dst, &tk, bar, half * 64, j % s.page_size, u.h, pg);
-                }
+                load_boxes(&tk, k_tile(st), bar, u, kb, pg);
+                __syncwarp();
             }
+            if (run && !publish(k + 1)) run = false;
         }
         // After an abort: copies in flight end before the CTA leaves.
         if (lane == 0 && *abort) {
             if (nq > 0) mbar_wait_drain(&bars[FP8 ? B_QR : B_Q], (nq - 1) & 1, a.status, lim);
             for (int i = (g > kKSt ? g - kKSt : 0); i < g; ++i)
-                mbar_wait_drain(&bars[(FP8 ? B_KR : B_KF) + i % kKSt], (i / kKSt) & 1, a.status, lim);
+                mbar_wait_drain(&bars[B_KF + i % kKSt], (i / kKSt) & 1, a.status, lim);
         }
     } else if (warp == 10) {
         warp_regs_dec<C::kRegsOther>();
@@ -310,14 +343,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
         Unit u;
         for (int k = 0; run; ++k) {
             if (!read_unit(k, u)) break;
-            const int bx = lane % nb, half = lane / nb;
-            const bool mine = half < (FP8 ? 1 : NBOX);
-            int page = 0;
-            if (mine) page = page_of(u, key_base(u, 0) + bx * box_keys);
+            int page = look_up(u, key_base(u, 0));
             for (int t = 0; t < u.n; ++t, ++g) {
                 const int st = g % kVSt;
-                const int kb = key_base(u, t), j = kb + bx * box_keys, pg = page;
-                if (mine && t + 1 < u.n) page = page_of(u, key_base(u, t + 1) + bx * box_keys);
+                const int kb = key_base(u, t), pg = page;
+                if (t + 1 < u.n) page = look_up(u, key_base(u, t + 1));
                 if (g >= kVSt && !warp_wait(&bars[B_VE + st], ((g / kVSt) - 1) & 1, abort, a.status, lim)) {
                     run = false;
                     break;
@@ -328,12 +358,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                 uint64_t *bar = &bars[(FP8 || ragged ? B_VR : B_VF) + st];
                 if (lane == 0) mbar_arrive_expect_tx(bar, FP8 ? C::kRaw : C::kTile);
                 __syncwarp();
-                uint8_t *tile = smem + C::kV + st * C::kTile;
-                if (mine) {
-                    uint8_t *dst = FP8 ? (C::kRawInside ? tile + C::kBox : smem + C::kRawArea + (kKSt + st) * C::kRaw) + bx * box_keys * D
-                                       : tile + half * C::kBox + bx * box_keys * 128;
-                    tma_load_4d(dst, &tv, bar, half * 64, j % s.page_size, u.h, pg);
-                }
+                uint8_t *tile = v_tile(st);
+                load_boxes(&tv, FP8 ? v_raw(st) : tile, bar, u, kb, pg);
+                __syncwarp();
                 const unsigned bit = 1u << st;
                 ragged_last = ragged ? ragged_last | bit : ragged_last & ~bit;
                 if (!FP8 && ragged) {
@@ -365,8 +392,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
     } else if (warp == 1) {
         warp_regs_dec<C::kRegsOther>();
         // -------------------------------------------- Q K^T
-        constexpr uint32_t id = FP8 ? idesc_f16(128, 128, false) : idesc_bf16(128, 128, false, false);
-        const uint64_t dQ = sdesc_sw128(smem_u32(smem + C::kQ), 16, 1024);
+        constexpr uint32_t id = FP8 ? idesc_e4m3(128, 128) : idesc_bf16(128, 128, false, false);
+        auto desc = [&](uint8_t *p) {             // K-major rows of 128 bytes, or of 64 (e4m3, d = 64)
+            return FP8 && D == 64 ? sdesc_sw64(smem_u32(p), 16, 512) : sdesc_sw128(smem_u32(p), 16, 1024);
+        };
+        const uint64_t dQ = desc(smem + C::kQ);
         int g = 0, nq = 0;
         bool run = true;
         for (int k = 0; run; ++k) {
@@ -383,11 +413,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t dK = sdesc_sw128(smem_u32(smem + C::kK + st * C::kTile), 16, 1024);
+                    const uint64_t dK = desc(k_tile(st));
+                    if (FP8) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * C::kBox + (kk & 3) * 32;
-                        mma_ss(tmem + sb * 128, sdesc_add(dQ, off), sdesc_add(dK, off), id, kk > 0);
+                        for (int term = 0; term < 2; ++term)
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk)   // K = 32 bytes per instruction
+                                mma_ss_e4m3(tmem + sb * 128, sdesc_add(dQ, term * C::kTerm + kk * 32), sdesc_add(dK, kk * 32), id, term + kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * C::kBox + (kk & 3) * 32;
+                            mma_ss(tmem + sb * 128, sdesc_add(dQ, off), sdesc_add(dK, off), id, kk > 0);
+                        }
                     }
                     tc_commit(&bars[B_S + sb]);
                     tc_commit(&bars[B_KE + st]);
@@ -451,87 +489,83 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
         }
     } else if (FP8 && warp >= 12) {
         warp_regs_dec<C::kRegsOther>();
-        // -------------------------------------------- e4m3 -> fp16
-        // Warps 12, 13: Q and K; 14, 15: V; each every other group of rows.  A
-        // row of a raw tile is read by d / 16 lanes, 16 values each, which become
-        // two 16-byte chunks of the swizzled operand; the two are stored in
-        // an order that keeps the lanes of a row on different banks.
-        const int mate = warp & 1;
-        const bool is_k = warp < 14;
-        constexpr int LPR = D / 16, RPI = 32 / LPR;       // lanes per row, rows per warp step
-        auto expand = [&](const uint8_t *raw, uint8_t *tile, int rows) {
-            const int l = lane % LPR;
-            constexpr int BATCH = 4;                      // steps whose loads are in flight together
-            for (int i0 = mate; i0 < 128 / RPI; i0 += 2 * BATCH) {
-                uint4 x[BATCH];
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b)
-                    x[b] = *reinterpret_cast<const uint4 *>(raw + ((i0 + 2 * b) * RPI + lane / LPR) * D + l * 16);
-                __syncwarp();                             // the rows' lanes have read them
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int row = (i0 + 2 * b) * RPI + lane / LPR;
-                    if (row >= rows) x[b] = make_uint4(0, 0, 0, 0);
-                    const uint4 y0 = make_uint4(f16x2_of_e4m3(x[b].x), f16x2_of_e4m3(x[b].x >> 16), f16x2_of_e4m3(x[b].y), f16x2_of_e4m3(x[b].y >> 16));
-                    const uint4 y1 = make_uint4(f16x2_of_e4m3(x[b].z), f16x2_of_e4m3(x[b].z >> 16), f16x2_of_e4m3(x[b].w), f16x2_of_e4m3(x[b].w >> 16));
-                    const int odd = (l >> 2) & 1;         // lanes 4-7 begin with their second chunk
-                    uint8_t *base = tile + (l >> 2) * C::kBox + row * 128;
-                    const int c0 = (2 * l + odd) & 7, c1 = (2 * l + 1 - odd) & 7;
-                    st_shared_v4(base + ((c0 ^ (row & 7)) << 4), odd ? y1 : y0);
-                    st_shared_v4(base + ((c1 ^ (row & 7)) << 4), odd ? y0 : y1);
-                }
-            }
-        };
+        // -------------------------------------------- conversions
+        // Four warps, each every fourth group of rows.  A row is read by d / 8 lanes,
+        // 8 values each: of V they become one 16-byte chunk of the swizzled operand (no
+        // bank conflict either way), of Q eight bytes of either term.
+        const int mate = warp & 3;
+        constexpr int LPR = D / 8, RPI = 32 / LPR;        // lanes per row, rows per warp step
+        constexpr int BATCH = 8;                          // steps whose loads are in flight together
+        const int l = lane % LPR, r_in = lane / LPR;
         int g = 0, nq = 0;
         bool run = true;
         Unit u;
         for (int k = 0; run; ++k) {
             if (!read_unit(k, u)) break;
-            if (is_k) {
-                // Q rows to scaled fp16, in place: d / 8 lanes a row, 16 bytes each.
-                if (!warp_wait(&bars[B_QR], nq & 1, abort, a.status, lim)) break;
-                constexpr int QL = D / 8, QR = 32 / QL;
-                const int l = lane % QL;
-                for (int i = mate; i < 128 / QR; i += 2) {
-                    const int row = i * QR + lane / QL;
-                    uint8_t *p = smem + C::kQ + (l >> 3) * C::kBox + row * 128 + (((l & 7) ^ (row & 7)) << 4);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    float amax = 0.f;
+            if (!warp_wait(&bars[B_QR], nq & 1, abort, a.status, lim)) break;
+            for (int i = mate; i < 128 / RPI; i += 4) {
+                const int row = i * RPI + r_in;
+                const uint4 x = *reinterpret_cast<const uint4 *>(q_raw + (l >> 3) * C::kBox + row * 128 + (((l & 7) ^ (row & 7)) << 4));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                float amax = 0.f;
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        amax = fmax3(amax, fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xffff0000u)));
+                for (int y = 0; y < 4; ++y)
+                    amax = fmax3(amax, fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xffff0000u)));
 #pragma unroll
-                    for (int y = 1; y < QL; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
-                    const float f = f16_row_factor(amax);
-                    uint32_t z[4];
+                for (int y = 1; y < LPR; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));   // the row's lanes have read it
+                // An infinite element makes the row NaN (it would saturate).
+                const float f = amax == INFINITY ? __uint_as_float(0x7fc00000u) : row_factor(amax, 7);
+                uint32_t hi[2] = {0u, 0u}, lw[2] = {0u, 0u};
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        z[y] = pack_f16x2(__uint_as_float(w[y] << 16) * f, __uint_as_float(w[y] & 0xffff0000u) * f);
-                    st_shared_v4(p, make_uint4(z[0], z[1], z[2], z[3]));
-                    if (l == 0) sQf[(nq & 1) * 128 + row] = 1.f / f;
+                for (int y = 0; y < 4; ++y) {
+                    const float q0 = __uint_as_float(w[y] << 16) * f, q1 = __uint_as_float(w[y] & 0xffff0000u) * f;
+                    const uint32_t h = pack_e4m3x2(q0, q1);
+                    float h0, h1;
+                    unpack_f16x2(f16x2_of_e4m3(h), h0, h1);
+                    hi[y >> 1] |= h << (16 * (y & 1));
+                    lw[y >> 1] |= pack_e4m3x2(q0 - h0, q1 - h1) << (16 * (y & 1));
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_Q]);
-                ++nq;
+                const uint32_t at = D == 128 ? row * 128 + (((l >> 1) ^ (row & 7)) << 4) : row * 64 + (((l >> 1) ^ ((row >> 1) & 3)) << 4);
+                uint8_t *p = smem + C::kQ + at + (l & 1) * 8;
+                *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(p + C::kTerm) = make_uint2(lw[0], lw[1]);
+                if (l == 0) sQf[(nq & 1) * 128 + row] = 1.f / f;
             }
-            const int stages = is_k ? kKSt : kVSt, raw0 = is_k ? B_KR : B_VR, full0 = is_k ? B_KF : B_VF;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_Q]);
+            ++nq;
             for (int t = 0; t < u.n; ++t, ++g) {
-                const int st = g % stages;
-                if (!warp_wait(&bars[raw0 + st], (g / stages) & 1, abort, a.status, lim)) {
+                const int st = g % kVSt;
+                if (!warp_wait(&bars[B_VR + st], (g / kVSt) & 1, abort, a.status, lim)) {
                     run = false;
                     break;
                 }
-                uint8_t *tile = smem + (is_k ? C::kK : C::kV) + st * C::kTile;
-                const uint8_t *raw = C::kRawInside ? tile + C::kBox : smem + C::kRawArea + ((is_k ? 0 : kKSt) + st) * C::kRaw;
-                expand(raw, tile, is_k ? 128 : u.seq - key_base(u, t));   // V behind the last token: zeros
+                const uint8_t *raw = v_raw(st);
+                uint8_t *tile = v_tile(st);
+                const int rows = u.seq - key_base(u, t);  // V behind the last token: zeros
+                for (int i0 = mate * BATCH; i0 < 128 / RPI; i0 += 4 * BATCH) {
+                    uint2 x[BATCH];
+#pragma unroll
+                    for (int b = 0; b < BATCH; ++b) x[b] = *reinterpret_cast<const uint2 *>(raw + ((i0 + b) * RPI + r_in) * D + l * 8);
+                    __syncwarp();                         // the rows' lanes have read them
+#pragma unroll
+                    for (int b = 0; b < BATCH; ++b) {
+                        const int row = (i0 + b) * RPI + r_in;
+                        if (row >= rows) x[b] = make_uint2(0, 0);
+                        st_shared_v4(tile + (l >> 3) * C::kBox + row * 128 + (((l & 7) ^ (row & 7)) << 4),
+                                     make_uint4(f16x2_of_e4m3(x[b].x), f16x2_of_e4m3(x[b].x >> 16), f16x2_of_e4m3(x[b].y),
+                                                f16x2_of_e4m3(x[b].y >> 16)));
+                    }
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[full0 + st]);
+                if (lane == 0) mbar_arrive(&bars[B_VF + st]);
             }
         }
-    } else if (warp < 10) {
+    } else if (warp >= 10) {
+        warp_regs_dec<C::kRegsOther>();     // idle warps too: the softmax warps' increase waits for every share
+    } else {
         warp_regs_inc<C::kRegsSoftmax>();
         // -------------------------------------------- softmax
         const int w = warp < 6 ? 0 : 1;                   // warpgroup: the tiles g with g & 1 == w
@@ -749,12 +783,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                 // lanes write a row's 64 bytes; rows behind the unit's tokens are left out.
                 uint8_t *stg = smem + C::kOst + (warp - 2) * 2048;
                 int64_t at[4];
-                unsigned mine = 0;
+                unsigned mine4 = 0;
+                const int64_t at0 = (int64_t)un[U_TOK0] * s.Hq + un[U_H] * G;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int x = quarter * 32 + i * 8 + (lane >> 2), xt = x / G;
-                    at[i] = ((int64_t)(un[U_TOK0] + xt) * s.Hq + un[U_H] * G + (x - xt * G)) * D + w * OC;
-                    mine |= (xt < un[U_NTOK] && xt < tpt) ? 1u << i : 0u;
+                for (int i = 0; i < 4; ++i) {       // row i * 8 + lane / 4 of the warp: its lane knows the place
+                    at[i] = (at0 + __shfl_sync(0xffffffffu, tk * s.Hq + gh, i * 8 + (lane >> 2))) * D + w * OC;
+                    mine4 |= __shfl_sync(0xffffffffu, valid ? 1 : 0, i * 8 + (lane >> 2)) ? 1u << i : 0u;
                 }
                 auto stage = [&](const uint4 (&pk)[4], int col_bytes, int esz) {
                     __syncwarp();
@@ -765,7 +799,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                     for (int i = 0; i < 4; ++i) {
                         const int x = i * 8 + (lane >> 2), q = lane & 3;
                         const uint4 v = *reinterpret_cast<const uint4 *>(stg + x * 64 + ((q ^ ((x >> 1) & 3)) << 4));
-                        if ((mine >> i) & 1)
+                        if ((mine4 >> i) & 1)
                             *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(a.o) + at[i] * esz + col_bytes + q * 16) = v;
                     }
                 };

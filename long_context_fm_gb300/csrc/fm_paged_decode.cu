@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 amax = fmax3(amax, fabsf(__uint_as_float(w[i][y] << 16)), fabsf(__uint_as_float(w[i][y] & 0xffff0000u)));
                         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                        f = f16_row_factor(amax);
+                        f = row_factor(amax, 14);
 #pragma unroll
                         for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     amax = fmax3(amax, fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u)));
 #pragma unroll
                 for (int y = 1; y < 8; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
-                f = f16_row_factor(amax);
+                f = row_factor(amax, 14);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);

@@ -323,6 +323,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
     return d;
 }
 
+// The same with the 64-byte swizzle (layout 4): K-major rows of 64 bytes, 8-row
+// groups `sbo` = 512 bytes apart, tiles 512-byte aligned.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+{
+    return (sdesc_sw128(saddr, lbo, sbo) & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
+}
+
 // Descriptor of the same operand `byte_off` bytes further on (the start
 // address field never carries out of its 14 bits inside shared memory).
 __device__ __forceinline__ uint64_t sdesc_add(uint64_t base, uint32_t byte_off)

@@ -8,6 +8,11 @@ scale * sum_i |q_i k_i| over the attended keys.
     in fp32 (2 roundings of at most S + max each), and exponentiated by ex2
     (2^-22 relative): every weight is within w = (2 d + 8) 2^-24 (S + 1) + 2^-21
     of its value, relatively, and so is their sum: 2 w A on the output.
+  * many rows over an e4m3 cache: q as two e4m3 terms, after a scale that puts the
+    row's largest element in [128, 256).  A term keeps four bits, so the two hold
+    bf16's eight while the last of them is at least 2^-9, that is for elements of 2^-9
+    of the largest or more; a smaller one is off by at most 2^-10, or 2^-17 of
+    the largest: 2^-17 scale max|q| max_j sum_i |k_ji| on a score, on top of w.
   * P enters the second product rounded: one bf16 term eps/2 = 2^-8, two terms
     2^-16, one fp16 term 2^-11, two fp16 terms 2^-22, all relative; fp16 below
     2^-14 of the row's largest weight is fixed point with steps of 2^-24, half a
@@ -52,6 +57,7 @@ def attend(q, k_cache, v_cache, table, ctx, new, scale, window=0, sink=0):
     S = torch.zeros(T, Hq, dtype=torch.float64)
     cnt = torch.zeros(T, 1, dtype=torch.float64)
     vmax = torch.zeros_like(o)
+    QK = torch.zeros(T, Hq, dtype=torch.float64)
     loose = torch.zeros(T, Hq, d, dtype=torch.bool)
     t0 = 0
     for r, (c, n) in enumerate(zip(ctx, new)):
@@ -79,13 +85,14 @@ def attend(q, k_cache, v_cache, table, ctx, new, scale, window=0, sink=0):
                 A[t0 + i, sl] = w @ v.abs()
                 lse[t0 + i, sl] = z
                 S[t0 + i, sl] = scale * (qq.abs() @ k.abs().T).amax(1)
+                QK[t0 + i, sl] = scale * qq.abs().amax(1) * k.abs().sum(1).max()
                 vmax[t0 + i, sl] = v.abs().amax(0)
             cnt[t0 + i] = len(keep)
         t0 += n
-    return dict(o=o, lse=lse, A=A, S=S, n=cnt, vmax=vmax, loose=loose)
+    return dict(o=o, lse=lse, A=A, S=S, n=cnt, vmax=vmax, loose=loose, QK=QK)
 
 
-def check_attention(ref, o, lse, d, p_err, fp16):
+def check_attention(ref, o, lse, d, p_err, fp16, q_terms=False):
     """Every element of o and lse (device tensors, rows of the step) within the bounds above."""
     got = o.double().cpu()
     # A value that is not finite (an e4m3 cast of torch's gives NaN above 464)
@@ -95,6 +102,8 @@ def check_attention(ref, o, lse, d, p_err, fp16):
     assert (torch.isfinite(got) == fin)[~loose].all() and not torch.isfinite(got)[~fin].any()
     fin = fin & torch.isfinite(got)
     w = (2 * d + 8) * 2.0 ** -24 * (ref["S"] + 1) + 2.0 ** -21
+    if q_terms:
+        w = w + 2.0 ** -17 * ref["QK"]
     out = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}[o.dtype]
     tol = (2 * w + p_err + ref["n"] * 2.0 ** -24)[..., None] * ref["A"]
     if fp16:

@@ -95,7 +95,7 @@ class Batch:
 
     def check(self, o_dtype, few=True):
         o, lse = self.run(o_dtype)
-        return ref.check_attention(self.reference(), o, lse, self.d, self.p_err(o_dtype, few), self.e4m3)
+        return ref.check_attention(self.reference(), o, lse, self.d, self.p_err(o_dtype, few), self.e4m3, self.e4m3 and not few)
 
 
 # ---- plan ---------------------------------------------------------------------------
