@@ -83,16 +83,37 @@ __device__ __forceinline__ int last_at_most(const T *a, int n, T x)
     return lo;
 }
 
-// Pieces per many-rows unit: whole units once they fill the GPU twice over; else
-// about three pieces per CTA, of at least eight tiles on average (a piece costs its
-// partial sums and the pipeline's start, together about four tiles).
+// Pieces per many-rows unit (called by a full warp): the number whose pieces are done
+// first, at a cost of `tiles` plus about eight tiles each (the pipeline's start, the
+// epilogue and the partial sums, measured): in one round when they fit on the
+// CTAs, else in the mean share of a CTA and one piece more.  16 units of 240 tiles:
+// 9 pieces 53 us, 19 pieces 62, 29 pieces 66; 264 units of up to 240 tiles: whole
+// 363 us, halves 304.
 __device__ __forceinline__ int split_of(int64_t units, int64_t tiles)
 {
     if (units == 0 || units > kMaxSplitUnits) return 1;
-    const int64_t want = (3 * kPagedCtas + units - 1) / units, most = kMaxPieces / units, by_len = tiles / units / 8;
-    int64_t x = want < most ? want : most;
-    x = x < by_len ? x : by_len;
-    return x > 1 ? (int)x : 1;
+    const float n = (float)tiles / (float)units, u = (float)units;
+    const int most = (int)min((int64_t)kMaxPieces / units, tiles / units / 2);
+    float best = INFINITY;
+    int at = 1;
+    for (int x = 1 + lane_id(); x <= max(most, 1); x += 32) {
+        const float len = n / (float)x + 8.f, pieces = u * (float)x;
+        const float t = pieces <= (float)kPagedCtas ? len : pieces * len / (float)kPagedCtas + len;
+        if (t < best) {
+            best = t;
+            at = x;
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float t = __shfl_xor_sync(0xffffffffu, best, o);
+        const int x = __shfl_xor_sync(0xffffffffu, at, o);
+        if (t < best || (t == best && x < at)) {
+            best = t;
+            at = x;
+        }
+    }
+    return at;
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanArgs a)
@@ -206,6 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
     }
     if (cta == 0) {
         const int ctas_few = (int)(W < kPagedCtas ? W : kPagedCtas);
+        const int splits = tid < 32 ? split_of(run[5], run[6]) : 1;
         if (tid == 0) {
             PagedHeader h{};
             h.magic = kPagedMagic;
@@ -216,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
             h.rows = total;
             h.n_many = err == FM_OK ? (int)run[4] : 0;
             h.units_many = err == FM_OK ? (int)run[5] : 0;
-            h.splits_many = split_of(run[5], run[6]);
+            h.splits_many = h.units_many > 0 ? splits : 1;
             *reinterpret_cast<PagedHeader *>(a.plan) = h;
             few_cum[n_few] = W;
             if (h.n_many > 0) many_cum[h.n_many] = h.units_many;
@@ -236,8 +258,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
             reinterpret_cast<int4 *>(a.plan + a.L.off_start)[i] = st;
             reinterpret_cast<uint32_t *>(a.plan + a.L.off_count)[i] = 0u;
         }
-        for (int i = tid; i < kMaxSplitUnits; i += kPlanThreads)
-            reinterpret_cast<uint32_t *>(a.plan + a.L.off_many_count)[i] = 0u;
     }
     // Every CTA has read the lengths and the head: they may be advanced in place.
     if (ctas > 1) cg::this_cluster().sync();

@@ -53,7 +53,6 @@ struct PagedLayout {
     int64_t off_many;      // PagedEntry [R]
     int64_t off_many_cum;  // int32 [R + 1]  units before entry i
     int64_t off_claim;     // uint32  next piece to claim
-    int64_t off_many_count;// uint32 [kMaxSplitUnits]  arrivals at a split unit
     int64_t off_many_o;    // fp32 [kMaxPieces][d / 4][128][4]  unnormalised partial outputs
     int64_t off_many_ml;   // fp32 [kMaxPieces][2][128]
     int64_t total;
@@ -73,7 +72,6 @@ inline PagedLayout paged_layout(const PagedShape &s)
     L.off_many = off;       off = align256(off + (many ? (int64_t)s.R * 16 : 0));
     L.off_many_cum = off;   off = align256(off + (many ? ((int64_t)s.R + 1) * 4 : 0));
     L.off_claim = off;      off = align256(off + 4);
-    L.off_many_count = off; off = align256(off + kMaxSplitUnits * 4);
     L.off_many_o = off;     off = align256(off + (many ? (int64_t)kMaxPieces * 128 * s.d * 4 : 0));
     L.off_many_ml = off;    off = align256(off + (many ? (int64_t)kMaxPieces * 2 * 128 * 4 : 0));
     L.total = off;
@@ -126,6 +124,12 @@ __device__ __forceinline__ float row_factor(float amax, int top)
     if (!(amax > 0.f) || amax == INFINITY) return 1.f;
     const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
     return exp2f((float)min(top - ex, 100));
+}
+
+// Natural log-sum-exp of a row from its maximum (base 2) and sum.
+__device__ __forceinline__ float row_lse(float mx, float sum)
+{
+    return sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : (sum == 0.f ? -INFINITY : sum);
 }
 #endif
 

@@ -131,6 +131,85 @@ struct Cursor {
 
 }  // namespace
 
+// Adds up the parts of the many-rows kernel's split units, in their order.  A warp
+// takes 32 rows (a lane each) and eight columns of a unit: the parts' loads of a
+// batch are all started before the first is used.
+template <int D>
+__device__ __forceinline__ void add_parts(const PagedArgs &a, const PagedHeader *hd, float vds)
+{
+    constexpr int COLS = D / 8, BP = 8;
+    const PagedShape &s = a.s;
+    const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_many);
+    const int32_t *cum = reinterpret_cast<const int32_t *>(a.plan + a.L.off_many_cum);
+    const float *ml = reinterpret_cast<const float *>(a.plan + a.L.off_many_ml);
+    const float4 *po = reinterpret_cast<const float4 *>(a.plan + a.L.off_many_o);
+    const int G = s.Hq / s.Hkv, tpt = 128 / G, splits = hd->splits_many;
+    const int items = hd->units_many * 4 * COLS;
+    for (int it = blockIdx.x * (blockDim.x >> 5) + warp_id(); it < items; it += gridDim.x * (blockDim.x >> 5)) {
+        const int u = it / (4 * COLS), rest = it - u * (4 * COLS), row = rest / COLS * 32 + lane_id(), c8 = rest % COLS;
+        int e = 0;
+        while (e + 1 < hd->n_many && cum[e + 1] <= u) ++e;
+        const PagedEntry en = list[e];
+        const int nqt = (en.n + tpt - 1) / tpt, local = u - cum[e], h = local / nqt, qt = nqt - 1 - (local - h * nqt);
+        const int ntok = min(tpt, en.n - qt * tpt), tk = row / G;
+        const int parts = min(splits, key_range(en.ctx + qt * tpt, en.ctx + qt * tpt + ntok - 1, s.window, s.sink).n);
+        if (parts == 1 || tk >= ntok) continue;
+        const float *m = ml + (int64_t)u * splits * 256 + row;
+        float mx = -INFINITY, sum = 0.f;
+        for (int p0 = 0; p0 < parts; p0 += BP) {
+            float y[BP], z[BP], top = mx;
+#pragma unroll
+            for (int i = 0; i < BP; ++i) {
+                y[i] = ld_cg(m + min(p0 + i, parts - 1) * 256);
+                z[i] = p0 + i < parts ? ld_cg(m + (p0 + i) * 256 + 128) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < BP; ++i) top = fmaxf(top, y[i]);
+            const float mu = top == -INFINITY ? 0.f : top;
+            sum *= ex2(mx - mu);
+#pragma unroll
+            for (int i = 0; i < BP; ++i) sum += ex2(y[i] - mu) * z[i];
+            mx = top;
+        }
+        const float mu = mx == -INFINITY ? 0.f : mx, inv = sum != 0.f ? vds / sum : 0.f;
+        const float4 *pc = po + ((int64_t)u * splits * (D / 4) + c8 * 2) * 128 + row;
+        float x[8] = {};
+        for (int p0 = 0; p0 < parts; p0 += BP) {
+            float y[BP];
+            float4 v[BP][2];
+#pragma unroll
+            for (int i = 0; i < BP; ++i) {
+                const int p = min(p0 + i, parts - 1);
+                y[i] = ld_cg(m + p * 256);
+                v[i][0] = ld_cg(pc + (int64_t)p * (D / 4) * 128);
+                v[i][1] = ld_cg(pc + (int64_t)p * (D / 4) * 128 + 128);
+            }
+#pragma unroll
+            for (int i = 0; i < BP; ++i) {
+                const float w = p0 + i < parts ? ex2(y[i] - mu) : 0.f;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    x[4 * z] += w * v[i][z].x;
+                    x[4 * z + 1] += w * v[i][z].y;
+                    x[4 * z + 2] += w * v[i][z].z;
+                    x[4 * z + 3] += w * v[i][z].w;
+                }
+            }
+        }
+        const int64_t at = (int64_t)(en.tok0 + qt * tpt + tk) * s.Hq + h * G + (row - tk * G);
+        if (c8 == 0) a.lse[at] = row_lse(mx, sum);
+        if (a.o_f32) {
+            float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + at * D + c8 * 8);
+            o[0] = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+            o[1] = make_float4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+        } else {
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.o) + at * D + c8 * 8) =
+                make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv), pack_bf16x2(x[4] * inv, x[5] * inv),
+                           pack_bf16x2(x[6] * inv, x[7] * inv));
+        }
+    }
+}
+
 // ROWS: 8, 16 or 32 rows of a unit at most; TERMS: 16-bit terms of P.
 template <int D, bool FP8, int ROWS, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -160,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_LENGTHS);
         return;
     }
+    if (hd->splits_many > 1) add_parts<D>(a, hd, FP8 ? *a.v_descale : 1.f);
     const int ctas = hd->ctas_few;
     const int64_t W = hd->tiles_few;
     if ((int)blockIdx.x >= ctas) return;
@@ -396,8 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto store_lse = [&](const PagedEntry &en, int h, int row, float mx, float sum) {
         const int tk = row / G;
-        a.lse[(int64_t)(en.tok0 + tk) * s.Hq + h * G + (row - tk * G)] =
-            sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994531f : (sum == 0.f ? -INFINITY : sum);
+        a.lse[(int64_t)(en.tok0 + tk) * s.Hq + h * G + (row - tk * G)] = row_lse(mx, sum);
     };
     // Pieces of the unit's output that a thread handles in the sums below: rows
     // 8 (z >> 2) + g, columns of 4 in the order of the fragments.
@@ -498,22 +577,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(kSumBar, kWarps * 32);
         if (!*flag) return;
         float *wt = reinterpret_cast<float *>(red);             // [part][row] weights
+        auto slot_of = [&](int p) { return (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)); };
         for (int row = warp; row < nrows; row += kWarps) {
-            float mx = -INFINITY;
-            for (int p = lane; p < parts; p += 32)
-                mx = fmaxf(mx, __ldcg(ws_ml + (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)) * 2 * kFewRows + row));
+            // A lane holds up to five parts (kPagedCtas of them at most).
+            constexpr int PL = (kPagedCtas + 31) / 32;
+            float y[PL], z[PL], mx = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int y = 1; y < 32; y <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, y));
-            const float mu = mx == -INFINITY ? 0.f : mx;
-            float sum = 0.f;
-            for (int p = lane; p < parts; p += 32) {
-                const float *pm = ws_ml + (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)) * 2 * kFewRows + row;
-                const float w = ex2(__ldcg(pm) - mu);
-                wt[p * ROWS + row] = w;
-                sum += w * __ldcg(pm + kFewRows);
+            for (int i = 0; i < PL; ++i) {
+                const int p = lane + 32 * i;
+                y[i] = p < parts ? ld_cg(ws_ml + slot_of(p) * 2 * kFewRows + row) : -INFINITY;
+                z[i] = p < parts ? ld_cg(ws_ml + slot_of(p) * 2 * kFewRows + kFewRows + row) : 0.f;
             }
 #pragma unroll
-            for (int y = 1; y < 32; y <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+            for (int i = 0; i < PL; ++i) mx = fmaxf(mx, y[i]);
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float mu = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                const float w = ex2(y[i] - mu);
+                if (lane + 32 * i < parts) wt[(lane + 32 * i) * ROWS + row] = w;
+                sum += w * z[i];
+            }
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
             if (lane == 0) {
                 store_lse(en, h, row, mx, sum);
                 sml[row] = sum != 0.f ? vds / sum : 0.f;
@@ -523,15 +610,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
             const int row = i / (D / 4), dim = (i % (D / 4)) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int p = 0; p < parts; ++p) {
-                const float w = wt[p * ROWS + row];
-                const float4 u = __ldcg(reinterpret_cast<const float4 *>(
-                    ws_o + ((int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)) * kFewRows + row) * D + dim));
-                v.x += u.x * w;
-                v.y += u.y * w;
-                v.z += u.z * w;
-                v.w += u.w * w;
+            constexpr int BP = 8;               // parts in flight: loads first, uses after
+            for (int p0 = 0; p0 < parts; p0 += BP) {
+                float4 u[BP];
+#pragma unroll
+                for (int y = 0; y < BP; ++y)
+                    u[y] = ld_cg(reinterpret_cast<const float4 *>(ws_o + (slot_of(min(p0 + y, parts - 1)) * kFewRows + row) * D + dim));
+#pragma unroll
+                for (int y = 0; y < BP; ++y) {
+                    const float w = p0 + y < parts ? wt[(p0 + y) * ROWS + row] : 0.f;
+                    v.x += u[y].x * w;
+                    v.y += u[y].y * w;
+                    v.z += u[y].z * w;
+                    v.w += u[y].w * w;
+                }
             }
             store4(en, h, row, dim, v, sml[row]);
         }

@@ -528,6 +528,22 @@ __device__ __forceinline__ uint32_t row_bits32(int lo, int hi)
     return __funnelshift_lc(0u, 0xffffffffu, (uint32_t)lo) & __funnelshift_rc(0xffffffffu, 0u, (uint32_t)(32 - hi));
 }
 
+// Loads that bypass L1 (data that other CTAs have written).  Volatile, so that
+// they stay behind the barrier that makes the data visible; several in a row are
+// in flight together when they are written before the first use.
+__device__ __forceinline__ float ld_cg(const float *p)
+{
+    float v;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 ld_cg(const float4 *p)
+{
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
 // ---- FP8 (e4m3) ---------------------------------------------------------------
 // Instruction descriptor, kind::f8f6f4 with e4m3 A and B (format code 0 in
 // both fields), fp32 accumulate, both operands K-major: the kind::f16 layout
