@@ -5,7 +5,9 @@ statically, so the library needs only the driver (libcuda) at run time and
 loads on a machine without a GPU (for the ABI checks).  ``build(debug=True)``
 builds the same sources with the FM_DEBUG definition (device-side checks that
 report FM_ERR_DEBUG_CHECK) into ``_lib/debug/libfm_debug.so``; the binding
-loads it when the FM_LIBRARY environment variable names it.
+loads it when the FM_LIBRARY environment variable names it.  Beside the library
+stands ``_lib/_fm_call.so``, a CPython extension against the installed torch that
+marshals the paged calls (host code only, whichever library is loaded).
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libfm.so")
+CALL = os.path.join(OUT_DIR, "_fm_call.so")
 DEBUG_DIR = os.path.join(OUT_DIR, "debug")
 DEBUG_LIB = os.path.join(DEBUG_DIR, "libfm_debug.so")
 SOURCES = ["fm_api.cu", "fm_classify.cu", "fm_fwd.cu", "fm_bwd.cu", "fm_fp8.cu", "fm_compress.cu", "fm_noalloc.cu",
@@ -40,9 +44,22 @@ def _deps():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _call_command(nvcc, out):
+    """g++ command of the CPython extension (csrc/fm_call.cpp)."""
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{p}" for p in inc], os.path.join(CSRC, "fm_call.cpp"), "-o", out, f"-L{os.path.join(root, 'lib')}",
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     out_dir, lib = (DEBUG_DIR, DEBUG_LIB) if debug else (OUT_DIR, LIB)
-    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (lib, CALL)):
         return lib
     os.makedirs(out_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -63,8 +80,18 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_call():
+        os.makedirs(OUT_DIR, exist_ok=True)
+        tmp = CALL + f".tmp{os.getpid()}"
+        r = subprocess.run(_call_command(nvcc, tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on fm_call.cpp:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, CALL)
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        call = ex.submit(compile_call)
         results = list(ex.map(compile_one, SOURCES))
+        call.result()
     if verbose:
         for _, err in results:
             if err:

@@ -7,6 +7,8 @@ forwards.  Importing it fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import numpy as np
@@ -19,6 +21,13 @@ if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with "
                       "`python -c 'import __graft_entry__ as g; g.build()'` (needs nvcc)")
 _lib = ctypes.CDLL(_LIB_PATH)
+# The paged calls' marshalling in C++ (csrc/fm_call.cpp), for the library loaded above.
+_CALL_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "_fm_call.so")
+if not os.path.exists(_CALL_PATH):
+    raise ImportError(f"{_CALL_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+_spec = importlib.util.spec_from_loader("_fm_call", importlib.machinery.ExtensionFileLoader("_fm_call", _CALL_PATH))
+_call = importlib.util.module_from_spec(_spec)
+_spec.loader.exec_module(_call)
 
 FM_OK, FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_UNREPRESENTABLE = 0, 1, 2, 3
 FM_ERR_BAD_BOUNDS, FM_ERR_PLAN_MISMATCH, FM_ERR_WORKSPACE, FM_ERR_CUDA, FM_ERR_TIMEOUT = 4, 5, 6, 7, 8
@@ -127,6 +136,7 @@ _lib.fm_paged_append.argtypes = [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.
                                  ctypes.POINTER(PagedCache), _P, _P]
 _lib.fm_attn_paged.argtypes = [ctypes.POINTER(PagedStep), _P, ctypes.c_int64, ctypes.c_int64, _I,
                                ctypes.POINTER(PagedCache), _P, _P, _SZ, _F, _P, _I, _P, _P, _P]
+_call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.fm_paged_plan, _lib.fm_paged_append, _lib.fm_attn_paged)])
 _lib.fm_step_graph_create.argtypes = [ctypes.POINTER(StepArgs), ctypes.POINTER(ctypes.c_void_p)]
 _lib.fm_step_graph_launch.argtypes = [_P, _P]
 _lib.fm_step_graph_destroy.argtypes = [_P]
@@ -436,7 +446,8 @@ def fm_attn_fwd_fp8(q8, k8, vt8, descale, bounds: Bounds, plan, scale, o, lse, d
 
 
 # The paged calls are made once per layer and decoding step, where the host's time
-# counts: their checks are written for few attribute reads and no wrappers.
+# counts.  What a program normally calls them with goes through _call; it answers
+# None to anything else, which these functions then check in full, and raise or run.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -525,6 +536,13 @@ def fm_paged_plan(step: PagedStep, ctx_lens, q_lens, block_table, seq_lens, cu_q
     ctx_lens, q_lens, seq_lens: int32 [requests]; block_table: int32 [requests,
     max_pages]; cu_q: int32 [requests + 1]; slots: int64, positions: int32 or
     None [max_tokens]; free_pages: int32 [n] with free_head and free_next int32 [1]."""
+    if stream is None:
+        code = _call.plan(ctypes.addressof(step), ctx_lens, q_lens, block_table, seq_lens, cu_q, slots, positions, plan,
+                          dev_status, free_pages, free_head, free_next)
+        if code == 0:
+            return
+        if code is not None:
+            raise FmError(code, "fm_paged_plan")
     dev, i32 = _on(ctx_lens, "ctx_lens"), torch.int32
     R, T = step.requests, step.max_tokens
     free = head = after = None
@@ -551,6 +569,12 @@ def fm_paged_plan(step: PagedStep, ctx_lens, q_lens, block_table, seq_lens, cu_q
 def fm_paged_append(k, v, slots, k_cache, v_cache, dev_status, k_descale=None, v_descale=None, stream=None):
     """Rows of k and v (bf16 [T, Hkv, d], any token and head strides) to the cache's
     slots (int64, T of them at least; negative ones are skipped)."""
+    if stream is None:
+        code = _call.append(k, v, slots, k_cache, v_cache, dev_status, k_descale, v_descale)
+        if code == 0:
+            return
+        if code is not None:
+            raise FmError(code, "fm_paged_append")
     cache = paged_cache(k_cache, v_cache, k_descale, v_descale)
     dev = k_cache.get_device()
     T, H, kt, kh = _rows(k, dev, "k", cache.d)
@@ -737,6 +761,13 @@ class PagedAttention:
     def attend(self, q, k_cache, v_cache, block_table, scale=None, o_dtype=torch.bfloat16, k_descale=None,
                v_descale=None):
         scale = 1.0 / self.step.d ** 0.5 if scale is None else scale
+        if o_dtype is torch.bfloat16 or o_dtype is torch.float32:
+            r = _call.attend(ctypes.addressof(self.step), q, k_cache, v_cache, block_table, self.plan_buffer, scale,
+                             o_dtype is torch.float32, self.status, k_descale, v_descale)
+            if type(r) is tuple:
+                return r
+            if r is not None:
+                raise FmError(r, "fm_attn_paged")
         shape = q.shape
         o = torch.empty(shape, dtype=o_dtype, device=q.device)
         lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
