@@ -38,35 +38,56 @@ struct PlanArgs {
 };
 
 
-// Exclusive scan over the block (every thread calls); *total gets the sums.
-template <int N>
-__device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t (*sh)[N])
+// What the planner adds up over the requests.  Tokens and pages saturate: a sum that
+// reaches the bound does not fit anyway.
+constexpr uint32_t kSumMax = 1u << 30;
+struct PlanSums {
+    uint32_t tokens, pages;
+    uint32_t entries;       // few-rows entries | many-rows entries << 16 (kMaxRequests fits)
+    int64_t few_tiles, units;
+    __device__ __forceinline__ void add(const PlanSums &o)
+    {
+        tokens = min(tokens + o.tokens, kSumMax);
+        pages = min(pages + o.pages, kSumMax);
+        entries += o.entries;
+        few_tiles += o.few_tiles;
+        units += o.units;
+    }
+    __device__ __forceinline__ PlanSums up(int o) const
+    {
+        return PlanSums{__shfl_up_sync(0xffffffffu, tokens, o), __shfl_up_sync(0xffffffffu, pages, o),
+                        __shfl_up_sync(0xffffffffu, entries, o), __shfl_up_sync(0xffffffffu, few_tiles, o),
+                        __shfl_up_sync(0xffffffffu, units, o)};
+    }
+};
+
+// Sums before this thread's (every thread of the block calls), and of the block.
+__device__ __forceinline__ void block_scan(const PlanSums &mine, PlanSums *before, PlanSums *total, PlanSums *sh)
 {
     const int lane = lane_id(), warp = threadIdx.x >> 5;
-    int64_t x[N];
+    PlanSums x = mine;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        x[i] = v[i];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x[i], o);
-            if (lane >= o) x[i] += y;
-        }
-        if (lane == 31) sh[warp][i] = x[i];
+    for (int o = 1; o < 32; o <<= 1) {
+        const PlanSums y = x.up(o);
+        if (lane >= o) x.add(y);
     }
+    if (lane == 31) sh[warp] = x;
     __syncthreads();
+    PlanSums w = lane < kPlanWarps ? sh[lane] : PlanSums{};     // every warp scans the warps' sums
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        int64_t before = 0, all = 0;
-#pragma unroll
-        for (int w = 0; w < kPlanWarps; ++w) {
-            const int64_t y = sh[w][i];
-            if (w < warp) before += y;
-            all += y;
-        }
-        v[i] = before + x[i] - v[i];
-        total[i] = all;
+    for (int o = 1; o < kPlanWarps; o <<= 1) {
+        const PlanSums y = w.up(o);
+        if (lane >= o) w.add(y);
     }
+    auto from = [&](const PlanSums &p, int l) {
+        return PlanSums{__shfl_sync(0xffffffffu, p.tokens, l), __shfl_sync(0xffffffffu, p.pages, l), __shfl_sync(0xffffffffu, p.entries, l),
+                        __shfl_sync(0xffffffffu, p.few_tiles, l), __shfl_sync(0xffffffffu, p.units, l)};
+    };
+    *total = from(w, kPlanWarps - 1);
+    *before = from(w, max(warp - 1, 0));
+    if (warp == 0) *before = PlanSums{};
+    const PlanSums y = x.up(1);
+    if (lane > 0) before->add(y);
     __syncthreads();
 }
 
@@ -119,24 +140,27 @@ __device__ __forceinline__ int split_of(int64_t units, int64_t tiles)
 __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanArgs a)
 {
     extern __shared__ __align__(16) uint8_t plan_smem[];
-    constexpr int NV = 7;   // tokens, pages; few: entries, tiles; many: entries, units, tiles (about)
-    __shared__ int64_t sh[kPlanWarps][NV];
+    __shared__ PlanSums sh[kPlanWarps];
+    __shared__ unsigned long long sh_tiles;
     const PagedShape &s = a.s;
     const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;
     int64_t *s_tiles = reinterpret_cast<int64_t *>(plan_smem);             // [R + 1] tiles before few-rows entry i
     int32_t *s_cu = reinterpret_cast<int32_t *>(s_tiles + s.R + 1);        // [R] tokens before request r
     int32_t *s_off = s_cu + s.R;                                           // [R] pages handed out before request r
+    int32_t *s_ctx = s_off + s.R;                                          // [R] tokens cached
     const int G = s.Hq / s.Hkv;
     const int64_t max_keys = (int64_t)s.max_pages * s.page_size;
     PagedEntry *few = reinterpret_cast<PagedEntry *>(a.plan + a.L.off_few);
     int64_t *few_cum = reinterpret_cast<int64_t *>(a.plan + a.L.off_few_cum);
-    const int32_t head = a.free_pages ? *a.free_head : 0;
-
     PagedEntry *many = reinterpret_cast<PagedEntry *>(a.plan + a.L.off_many);
     int32_t *many_cum = reinterpret_cast<int32_t *>(a.plan + a.L.off_many_cum);
     const int tpt = 128 / G;                 // tokens of a many-rows unit
-    int64_t run[NV] = {};
+    const int32_t head = a.free_pages ? *a.free_head : 0;
+
+    PlanSums run{};
+    int64_t many_tiles = 0;                  // of this thread's requests, about
     bool bad = false;
+    if (tid == 0) sh_tiles = 0;
     for (int r0 = 0; r0 < s.R; r0 += kPlanThreads) {
         const int r = r0 + tid;
         int ctx = 0, n = 0;
@@ -148,86 +172,94 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
                 ctx = n = 0;
             }
         }
-        const bool is_few = n > 0 && (int64_t)n * G <= kFewRows;
+        const bool is_few = n > 0 && n * G <= kFewRows;       // n <= 2^24, G <= 32
         const bool is_many = n > 0 && !is_few;
-        KeyRange kr{};
-        if (is_few) kr = key_range(ctx, ctx + n - 1, s.window, s.sink);
-        const int64_t units = is_many ? (int64_t)((n + tpt - 1) / tpt) * s.Hkv : 0;
-        int64_t v[NV], total[NV];
-        v[0] = n;
-        v[1] = (ctx + n + s.page_size - 1) / s.page_size - (ctx + s.page_size - 1) / s.page_size;
-        v[2] = is_few;
-        v[3] = is_few ? (int64_t)kr.n * s.Hkv : 0;
-        v[4] = is_many;
-        v[5] = units;
-        v[6] = 0;
-        if (is_many)        // the units' mean length lies between the first one's and the last one's
-            v[6] = units * (key_range(ctx, ctx + min(n, tpt) - 1, s.window, s.sink).n +
-                            key_range(ctx + (n - 1) / tpt * tpt, ctx + n - 1, s.window, s.sink).n) / 2;
-        block_scan(v, total, sh);
+        PlanSums v{};
+        v.tokens = n;
+        v.pages = (ctx + n + s.page_size - 1) / s.page_size - (ctx + s.page_size - 1) / s.page_size;
+        v.entries = (is_few ? 1u : 0u) | (is_many ? 1u << 16 : 0u);
+        if (is_few) v.few_tiles = (int64_t)key_range(ctx, ctx + n - 1, s.window, s.sink).n * s.Hkv;
+        if (is_many) {
+            v.units = (int64_t)((n + tpt - 1) / tpt) * s.Hkv;
+            // The units' mean length lies between the first one's and the last one's.
+            many_tiles += v.units * (key_range(ctx, ctx + min(n, tpt) - 1, s.window, s.sink).n +
+                                     key_range(ctx + (n - 1) / tpt * tpt, ctx + n - 1, s.window, s.sink).n) / 2;
+        }
+        PlanSums before, total;
+        block_scan(v, &before, &total, sh);
+        before.add(run);
         if (r < s.R) {
-            s_cu[r] = (int32_t)(run[0] + v[0]);     // meaningful when the total fits (checked below)
-            s_off[r] = (int32_t)(run[1] + v[1]);
+            s_cu[r] = (int32_t)before.tokens;
+            s_off[r] = (int32_t)before.pages;
+            s_ctx[r] = ctx;
             if (is_few) {
-                const int e = (int)(run[2] + v[2]);
-                s_tiles[e] = run[3] + v[3];
+                const int e = (int)(before.entries & 0xffffu);
+                s_tiles[e] = before.few_tiles;
                 if (cta == 0) {
-                    few[e] = PagedEntry{r, (int32_t)(run[0] + v[0]), n, ctx};
-                    few_cum[e] = run[3] + v[3];
+                    few[e] = PagedEntry{r, (int32_t)before.tokens, n, ctx};
+                    few_cum[e] = before.few_tiles;
                 }
             }
             if (is_many && cta == 0) {
-                const int e = (int)(run[4] + v[4]);
-                many[e] = PagedEntry{r, (int32_t)(run[0] + v[0]), n, ctx};
-                many_cum[e] = (int32_t)(run[5] + v[5]);
+                const int e = (int)(before.entries >> 16);
+                many[e] = PagedEntry{r, (int32_t)before.tokens, n, ctx};
+                many_cum[e] = (int32_t)before.units;
             }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) run[i] += total[i];
+        run.add(total);
     }
+    if (cta == 0 && many_tiles > 0) atomicAdd(&sh_tiles, (unsigned long long)many_tiles);
     // Every CTA comes to the same verdict.  A plan that fails hands out nothing
     // and is empty: no slot, no row of attention.
     int32_t err = FM_OK;
-    if (__syncthreads_or(bad) || run[0] > s.T || run[5] >= ((int64_t)1 << 31) - kPagedCtas) err = FM_ERR_LENGTHS;
-    else if (a.free_pages && (head < 0 || head > a.n_free || run[1] > a.n_free - head)) err = FM_ERR_PAGES;
+    if (__syncthreads_or(bad) || run.tokens > (uint32_t)s.T || run.units >= ((int64_t)1 << 31) - kPagedCtas) err = FM_ERR_LENGTHS;
+    else if (a.free_pages && (head < 0 || head > a.n_free || run.pages > (uint32_t)(a.n_free - head))) err = FM_ERR_PAGES;
     if (err != FM_OK && cta == 0 && tid == 0) set_status(a.status, err);
-    const int total = err == FM_OK ? (int)run[0] : 0;
-    const int handed = err == FM_OK && a.free_pages ? (int)run[1] : 0;
-    const int n_few = err == FM_OK ? (int)run[2] : 0;
-    const int64_t W = err == FM_OK ? run[3] : 0;
+    const int total = err == FM_OK ? (int)run.tokens : 0;
+    const int handed = err == FM_OK && a.free_pages ? (int)run.pages : 0;
+    const int n_few = err == FM_OK ? (int)(run.entries & 0xffffu) : 0;
+    const int64_t W = err == FM_OK ? run.few_tiles : 0;
 
-    // Page b of request r, as the step leaves the table.
-    auto page_at = [&](int r, int b, int ctx) -> int {
-        const int have = (ctx + s.page_size - 1) / s.page_size;
-        if (a.free_pages && b >= have) return a.free_pages[head + s_off[r] + b - have];
-        return a.table[(int64_t)r * s.max_pages + b];
-    };
+    // Slots and positions, four tokens of a thread at a time: the pages' loads are
+    // in flight together.
     const int stride = ctas * kPlanThreads;
-    for (int t = cta * kPlanThreads + tid; t < s.T; t += stride) {
-        int64_t slot = -1;
-        int p = -1;
-        if (t < total) {
-            const int r = last_at_most(s_cu, s.R, t);
-            const int ctx = a.ctx[r];
-            p = ctx + t - s_cu[r];
-            const int b = p / s.page_size;
-            const int page = page_at(r, b, ctx);
-            if (page >= 0 && page < s.num_pages)
-                slot = (int64_t)page * s.page_size + (p - b * s.page_size);
-            else
-                set_status(a.status, FM_ERR_PAGES);
+    for (int t0 = cta * kPlanThreads + tid; t0 < s.T; t0 += 4 * stride) {
+        int p[4], in[4], page[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + i * stride;
+            p[i] = page[i] = -1;
+            in[i] = 0;
+            if (t < total) {
+                const int r = last_at_most(s_cu, s.R, t), ctx = s_ctx[r];
+                p[i] = ctx + t - s_cu[r];
+                const int b = p[i] / s.page_size, have = (ctx + s.page_size - 1) / s.page_size;
+                in[i] = p[i] - b * s.page_size;
+                // Page b of the request, as the step leaves the table.
+                page[i] = (a.free_pages && b >= have) ? a.free_pages[head + s_off[r] + b - have] : a.table[(int64_t)r * s.max_pages + b];
+            }
         }
-        a.slots[t] = slot;
-        if (a.pos) a.pos[t] = p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + i * stride;
+            if (t >= s.T) break;
+            int64_t slot = -1;
+            if (t < total) {
+                if (page[i] >= 0 && page[i] < s.num_pages) slot = (int64_t)page[i] * s.page_size + in[i];
+                else set_status(a.status, FM_ERR_PAGES);
+            }
+            a.slots[t] = slot;
+            if (a.pos) a.pos[t] = p[i];
+        }
     }
     for (int x = cta * kPlanThreads + tid; x < handed; x += stride) {
         const int r = last_at_most(s_off, s.R, x);
-        const int have = (a.ctx[r] + s.page_size - 1) / s.page_size;
+        const int have = (s_ctx[r] + s.page_size - 1) / s.page_size;
         a.table[(int64_t)r * s.max_pages + have + x - s_off[r]] = a.free_pages[head + x];
     }
     if (cta == 0) {
         const int ctas_few = (int)(W < kPagedCtas ? W : kPagedCtas);
-        const int splits = tid < 32 ? split_of(run[5], run[6]) : 1;
+        const int splits = tid < 32 ? split_of(run.units, (int64_t)sh_tiles) : 1;
         if (tid == 0) {
             PagedHeader h{};
             h.magic = kPagedMagic;
@@ -236,8 +268,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
             h.ctas_few = ctas_few;
             h.tiles_few = W;
             h.rows = total;
-            h.n_many = err == FM_OK ? (int)run[4] : 0;
-            h.units_many = err == FM_OK ? (int)run[5] : 0;
+            h.n_many = err == FM_OK ? (int)(run.entries >> 16) : 0;
+            h.units_many = err == FM_OK ? (int)run.units : 0;
             h.splits_many = h.units_many > 0 ? splits : 1;
             *reinterpret_cast<PagedHeader *>(a.plan) = h;
             few_cum[n_few] = W;
@@ -272,9 +304,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
 }
 
 // ---- append -----------------------------------------------------------------------
-// cache[slot] = x, 8 elements (16 bytes of bf16) of K and of V per thread and
-// step: bound by the bytes.  e4m3: code = e4m3(x / descale), the division in
-// fp32, nearest even, saturating: the quantizer's rule.
+// cache[slot] = x, one piece of 16 bytes of the cache of K and of V per thread: bound by
+// the bytes (13,000 tokens of 8 heads: bf16 9.1 us, e4m3 12.1; two or four pieces
+// in flight per thread: 9.1 to 10.4 and, then with plain divisions, 15.1 to 16.7 for 14.4).
+// e4m3: code = e4m3(x / descale), the quotient in fp32, nearest even, saturating:
+// the quantizer's rule.
+constexpr int kAppendThreads = 256;
+
 struct AppendArgs {
     const uint8_t *k, *v;                        // bf16; strides in bytes
     int64_t k_tok, k_head, v_tok, v_head;
@@ -283,40 +319,62 @@ struct AppendArgs {
     const int64_t *slots;
     const float *k_descale, *v_descale;
     int64_t n_slots;                             // num_pages * page_size
-    int32_t page_size, Hkv, per_row;             // per_row: 16-byte pieces of a row of x
-    int64_t total;                               // T * Hkv * per_row
+    int32_t page_size, T, block_tokens;
+    int32_t per_tok, per_row;                    // pieces of a token, of a row
+    uint64_t tok_magic, row_magic;               // 2^40 / per_tok and / per_row, rounded up
     int32_t *status;
 };
 
-template <bool FP8>
-__global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a)
+// Correctly rounded quotients by one divisor, from its correctly rounded
+// reciprocal and one correction (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990: q = x r, q + (x - q d) r): three instructions
+// each.  A divisor outside [2^-80, 2^80], where the remainder could underflow,
+// divides.
+struct Divisor {
+    float d, r;
+    bool plain;
+    __device__ __forceinline__ explicit Divisor(float x) : d(x), r(1.f / x), plain(!(x >= 8.271806e-25f && x <= 1.2089258e24f)) {}
+    __device__ __forceinline__ float operator()(float x) const
+    {
+        if (plain) return x / d;
+        const float q = x * r, c = fmaf(fmaf(-q, d, x), r, q);
+        return fabsf(q) == INFINITY ? q : copysignf(c, q);      // (the correction loses the sign of a zero)
+    }
+};
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, const Divisor &ds)
 {
-    const float kd = FP8 ? *a.k_descale : 1.f, vd = FP8 ? *a.v_descale : 1.f;
-    const int per_tok = a.Hkv * a.per_row;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < a.total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t t = i / per_tok;
-        const int rest = (int)(i - t * per_tok), h = rest / a.per_row, ch = rest - h * a.per_row;
-        const int64_t slot = a.slots[t];
+    return pack_e4m3x2(ds(__uint_as_float(w << 16)), ds(__uint_as_float(w & 0xffff0000u)));
+}
+__device__ __forceinline__ uint4 e4m3_piece(const uint4 &x, const uint4 &y, const Divisor &ds)
+{
+    return make_uint4(e4m3_pair(x.x, ds) | e4m3_pair(x.y, ds) << 16, e4m3_pair(x.z, ds) | e4m3_pair(x.w, ds) << 16,
+                      e4m3_pair(y.x, ds) | e4m3_pair(y.y, ds) << 16, e4m3_pair(y.z, ds) | e4m3_pair(y.w, ds) << 16);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a)
+{
+    constexpr int IN = FP8 ? 2 : 1;              // 16-byte loads of a piece
+    const int t0 = blockIdx.x * a.block_tokens;
+    const int pieces = min(a.block_tokens, a.T - t0) * a.per_tok;
+    const Divisor kd(FP8 ? *a.k_descale : 1.f), vd(FP8 ? *a.v_descale : 1.f);
+    for (int j = threadIdx.x; j < pieces; j += kAppendThreads) {      // once, unless a token has more pieces than that
+        const int t = (int)(((uint64_t)j * a.tok_magic) >> 40), in = j - t * a.per_tok;
+        const int h = (int)(((uint64_t)in * a.row_magic) >> 40), ch = in - h * a.per_row;
+        const int64_t slot = a.slots[t0 + t];
         if (slot < 0) continue;
         if (slot >= a.n_slots) {
             set_status(a.status, FM_ERR_PAGES);
             continue;
         }
-        const int64_t page = slot / a.page_size, in = slot - page * a.page_size;
-        const uint4 k = *reinterpret_cast<const uint4 *>(a.k + t * a.k_tok + h * a.k_head + ch * 16);
-        const uint4 v = *reinterpret_cast<const uint4 *>(a.v + t * a.v_tok + h * a.v_head + ch * 16);
-        uint8_t *kd_ = a.kc + page * a.kc_page + h * a.kc_head + in * a.kc_tok + ch * (FP8 ? 8 : 16);
-        uint8_t *vd_ = a.vc + page * a.vc_page + h * a.vc_head + in * a.vc_tok + ch * (FP8 ? 8 : 16);
-        if (!FP8) {
-            *reinterpret_cast<uint4 *>(kd_) = k;
-            *reinterpret_cast<uint4 *>(vd_) = v;
-        } else {
-            auto codes = [](uint32_t w, float ds) {
-                return pack_e4m3x2(__uint_as_float(w << 16) / ds, __uint_as_float(w & 0xffff0000u) / ds);
-            };
-            *reinterpret_cast<uint2 *>(kd_) = make_uint2(codes(k.x, kd) | codes(k.y, kd) << 16, codes(k.z, kd) | codes(k.w, kd) << 16);
-            *reinterpret_cast<uint2 *>(vd_) = make_uint2(codes(v.x, vd) | codes(v.y, vd) << 16, codes(v.z, vd) | codes(v.w, vd) << 16);
-        }
+        const uint4 *kp = reinterpret_cast<const uint4 *>(a.k + (int64_t)(t0 + t) * a.k_tok + (int64_t)h * a.k_head + ch * (16 * IN));
+        const uint4 *vp = reinterpret_cast<const uint4 *>(a.v + (int64_t)(t0 + t) * a.v_tok + (int64_t)h * a.v_head + ch * (16 * IN));
+        const uint4 k0 = __ldg(kp), v0 = __ldg(vp);
+        const uint4 k1 = FP8 ? __ldg(kp + 1) : k0, v1 = FP8 ? __ldg(vp + 1) : v0;
+        const int64_t page = slot <= INT32_MAX ? (int64_t)((uint32_t)slot / (uint32_t)a.page_size) : slot / a.page_size;
+        const int64_t at = slot - page * a.page_size;
+        *reinterpret_cast<uint4 *>(a.kc + page * a.kc_page + h * a.kc_head + at * a.kc_tok + ch * 16) = FP8 ? e4m3_piece(k0, k1, kd) : k0;
+        *reinterpret_cast<uint4 *>(a.vc + page * a.vc_page + h * a.vc_head + at * a.vc_tok + ch * 16) = FP8 ? e4m3_piece(v0, v1, vd) : v0;
     }
 }
 
@@ -354,6 +412,7 @@ fm_status check_cache(const fm_paged_cache *c)
 {
     if (!c || !aligned16(c->k) || !aligned16(c->v)) return FM_ERR_INVALID_ARG;
     if (c->num_pages <= 0 || c->page_size <= 0 || c->Hkv <= 0) return FM_ERR_INVALID_ARG;
+    if (c->Hkv > 4096) return FM_ERR_UNSUPPORTED;
     if (c->dtype != FM_DT_BF16 && c->dtype != FM_DT_E4M3) return FM_ERR_INVALID_ARG;
     if (c->d != 64 && c->d != 128) return FM_ERR_UNSUPPORTED;
     if (c->page_size % kPageGranule != 0) return FM_ERR_UNSUPPORTED;
@@ -386,7 +445,7 @@ fm_status device_ok()
             return FM_ERR_CUDA;
         k = (major == 10 && minor == 3) ? 1 : 2;
         if (k == 1 && cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kMaxRequests * 16 + 16) != cudaSuccess)
+                                           kMaxRequests * 20 + 16) != cudaSuccess)
             return FM_ERR_CUDA;
         known[dev].store(k, std::memory_order_release);
     }
@@ -437,7 +496,7 @@ fm_status fm_paged_plan(const fm_paged_step *step, const int32_t *ctx_lens, cons
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = (size_t)a.s.R * 16 + 16;
+    cfg.dynamicSmemBytes = (size_t)a.s.R * 20 + 16;
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -482,15 +541,17 @@ fm_status fm_paged_append(const void *k, int64_t k_tok, int64_t k_head, const vo
     a.v_descale = cache->v_descale;
     a.n_slots = (int64_t)cache->num_pages * cache->page_size;
     a.page_size = cache->page_size;
-    a.Hkv = cache->Hkv;
-    a.per_row = cache->d / 8;
-    a.total = (int64_t)T * cache->Hkv * a.per_row;
+    a.T = T;
+    a.per_row = (int)(cache->d * esz / 16);
+    a.per_tok = cache->Hkv * a.per_row;
+    a.block_tokens = a.per_tok < kAppendThreads ? kAppendThreads / a.per_tok : 1;
+    a.tok_magic = ((uint64_t)1 << 40) / a.per_tok + 1;
+    a.row_magic = ((uint64_t)1 << 40) / a.per_row + 1;
     a.status = dev_status;
-    const int64_t want = (a.total + 255) / 256;
-    const int blocks = (int)(want < 152 * 8 ? want : 152 * 8);
+    const int blocks = (T + a.block_tokens - 1) / a.block_tokens;
     ProfScope ps(kKPagedAppend, stream);
-    if (fp8) paged_append_kernel<true><<<blocks, 256, 0, (cudaStream_t)stream>>>(a);
-    else paged_append_kernel<false><<<blocks, 256, 0, (cudaStream_t)stream>>>(a);
+    if (fp8) paged_append_kernel<true><<<blocks, kAppendThreads, 0, (cudaStream_t)stream>>>(a);
+    else paged_append_kernel<false><<<blocks, kAppendThreads, 0, (cudaStream_t)stream>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 

@@ -221,6 +221,21 @@ def test_append_writes_nan_and_infinity(fm):
     assert got[0].isnan() and got[1] == 448 and got[2] == -448
 
 
+@pytest.mark.parametrize("descale", [1.0, 0.02, 0.0131, 1 / 3, 0.7, 448.0, 1.9999999, 3e-24, 5e-25, 1e-38, 7e23, 1e30, 1.17e-38])
+def test_append_rounds_every_value_as_a_division_does(fm, descale):
+    """All 65,536 bf16 values: the codes are those of the fp32 quotient, saturated."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).cuda().view(1024, 1, 64)
+    kc = torch.zeros(64, 1, 16, 64, dtype=torch.uint8, device="cuda")
+    vc, status, ds = torch.zeros_like(kc), i32([0]), torch.tensor([descale], device="cuda")
+    fm.fm_paged_append(x, x, torch.arange(1024, device="cuda"), kc, vc, status, ds, ds)
+    q = x.float() / ds
+    want = q.clamp(-448, 448).to(torch.float8_e4m3fn)
+    got = kc.view(1024, 64).view(torch.float8_e4m3fn)
+    assert torch.equal(got.float().isnan(), q.view(1024, 64).isnan()) and torch.equal(kc, vc)
+    fine = ~q.view(1024, 64).isnan()
+    assert torch.equal(got.view(torch.uint8)[fine], want.view(1024, 64).view(torch.uint8)[fine])
+
+
 # ---- attention of few rows --------------------------------------------------------------
 FEW = [
     # ctx, new, Hq, Hkv, page, window, sink
