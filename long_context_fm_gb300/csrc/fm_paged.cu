@@ -142,6 +142,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
     extern __shared__ __align__(16) uint8_t plan_smem[];
     __shared__ PlanSums sh[kPlanWarps];
     __shared__ unsigned long long sh_tiles;
+    __shared__ int32_t s_key[kPlanThreads], s_units[kPlanThreads];
+    __shared__ int32_t s_warp[kPlanWarps];
     const PagedShape &s = a.s;
     const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;
     int64_t *s_tiles = reinterpret_cast<int64_t *>(plan_smem);             // [R + 1] tiles before few-rows entry i
@@ -258,6 +260,34 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
         a.table[(int64_t)r * s.max_pages + have + x - s_off[r]] = a.free_pages[head + x];
     }
     if (cta == 0) {
+        // Many-rows entries, the longest keys first (up to a block of them; beyond that
+        // there are units enough to fill the gaps): the CTAs claim in this order.
+        const int n_many = err == FM_OK ? (int)(run.entries >> 16) : 0;
+        if (n_many > 1 && n_many <= kPlanThreads) {
+            __syncthreads();
+            PagedEntry en{};
+            if (tid < n_many) en = many[tid];
+            s_key[tid] = tid < n_many ? en.ctx + en.n : 0;
+            __syncthreads();
+            int rank = 0;
+            if (tid < n_many) {
+                for (int i = 0; i < n_many; ++i) rank += s_key[i] > s_key[tid] || (s_key[i] == s_key[tid] && i < tid) ? 1 : 0;
+                s_units[rank] = (en.n + tpt - 1) / tpt * s.Hkv;
+                many[rank] = en;
+            }
+            __syncthreads();
+            const int u = tid < n_many ? s_units[tid] : 0;      // the sum fits 31 bits (checked above)
+            int x = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane_id() >= o) x += y;
+            }
+            if (lane_id() == 31) s_warp[tid >> 5] = x;
+            __syncthreads();
+            for (int w = 0; w < tid >> 5; ++w) x += s_warp[w];
+            if (tid < n_many) many_cum[tid] = x - u;
+        }
         const int ctas_few = (int)(W < kPagedCtas ? W : kPagedCtas);
         const int splits = tid < 32 ? split_of(run.units, (int64_t)sh_tiles) : 1;
         if (tid == 0) {
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
             h.ctas_few = ctas_few;
             h.tiles_few = W;
             h.rows = total;
-            h.n_many = err == FM_OK ? (int)(run.entries >> 16) : 0;
+            h.n_many = n_many;
             h.units_many = err == FM_OK ? (int)run.units : 0;
             h.splits_many = h.units_many > 0 ? splits : 1;
             *reinterpret_cast<PagedHeader *>(a.plan) = h;

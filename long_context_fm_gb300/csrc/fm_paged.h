@@ -123,7 +123,7 @@ __device__ __forceinline__ float row_factor(float amax, int top)
 {
     if (!(amax > 0.f) || amax == INFINITY) return 1.f;
     const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-    return exp2f((float)min(top - ex, 100));
+    return __uint_as_float((uint32_t)(min(top - ex, 100) + 127) << 23);
 }
 
 // Natural log-sum-exp of a row from its maximum (base 2) and sum.

@@ -63,7 +63,7 @@ template <int D, bool FP8>
 struct ChunkCfg {
     static constexpr int kThreads = FP8 ? 512 : 384;
     // Registers: softmax warps take what the others give back; the sum is the launch's total.
-    static constexpr int kRegsLaunch = FP8 ? 128 : 168, kRegsSoftmax = FP8 ? 216 : 224, kRegsOther = FP8 ? 40 : 56;
+    static constexpr int kRegsLaunch = FP8 ? 128 : 168, kRegsSoftmax = FP8 ? (D == 64 ? 200 : 216) : 224, kRegsOther = FP8 ? (D == 64 ? 56 : 40) : 56;
     static_assert(8 * 32 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * kRegsLaunch, "register split");
     static constexpr int kBox = 128 * 128;                     // 128 rows of 128 bytes (64 values of 16 bits)
     static constexpr int kTile = 128 * D * 2;                  // 16-bit Q or V
@@ -504,33 +504,51 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
         for (int k = 0; run; ++k) {
             if (!read_unit(k, u)) break;
             if (!warp_wait(&bars[B_QR], nq & 1, abort, a.status, lim)) break;
-            for (int i = mate; i < 128 / RPI; i += 4) {
-                const int row = i * RPI + r_in;
-                const uint4 x = *reinterpret_cast<const uint4 *>(q_raw + (l >> 3) * C::kBox + row * 128 + (((l & 7) ^ (row & 7)) << 4));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                float amax = 0.f;
+            // Four steps' rows at a time: their chains of loads, maxima and roundings overlap
+            // (one by one they took 7,000 cycles of a unit's start).
+            constexpr int QB = 2;
+            for (int i0 = mate * QB; i0 < 128 / RPI; i0 += 4 * QB) {
+                uint4 x[QB];
+                float amax[QB];
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    amax = fmax3(amax, fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xffff0000u)));
-#pragma unroll
-                for (int y = 1; y < LPR; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));   // the row's lanes have read it
-                // An infinite element makes the row NaN (it would saturate).
-                const float f = amax == INFINITY ? __uint_as_float(0x7fc00000u) : row_factor(amax, 7);
-                uint32_t hi[2] = {0u, 0u}, lw[2] = {0u, 0u};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const float q0 = __uint_as_float(w[y] << 16) * f, q1 = __uint_as_float(w[y] & 0xffff0000u) * f;
-                    const uint32_t h = pack_e4m3x2(q0, q1);
-                    float h0, h1;
-                    unpack_f16x2(f16x2_of_e4m3(h), h0, h1);
-                    hi[y >> 1] |= h << (16 * (y & 1));
-                    lw[y >> 1] |= pack_e4m3x2(q0 - h0, q1 - h1) << (16 * (y & 1));
+                for (int b = 0; b < QB; ++b) {
+                    const int row = (i0 + b) * RPI + r_in;
+                    x[b] = *reinterpret_cast<const uint4 *>(q_raw + (l >> 3) * C::kBox + row * 128 + (((l & 7) ^ (row & 7)) << 4));
                 }
-                const uint32_t at = D == 128 ? row * 128 + (((l >> 1) ^ (row & 7)) << 4) : row * 64 + (((l >> 1) ^ ((row >> 1) & 3)) << 4);
-                uint8_t *p = smem + C::kQ + at + (l & 1) * 8;
-                *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2 *>(p + C::kTerm) = make_uint2(lw[0], lw[1]);
-                if (l == 0) sQf[(nq & 1) * 128 + row] = 1.f / f;
+#pragma unroll
+                for (int b = 0; b < QB; ++b) {
+                    const uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+                    amax[b] = 0.f;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        amax[b] = fmax3(amax[b], fabsf(__uint_as_float(w[y] << 16)), fabsf(__uint_as_float(w[y] & 0xffff0000u)));
+                }
+#pragma unroll
+                for (int y = 1; y < LPR; y <<= 1)
+#pragma unroll
+                    for (int b = 0; b < QB; ++b) amax[b] = fmaxf(amax[b], __shfl_xor_sync(0xffffffffu, amax[b], y));   // the rows' lanes have read them
+#pragma unroll
+                for (int b = 0; b < QB; ++b) {
+                    const int row = (i0 + b) * RPI + r_in;
+                    const uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+                    // An infinite element makes the row NaN (it would saturate).
+                    const float f = amax[b] == INFINITY ? __uint_as_float(0x7fc00000u) : row_factor(amax[b], 7);
+                    uint32_t hi[2] = {0u, 0u}, lw[2] = {0u, 0u};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float q0 = __uint_as_float(w[y] << 16) * f, q1 = __uint_as_float(w[y] & 0xffff0000u) * f;
+                        const uint32_t h = pack_e4m3x2(q0, q1);
+                        float h0, h1;
+                        unpack_f16x2(f16x2_of_e4m3(h), h0, h1);
+                        hi[y >> 1] |= h << (16 * (y & 1));
+                        lw[y >> 1] |= pack_e4m3x2(q0 - h0, q1 - h1) << (16 * (y & 1));
+                    }
+                    const uint32_t at = D == 128 ? row * 128 + (((l >> 1) ^ (row & 7)) << 4) : row * 64 + (((l >> 1) ^ ((row >> 1) & 3)) << 4);
+                    uint8_t *p = smem + C::kQ + at + (l & 1) * 8;
+                    *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(p + C::kTerm) = make_uint2(lw[0], lw[1]);
+                    if (l == 0) sQf[(nq & 1) * 128 + row] = 1.f / f;
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -628,7 +646,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                             keep[c] = row_bits32(lo - b0, pos + 1 - b0) | row_bits32(0, min(s.sink, pos + 1) - b0);
                         }
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) sv[i] = (keep[i >> 5] & (1u << (i & 31))) ? sv[i] : 0xff800000u;
+                        for (int c = 0; c < 4; ++c)
+                            if (__any_sync(0xffffffffu, keep[c] != 0xffffffffu)) {    // 32 keys that every row keeps take no select
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) sv[32 * c + i] = (keep[c] & (1u << i)) ? sv[32 * c + i] : 0xff800000u;
+                            }
                     }
                     float mx4[4] = {__uint_as_float(sv[0]), __uint_as_float(sv[1]), __uint_as_float(sv[2]), __uint_as_float(sv[3])};
 #pragma unroll
