@@ -371,19 +371,23 @@ FM_API fm_status fm_attn_fwd_fp8(const uint8_t *q8, const uint8_t *k8, const uin
  *   and what a page holds behind the request's last token may be NaN.  The
  *   request's own tokens are expected to be finite: a value that is not may reach
  *   rows of the same request whose mask excludes it.  A page number outside
- *   [0, num_pages) among the attended gives FM_ERR_PAGES and its keys read as zeros.  Outputs are rounded once; P
- *   keeps 16 bits or more in the second product when o is fp32 or the rows are few
- *   (see the kernels).
+ *   [0, num_pages) among the attended gives FM_ERR_PAGES and its keys read as zeros.
+ *   Scores, maxima, sums and products are fp32 (fp32 accumulation).  P enters the
+ *   second product with 24 bits (o fp32, at most 32 rows of new tokens times Hq / Hkv per
+ *   request), 16 bits (otherwise where o is fp32 or the rows are as few) or 8 bits
+ *   (bf16 o, more rows); over an e4m3 cache with 22 or 11 bits, and Q, where the
+ *   rows are more, as two e4m3 terms (exact for elements of 2^-9 of the row's largest or
+ *   more, off by at most 2^-17 of it for smaller ones).  o is rounded once.
  *   The plan holds the workspace as well: calls that share a plan (any number of layers
  *   per step) have to follow one another on the GPU, and so have replays of graphs
  *   that share one.  After a status other than 0, plan again.
  *
- * Sizes: d = 64 or 128; page_size a multiple of 16; Hq / Hkv whole and at most 32;
- * at most 8192 requests and 2^24 rows; max_pages * page_size below 2^31 - 256;
- * a sink needs a window.  Caches: page (p, h, t) of k begins at element p * k_page
+ * Sizes: d = 64 or 128; page_size a multiple of 16, 65536 at most; Hq / Hkv whole and at
+ * most 32, Hq at most 4096; at most 8192 requests and 2^24 rows; max_pages * page_size
+ * below 2^31 - 2^17; a sink needs a window.  Caches: page (p, h, t) of k begins at element p * k_page
  * + h * k_head + t * k_tok, its d elements contiguous; strides and pointers are
- * multiples of 16 bytes.  Values are code * descale for e4m3 (device
- * float each; ignored for bf16).
+ * multiples of 16 bytes.  Values are code * descale for e4m3 (device float each,
+ * positive; ignored for bf16).
  */
 typedef struct {
     int32_t requests, max_tokens, max_q, max_pages;

@@ -426,11 +426,11 @@ fm_status check_step(const fm_paged_step *p, PagedShape *out)
         return FM_ERR_INVALID_ARG;
     if (p->max_q > p->max_tokens || p->Hq % p->Hkv != 0 || (p->sink > 0 && p->window == 0)) return FM_ERR_INVALID_ARG;
     if (p->d != 64 && p->d != 128) return FM_ERR_UNSUPPORTED;
-    if (p->requests > kMaxRequests || p->max_tokens > (1 << 24) || p->page_size % kPageGranule != 0 || p->Hq > 4096 ||
-        p->Hq / p->Hkv > kFewRows)
+    if (p->requests > kMaxRequests || p->max_tokens > (1 << 24) || p->page_size % kPageGranule != 0 || p->page_size > kMaxPage ||
+        p->Hq > 4096 || p->Hq / p->Hkv > kFewRows)
         return FM_ERR_UNSUPPORTED;
-    // Positions are int32, and a tile's last key must be one too.
-    if ((int64_t)p->max_pages * p->page_size > (int64_t)0x7fffffff - 2 * kKeyTile) return FM_ERR_UNSUPPORTED;
+    // Positions are int32, and so are a page's and a tile's last key behind them.
+    if ((int64_t)p->max_pages * p->page_size > (int64_t)0x7fffffff - 2 * kMaxPage) return FM_ERR_UNSUPPORTED;
     if (p->window > (1 << 30) || p->sink > (1 << 30)) return FM_ERR_UNSUPPORTED;
     *out = PagedShape{p->requests, p->max_tokens, p->max_q, p->max_pages, p->num_pages, p->page_size, p->Hq, p->Hkv, p->d,
                       p->window, p->sink};
@@ -445,7 +445,7 @@ fm_status check_cache(const fm_paged_cache *c)
     if (c->Hkv > 4096) return FM_ERR_UNSUPPORTED;
     if (c->dtype != FM_DT_BF16 && c->dtype != FM_DT_E4M3) return FM_ERR_INVALID_ARG;
     if (c->d != 64 && c->d != 128) return FM_ERR_UNSUPPORTED;
-    if (c->page_size % kPageGranule != 0) return FM_ERR_UNSUPPORTED;
+    if (c->page_size % kPageGranule != 0 || c->page_size > kMaxPage) return FM_ERR_UNSUPPORTED;
     const int esz = c->dtype == FM_DT_E4M3 ? 1 : 2;
     const int64_t st[6] = {c->k_page, c->k_head, c->k_tok, c->v_page, c->v_head, c->v_tok};
     for (int64_t x : st)
@@ -535,7 +535,7 @@ fm_status fm_paged_plan(const fm_paged_step *step, const int32_t *ctx_lens, cons
     cfg.attrs = at;
     cfg.numAttrs = 1;
     ProfScope ps(kKPagedPlan, stream);
-    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, (const PlanArgs)a) == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, a) == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 fm_status fm_paged_append(const void *k, int64_t k_tok, int64_t k_head, const void *v, int64_t v_tok, int64_t v_head,

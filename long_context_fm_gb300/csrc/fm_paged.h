@@ -13,6 +13,7 @@ namespace fm {
 constexpr uint32_t kPagedMagic = 0x464D5047u;   // "FMPG"
 constexpr int kKeyTile = 128;                   // keys per tile of work, a multiple of every page granule
 constexpr int kPageGranule = 16;                // page sizes are multiples of this: 16 aligned keys share a page
+constexpr int kMaxPage = 1 << 16;               // tokens of a page at most
 constexpr int kFewRows = 32;                    // (new tokens x query heads per KV head) up to which a request is "few rows"
 constexpr int kPagedCtas = 152;                 // CTAs of the persistent attention kernels (no CTA waits for another)
 constexpr int kMaxRequests = 8192;

@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
 
     const int warp = warp_id(), lane = lane_id();
+    grid_launch_dependents();           // the few-rows kernel takes over SM by SM
     const PagedShape &s = a.s;
     const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
     // The same verdict in every CTA: none claims a unit of a plan that does not fit.

@@ -233,19 +233,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const PagedShape &s = a.s;
     if (!paged_plan_fits(hd, s)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_PLAN_MISMATCH);
+        grid_wait_before();
         return;
     }
     if (hd->rows > a.rows) {            // more rows than the caller's tensors have
         if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_LENGTHS);
+        grid_wait_before();
         return;
     }
+    // The many-rows kernel may still run on other SMs (see the launch): its parts are
+    // added up after it, the few rows meanwhile; and no CTA ends before it has, so
+    // that whatever comes behind this kernel comes behind both.
+    if (hd->splits_many > 1) grid_wait_before();
     if (hd->splits_many > 1) add_parts<D>(a, hd, FP8 ? *a.v_descale : 1.f);
     const int ctas = hd->ctas_few;
     const int64_t W = hd->tiles_few;
-    if ((int)blockIdx.x >= ctas) return;
-    const int64_t x0 = share_begin(W, ctas, blockIdx.x);
-    int left = (int)(share_begin(W, ctas, blockIdx.x + 1) - x0);   // tiles to compute
-    if (left == 0) return;
+    const bool idle = (int)blockIdx.x >= ctas;
+    const int64_t x0 = idle ? 0 : share_begin(W, ctas, blockIdx.x);
+    int left = idle ? 0 : (int)(share_begin(W, ctas, blockIdx.x + 1) - x0);   // tiles to compute
+    if (left == 0) {
+        grid_wait_before();
+        return;
+    }
 
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBar), *empty = full + ST;
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
@@ -335,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // After a wait that ran out: the copies end before the CTA leaves.
         if (*abort && lane == 0)
             for (int i = max(t - ST, 0); i < t; ++i) mbar_wait_drain(&full[i % ST], (i / ST) & 1, a.status);
+        grid_wait_before();
         return;
     }
     warp_regs_inc<kRegsCompute>();
@@ -887,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         advance(cu, left > 0);
         if (last_of_unit && left > 0) begin_unit();
     }
+    grid_wait_before();
 }
 
 }  // namespace fm
@@ -913,9 +924,21 @@ fm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &
             return FM_ERR_CUDA;
         done[dev].store(1, std::memory_order_release);
     }
+    // Behind a many-rows launch this one may start before it ends: its CTAs need a whole
+    // SM's shared memory, so each comes when the SM's own CTA of that kernel has left.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kPagedCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = (int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv) > kFewRows ? 1 : 0;
     ProfScope ps(kKPagedDecode, stream);
-    fm_paged_decode_kernel<D, FP8, ROWS, TERMS><<<kPagedCtas, kThreads, smem, stream>>>(tk, tv, a, box_keys);
-    return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fm_paged_decode_kernel<D, FP8, ROWS, TERMS>, tk, tv, a, box_keys);
+    return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 // By the rows that a request of the step can have at most.

@@ -138,6 +138,40 @@ def test_a_captured_decoding_step_replays(fm, e4m3):
     assert s.lens.tolist() == [96, 36, 21]
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_captured_mixed_batch_replays_to_the_same_bits(fm, e4m3):
+    """Chunks, split chunks and single tokens in one captured step: the two attention kernels overlap."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    ctx, new, page, P, width = [3000, 40, 700, 9, 2500], [30, 1, 100, 2, 0], 32, 240, 96
+    att = fm.PagedAttention(5, 8, 2, 128, page, P, width, 140, 100)
+    table = torch.full((5, width), -1, dtype=torch.int32, device="cuda")
+    order = torch.randperm(P, generator=g, device="cuda").to(torch.int32)
+    for r, (c, n) in enumerate(zip(ctx, new)):
+        held = -(-(c + n) // page)
+        table[r, :held], order = order[:held], order[held:]
+    kc, vc = (torch.randn(P, 2, page, 128, generator=g, device="cuda").bfloat16() for _ in range(2))
+    ds = torch.tensor([0.013], device="cuda") if e4m3 else None
+    if e4m3:
+        kc, vc = ((x.float() / ds).clamp(-448, 448).to(torch.float8_e4m3fn) for x in (kc, vc))
+    q = torch.randn(133, 8, 128, generator=g, device="cuda").bfloat16()
+    lens, fresh = i32(ctx), i32(new)
+    att.plan(lens, fresh, table)
+    want = att.attend(q, kc, vc, table, k_descale=ds, v_descale=ds)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        att.plan(lens, fresh, table)
+        first = att.attend(q, kc, vc, table, k_descale=ds, v_descale=ds)
+        second = att.attend(q, kc, vc, table, k_descale=ds, v_descale=ds)       # another layer on the same plan
+    for _ in range(4):
+        for x in first + second:
+            x.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        att.check_status()
+        for got in (first, second):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_side_streams_and_both_ways_of_marshalling_agree(fm):
     """The current stream through the extension, a stream argument through ctypes: the same bits."""
     g = torch.Generator(device="cuda").manual_seed(1)

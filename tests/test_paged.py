@@ -26,7 +26,7 @@ BAD_STEPS = [
     (dict(requests=0), 1), (dict(max_tokens=0), 1), (dict(max_q=0), 1), (dict(max_q=65), 1), (dict(max_pages=0), 1),
     (dict(num_pages=0), 1), (dict(page_size=0), 1), (dict(Hq=6), 1), (dict(Hkv=0), 1), (dict(window=-1), 1), (dict(sink=3), 1),
     (dict(d=96), 2), (dict(page_size=24), 2), (dict(Hq=132, Hkv=4), 2), (dict(requests=8193), 2),
-    (dict(max_pages=1 << 26), 2), (dict(max_tokens=(1 << 24) + 1), 2),
+    (dict(max_pages=1 << 26), 2), (dict(max_tokens=(1 << 24) + 1), 2), (dict(page_size=65552), 2), (dict(Hq=8192, Hkv=8192), 2),
 ]
 
 
@@ -72,7 +72,7 @@ def cache_of(fm, **kw):
 
 BAD_CACHES = [(dict(k=None), 1), (dict(v=A + 8), 1), (dict(k_tok=127), 1), (dict(k_tok=64), 1), (dict(v_head=-128), 1), (dict(v_page=0), 1),
               (dict(k_page=4), 1), (dict(dtype=1), 1), (dict(dtype=3), 1), (dict(dtype=2, k_descale=None), 1), (dict(dtype=2, v_tok=136), 1),
-              (dict(num_pages=0), 1), (dict(d=256), 2), (dict(page_size=40), 2)]
+              (dict(num_pages=0), 1), (dict(d=256), 2), (dict(page_size=40), 2), (dict(page_size=65552), 2), (dict(Hkv=4097), 2)]
 
 
 @pytest.mark.parametrize("change,code", BAD_CACHES)
