@@ -16,14 +16,18 @@
 // finished by the CTA that arrives last at it, which adds the partial results
 // in the order of the CTAs: the result does not depend on who is last.
 //
-// A warp takes 16 keys of every tile and works alone until its unit ends: one
-// lane loads them by TMA through a ring of the warp's own (an mbarrier per slot,
-// no barrier between warps), 16 aligned keys always lying in one page.  Fragment
-// layouts: the head-dim order of the score product is free as long as Q and K
-// agree, the order of keys as long as P and V do, and the order of output columns
-// altogether, so K and V fragments are read with 16-byte shared loads in an
-// order that meets no bank conflict under TMA's swizzle, and V is transposed by
-// byte permutes of two keys' registers.
+// Four warps load whole tiles by TMA, boxes of up to 128 consecutive keys of a page,
+// through a ring of 192 KB; eight compute, each on 16 or 32 keys of a tile with a
+// running maximum and sum of its own, so that they meet only when a unit ends.  (With
+// every warp loading its own 16 keys the loads' bookkeeping and the boxes' start, about
+// 130 cycles each, bounded it: 96 ragged requests of up to 16K tokens 0.320 ms, now
+// 0.289 to 0.297, 6.65 to 6.85 TB/s; per-thread copies before that 0.374.)  Fragment
+// layouts: the head-dim order of the score product is free as long as Q and K agree, the
+// order of keys as long as P and V do, and the order of output columns altogether, so K
+// and V fragments are read with 16-byte shared loads in an order that meets no bank
+// conflict under TMA's swizzle, and V is transposed by byte permutes of two keys'
+// registers.  e4m3 caches halve the bytes but not the products and their latencies,
+// which then bound it: 64 requests of two tokens 0.136 to 0.145 ms (5.0 to 5.4 TB/s).
 //
 // P enters the second product as two 16-bit terms (hi + lo, about 16
 // significant bits), so that the rounding of a 16-bit output is the only one
@@ -306,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ loads
         // Warps 0 and 1 of the group load the even and the odd boxes of K, 2 and 3
         // those of V, a lane each with its own page, looked up a tile ahead.  (One
-        // warp alone takes about 130 cycles per box one after the other: 16-token
-        // pages of e4m3, 0.160 ms where four warps need ... see below.)
+        // warp alone starts its boxes one after the other, about 130 cycles each:
+        // 16-token pages of e4m3, 0.160 ms where four warps need 0.136.)
         const int part = warp - kWarps, bx = (part & 1) + 2 * lane;
         const bool mine = bx < n_box;
         const CUtensorMap *map = part < 2 ? &tk : &tv;
@@ -677,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             st_shared_v4(smem + st * C::kStage + V0 + group[q] + (ch >> 3) * half_box + chunk_at<NARROW>(row, ch & 7),
                                          make_uint4(0, 0, 0, 0));
                     }
+                fence_proxy_async_smem();       // before a later tile's copy into the stage
                 __syncwarp();
             }
             float sc[MT][2 * SUB][4];
@@ -832,54 +837,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
 #pragma unroll
             for (int q = 0; q < SUB; ++q) {
-            const uint32_t vq = base + group[q];
-            if (!FP8) {
+                const uint32_t vq = base + group[q];
+                if (!FP8) {
 #pragma unroll
-                for (int np = 0; np < NP; ++np) {
-                    uint32_t w[4][4];
+                    for (int np = 0; np < NP; ++np) {
+                        uint32_t w[4][4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const uint4 v = lds128(vq + v_at[r & 1] + np * half_box + (r >> 1) * ROW8);
+                            w[r][0] = v.x;
+                            w[r][1] = v.y;
+                            w[r][2] = v.z;
+                            w[r][3] = v.w;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            pv(q, np * 8 + 2 * x, __byte_perm(w[0][x], w[1][x], 0x5410), __byte_perm(w[2][x], w[3][x], 0x5410));
+                            pv(q, np * 8 + 2 * x + 1, __byte_perm(w[0][x], w[1][x], 0x7632), __byte_perm(w[2][x], w[3][x], 0x7632));
+                        }
+                    }
+                } else {
+                    constexpr int WD = D / 32;      // words of e4m3 per key and thread
+                    uint32_t w[4][WD];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const uint4 v = lds128(vq + v_at[r & 1] + np * half_box + (r >> 1) * ROW8);
-                        w[r][0] = v.x;
-                        w[r][1] = v.y;
-                        w[r][2] = v.z;
-                        w[r][3] = v.w;
+                        const uint32_t at = vq + v_at[r & 1] + (r >> 1) * ROW8;
+                        if (WD == 4) {
+                            const uint4 v = lds128(at);
+                            w[r][0] = v.x;
+                            w[r][1] = v.y;
+                            w[r][2 % WD] = v.z;
+                            w[r][3 % WD] = v.w;
+                        } else {
+                            const uint2 v = lds64(at);
+                            w[r][0] = v.x;
+                            w[r][1] = v.y;
+                        }
                     }
+                    // The bytes of two keys are paired before they are expanded.
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        pv(q, np * 8 + 2 * x, __byte_perm(w[0][x], w[1][x], 0x5410), __byte_perm(w[2][x], w[3][x], 0x5410));
-                        pv(q, np * 8 + 2 * x + 1, __byte_perm(w[0][x], w[1][x], 0x7632), __byte_perm(w[2][x], w[3][x], 0x7632));
-                    }
-                }
-            } else {
-                constexpr int WD = D / 32;      // words of e4m3 per key and thread
-                uint32_t w[4][WD];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t at = vq + v_at[r & 1] + (r >> 1) * ROW8;
-                    if (WD == 4) {
-                        const uint4 v = lds128(at);
-                        w[r][0] = v.x;
-                        w[r][1] = v.y;
-                        w[r][2 % WD] = v.z;
-                        w[r][3 % WD] = v.w;
-                    } else {
-                        const uint2 v = lds64(at);
-                        w[r][0] = v.x;
-                        w[r][1] = v.y;
+                    for (int x = 0; x < WD; ++x) {
+                        const uint32_t lo01 = __byte_perm(w[0][x], w[1][x], 0x5140), hi01 = __byte_perm(w[0][x], w[1][x], 0x7362);
+                        const uint32_t lo23 = __byte_perm(w[2][x], w[3][x], 0x5140), hi23 = __byte_perm(w[2][x], w[3][x], 0x7362);
+                        pv(q, 4 * x, f16x2_of_e4m3(lo01), f16x2_of_e4m3(lo23));
+                        pv(q, 4 * x + 1, f16x2_of_e4m3(lo01 >> 16), f16x2_of_e4m3(lo23 >> 16));
+                        pv(q, 4 * x + 2, f16x2_of_e4m3(hi01), f16x2_of_e4m3(hi23));
+                        pv(q, 4 * x + 3, f16x2_of_e4m3(hi01 >> 16), f16x2_of_e4m3(hi23 >> 16));
                     }
                 }
-                // The bytes of two keys are paired before they are expanded.
-#pragma unroll
-                for (int x = 0; x < WD; ++x) {
-                    const uint32_t lo01 = __byte_perm(w[0][x], w[1][x], 0x5140), hi01 = __byte_perm(w[0][x], w[1][x], 0x7362);
-                    const uint32_t lo23 = __byte_perm(w[2][x], w[3][x], 0x5140), hi23 = __byte_perm(w[2][x], w[3][x], 0x7362);
-                    pv(q, 4 * x, f16x2_of_e4m3(lo01), f16x2_of_e4m3(lo23));
-                    pv(q, 4 * x + 1, f16x2_of_e4m3(lo01 >> 16), f16x2_of_e4m3(lo23 >> 16));
-                    pv(q, 4 * x + 2, f16x2_of_e4m3(hi01), f16x2_of_e4m3(hi23));
-                    pv(q, 4 * x + 3, f16x2_of_e4m3(hi01 >> 16), f16x2_of_e4m3(hi23 >> 16));
-                }
-            }
             }
         }
         if (step % SUB == turn) {
