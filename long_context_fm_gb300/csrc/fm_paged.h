@@ -44,10 +44,20 @@ struct PagedEntry {
     int32_t r, tok0, n, ctx;   // request, its first row of q, new tokens, tokens cached before them
 };
 
+// Where a CTA's share of the few-rows list begins: all that its first loads need, so that
+// they wait for one read of the plan and one of the block table.
+struct PagedStart {
+    int32_t e, h, x, count;    // entry, KV head, tile of the entry's range; tiles of the share
+    PagedEntry ent;            // the entry
+    int64_t cum;               // tiles before it
+    int32_t pad[2];
+};
+static_assert(sizeof(PagedStart) == 48, "start record size");
+
 struct PagedLayout {
     int64_t off_few;       // PagedEntry [R]
     int64_t off_few_cum;   // int64 [R + 1]  tiles before entry i, over all KV heads
-    int64_t off_start;     // int4 [kPagedCtas]  entry, head, tile of a CTA's first tile
+    int64_t off_start;     // PagedStart [kPagedCtas]
     int64_t off_count;     // uint32 [kPagedCtas]  arrivals at the split unit that begins in CTA c
     int64_t off_few_o;     // fp32 [2 kPagedCtas][kFewRows][d]  unnormalised partial outputs
     int64_t off_few_ml;    // fp32 [2 kPagedCtas][2][kFewRows]  their row maxima (base 2) and sums
@@ -65,7 +75,7 @@ inline PagedLayout paged_layout(const PagedShape &s)
     int64_t off = 256;
     L.off_few = off;      off = align256(off + (int64_t)s.R * 16);
     L.off_few_cum = off;  off = align256(off + ((int64_t)s.R + 1) * 8);
-    L.off_start = off;    off = align256(off + kPagedCtas * 16);
+    L.off_start = off;    off = align256(off + kPagedCtas * 48);
     L.off_count = off;    off = align256(off + kPagedCtas * 4);
     L.off_few_o = off;    off = align256(off + (int64_t)2 * kPagedCtas * kFewRows * s.d * 4);
     L.off_few_ml = off;   off = align256(off + (int64_t)2 * kPagedCtas * 2 * kFewRows * 4);

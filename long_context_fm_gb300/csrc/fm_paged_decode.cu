@@ -130,6 +130,7 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int ch)
 struct Cursor {
     int e, h, x;          // entry, KV head, tile of the entry's range
     PagedEntry ent;
+    int64_t cum;          // tiles before the entry
     KeyRange kr;
 };
 
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kg = key_of<NARROW>(g), ka = key_of<NARROW>(2 * c), kb2 = key_of<NARROW>(2 * c + 1);
     const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
     const PagedShape &s = a.s;
+    const PagedStart start = reinterpret_cast<const PagedStart *>(a.plan + a.L.off_start)[blockIdx.x];   // used if the plan fits
     if (!paged_plan_fits(hd, s)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_PLAN_MISMATCH);
         grid_wait_before();
@@ -252,9 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (hd->splits_many > 1) add_parts<D>(a, hd, FP8 ? *a.v_descale : 1.f);
     const int ctas = hd->ctas_few;
     const int64_t W = hd->tiles_few;
-    const bool idle = (int)blockIdx.x >= ctas;
-    const int64_t x0 = idle ? 0 : share_begin(W, ctas, blockIdx.x);
-    int left = idle ? 0 : (int)(share_begin(W, ctas, blockIdx.x + 1) - x0);   // tiles to compute
+    int left = (int)blockIdx.x < ctas ? start.count : 0;    // tiles to compute
     if (left == 0) {
         grid_wait_before();
         return;
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto enter = [&](Cursor &u) {
         const int4 v = *reinterpret_cast<const int4 *>(list + u.e);
         u.ent = PagedEntry{v.x, v.y, v.z, v.w};
+        u.cum = cum[u.e];
         u.kr = key_range(v.w, v.w + v.z - 1, s.window, s.sink);
     };
     // Next tile of the walk; true when it begins another unit.
@@ -292,14 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
     };
 
-    Cursor cu;
-    {
-        const int4 v = *reinterpret_cast<const int4 *>(a.plan + a.L.off_start + (int64_t)blockIdx.x * 16);
-        cu.e = v.x;
-        cu.h = v.y;
-        cu.x = v.z;
-        enter(cu);
-    }
+    Cursor cu{start.e, start.h, start.x, start.ent, start.cum, key_range(start.ent.ctx, start.ent.ctx + start.ent.n - 1, s.window, s.sink)};
     // A tile's boxes of box_keys consecutive keys of one page: [128-byte box of a
     // row][key][128 bytes] each.  Some: a row attends one of the n keys from j on.
     const int n_box = kKeyTile / box_keys;
@@ -501,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto end_unit = [&]() {
         const PagedEntry en = cu.ent;
         const int h = cu.h, nrows = en.n * G;
-        const int64_t ub = cum[cu.e] + (int64_t)cu.h * cu.kr.n;   // the unit's tiles are [ub, ub + n) of the list
+        const int64_t ub = cu.cum + (int64_t)cu.h * cu.kr.n;   // the unit's tiles are [ub, ub + n) of the list
         const int c_first = share_owner(W, ctas, ub), c_last = share_owner(W, ctas, ub + cu.kr.n - 1);
         const int parts = c_last - c_first + 1;
         if (NR == 1) {                  // the low terms' products stand in the idle rows
