@@ -170,13 +170,8 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (!table || !buf || !status || scale <= 0 || tensor(a[4])->size(0) != s->requests || q->size(0) == 0) return none();
     const bool f32 = a[7] == Py_True;
     const auto opt = at::TensorOptions().device(q->device());
-    at::Tensor o, lse;
-    try {
-        o = at::empty(q->sizes(), opt.dtype(f32 ? at::kFloat : at::kBFloat16));
-        lse = at::empty({q->size(0), q->size(1)}, opt.dtype(at::kFloat));
-    } catch (const std::exception &) {
-        return none();                      // the other way raises it as torch does
-    }
+    at::Tensor o = at::empty(q->sizes(), opt.dtype(f32 ? at::kFloat : at::kBFloat16));
+    at::Tensor lse = at::empty({q->size(0), q->size(1)}, opt.dtype(at::kFloat));
     const fm_status st = g_attn(s, q->data_ptr(), qt, qh, (int)q->size(0), &c, (const int32_t *)table, buf, (size_t)tensor(a[5])->numel(),
                                 (float)scale, o.data_ptr(), f32 ? FM_DT_F32 : FM_DT_BF16, (float *)lse.data_ptr(), (int32_t *)status,
                                 stream_of(dev));
@@ -193,10 +188,23 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n)
     return r;
 }
 
+// No exception of torch's (a tensor without storage, a failing CUDA call) leaves a
+// function: the other way meets it again and raises it.
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    try {
+        return F(self, a, n);
+    } catch (...) {
+        PyErr_Clear();
+        return none();
+    }
+}
+
 PyMethodDef methods[] = {{"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
-                         {"plan", (PyCFunction)(void (*)(void))plan, METH_FASTCALL, nullptr},
-                         {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
-                         {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, nullptr},
+                         {"plan", (PyCFunction)(void (*)(void))guarded<plan>, METH_FASTCALL, nullptr},
+                         {"append", (PyCFunction)(void (*)(void))guarded<append>, METH_FASTCALL, nullptr},
+                         {"attend", (PyCFunction)(void (*)(void))guarded<attend>, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fm_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -117,3 +117,41 @@ def test_python_refuses_what_is_not_on_the_gpu(fm):
         fm.fm_paged_append(x, x, torch.zeros(4, dtype=torch.int64), cache, cache, torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         fm.PagedAttention(4, 6, 4, 128, 32, 40, 10, 64, 8, device="cpu")
+
+
+FAKE = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from long_context_fm_gb300 import fm
+with FakeTensorMode():
+    k = torch.empty(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cache = torch.empty(8, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.empty(4, dtype=torch.int64, device="cuda")
+    word = torch.empty(1, dtype=torch.int32, device="cuda")
+    table = torch.empty(1, 8, dtype=torch.int32, device="cuda")
+    two = torch.empty(2, dtype=torch.int32, device="cuda")
+    plan = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    o = torch.empty(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(4, 2, device="cuda")
+step = fm.PagedStep(1, 4, 4, 8, 8, 16, 2, 2, 64, 0, 0)
+raised = 0
+for call in (lambda: fm.fm_paged_append(k, k, slots, cache, cache, word),
+             lambda: fm.fm_paged_plan(step, word, word, table, word, two, slots, word, plan, word),
+             lambda: fm._call.attend(__import__("ctypes").addressof(step), k, cache, cache, table, plan, 0.1, False, word, None, None) or 1 / 0):
+    try:
+        call()
+    except Exception:
+        raised += 1
+print("raised", raised)
+"""
+
+
+def test_a_tensor_without_memory_raises(fm):
+    """torch's exceptions (here: no device, or a tensor without storage) end as Python's."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FAKE], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and "raised 3" in r.stdout, r.stderr
