@@ -554,6 +554,7 @@ def fm_paged_plan(step: PagedStep, ctx_lens, q_lens, block_table, seq_lens, cu_q
         free = _flat(free_pages, i32, dev, "free_pages", (n_free,))
         head = _flat(free_head, i32, dev, "free_head", (1,))
         after = _flat(free_next, i32, dev, "free_next", (1,))
+        free = free or head         # an empty tensor has no address, but an empty list is not "no list"
     code = _lib.fm_paged_plan(
         step, _flat(ctx_lens, i32, dev, "ctx_lens", (R,)), _flat(q_lens, i32, dev, "q_lens", (R,)),
         _flat(block_table, i32, dev, "block_table", (R, step.max_pages)), free, n_free, head, after,

@@ -175,6 +175,16 @@ def test_a_free_page_outside_the_pool(fm):
     assert att.slots.tolist() == [-1, -1, 80, 81] + [-1] * 4
 
 
+@pytest.mark.parametrize("new,code", [([0, 3], 0), ([1, 0], 11)])
+def test_an_empty_free_list(fm, new, code):
+    """No page is left: steps that need none go on, others fail, whatever the table holds behind the tokens."""
+    att = fm.PagedAttention(2, 4, 4, 64, 16, 40, 4, 8, 8)
+    table = i32([[1, 2, 3, 4], [5, 6, 7, 8]])
+    att.plan(i32([16, 10]), i32(new), table, free_pages=torch.empty(0, dtype=torch.int32, device="cuda"), free_head=i32([0]))
+    assert int(att.status.item()) == code and int(att.free_next.item()) == 0
+    assert att.slots.tolist() == ([90, 91, 92] + [-1] * 5 if code == 0 else [-1] * 8)
+
+
 # ---- append --------------------------------------------------------------------------
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Hkv", [1, 3, 8])
