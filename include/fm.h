@@ -352,7 +352,8 @@ FM_API fm_status fm_attn_fwd_fp8(const uint8_t *q8, const uint8_t *k8, const uin
  *   seq_lens may be ctx_lens and free_next may be free_head: they are advanced in
  *   place (a captured step can be replayed); no other two arrays may overlap.
  *   Lengths that do not fit the step's sizes (negative, a chunk over max_q, more than
- *   max_tokens rows, more than max_pages pages) give FM_ERR_LENGTHS, too few free
+ *   max_tokens rows, more than max_pages pages, or 2^31 tiles of 128 keys and more over
+ *   the KV heads of the requests of at most 32 rows) give FM_ERR_LENGTHS, too few free
  *   pages FM_ERR_PAGES, in dev_status; the plan is then empty: no page is taken,
  *   cu_q is 0, every slot -1, seq_lens = ctx_lens, and fm_attn_paged does
  *   nothing.  A page number outside [0, num_pages) gives FM_ERR_PAGES and slot -1 for

@@ -212,9 +212,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
     }
     if (cta == 0 && many_tiles > 0) atomicAdd(&sh_tiles, (unsigned long long)many_tiles);
     // Every CTA comes to the same verdict.  A plan that fails hands out nothing
-    // and is empty: no slot, no row of attention.
+    // and is empty: no slot, no row of attention.  (Tiles of the few-rows list are counted in
+    // 31 bits from here on; units fit them: at least 104 rows each of 2^36, and one
+    // per request and KV head.)
     int32_t err = FM_OK;
-    if (__syncthreads_or(bad) || run.tokens > (uint32_t)s.T || run.units >= ((int64_t)1 << 31) - kPagedCtas) err = FM_ERR_LENGTHS;
+    if (__syncthreads_or(bad) || run.tokens > (uint32_t)s.T || run.few_tiles > INT32_MAX) err = FM_ERR_LENGTHS;
     else if (a.free_pages && (head < 0 || head > a.n_free || run.pages > (uint32_t)(a.n_free - head))) err = FM_ERR_PAGES;
     if (err != FM_OK && cta == 0 && tid == 0) set_status(a.status, err);
     const int total = err == FM_OK ? (int)run.tokens : 0;

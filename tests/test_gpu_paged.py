@@ -185,6 +185,17 @@ def test_an_empty_free_list(fm, new, code):
     assert att.slots.tolist() == ([90, 91, 92] + [-1] * 5 if code == 0 else [-1] * 8)
 
 
+@pytest.mark.parametrize("pages,code", [(4090, 0), (4097, 10)])
+def test_more_key_tiles_than_31_bits(fm, pages, code):
+    """Tables may name a page again and again: 512 tiles of 128 keys a page, 1024 KV heads."""
+    att = fm.PagedAttention(1, 1024, 1024, 64, 65536, 1, 4100, 1, 1)
+    att.plan(i32([pages * 65536 - 1]), i32([1]), torch.zeros(1, 4100, dtype=torch.int32, device="cuda"))
+    assert int(att.status.item()) == code
+    header = att.plan_buffer[:256].view(torch.int32).tolist()      # the sizes of the step, then n_few, ctas_few, tiles (64 bits)
+    assert header[12:14] == ([1, 152] if code == 0 else [0, 0])
+    assert att.plan_buffer[:256].view(torch.int64)[7] == (pages * 512 * 1024 if code == 0 else 0)
+
+
 # ---- append --------------------------------------------------------------------------
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Hkv", [1, 3, 8])
