@@ -80,6 +80,13 @@ class PagedStep(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("requests", "max_tokens", "max_q", "max_pages", "num_pages", "page_size",
                                               "Hq", "Hkv", "d", "window", "sink")]
 
+    def __init__(self, *sizes, **named):
+        for name, x in [*((n, x) for (n, _), x in zip(self._fields_, sizes)), *named.items()]:
+            # (ctypes would keep the low 32 bits)
+            if not -1 << 31 <= x < 1 << 31:
+                raise ValueError(f"{name} = {x} does not fit 32 bits")
+        super().__init__(*sizes, **named)
+
 
 class PagedCache(ctypes.Structure):
     """fm_paged_cache of include/fm.h."""
@@ -488,6 +495,8 @@ def _rows(t, dev, name, d):
     if se != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     T, H, _ = shape
+    if T >= 1 << 31:
+        raise ValueError(f"{name} has 2^31 - 1 rows at most")
     return T, H, st if T > 1 else d, sh if H > 1 else d     # the stride of a dimension of size one is never used
 
 
@@ -551,6 +560,8 @@ def fm_paged_plan(step: PagedStep, ctx_lens, q_lens, block_table, seq_lens, cu_q
         if free_head is None or free_next is None:
             raise ValueError("free_pages comes with free_head and free_next")
         n_free = free_pages.numel()
+        if n_free >= 1 << 31:
+            raise ValueError("free_pages has 2^31 - 1 entries at most")
         free = _flat(free_pages, i32, dev, "free_pages", (n_free,))
         head = _flat(free_head, i32, dev, "free_head", (1,))
         after = _flat(free_next, i32, dev, "free_next", (1,))

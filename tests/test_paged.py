@@ -155,3 +155,10 @@ def test_a_tensor_without_memory_raises(fm):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FAKE], capture_output=True, text=True, cwd=root, timeout=300)
     assert r.returncode == 0 and "raised 3" in r.stdout, r.stderr
+
+
+@pytest.mark.parametrize("name", ["max_tokens", "window", "num_pages"])
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 64, -(1 << 31) - 1])
+def test_sizes_past_32_bits_are_refused(fm, name, value):
+    with pytest.raises(ValueError):
+        step_of(fm, **{name: value})
