@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
     int32_t *s_cu = reinterpret_cast<int32_t *>(s_tiles + s.R + 1);        // [R] tokens before request r
     int32_t *s_off = s_cu + s.R;                                           // [R] pages handed out before request r
     int32_t *s_ctx = s_off + s.R;                                          // [R] tokens cached
+    uint8_t *s_rows = reinterpret_cast<uint8_t *>(s_ctx + s.R);            // [R] rows of few-rows entry i
     const int G = s.Hq / s.Hkv;
     const int64_t max_keys = (int64_t)s.max_pages * s.page_size;
     PagedEntry *few = reinterpret_cast<PagedEntry *>(a.plan + a.L.off_few);
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
             if (is_few) {
                 const int e = (int)(before.entries & 0xffffu);
                 s_tiles[e] = before.few_tiles;
+                s_rows[e] = (uint8_t)(n * G);
                 if (cta == 0) {
                     few[e] = PagedEntry{r, (int32_t)before.tokens, n, ctx};
                     few_cum[e] = before.few_tiles;
@@ -325,6 +327,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
                 st.count = (int)(share_begin(W, ctas_few, i + 1) - x);
                 st.ent = few[e];        // written by this CTA, before the barrier above
                 st.cum = s_tiles[e];
+                for (int y = e; y < n_few && s_tiles[y] < x + st.count; ++y) st.rows = max(st.rows, (int)s_rows[y]);
             }
             reinterpret_cast<PagedStart *>(a.plan + a.L.off_start)[i] = st;
             reinterpret_cast<uint32_t *>(a.plan + a.L.off_count)[i] = 0u;
@@ -484,7 +487,7 @@ fm_status device_ok()
             return FM_ERR_CUDA;
         k = (major == 10 && minor == 3) ? 1 : 2;
         if (k == 1 && cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kMaxRequests * 20 + 16) != cudaSuccess)
+                                           kMaxRequests * 21 + 16) != cudaSuccess)
             return FM_ERR_CUDA;
         known[dev].store(k, std::memory_order_release);
     }
@@ -535,7 +538,7 @@ fm_status fm_paged_plan(const fm_paged_step *step, const int32_t *ctx_lens, cons
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = (size_t)a.s.R * 20 + 16;
+    cfg.dynamicSmemBytes = (size_t)a.s.R * 21 + 16;
     cfg.stream = (cudaStream_t)stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

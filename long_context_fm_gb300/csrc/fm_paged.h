@@ -50,7 +50,8 @@ struct PagedStart {
     int32_t e, h, x, count;    // entry, KV head, tile of the entry's range; tiles of the share
     PagedEntry ent;            // the entry
     int64_t cum;               // tiles before it
-    int32_t pad[2];
+    int32_t rows;              // rows of the share's units at most
+    int32_t pad;
 };
 static_assert(sizeof(PagedStart) == 48, "start record size");
 

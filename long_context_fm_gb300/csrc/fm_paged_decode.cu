@@ -215,11 +215,10 @@ __device__ __forceinline__ void add_parts(const PagedArgs &a, const PagedHeader 
     }
 }
 
-// ROWS: 8, 16 or 32 rows of a unit at most; TERMS: 16-bit terms of P.
+// A CTA's share.  ROWS: 8, 16 or 32 rows of a unit at most; TERMS: 16-bit terms of P.
 template <int D, bool FP8, int ROWS, int TERMS>
-__global__ void __launch_bounds__(kThreads, 1)
-    fm_paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PagedArgs a,
-                           const int box_keys)
+__device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, const int box_keys,
+                                           const PagedHeader *hd, const PagedStart &start, uint8_t *smem)
 {
     using C = DecodeCfg<D, FP8, ROWS>;
     constexpr int ST = C::kStages, SUB = C::kSub;
@@ -230,35 +229,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KS = D / 16;              // score product: k-steps
     constexpr int NT = D / 8;               // output product: 8-column tiles
     constexpr int NP = NT / 8;              // groups of 8 tiles
-    extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = warp_id(), lane = lane_id();
     const int g = lane >> 2, c = lane & 3;
     const int kg = key_of<NARROW>(g), ka = key_of<NARROW>(2 * c), kb2 = key_of<NARROW>(2 * c + 1);
-    const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
     const PagedShape &s = a.s;
-    const PagedStart start = reinterpret_cast<const PagedStart *>(a.plan + a.L.off_start)[blockIdx.x];   // used if the plan fits
-    if (!paged_plan_fits(hd, s)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_PLAN_MISMATCH);
-        grid_wait_before();
-        return;
-    }
-    if (hd->rows > a.rows) {            // more rows than the caller's tensors have
-        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_LENGTHS);
-        grid_wait_before();
-        return;
-    }
-    // The many-rows kernel may still run on other SMs (see the launch): its parts are
-    // added up after it, the few rows meanwhile; and no CTA ends before it has, so
-    // that whatever comes behind this kernel comes behind both.
-    if (hd->splits_many > 1) grid_wait_before();
-    if (hd->splits_many > 1) add_parts<D>(a, hd, FP8 ? *a.v_descale : 1.f);
     const int ctas = hd->ctas_few;
     const int64_t W = hd->tiles_few;
-    int left = (int)blockIdx.x < ctas ? start.count : 0;    // tiles to compute
-    if (left == 0) {
-        grid_wait_before();
-        return;
-    }
+    int left = start.count;                 // tiles to compute
 
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBar), *empty = full + ST;
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
@@ -899,16 +876,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_wait_before();
 }
 
+// 16-bit terms of P (see above).
+FM_HD constexpr int terms_of(bool fp8, int rows, bool f32) { return fp8 ? (rows == 8 || f32 ? 2 : 1) : (f32 ? 3 : 2); }
+
+// RMAX: rows that a request of the step can have at most, 8, 16 or 32.
+template <int D, bool FP8, bool F32, int RMAX>
+__global__ void __launch_bounds__(kThreads, 1)
+    fm_paged_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PagedArgs a,
+                           const int box_keys)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
+    const PagedStart start = reinterpret_cast<const PagedStart *>(a.plan + a.L.off_start)[blockIdx.x];   // used if the plan fits
+    if (!paged_plan_fits(hd, a.s)) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_PLAN_MISMATCH);
+        grid_wait_before();
+        return;
+    }
+    if (hd->rows > a.rows) {            // more rows than the caller's tensors have
+        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, FM_ERR_LENGTHS);
+        grid_wait_before();
+        return;
+    }
+    // The many-rows kernel may still run on other SMs (see the launch): its parts are
+    // added up after it, the few rows meanwhile; and no CTA ends before it has, so
+    // that whatever comes behind this kernel comes behind both.
+    if (hd->splits_many > 1) grid_wait_before();
+    if (hd->splits_many > 1) add_parts<D>(a, hd, FP8 ? *a.v_descale : 1.f);
+    if ((int)blockIdx.x >= hd->ctas_few) {
+        grid_wait_before();
+        return;
+    }
+    // By the rows that the units of this CTA's share have at most (parts of a unit fit together
+    // whichever way they are computed): a step that could have 32 rows seldom has.  64
+    // requests of one token and four heads per KV head in a step of up to 512: bf16 437 us as
+    // 32 rows, 364 as 8; e4m3 361 and 216.  16 rows in such a step: e4m3 104 and 78.
+    if (RMAX > 16 && start.rows > 16) {
+        walk_share<D, FP8, 32, terms_of(FP8, 32, F32)>(tk, tv, a, box_keys, hd, start, smem);
+        return;
+    }
+    if (RMAX > 8 && start.rows > 8) {
+        walk_share<D, FP8, 16, terms_of(FP8, 16, F32)>(tk, tv, a, box_keys, hd, start, smem);
+        return;
+    }
+    walk_share<D, FP8, 8, terms_of(FP8, 8, F32)>(tk, tv, a, box_keys, hd, start, smem);
+}
+
 }  // namespace fm
 
 using namespace fm;
 
 namespace {
 
-template <int D, bool FP8, int ROWS, int TERMS>
+template <int D, bool FP8, bool F32, int RMAX>
 fm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int box_keys, cudaStream_t stream)
 {
-    constexpr int smem = DecodeCfg<D, FP8, ROWS>::kBytes;
+    constexpr int smem = DecodeCfg<D, FP8, RMAX>::kBytes;
+    static_assert(DecodeCfg<D, FP8, 8>::kBytes <= smem && (RMAX < 32 || DecodeCfg<D, FP8, 16>::kBytes <= smem), "shared memory of either way");
     static std::atomic<uint8_t> done[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FM_ERR_CUDA;
@@ -916,10 +940,9 @@ fm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &
         // The register split adds up to the launch's registers only if the
         // kernel was compiled to that many per thread.
         cudaFuncAttributes fa{};
-        if (cudaFuncGetAttributes(&fa, fm_paged_decode_kernel<D, FP8, ROWS, TERMS>) != cudaSuccess || fa.numRegs != kLaunchRegs)
+        if (cudaFuncGetAttributes(&fa, fm_paged_decode_kernel<D, FP8, F32, RMAX>) != cudaSuccess || fa.numRegs != kLaunchRegs)
             return FM_ERR_CUDA;
-        if (cudaFuncSetAttribute(fm_paged_decode_kernel<D, FP8, ROWS, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess)
+        if (cudaFuncSetAttribute(fm_paged_decode_kernel<D, FP8, F32, RMAX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return FM_ERR_CUDA;
         done[dev].store(1, std::memory_order_release);
     }
@@ -936,26 +959,22 @@ fm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &
     cfg.attrs = at;
     cfg.numAttrs = (int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv) > kFewRows ? 1 : 0;
     ProfScope ps(kKPagedDecode, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fm_paged_decode_kernel<D, FP8, ROWS, TERMS>, tk, tv, a, box_keys);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fm_paged_decode_kernel<D, FP8, F32, RMAX>, tk, tv, a, box_keys);
     return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
-// By the rows that a request of the step can have at most.
+// By the rows that a request of the step can have at most: a kernel with fewer ways in it is
+// faster where they are enough (8 rows alone 295 us, beside the others 301; 32 rows alone 252,
+// now 258).
 template <int D, bool FP8>
 fm_status launch_rows(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int box_keys, cudaStream_t stream)
 {
     const int64_t rows = (int64_t)a.s.max_q * (a.s.Hq / a.s.Hkv);
-    if constexpr (FP8) {
-        if (rows <= 8) return launch<D, FP8, 8, 2>(tk, tv, a, box_keys, stream);
-        if (a.o_f32) return rows <= 16 ? launch<D, FP8, 16, 2>(tk, tv, a, box_keys, stream) : launch<D, FP8, 32, 2>(tk, tv, a, box_keys, stream);
-        return rows <= 16 ? launch<D, FP8, 16, 1>(tk, tv, a, box_keys, stream) : launch<D, FP8, 32, 1>(tk, tv, a, box_keys, stream);
-    } else {
-        if (a.o_f32)
-            return rows <= 8 ? launch<D, FP8, 8, 3>(tk, tv, a, box_keys, stream)
-                             : rows <= 16 ? launch<D, FP8, 16, 3>(tk, tv, a, box_keys, stream) : launch<D, FP8, 32, 3>(tk, tv, a, box_keys, stream);
-        return rows <= 8 ? launch<D, FP8, 8, 2>(tk, tv, a, box_keys, stream)
-                         : rows <= 16 ? launch<D, FP8, 16, 2>(tk, tv, a, box_keys, stream) : launch<D, FP8, 32, 2>(tk, tv, a, box_keys, stream);
-    }
+    if (a.o_f32)                        // (8 rows of e4m3 take two terms for either output)
+        return rows <= 8 ? launch<D, FP8, !FP8, 8>(tk, tv, a, box_keys, stream)
+                         : rows <= 16 ? launch<D, FP8, true, 16>(tk, tv, a, box_keys, stream) : launch<D, FP8, true, 32>(tk, tv, a, box_keys, stream);
+    return rows <= 8 ? launch<D, FP8, false, 8>(tk, tv, a, box_keys, stream)
+                     : rows <= 16 ? launch<D, FP8, false, 16>(tk, tv, a, box_keys, stream) : launch<D, FP8, false, 32>(tk, tv, a, box_keys, stream);
 }
 
 }  // namespace

@@ -315,6 +315,16 @@ MANY = [
 ]
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,q_max", [(64, 8), (128, 8), (128, 34), (64, 4), (128, 4)])
+def test_requests_of_few_and_fewer_rows(fm, e4m3, o_dtype, d, q_max):
+    """4 to 32 rows beside one another, each unit's keys over several CTAs: parts of a unit computed in different ways."""
+    new = [1, 8, 2, 4, 0, 3, 1, 5, 1, 8] if q_max >= 8 else [1, 4, 2, 4, 0, 3, 1, 2, 1, 4]
+    b = Batch(fm, [2100, 1777, 300, 1290, 50, 2047, 3, 900, 1600, 0], new, 12, 3, d, 16, e4m3=e4m3, seed=5, q_max=q_max)
+    b.check(o_dtype)
+
+
 @pytest.mark.parametrize("o_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
