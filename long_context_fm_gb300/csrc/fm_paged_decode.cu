@@ -65,7 +65,7 @@ struct DecodeCfg {
     static constexpr int kSub = (kRow == 256 || ROWS == 32) ? 1 : 2;
     static constexpr int kStage = 2 * kKeyTile * kRow;      // a tile: K boxes, then V boxes
     static constexpr int kStages = 192 * 1024 / kStage < 8 ? 192 * 1024 / kStage : 8;
-    static constexpr int kPieces = ROWS == 8 ? 4 : 8;
+    static constexpr int kPieces = ROWS == 8 && D == 64 ? 4 : 8;     // that a warp leaves at a time when a unit ends
     static constexpr int kRed = kStages * kStage;           // float4 [warps][pieces][32 lanes]; Q of 32 rows between units
     static constexpr int kMl = kRed + kWarps * kPieces * 32 * 16;   // float [warps][2][kFewRows]
     static constexpr int kBar = kMl + kWarps * 2 * kFewRows * 4;    // mbarrier [2][stages]: loaded, read
@@ -441,9 +441,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         }
     };
 
-    // Sums the unit over the warps, in groups of eight output tiles through
-    // shared memory, and writes the rows or this CTA's partial result of them.
-    const uint32_t bid = blockIdx.x;
+    const int bid = blockIdx.x;
     float4 *red = reinterpret_cast<float4 *>(smem + C::kRed);
     float *sml = reinterpret_cast<float *>(smem + C::kMl);
     volatile int *flag = reinterpret_cast<volatile int *>(smem + C::kMisc);
@@ -469,12 +467,21 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         const int cc = piece_of<NARROW>(2 * c + ((z >> 1) & 1)), jq = (z & 1) * 4;
         return (FP8 && D == 128) ? 16 * cc + 8 * np + jq : 64 * np + 8 * cc + jq;
     };
+    // Whether the unit at the cursor begins in this CTA's share, and whether it ends there too.
+    auto begins = [&]() { return cu.e != start.e || cu.h != start.h || start.x == 0; };
+    // Sums the unit over the warps and writes its rows, or this CTA's partial result of
+    // them: every warp leaves its maxima, sums and output in shared memory, eight pieces
+    // of the output at a time, and then adds one piece up.  (5 us a unit when it took an
+    // exchange more for the maxima, twice the passes, and a fence and an atomic for a split
+    // unit in the middle of the walk: 64 requests of two tokens over e4m3 0.138 ms.)
+    constexpr int ZP = 4 * NR * (NR == 1 ? NP : 1);         // pieces of a pass
+    static_assert(ZP <= C::kPieces && ZP <= kWarps, "pieces of a pass");
     auto end_unit = [&]() {
         const PagedEntry en = cu.ent;
         const int h = cu.h, nrows = en.n * G;
-        const int64_t ub = cu.cum + (int64_t)cu.h * cu.kr.n;   // the unit's tiles are [ub, ub + n) of the list
-        const int c_first = share_owner(W, ctas, ub), c_last = share_owner(W, ctas, ub + cu.kr.n - 1);
-        const int parts = c_last - c_first + 1;
+        const bool first = begins(), whole = first && cu.x + 1 == cu.kr.n;
+        // Slot of a partial result: 2 c + 1 when the unit begins in this CTA's share, 2 c when it comes in from the left.
+        const int slot = 2 * bid + (first ? 1 : 0);
         if (NR == 1) {                  // the low terms' products stand in the idle rows
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -486,133 +493,157 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         for (int b = 0; b < MT; ++b)
 #pragma unroll
             for (int hf = 0; hf < NR; ++hf) {
-                float sum = l[b][hf];
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (c == 0) {
-                    sml[(warp * 2) * kFewRows + b * 16 + hf * 8 + g] = m[b][hf];
-                    sml[(warp * 2 + 1) * kFewRows + b * 16 + hf * 8 + g] = sum;
-                }
-            }
-        named_bar_sync(kSumBar, kWarps * 32);
-        // Slot of a partial result: 2 c + 1 when the unit begins in this CTA's share, 2 c when it comes in from the left.
-        const int slot = 2 * (int)bid + ((int)bid == c_first ? 1 : 0);
-#pragma unroll
-        for (int b = 0; b < MT; ++b) {
-            float f[NR], inv[NR];
-#pragma unroll
-            for (int hf = 0; hf < NR; ++hf) {
-                const int row = b * 16 + hf * 8 + g;
-                float mx = -INFINITY, sum = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sml[(w * 2) * kFewRows + row]);
-                const float mu = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) sum += sml[(w * 2 + 1) * kFewRows + row] * ex2(sml[(w * 2) * kFewRows + row] - mu);
-                f[hf] = ex2(m[b][hf] - mu);
-                inv[hf] = sum != 0.f ? vds / sum : 0.f;
-                if (warp == 0 && c == 0 && row < nrows) {
-                    if (parts == 1) {
-                        store_lse(en, h, row, mx, sum);
-                    } else {
-                        __stcg(ws_ml + (int64_t)slot * 2 * kFewRows + row, mx);
-                        __stcg(ws_ml + (int64_t)slot * 2 * kFewRows + kFewRows + row, sum);
-                    }
-                }
+                l[b][hf] += __shfl_xor_sync(0xffffffffu, l[b][hf], 1);
+                l[b][hf] += __shfl_xor_sync(0xffffffffu, l[b][hf], 2);
             }
 #pragma unroll
-            for (int np = 0; np < NP; ++np) {
-                if (b > 0 || np > 0) named_bar_sync(kSumBar, kWarps * 32);
-                // piece z = (row half, column half, 4 of 8 tiles)
+        for (int b = 0; b < MT; ++b)
 #pragma unroll
-                for (int z = 0; z < 4 * NR; ++z) {
-                    const int hf = z >> 2, y = 2 * hf + ((z >> 1) & 1), t = np * 8 + (z & 1) * 4;
+            for (int pass = 0; pass < (NR == 1 ? 1 : NP); ++pass) {
+                named_bar_sync(kSumBar, kWarps * 32);           // what was there has been read
+                if (b == 0 && pass == 0 && c == 0)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int hf = 0; hf < NR; ++hf) {
+                            sml[(warp * 2) * kFewRows + i * 16 + hf * 8 + g] = m[i][hf];
+                            sml[(warp * 2 + 1) * kFewRows + i * 16 + hf * 8 + g] = l[i][hf];
+                        }
+                // piece z = (row half or group of 8 tiles, column half, 4 of 8 tiles)
+#pragma unroll
+                for (int z = 0; z < ZP; ++z) {
+                    const int hf = NR == 1 ? 0 : z >> 2, np = NR == 1 ? z >> 2 : pass;
+                    const int y = 2 * hf + ((z >> 1) & 1), t = np * 8 + (z & 1) * 4;
                     if (b * 16 + hf * 8 < nrows)
-                        red[(warp * 4 * NR + z) * 32 + lane] = make_float4(oa[b][t][y] * f[hf], oa[b][t + 1][y] * f[hf],
-                                                                      oa[b][t + 2][y] * f[hf], oa[b][t + 3][y] * f[hf]);
+                        red[(warp * ZP + z) * 32 + lane] = make_float4(oa[b][t][y], oa[b][t + 1][y], oa[b][t + 2][y], oa[b][t + 3][y]);
                 }
                 named_bar_sync(kSumBar, kWarps * 32);
-                const int z = warp, row = b * 16 + (z >> 2) * 8 + g;
-                if (z < 4 * NR && row < nrows) {
-                    float4 v = red[z * 32 + lane];
+                const int z = warp, hf = NR == 1 ? 0 : z >> 2, np = NR == 1 ? z >> 2 : pass, row = b * 16 + hf * 8 + g;
+                if (z < ZP && row < nrows) {
+                    float f[kWarps], mx = -INFINITY, sum = 0.f;
 #pragma unroll
-                    for (int w = 1; w < kWarps; ++w) {
-                        const float4 u = red[(w * 4 * NR + z) * 32 + lane];
-                        v.x += u.x;
-                        v.y += u.y;
-                        v.z += u.z;
-                        v.w += u.w;
+                    for (int w = 0; w < kWarps; ++w) {
+                        f[w] = sml[(w * 2) * kFewRows + row];
+                        mx = fmaxf(mx, f[w]);
                     }
-                    if (parts == 1)
-                        store4(en, h, row, dim_of(np, z), v, inv[NR == 1 ? 0 : z >> 2]);
-                    else
-                        __stcg(reinterpret_cast<float4 *>(ws_o + ((int64_t)slot * kFewRows + row) * D + dim_of(np, z)), v);
+                    const float mu = mx == -INFINITY ? 0.f : mx;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        f[w] = ex2(f[w] - mu);
+                        sum += sml[(w * 2 + 1) * kFewRows + row] * f[w];
+                        const float4 u = red[(w * ZP + z) * 32 + lane];
+                        v.x += u.x * f[w];
+                        v.y += u.y * f[w];
+                        v.z += u.z * f[w];
+                        v.w += u.w * f[w];
+                    }
+                    if (whole) store4(en, h, row, dim_of(np, z), v, sum != 0.f ? vds / sum : 0.f);
+                    else __stcg(reinterpret_cast<float4 *>(ws_o + ((int64_t)slot * kFewRows + row) * D + dim_of(np, z)), v);
+                    if (c == 0 && np == 0 && (z & 3) == 0) {
+                        if (whole) {
+                            store_lse(en, h, row, mx, sum);
+                        } else {
+                            __stcg(ws_ml + (int64_t)slot * 2 * kFewRows + row, mx);
+                            __stcg(ws_ml + (int64_t)slot * 2 * kFewRows + kFewRows + row, sum);
+                        }
+                    }
                 }
             }
-        }
-        if (parts == 1) return;
-        // A split unit: the last of its CTAs adds the partial results up, in the CTAs' order.
+    };
+    // After the walk: the units that began before this share or go on behind it, the
+    // share's first and last at most.  The last of a unit's CTAs adds the partial results
+    // up, in the CTAs' order.  (At the cursor: the share's last unit.)
+    auto join_units = [&]() {
+        const bool first = begins(), last_cut = !(first && cu.x + 1 == cu.kr.n);
+        const bool one = cu.e == start.e && cu.h == start.h;    // the share lies in one unit
+        const bool first_cut = start.x > 0 && !one;             // (a first unit that goes on is the last one, too)
+        if (!first_cut && !last_cut) return;
+        // (The share's first entry is read again: in registers it would be there all the way.)
+        const PagedStart *again = reinterpret_cast<const PagedStart *>(a.plan + a.L.off_start) + bid;
+        const int4 e0 = __ldcg(reinterpret_cast<const int4 *>(&again->ent));       // r, tok0, n, ctx
+        const int64_t cum0 = __ldcg(reinterpret_cast<const long long *>(&again->cum));
+        const KeyRange kr0 = key_range(e0.w, e0.w + e0.z - 1, s.window, s.sink);
         __threadfence();
         named_bar_sync(kSumBar, kWarps * 32);
-        if (threadIdx.x == 0) {
-            unsigned *cnt = reinterpret_cast<unsigned *>(a.plan + a.L.off_count) + c_first;
-            *flag = atomicInc(cnt, (unsigned)(parts - 1)) == (unsigned)(parts - 1);   // returns to 0 by itself
-            __threadfence();
+        // CTAs of the unit, from the first one: tiles [ub, ub + n) of the list.
+        auto from_of = [&](int i) {
+            return share_owner(W, ctas, i == 0 ? cum0 + (int64_t)start.h * kr0.n : cu.cum + (int64_t)cu.h * cu.kr.n);
+        };
+        auto to_of = [&](int i) {
+            return share_owner(W, ctas, i == 0 ? cum0 + (int64_t)(start.h + 1) * kr0.n - 1 : cu.cum + (int64_t)(cu.h + 1) * cu.kr.n - 1);
+        };
+        if (threadIdx.x == 0 || threadIdx.x == 32) {
+            const int i = threadIdx.x == 0 ? 0 : 1;
+            int mine = 0;
+            if (i == 0 ? first_cut : last_cut) {
+                const int from = from_of(i), more = to_of(i) - from;
+                unsigned *cnt = reinterpret_cast<unsigned *>(a.plan + a.L.off_count) + from;
+                mine = atomicInc(cnt, (unsigned)more) == (unsigned)more ? 1 : 0;        // returns to 0 by itself
+                __threadfence();
+            }
+            flag[2 * i] = mine;
         }
         named_bar_sync(kSumBar, kWarps * 32);
-        if (!*flag) return;
-        float *wt = reinterpret_cast<float *>(red);             // [part][row] weights
-        auto slot_of = [&](int p) { return (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)); };
-        for (int row = warp; row < nrows; row += kWarps) {
-            // A lane holds up to five parts (kPagedCtas of them at most).
-            constexpr int PL = (kPagedCtas + 31) / 32;
-            float y[PL], z[PL], mx = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            if (!flag[2 * i]) continue;
+            const PagedEntry en{0, i == 0 ? e0.y : cu.ent.tok0, i == 0 ? e0.z : cu.ent.n, 0};
+            const int h = i == 0 ? start.h : cu.h, nrows = en.n * G;
+            const int c_first = from_of(i), parts = to_of(i) - c_first + 1;
+            float *wt = reinterpret_cast<float *>(red);             // [part][row] weights
+            auto slot_of = [&](int p) { return (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)); };
+            for (int row = warp; row < nrows; row += kWarps) {
+                // A lane holds up to five parts (kPagedCtas of them at most).
+                constexpr int PL = (kPagedCtas + 31) / 32;
+                float y[PL], z[PL], mx = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < PL; ++i) {
-                const int p = lane + 32 * i;
-                y[i] = p < parts ? ld_cg(ws_ml + slot_of(p) * 2 * kFewRows + row) : -INFINITY;
-                z[i] = p < parts ? ld_cg(ws_ml + slot_of(p) * 2 * kFewRows + kFewRows + row) : 0.f;
-            }
+                for (int x = 0; x < PL; ++x) {
+                    const int p = lane + 32 * x;
+                    y[x] = p < parts ? ld_cg(ws_ml + slot_of(p) * 2 * kFewRows + row) : -INFINITY;
+                    z[x] = p < parts ? ld_cg(ws_ml + slot_of(p) * 2 * kFewRows + kFewRows + row) : 0.f;
+                }
 #pragma unroll
-            for (int i = 0; i < PL; ++i) mx = fmaxf(mx, y[i]);
+                for (int x = 0; x < PL; ++x) mx = fmaxf(mx, y[x]);
 #pragma unroll
-            for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-            const float mu = mx == -INFINITY ? 0.f : mx;
+                for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                const float mu = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-            for (int i = 0; i < PL; ++i) {
-                const float w = ex2(y[i] - mu);
-                if (lane + 32 * i < parts) wt[(lane + 32 * i) * ROWS + row] = w;
-                sum += w * z[i];
-            }
+                for (int x = 0; x < PL; ++x) {
+                    const float w = ex2(y[x] - mu);
+                    if (lane + 32 * x < parts) wt[(lane + 32 * x) * ROWS + row] = w;
+                    sum += w * z[x];
+                }
 #pragma unroll
-            for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            if (lane == 0) {
-                store_lse(en, h, row, mx, sum);
-                sml[row] = sum != 0.f ? vds / sum : 0.f;
-            }
-        }
-        named_bar_sync(kSumBar, kWarps * 32);
-        for (int i = threadIdx.x; i < nrows * (D / 4); i += kWarps * 32) {
-            const int row = i / (D / 4), dim = (i % (D / 4)) * 4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int BP = 8;               // parts in flight: loads first, uses after
-            for (int p0 = 0; p0 < parts; p0 += BP) {
-                float4 u[BP];
-#pragma unroll
-                for (int y = 0; y < BP; ++y)
-                    u[y] = ld_cg(reinterpret_cast<const float4 *>(ws_o + (slot_of(min(p0 + y, parts - 1)) * kFewRows + row) * D + dim));
-#pragma unroll
-                for (int y = 0; y < BP; ++y) {
-                    const float w = p0 + y < parts ? wt[(p0 + y) * ROWS + row] : 0.f;
-                    v.x += u[y].x * w;
-                    v.y += u[y].y * w;
-                    v.z += u[y].z * w;
-                    v.w += u[y].w * w;
+                for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                if (lane == 0) {
+                    store_lse(en, h, row, mx, sum);
+                    sml[row] = sum != 0.f ? vds / sum : 0.f;
                 }
             }
-            store4(en, h, row, dim, v, sml[row]);
+            named_bar_sync(kSumBar, kWarps * 32);
+            for (int x = threadIdx.x; x < nrows * (D / 4); x += kWarps * 32) {
+                const int row = x / (D / 4), dim = (x % (D / 4)) * 4;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                constexpr int BP = 8;               // parts in flight: loads first, uses after
+                for (int p0 = 0; p0 < parts; p0 += BP) {
+                    float4 u[BP];
+#pragma unroll
+                    for (int y = 0; y < BP; ++y)
+                        u[y] = ld_cg(reinterpret_cast<const float4 *>(ws_o + (slot_of(min(p0 + y, parts - 1)) * kFewRows + row) * D + dim));
+#pragma unroll
+                    for (int y = 0; y < BP; ++y) {
+                        const float w = p0 + y < parts ? wt[(p0 + y) * ROWS + row] : 0.f;
+                        v.x += u[y].x * w;
+                        v.y += u[y].y * w;
+                        v.z += u[y].z * w;
+                        v.w += u[y].w * w;
+                    }
+                }
+                store4(en, h, row, dim, v, sml[row]);
+            }
+            named_bar_sync(kSumBar, kWarps * 32);
         }
-        named_bar_sync(kSumBar, kWarps * 32);
     };
 
     // ---- the walk -------------------------------------------------------------
@@ -632,7 +663,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
     constexpr uint32_t ROW8 = NARROW ? 512 : 1024;          // eight rows further
     int st = 0, step = 0;
     uint32_t phase = 0;
-    while (left > 0) {
+    while (true) {
         const int kw = cu.kr.tile(cu.x) * kKeyTile + key0;
         // A wait that ran out has set the status: the walk goes on, so that every
         // barrier is reached, and what it writes does not count.
@@ -870,9 +901,11 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         --left;
         const bool last_of_unit = cu.x + 1 == cu.kr.n || left == 0;
         if (last_of_unit) end_unit();
-        advance(cu, left > 0);
-        if (last_of_unit && left > 0) begin_unit();
+        if (left == 0) break;
+        advance(cu, true);
+        if (last_of_unit) begin_unit();
     }
+    join_units();
     grid_wait_before();
 }
 
