@@ -336,6 +336,23 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
     uint8_t *sq = smem + C::kRed;           // two blocks: Q in shared memory between units
     const float kds = FP8 ? *a.k_descale : 1.f, vds = FP8 ? *a.v_descale : 1.f;
 
+    // Q rows of a unit, in up to 16 rows: thread c of a row holds the dims that it reads of K (see
+    // the product below).
+    uint4 qw[MT == 1 ? NR : 1][D / 32];
+    auto fetch_q = [&](const Cursor &u) {
+#pragma unroll
+        for (int hf = 0; hf < NR; ++hf) {
+            const int row = hf * 8 + g, tk = row / G;
+            const bool in = tk < u.ent.n;
+            const uint8_t *qp = a.q + (int64_t)(u.ent.tok0 + (in ? tk : 0)) * a.q_tok + (int64_t)(u.h * G + (in ? row - tk * G : 0)) * a.q_head;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int ch = FP8 ? (c + 4 * (i >> 1)) * 2 + (i & 1) : c + 4 * i;
+                qw[MT == 1 ? hf : 0][i] = make_uint4(0, 0, 0, 0);
+                if (in) qw[MT == 1 ? hf : 0][i] = *reinterpret_cast<const uint4 *>(qp + ch * 16);
+            }
+        }
+    };
     auto begin_unit = [&]() {
         const int nrows = cu.ent.n * G;
 #pragma unroll
@@ -348,16 +365,12 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
                 pos[b][hf] = in ? cu.ent.ctx + tk : -1;
                 m[b][hf] = -INFINITY;
                 l[b][hf] = 0.f;
-                const uint8_t *qp = a.q + (int64_t)(cu.ent.tok0 + tk) * a.q_tok + (int64_t)(cu.h * G + (in ? row - tk * G : 0)) * a.q_head;
                 if (MT == 1) {
-                    // Thread c holds the dims that it reads of K (see the product below).
                     float amax = 0.f;
                     uint32_t w[KS][2];
 #pragma unroll
-                    for (int i = 0; i < KS * 8 / 16; ++i) {      // 16 bytes of Q each
-                        const int ch = FP8 ? (c + 4 * (i >> 1)) * 2 + (i & 1) : c + 4 * i;
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (in) v = *reinterpret_cast<const uint4 *>(qp + ch * 16);
+                    for (int i = 0; i < KS / 2; ++i) {
+                        const uint4 &v = qw[MT == 1 ? hf : 0][i];
                         w[2 * i][0] = v.x;
                         w[2 * i][1] = v.y;
                         w[2 * i + 1][0] = v.z;
@@ -647,6 +660,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
     };
 
     // ---- the walk -------------------------------------------------------------
+    if (MT == 1) fetch_q(cu);
     begin_unit();
     // Byte offsets of this thread's fragments in a stage.
     uint32_t group[SUB], k_at[2], v_at[2];  // groups of 16 keys; K: even and odd load of a box; V: keys ka and kb2
@@ -900,10 +914,21 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         ++step;
         --left;
         const bool last_of_unit = cu.x + 1 == cu.kr.n || left == 0;
-        if (last_of_unit) end_unit();
+        if (!last_of_unit) {
+            ++cu.x;
+            continue;
+        }
+        // The next unit's Q is on its way while this one ends (more rows lack the registers).
+        Cursor next = cu;
+        if (left > 0) {
+            advance(next, true);
+            if (NR == 1) fetch_q(next);
+        }
+        end_unit();
         if (left == 0) break;
-        advance(cu, true);
-        if (last_of_unit) begin_unit();
+        cu = next;
+        if (MT == 1 && NR == 2) fetch_q(cu);
+        begin_unit();
     }
     join_units();
     grid_wait_before();
