@@ -70,7 +70,7 @@ struct DecodeCfg {
     static constexpr int kMl = kRed + kWarps * kPieces * 32 * 16;   // float [warps][2][kFewRows]
     static constexpr int kBar = kMl + kWarps * 2 * kFewRows * 4;    // mbarrier [2][stages]: loaded, read
     static constexpr int kMisc = kBar + 2 * kStages * 8;
-    static constexpr int kBytes = kMisc + 16;
+    static constexpr int kBytes = kMisc + 32;                       // int [8]: flags, abort, a split unit's first CTA and their number
     static_assert(kBytes <= 227 * 1024, "shared memory of the few-rows kernel");
     static_assert(kPagedCtas * ROWS * 4 <= kMl - kRed, "weights of a split unit's parts");
     static_assert(ROWS != 32 || kFewRows * (D * 2 + 4) <= kMl - kRed, "Q of 32 rows");
@@ -577,33 +577,33 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         const int4 e0 = __ldcg(reinterpret_cast<const int4 *>(&again->ent));       // r, tok0, n, ctx
         const int64_t cum0 = __ldcg(reinterpret_cast<const long long *>(&again->cum));
         const KeyRange kr0 = key_range(e0.w, e0.w + e0.z - 1, s.window, s.sink);
+        // The unit's CTAs, from the first one (tiles [ub, ub + n) of the list), beside the flags.
+        const int who = threadIdx.x == 0 ? 0 : threadIdx.x == 32 ? 1 : -1;
+        int from = 0, more = 0;
+        if (who >= 0) {
+            const int64_t ub = who == 0 ? cum0 + (int64_t)start.h * kr0.n : cu.cum + (int64_t)cu.h * cu.kr.n;
+            from = share_owner(W, ctas, ub);
+            more = share_owner(W, ctas, ub + (who == 0 ? kr0.n : cu.kr.n) - 1) - from;
+            flag[4 + who] = from;
+            flag[6 + who] = more + 1;
+        }
         __threadfence();
         named_bar_sync(kSumBar, kWarps * 32);
-        // CTAs of the unit, from the first one: tiles [ub, ub + n) of the list.
-        auto from_of = [&](int i) {
-            return share_owner(W, ctas, i == 0 ? cum0 + (int64_t)start.h * kr0.n : cu.cum + (int64_t)cu.h * cu.kr.n);
-        };
-        auto to_of = [&](int i) {
-            return share_owner(W, ctas, i == 0 ? cum0 + (int64_t)(start.h + 1) * kr0.n - 1 : cu.cum + (int64_t)(cu.h + 1) * cu.kr.n - 1);
-        };
-        if (threadIdx.x == 0 || threadIdx.x == 32) {
-            const int i = threadIdx.x == 0 ? 0 : 1;
+        if (who >= 0) {
             int mine = 0;
-            if (i == 0 ? first_cut : last_cut) {
-                const int from = from_of(i), more = to_of(i) - from;
+            if (who == 0 ? first_cut : last_cut) {
                 unsigned *cnt = reinterpret_cast<unsigned *>(a.plan + a.L.off_count) + from;
                 mine = atomicInc(cnt, (unsigned)more) == (unsigned)more ? 1 : 0;        // returns to 0 by itself
                 __threadfence();
             }
-            flag[2 * i] = mine;
+            flag[2 * who] = mine;
         }
         named_bar_sync(kSumBar, kWarps * 32);
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             if (!flag[2 * i]) continue;
             const PagedEntry en{0, i == 0 ? e0.y : cu.ent.tok0, i == 0 ? e0.z : cu.ent.n, 0};
-            const int h = i == 0 ? start.h : cu.h, nrows = en.n * G;
-            const int c_first = from_of(i), parts = to_of(i) - c_first + 1;
+            const int h = i == 0 ? start.h : cu.h, nrows = en.n * G, c_first = flag[4 + i], parts = flag[6 + i];
             float *wt = reinterpret_cast<float *>(red);             // [part][row] weights
             auto slot_of = [&](int p) { return (int64_t)(2 * (c_first + p) + (p == 0 ? 1 : 0)); };
             for (int row = warp; row < nrows; row += kWarps) {
