@@ -84,8 +84,11 @@ struct ChunkCfg {
     static constexpr int kMax = kOst + 8 * 2048;               // float [2][2][128]
     static constexpr int kSum = kMax + 2 * 2 * 128 * 4;        // float [2][2][128]
     static constexpr int kChain = kSum + 2 * 2 * 128 * 4;      // float [128]
-    static constexpr int kQf = kChain + 128 * 4;               // float [2][128]: 1 / factor of Q rows
-    static constexpr int kUnit = kQf + 2 * 128 * 4;            // int [kRing][kUnitInts]
+    // float [kRing][128]: 1 / factor of Q rows.  As long as the units' ring: the softmax may still
+    // be at the end of a short unit when Q of the one after the next is converted, but has
+    // released the entry that a new unit takes.
+    static constexpr int kQf = kChain + 128 * 4;
+    static constexpr int kUnit = kQf + kRing * 128 * 4;        // int [kRing][kUnitInts]
     static constexpr int kFlag = kUnit + kRing * kUnitInts * 4;   // int [2][8]
     static constexpr int kBar = kFlag + 16 * 4;
     static constexpr int kMisc = kBar + B_COUNT * 8;
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                     uint8_t *p = smem + C::kQ + at + (l & 1) * 8;
                     *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2 *>(p + C::kTerm) = make_uint2(lw[0], lw[1]);
-                    if (l == 0) sQf[(nq & 1) * 128 + row] = 1.f / f;
+                    if (l == 0) sQf[(nq % kRing) * 128 + row] = 1.f / f;
                 }
             }
             fence_proxy_async_smem();
@@ -632,7 +635,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                 float mx = -INFINITY;
                 if (live) {
                     tc_fence_after();
-                    if (FP8) sl2 = scale * sQf[(nu & 1) * 128 + row];
+                    if (FP8) sl2 = scale * sQf[(nu % kRing) * 128 + row];
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         tmem_ld32(tS + lane_off + c * 32, reinterpret_cast<uint32_t (&)[32]>(sv[c * 32]));

@@ -349,3 +349,18 @@ def test_many_units_of_every_length(fm):
     rng = np.random.default_rng(3)
     ctx, new = rng.integers(0, 300, 40).tolist(), rng.integers(0, 90, 40).tolist()
     Batch(fm, ctx, new, 8, 8, 64, 16, seed=7).check(torch.bfloat16, few=False)
+
+
+def test_short_units_of_scaled_rows_over_e4m3(fm):
+    """One or two tiles a unit, nine or so per CTA, every row of q at a power of two of its own."""
+    rng = np.random.default_rng(8)
+    b = Batch(fm, rng.integers(0, 150, 90).tolist(), rng.integers(9, 70, 90).tolist(), 32, 8, 128, 16, e4m3=True, seed=8)
+    f = torch.exp2(torch.randint(-12, 3, b.q.shape[:2], generator=torch.Generator().manual_seed(8)).double())[..., None]
+    b.q64 = b.q64 * f
+    b.q = (b.q.double() * f.cuda()).bfloat16()
+    for o_dtype in (torch.bfloat16, torch.float32):
+        first = b.run(o_dtype)
+        b.check(o_dtype, few=False)
+        for _ in range(3):
+            for x, y in zip(first, b.run(o_dtype)):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
