@@ -21,13 +21,17 @@
 // running maximum and sum of its own, so that they meet only when a unit ends.  (With
 // every warp loading its own 16 keys the loads' bookkeeping and the boxes' start, about
 // 130 cycles each, bounded it: 96 ragged requests of up to 16K tokens 0.320 ms, now
-// 0.289 to 0.297, 6.65 to 6.85 TB/s; per-thread copies before that 0.374.)  Fragment
+// 0.287, 6.88 TB/s; per-thread copies before that 0.374.)  Fragment
 // layouts: the head-dim order of the score product is free as long as Q and K agree, the
 // order of keys as long as P and V do, and the order of output columns altogether, so K
 // and V fragments are read with 16-byte shared loads in an order that meets no bank
 // conflict under TMA's swizzle, and V is transposed by byte permutes of two keys'
-// registers.  e4m3 caches halve the bytes but not the products and their latencies,
-// which then bound it: 64 requests of two tokens 0.136 to 0.145 ms (5.0 to 5.4 TB/s).
+// registers.  e4m3 caches halve the bytes but not the products: 64 requests of two tokens
+// 0.122 ms, 5.9 TB/s, where the loads alone take 0.117 and the products alone 0.123.  A
+// unit's end is what stands between the two (the ring of loads fills up meanwhile): it is
+// one exchange between the warps, with the next unit's Q on its way (0.138 before).
+// For 8 rows, Q K in e4m3 instructions (half the products) was no faster, for more rows
+// slower; so were twelve computing warps.
 //
 // P enters the second product as two 16-bit terms (hi + lo, about 16
 // significant bits), so that the rounding of a 16-bit output is the only one
@@ -486,7 +490,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
     // them: every warp leaves its maxima, sums and output in shared memory, eight pieces
     // of the output at a time, and then adds one piece up.  (5 us a unit when it took an
     // exchange more for the maxima, twice the passes, and a fence and an atomic for a split
-    // unit in the middle of the walk: 64 requests of two tokens over e4m3 0.138 ms.)
+    // unit in the middle of the walk: 64 requests of two tokens over e4m3 0.138 ms, 0.132 so.)
     constexpr int ZP = 4 * NR * (NR == 1 ? NP : 1);         // pieces of a pass
     static_assert(ZP <= C::kPieces && ZP <= kWarps, "pieces of a pass");
     auto end_unit = [&]() {
