@@ -385,7 +385,7 @@ FM_API fm_status fm_attn_fwd_fp8(const uint8_t *q8, const uint8_t *k8, const uin
  *
  * Sizes: d = 64 or 128; page_size a multiple of 16, 65536 at most; Hq / Hkv whole and at
  * most 32, Hq at most 4096; at most 8192 requests and 2^24 rows; max_pages * page_size
- * below 2^31 - 2^17; a sink needs a window.  Caches: page (p, h, t) of k begins at element p * k_page
+ * below 2^31 - 2^17; without a window a sink changes nothing.  Caches: page (p, h, t) of k begins at element p * k_page
  * + h * k_head + t * k_tok, its d elements contiguous; strides and pointers are
  * multiples of 16 bytes.  Values are code * descale for e4m3 (device float each,
  * positive; ignored for bf16).

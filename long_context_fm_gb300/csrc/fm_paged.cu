@@ -436,7 +436,7 @@ fm_status check_step(const fm_paged_step *p, PagedShape *out)
     if (p->requests <= 0 || p->max_tokens <= 0 || p->max_q <= 0 || p->max_pages <= 0 || p->num_pages <= 0 || p->page_size <= 0 ||
         p->Hq <= 0 || p->Hkv <= 0 || p->window < 0 || p->sink < 0)
         return FM_ERR_INVALID_ARG;
-    if (p->max_q > p->max_tokens || p->Hq % p->Hkv != 0 || (p->sink > 0 && p->window == 0)) return FM_ERR_INVALID_ARG;
+    if (p->max_q > p->max_tokens || p->Hq % p->Hkv != 0) return FM_ERR_INVALID_ARG;
     if (p->d != 64 && p->d != 128) return FM_ERR_UNSUPPORTED;
     if (p->requests > kMaxRequests || p->max_tokens > (1 << 24) || p->page_size % kPageGranule != 0 || p->page_size > kMaxPage ||
         p->Hq > 4096 || p->Hq / p->Hkv > kFewRows)
@@ -445,7 +445,7 @@ fm_status check_step(const fm_paged_step *p, PagedShape *out)
     if ((int64_t)p->max_pages * p->page_size > (int64_t)0x7fffffff - 2 * kMaxPage) return FM_ERR_UNSUPPORTED;
     if (p->window > (1 << 30) || p->sink > (1 << 30)) return FM_ERR_UNSUPPORTED;
     *out = PagedShape{p->requests, p->max_tokens, p->max_q, p->max_pages, p->num_pages, p->page_size, p->Hq, p->Hkv, p->d,
-                      p->window, p->sink};
+                      p->window, p->window > 0 ? p->sink : 0};     // (no window: every key is attended anyway)
     return FM_OK;
 }
 

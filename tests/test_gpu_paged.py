@@ -364,3 +364,11 @@ def test_short_units_of_scaled_rows_over_e4m3(fm):
         for _ in range(3):
             for x, y in zip(first, b.run(o_dtype)):
                 assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("new", [[1, 2, 0], [70, 1, 9]])
+def test_a_sink_without_a_window_changes_nothing(fm, new):
+    a, b = (Batch(fm, [300, 40, 5], new, 8, 2, 64, 16, sink=sink, seed=9) for sink in (0, 7))
+    for x, y in zip(a.run(torch.float32), b.run(torch.float32)):
+        assert torch.equal(x, y)
+    b.check(torch.float32, few=max(new) * 4 <= 32)

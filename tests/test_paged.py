@@ -24,7 +24,7 @@ def step_of(fm, **kw):
 
 BAD_STEPS = [
     (dict(requests=0), 1), (dict(max_tokens=0), 1), (dict(max_q=0), 1), (dict(max_q=65), 1), (dict(max_pages=0), 1),
-    (dict(num_pages=0), 1), (dict(page_size=0), 1), (dict(Hq=6), 1), (dict(Hkv=0), 1), (dict(window=-1), 1), (dict(sink=3), 1),
+    (dict(num_pages=0), 1), (dict(page_size=0), 1), (dict(Hq=6), 1), (dict(Hkv=0), 1), (dict(window=-1), 1), (dict(sink=-3), 1),
     (dict(d=96), 2), (dict(page_size=24), 2), (dict(Hq=132, Hkv=4), 2), (dict(requests=8193), 2),
     (dict(max_pages=1 << 26), 2), (dict(max_tokens=(1 << 24) + 1), 2), (dict(page_size=65552), 2), (dict(Hq=8192, Hkv=8192), 2),
 ]
@@ -36,6 +36,10 @@ def test_sizes_of_a_step_that_are_refused(fm, change, code):
     assert fm.fm_paged_plan_bytes(s) == 0
     got = fm._lib.fm_paged_plan(ctypes.byref(s), *[None] * 4, 0, *[None] * 7, 0, None, None)
     assert got == code
+
+
+def test_a_sink_without_a_window_is_a_step(fm):
+    assert fm.fm_paged_plan_bytes(step_of(fm, sink=3)) == fm.fm_paged_plan_bytes(step_of(fm)) > 0
 
 
 def test_plan_bytes(fm):
