@@ -142,7 +142,7 @@ struct Cursor {
 
 // Adds up the parts of the many-rows kernel's split units, in their order.  A warp
 // takes 32 rows (a lane each) and eight columns of a unit: the parts' loads of a
-// batch are all started before the first is used.
+// batch are all started before the first is used.  (Called by the computing warps.)
 template <int D>
 __device__ __forceinline__ void add_parts(const PagedArgs &a, const PagedHeader *hd, float vds)
 {
@@ -154,7 +154,7 @@ __device__ __forceinline__ void add_parts(const PagedArgs &a, const PagedHeader 
     const float4 *po = reinterpret_cast<const float4 *>(a.plan + a.L.off_many_o);
     const int G = s.Hq / s.Hkv, tpt = 128 / G, splits = hd->splits_many;
     const int items = hd->units_many * 4 * COLS;
-    for (int it = blockIdx.x * (blockDim.x >> 5) + warp_id(); it < items; it += gridDim.x * (blockDim.x >> 5)) {
+    for (int it = blockIdx.x * kWarps + warp_id(); it < items; it += gridDim.x * kWarps) {
         const int u = it / (4 * COLS), rest = it - u * (4 * COLS), row = rest / COLS * 32 + lane_id(), c8 = rest % COLS;
         int e = 0;
         while (e + 1 < hd->n_many && cum[e + 1] <= u) ++e;
@@ -935,7 +935,9 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         begin_unit();
     }
     join_units();
+    // The many-rows kernel may still run on other SMs (see the launch).
     grid_wait_before();
+    if (hd->splits_many > 1) add_parts<D>(a, hd, vds);
 }
 
 // 16-bit terms of P (see above).
@@ -960,13 +962,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         grid_wait_before();
         return;
     }
-    // The many-rows kernel may still run on other SMs (see the launch): its parts are
-    // added up after it, the few rows meanwhile; and no CTA ends before it has, so
-    // that whatever comes behind this kernel comes behind both.
-    if (hd->splits_many > 1) grid_wait_before();
-    if (hd->splits_many > 1) add_parts<D>(a, hd, FP8 ? *a.v_descale : 1.f);
+    // No CTA ends before the many-rows kernel, which may still run on other SMs (see the launch), so
+    // that whatever comes behind this kernel comes behind both; its parts are added up
+    // after the few rows.
     if ((int)blockIdx.x >= hd->ctas_few) {
         grid_wait_before();
+        if (hd->splits_many > 1 && warp_id() < kWarps) add_parts<D>(a, hd, FP8 ? *a.v_descale : 1.f);
         return;
     }
     // By the rows that the units of this CTA's share have at most (parts of a unit fit together
