@@ -372,3 +372,14 @@ def test_a_sink_without_a_window_changes_nothing(fm, new):
     for x, y in zip(a.run(torch.float32), b.run(torch.float32)):
         assert torch.equal(x, y)
     b.check(torch.float32, few=max(new) * 4 <= 32)
+
+
+def test_as_many_requests_as_there_may_be(fm):
+    b = Batch(fm, [r % 37 for r in range(8192)], [int(r % 3 > 0) for r in range(8192)], 2, 1, 64, 16, seed=10)
+    b.check(torch.bfloat16)
+
+
+def test_more_chunks_than_are_sorted(fm):
+    """The planner sorts up to 512 chunks by their keys; more keep the requests' order."""
+    b = Batch(fm, [r % 50 for r in range(700)], [9 + r % 7 if r % 8 else 1 for r in range(700)], 4, 1, 64, 16, seed=11)
+    b.check(torch.bfloat16, few=False)
