@@ -376,7 +376,8 @@ FM_API fm_status fm_attn_fwd_fp8(const uint8_t *q8, const uint8_t *k8, const uin
  *   Scores, maxima, sums and products are fp32 (fp32 accumulation).  P enters the
  *   second product with 24 bits (o fp32, at most 32 rows of new tokens times Hq / Hkv per
  *   request), 16 bits (otherwise where o is fp32 or the rows are as few) or 8 bits
- *   (bf16 o, more rows); over an e4m3 cache with 22 or 11 bits, and Q, where the
+ *   (bf16 o, more rows); over an e4m3 cache with 22 or 11 bits, but in steps of 2^-31 of the
+ *   row's largest weight at the finest (a weight is off by at most 2^-32 of the largest), and Q, where the
  *   rows are more, as two e4m3 terms (exact for elements of 2^-9 of the row's largest or
  *   more, off by at most 2^-17 of it for smaller ones).  o is rounded once.
  *   The plan holds the workspace as well: calls that share a plan (any number of layers

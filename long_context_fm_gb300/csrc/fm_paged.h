@@ -138,6 +138,13 @@ __device__ __forceinline__ float row_factor(float amax, int top)
     return __uint_as_float((uint32_t)(min(top - ex, 100) + 127) << 23);
 }
 
+// P beside e4m3 values enters its product as fp16, whose steps end at 2^-24: it is held
+// as 2^kLift exp2(s - m), so that with the lazy maximum's 2^8 it stays below fp16's
+// 65504 and a weight of 2^-32 of the row's largest still counts half a step (without
+// the lift 2^-25: a key 18 nats above 100,000 others lost them all, 0.15 % of the
+// output).  Sums are of the lifted P, and the maxima that belong to them are less kLift.
+constexpr float kLift = 7.f;
+
 // Natural log-sum-exp of a row from its maximum (base 2) and sum.
 __device__ __forceinline__ float row_lse(float mx, float sum)
 {

@@ -25,7 +25,7 @@
 // ones are off by at most 2^-17 of it.  V becomes fp16, exactly, because P needs
 // more bits than e4m3 has.
 // P: bf16 caches one bf16 term for 16-bit outputs, two (hi + lo) for fp32
-// outputs; e4m3 caches fp16 terms likewise.
+// outputs; e4m3 caches fp16 terms likewise, lifted by 2^kLift.
 //
 // The mask is arithmetic: a row at position p attends keys j <= p, j > p -
 // window or j < sink, so a tile is either free of it or compared element by
@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                           const __grid_constant__ CUtensorMap tv, const PagedArgs a, const int box_keys)
 {
     using C = ChunkCfg<D, FP8>;
-    constexpr float kLazy = FP8 ? 8.f : 32.f;     // fp16 P stays <= 2^8; bf16 P may grow to 2^32
+    constexpr float kLazy = FP8 ? 8.f : 32.f;     // fp16 P stays <= 2^(8 + kLift); bf16 P may grow to 2^32
+    constexpr float kUp = FP8 ? kLift : 0.f;
     constexpr int NBOX = D / 64;                  // 128-byte boxes of a 16-bit row
     constexpr int kKSt = C::kKSt, kVSt = C::kVSt;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -691,7 +692,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                     }
                 }
                 const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-                const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_use, -m_use);
+                const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(kUp - m_use, kUp - m_use);
                 uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
                 for (int hh = 0; hh < 4; ++hh) {
@@ -746,6 +747,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
                 const float l0 = sSum[(su * 2) * 128 + row], l1 = sSum[(su * 2 + 1) * 128 + row];
                 mf = fmaxf(m0, m1);
                 lt = (l0 != 0.f ? l0 * ex2(m0 - mf) : 0.f) + (l1 != 0.f ? l1 * ex2(m1 - mf) : 0.f);
+                mf -= kUp;
 #pragma unroll
                 for (int cc = 0; cc < OC / 32; ++cc)
                     tmem_ld32(tO + lane_off + w * OC + cc * 32, reinterpret_cast<uint32_t (&)[32]>(ov[cc * 32]));

@@ -37,8 +37,8 @@
 // significant bits), so that the rounding of a 16-bit output is the only one
 // that counts, and as three when the output is fp32.  With at most 8 rows the low
 // terms use the 8 idle rows of the 16-row operand, and are free.  e4m3 caches
-// take P as fp16 (11 bits a term; one term for 16-bit outputs of more rows): e4m3
-// values are exact in fp16, and so is Q after a power-of-two factor per row
+// take P as fp16 (11 bits a term; one term for 16-bit outputs of more rows), lifted by
+// 2^kLift: e4m3 values are exact in fp16, and so is Q after a power-of-two factor per row
 // that puts its largest element in [2^14, 2^15).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -51,7 +51,7 @@
 namespace fm {
 namespace {
 
-constexpr float kBand = 8.f;   // lazy rescale: P stays <= 2^8, sums are rescaled when a maximum grows by more
+constexpr float kBand = 8.f;   // lazy rescale: P stays <= 2^8 (2^(8 + kLift) over e4m3), sums are rescaled when a maximum grows by more
 
 constexpr int kWarps = 8;              // that compute; a warpgroup behind them has the one that loads
 constexpr int kThreads = (kWarps + 4) * 32;
@@ -233,6 +233,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
     constexpr int KS = D / 16;              // score product: k-steps
     constexpr int NT = D / 8;               // output product: 8-column tiles
     constexpr int NP = NT / 8;              // groups of 8 tiles
+    constexpr float kUp = FP8 ? kLift : 0.f;
     const int warp = warp_id(), lane = lane_id();
     const int g = lane >> 2, c = lane & 3;
     const int kg = key_of<NARROW>(g), ka = key_of<NARROW>(2 * c), kb2 = key_of<NARROW>(2 * c + 1);
@@ -335,7 +336,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
     uint32_t qf[MT == 1 ? KS : 1][4];       // one 16-row block: Q fragments in registers
     float qs[MT][NR];                       // score factor of rows g, g + 8 (softmax scale, log2 e, descale, Q's own factor)
     int pos[MT][NR];                        // position of rows g, g + 8 of each block
-    float m[MT][NR], l[MT][NR];
+    float m[MT][NR], l[MT][NR];             // maxima less kUp, sums
     float oa[MT][NT][4];
     uint8_t *sq = smem + C::kRed;           // two blocks: Q in shared memory between units
     const float kds = FP8 ? *a.k_descale : 1.f, vds = FP8 ? *a.v_descale : 1.f;
@@ -788,7 +789,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
             for (int b = 0; b < MT; ++b)
 #pragma unroll
                 for (int hf = 0; hf < NR; ++hf)
-                    raise = raise || row_max(b, hf) > m[b][hf] + kBand;
+                    raise = raise || row_max(b, hf) > m[b][hf] + (kBand + kUp);
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                 for (int b = 0; b < MT; ++b)
@@ -796,7 +797,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
                     for (int hf = 0; hf < NR; ++hf) {
                         float x = row_max(b, hf);
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)) - kUp;
                         if (x > m[b][hf]) {
                             const float f = ex2(m[b][hf] - x);
                             m[b][hf] = x;
