@@ -211,20 +211,24 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
     };
     const int nb = kKeyTile / box_keys;         // boxes of a tile; lane i looks up the page of box i
     // Number of the page that holds the lane's box of the unit's tile at kb, as the
-    // table has it; `none` when no row of the unit needs the page (it arrives as
-    // zeros).  The page as a whole decides: one that is partly attended is held.
-    const int none = -1 - s.num_pages;
-    auto look_up = [&](const Unit &u, int kb) -> int {
+    // table has it; not `need` when no row of the unit needs the page (it arrives as
+    // zeros; any number may stand in a table, so none of them can say that).  The page as a whole
+    // decides: one that is partly attended is held.
+    struct Page {
+        int at;
+        bool need;
+    };
+    auto look_up = [&](const Unit &u, int kb) -> Page {
         const int j = kb + lane * box_keys;
-        if (lane >= nb) return none;
         const int b = a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size, b0 = b * s.page_size;
-        if (j >= u.hi || (b0 + s.page_size <= u.lo && b0 >= s.sink)) return none;
-        return __ldg(a.table + (int64_t)u.r * s.max_pages + b);
+        if (lane >= nb || j >= u.hi || (b0 + s.page_size <= u.lo && b0 >= s.sink)) return Page{0, false};
+        return Page{__ldg(a.table + (int64_t)u.r * s.max_pages + b), true};
     };
     // Starts a tile's boxes, one per lane (all lanes call).
-    auto load_boxes = [&](const CUtensorMap *map, uint8_t *tile, uint64_t *bar, const Unit &u, int kb, int page) {
-        if (page < 0 || page >= s.num_pages) {
-            if (page != none) set_status(a.status, FM_ERR_PAGES);
+    auto load_boxes = [&](const CUtensorMap *map, uint8_t *tile, uint64_t *bar, const Unit &u, int kb, const Page &pg) {
+        int page = pg.at;
+        if (!pg.need || page < 0 || page >= s.num_pages) {
+            if (pg.need) set_status(a.status, FM_ERR_PAGES);
             page = s.num_pages;                 // outside the pool: zeros
         }
         const int in0 = a.page_shift >= 0 ? kb & (s.page_size - 1) : kb % s.page_size;
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
             const volatile int *p = sUnit + (k % kRing) * kUnitInts;
             const Unit u{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], p[10], p[11], p[12], p[13], p[14]};
             if (u.n < 0) break;
-            int page = look_up(u, key_base(u, 0));
+            Page page = look_up(u, key_base(u, 0));
             if (nq > 0 && !warp_wait(&bars[B_QE], (nq - 1) & 1, abort, a.status, lim)) break;
             if (lane == 0) {
                 uint64_t *qb = &bars[FP8 ? B_QR : B_Q];
@@ -320,7 +324,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
             ++nq;
             for (int t = 0; t < u.n; ++t, ++g) {
                 const int st = g % kKSt;
-                const int kb = key_base(u, t), pg = page;
+                const int kb = key_base(u, t);
+                const Page pg = page;
                 if (t + 1 < u.n) page = look_up(u, key_base(u, t + 1));
                 if (g >= kKSt && !warp_wait(&bars[B_KE + st], ((g / kKSt) - 1) & 1, abort, a.status, lim)) {
                     run = false;
@@ -349,10 +354,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
         Unit u;
         for (int k = 0; run; ++k) {
             if (!read_unit(k, u)) break;
-            int page = look_up(u, key_base(u, 0));
+            Page page = look_up(u, key_base(u, 0));
             for (int t = 0; t < u.n; ++t, ++g) {
                 const int st = g % kVSt;
-                const int kb = key_base(u, t), pg = page;
+                const int kb = key_base(u, t);
+                const Page pg = page;
                 if (t + 1 < u.n) page = look_up(u, key_base(u, t + 1));
                 if (g >= kVSt && !warp_wait(&bars[B_VE + st], ((g / kVSt) - 1) & 1, abort, a.status, lim)) {
                     run = false;

@@ -292,27 +292,31 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         const bool mine = bx < n_box;
         const CUtensorMap *map = part < 2 ? &tk : &tv;
         const uint32_t box_bytes = (uint32_t)box_keys * C::kRow;
-        const int none = -1 - s.num_pages;      // no page number of a box without attended keys
-        auto look_up = [&]() -> int {
+        // Page of the lane's box of the tile at the cursor; *need: some row attends one of its keys.
+        // (Any number may stand in a table, so none of them can mark a box that is not needed.)
+        auto look_up = [&](bool *need) -> int {
             const int j = cu.kr.tile(cu.x) * kKeyTile + bx * box_keys;
-            if (!mine || !some(j, box_keys)) return none;
+            *need = mine && some(j, box_keys);
+            if (!*need) return 0;
             return __ldg(a.table + (int64_t)cu.ent.r * s.max_pages + (a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size));
         };
-        int next = look_up(), t = 0;
+        bool next_need;
+        int next = look_up(&next_need), t = 0;
         for (; t < left; ++t) {
             const int st = t % ST;
             int page = next;
+            const bool need = next_need;
             const int j = cu.kr.tile(cu.x) * kKeyTile + bx * box_keys, h = cu.h;
             advance(cu, t + 1 < left);
-            if (t + 1 < left) next = look_up();
+            if (t + 1 < left) next = look_up(&next_need);
             if (t >= ST && !warp_wait(&empty[st], ((t / ST) - 1) & 1, abort, a.status)) break;
-            const unsigned used = __ballot_sync(0xffffffffu, page != none);
+            const unsigned used = __ballot_sync(0xffffffffu, need);
             if (lane == 0) {
                 if (used) mbar_arrive_expect_tx(&full[st], __popc(used) * box_bytes);
                 else mbar_arrive(&full[st]);
             }
             __syncwarp();
-            if (page != none) {
+            if (need) {
                 if (page < 0 || page >= s.num_pages) {
                     set_status(a.status, FM_ERR_PAGES);
                     page = s.num_pages;         // outside the pool: arrives as zeros
