@@ -7,7 +7,9 @@ builds the same sources with the FM_DEBUG definition (device-side checks that
 report FM_ERR_DEBUG_CHECK) into ``_lib/debug/libfm_debug.so``; the binding
 loads it when the FM_LIBRARY environment variable names it.  Beside the library
 stands ``_lib/_fm_call.so``, a CPython extension against the installed torch that
-marshals the paged calls (host code only, whichever library is loaded).
+marshals the paged calls (host code only, whichever library is loaded), with a tag of the
+torch and Python it fits.  The library does not need it: where it cannot be built
+(no torch, no headers) build() warns, and the binding goes its slower way through ctypes.
 """
 from __future__ import annotations
 
@@ -16,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -38,6 +41,24 @@ def _nvcc():
     return p
 
 
+def call_tag():
+    """The torch and Python that an extension built now would fit; empty without torch."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def call_fits():
+    """Whether the extension there was built against the installed torch and Python."""
+    try:
+        with open(CALL[:-2] + "tag") as f:
+            return os.path.exists(CALL) and f.read() == call_tag() != ""
+    except OSError:
+        return False
+
+
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "fm.h"),
                                                                  os.path.abspath(__file__)]
@@ -57,10 +78,36 @@ def _call_command(nvcc, out):
             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _build_call(nvcc):
+    """Compiles the extension and writes its tag."""
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = CALL + f".tmp{os.getpid()}"
+    r = subprocess.run(_call_command(nvcc, tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fm_call.cpp:\n{r.stdout}\n{r.stderr}")
+    with open(tmp + ".tag", "w") as f:
+        f.write(call_tag())
+    os.replace(tmp, CALL)
+    os.replace(tmp + ".tag", CALL[:-2] + "tag")
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    out_dir, lib = (DEBUG_DIR, DEBUG_LIB) if debug else (OUT_DIR, LIB)
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps() for f in (lib, CALL)):
-        return lib
+    lib = DEBUG_LIB if debug else LIB
+    fresh = lambda f: not force and os.path.exists(f) and os.path.getmtime(f) >= _deps()  # noqa: E731
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        call = None if fresh(CALL) and call_fits() else ex.submit(lambda: _build_call(_nvcc()))
+        if not fresh(lib):
+            _build_lib(lib, verbose, debug)
+        try:
+            if call is not None:
+                call.result()
+        except (ImportError, OSError, RuntimeError) as e:
+            warnings.warn(f"the paged calls go through ctypes, about 10 us more each: {e}", RuntimeWarning, stacklevel=2)
+    return lib
+
+
+def _build_lib(lib, verbose, debug):
+    out_dir = os.path.dirname(lib)
     os.makedirs(out_dir, exist_ok=True)
     nvcc = _nvcc()
     common = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -80,18 +127,8 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    def compile_call():
-        os.makedirs(OUT_DIR, exist_ok=True)
-        tmp = CALL + f".tmp{os.getpid()}"
-        r = subprocess.run(_call_command(nvcc, tmp), capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on fm_call.cpp:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, CALL)
-
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        call = ex.submit(compile_call)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        call.result()
     if verbose:
         for _, err in results:
             if err:
@@ -103,7 +140,6 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":

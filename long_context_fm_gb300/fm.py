@@ -10,9 +10,12 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import numpy as np
 import torch
+
+from . import build as _build
 
 # FM_LIBRARY selects another build of the same library (the FM_DEBUG build of
 # build.build(debug=True)); by default the in-tree release build.
@@ -21,13 +24,6 @@ if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with "
                       "`python -c 'import __graft_entry__ as g; g.build()'` (needs nvcc)")
 _lib = ctypes.CDLL(_LIB_PATH)
-# The paged calls' marshalling in C++ (csrc/fm_call.cpp), for the library loaded above.
-_CALL_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "_fm_call.so")
-if not os.path.exists(_CALL_PATH):
-    raise ImportError(f"{_CALL_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
-_spec = importlib.util.spec_from_loader("_fm_call", importlib.machinery.ExtensionFileLoader("_fm_call", _CALL_PATH))
-_call = importlib.util.module_from_spec(_spec)
-_spec.loader.exec_module(_call)
 
 FM_OK, FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_UNREPRESENTABLE = 0, 1, 2, 3
 FM_ERR_BAD_BOUNDS, FM_ERR_PLAN_MISMATCH, FM_ERR_WORKSPACE, FM_ERR_CUDA, FM_ERR_TIMEOUT = 4, 5, 6, 7, 8
@@ -143,7 +139,6 @@ _lib.fm_paged_append.argtypes = [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.
                                  ctypes.POINTER(PagedCache), _P, _P]
 _lib.fm_attn_paged.argtypes = [ctypes.POINTER(PagedStep), _P, ctypes.c_int64, ctypes.c_int64, _I,
                                ctypes.POINTER(PagedCache), _P, _P, _SZ, _F, _P, _I, _P, _P, _P]
-_call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.fm_paged_plan, _lib.fm_paged_append, _lib.fm_attn_paged)])
 _lib.fm_step_graph_create.argtypes = [ctypes.POINTER(StepArgs), ctypes.POINTER(ctypes.c_void_p)]
 _lib.fm_step_graph_launch.argtypes = [_P, _P]
 _lib.fm_step_graph_destroy.argtypes = [_P]
@@ -455,8 +450,30 @@ def fm_attn_fwd_fp8(q8, k8, vt8, descale, bounds: Bounds, plan, scale, o, lse, d
 # The paged calls are made once per layer and decoding step, where the host's time
 # counts.  What a program normally calls them with goes through _call; it answers
 # None to anything else, which these functions then check in full, and raise or run.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # (a torch without CUDA has neither)
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: -1)
+
+
+class _NoCall:
+    """In _call's place where the extension was not built, or against another torch: the functions here then do it all."""
+    plan = append = attend = staticmethod(lambda *args: None)
+
+
+def _load_call():
+    """The marshalling in C++ (csrc/fm_call.cpp), bound to the library loaded above."""
+    if not _build.call_fits():
+        return _NoCall
+    try:
+        spec = importlib.util.spec_from_loader("_fm_call", importlib.machinery.ExtensionFileLoader("_fm_call", _build.CALL))
+        call = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(call)
+    except ImportError:
+        return _NoCall
+    call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.fm_paged_plan, _lib.fm_paged_append, _lib.fm_attn_paged)])
+    return call
+
+
+_call = _load_call()
 
 
 def _on(t, name):
@@ -751,6 +768,9 @@ class PagedAttention:
         n = fm_paged_plan_bytes(self.step)
         if n == 0:
             raise ValueError("sizes of the step outside what fm.h allows")
+        if _call is _NoCall:
+            warnings.warn("the paged calls go through ctypes, about 10 us more each: _lib/_fm_call.so is missing or does not fit this torch "
+                          "(build it with `python -c 'import __graft_entry__ as g; g.build()'`)", RuntimeWarning, stacklevel=2)
         i32 = dict(dtype=torch.int32, device=device)
         self.plan_buffer = torch.empty(n, dtype=torch.uint8, device=device)
         self.cu_q = torch.empty(requests + 1, **i32)
