@@ -153,23 +153,11 @@ fm_status check_bounds(const fm_bounds &m, int B, int H, int N)
 }
 
 // ---- wait test hook --------------------------------------------------------------
-// One-shot, set only by fm_debug_wait_test: the next forward (kernel 0) or
-// backward main (kernel 1) launch runs with a short wait bound and its first
-// CTA withholds one tile load.
+// One-shot, set only by fm_debug_wait_test: the next launch of that kernel
+// (forward 0, backward main 1, paged kernels by their profiler ids) runs with a
+// short wait bound and its first CTA withholds one tile load.
 std::atomic<int> g_dbg_kernel{-1};
 std::atomic<long long> g_dbg_limit{0};
-
-void wait_test_args(int kernel, long long *limit, int *withhold)
-{
-    *limit = kWaitLimitCycles;
-    *withhold = 0;
-    int want = kernel;
-    if (g_dbg_kernel.load(std::memory_order_acquire) == kernel &&
-        g_dbg_kernel.compare_exchange_strong(want, -1, std::memory_order_acq_rel)) {
-        *limit = g_dbg_limit.load(std::memory_order_acquire);
-        *withhold = 1;
-    }
-}
 
 // ---- profiler ------------------------------------------------------------------
 struct ProfRec {
@@ -184,6 +172,18 @@ constexpr size_t kProfMax = 4096;
 }  // namespace
 
 namespace fm {
+void wait_test_args(int kernel, long long *limit, int *withhold)
+{
+    *limit = kWaitLimitCycles;
+    *withhold = 0;
+    int want = kernel;
+    if (g_dbg_kernel.load(std::memory_order_acquire) == kernel &&
+        g_dbg_kernel.compare_exchange_strong(want, -1, std::memory_order_acq_rel)) {
+        *limit = g_dbg_limit.load(std::memory_order_acquire);
+        *withhold = 1;
+    }
+}
+
 bool make_tmap_strided(CUtensorMap *map, const void *base, bool u8, int rank, const uint64_t *dims, const uint64_t *strides,
                        const uint32_t *box, int swizzle)
 {
@@ -585,9 +585,8 @@ int fm_profile_end(fm_kernel_time *out, int max_entries)
 
 fm_status fm_debug_wait_test(int kernel, long long limit_cycles)
 {
-    if ((kernel != 0 && kernel != 1 && kernel != -1) || (kernel >= 0 && (limit_cycles < 100000 ||
-                                                                        limit_cycles > kWaitLimitCycles)))
-        return FM_ERR_INVALID_ARG;
+    const bool known = kernel == 0 || kernel == 1 || kernel == FM_K_PAGED_DECODE || kernel == FM_K_PAGED_CHUNK;
+    if ((!known && kernel != -1) || (known && (limit_cycles < 100000 || limit_cycles > kWaitLimitCycles))) return FM_ERR_INVALID_ARG;
     g_dbg_limit.store(limit_cycles, std::memory_order_release);
     g_dbg_kernel.store(kernel, std::memory_order_release);
     return FM_OK;

@@ -214,6 +214,9 @@ namespace fm {
 // grid of the persistent attention kernels.
 int device_sm_count();
 
+// Wait bound of a launch, and whether it withholds a load (fm_debug_wait_test).
+void wait_test_args(int kernel, long long *limit, int *withhold);
+
 // Shape checks shared by every attention entry point: FM_ERR_INVALID_ARG for
 // non-positive or overflowing sizes, FM_ERR_UNSUPPORTED for a head dim other
 // than 64 / 128 or B, H beyond the launch grid.

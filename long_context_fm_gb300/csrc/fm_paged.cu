@@ -652,6 +652,7 @@ fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok,
         if (!make_tmap_strided(&tq, q, false, 3, qd, qs, qb, 128) || !make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, fp8 ? a.s.d : 128) ||
             !make_tmap_strided(&tv, cache->v, fp8, 4, cd, vs, cb, fp8 ? 0 : 128))
             return FM_ERR_CUDA;
+        wait_test_args(kKPagedChunk, &a.wait_limit, &a.withhold);
         if ((st = fm_paged_chunk_launch(tq, tk, tv, a, box_keys, fp8, (cudaStream_t)stream)) != FM_OK) return st;
     }
     // Rows of 128 bytes (bf16, d = 128: two of them, as a
@@ -665,6 +666,7 @@ fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t q_tok,
     const int swizzle = (int)(wide * esz);
     if (!make_tmap_strided(&tk, cache->k, fp8, 5, cd, ks, cb, swizzle) || !make_tmap_strided(&tv, cache->v, fp8, 5, cd, vs, cb, swizzle))
         return FM_ERR_CUDA;
+    wait_test_args(kKPagedDecode, &a.wait_limit, &a.withhold);
     return fm_paged_decode_launch(tk, tv, a, box_keys, fp8, (cudaStream_t)stream);
 }
 

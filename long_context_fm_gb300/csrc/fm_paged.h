@@ -168,6 +168,8 @@ struct PagedArgs {
     int o_f32;
     int rows;                       // rows that q, o and lse have
     int page_shift;                 // log2 of the page size, -1 if it is no power of two
+    long long wait_limit;           // cycles after which a wait gives up
+    int withhold;                   // wait test, 0 or 1: the first CTA leaves its second tile out (few rows), K's loads never end (many rows)
 };
 
 // Tensor map of bf16 or 8-bit data with any strides (bytes, of dimensions 1 and

@@ -300,6 +300,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
             if (!*need) return 0;
             return __ldg(a.table + (int64_t)cu.ent.r * s.max_pages + (a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size));
         };
+        const int withheld = a.withhold && blockIdx.x == 0 ? 1 : -1;      // test hook
         bool next_need;
         int next = look_up(&next_need), t = 0;
         for (; t < left; ++t) {
@@ -309,7 +310,8 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
             const int j = cu.kr.tile(cu.x) * kKeyTile + bx * box_keys, h = cu.h;
             advance(cu, t + 1 < left);
             if (t + 1 < left) next = look_up(&next_need);
-            if (t >= ST && !warp_wait(&empty[st], ((t / ST) - 1) & 1, abort, a.status)) break;
+            if (t >= ST && !warp_wait(&empty[st], ((t / ST) - 1) & 1, abort, a.status, a.wait_limit)) break;
+            if (t == withheld) continue;
             const unsigned used = __ballot_sync(0xffffffffu, need);
             if (lane == 0) {
                 if (used) mbar_arrive_expect_tx(&full[st], __popc(used) * box_bytes);
@@ -327,7 +329,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         }
         // After a wait that ran out: the copies end before the CTA leaves.
         if (*abort && lane == 0)
-            for (int i = max(t - ST, 0); i < t; ++i) mbar_wait_drain(&full[i % ST], (i / ST) & 1, a.status);
+            for (int i = max(t - ST, 0); i < t; ++i) mbar_wait_drain(&full[i % ST], (i / ST) & 1, a.status, a.wait_limit);
         grid_wait_before();
         return;
     }
@@ -690,7 +692,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
         const int kw = cu.kr.tile(cu.x) * kKeyTile + key0;
         // A wait that ran out has set the status: the walk goes on, so that every
         // barrier is reached, and what it writes does not count.
-        if (step % SUB == turn) warp_wait(&full[st], phase, abort, a.status);
+        if (step % SUB == turn) warp_wait(&full[st], phase, abort, a.status, a.wait_limit);
         if (step % SUB == turn && some(kw, 16 * SUB)) {
             const uint32_t base = smem_u32(smem) + st * C::kStage;
             const bool whole = kw + 16 * SUB <= cu.kr.hi && (kw >= cu.kr.lo || kw + 16 * SUB <= s.sink);

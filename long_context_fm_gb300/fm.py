@@ -342,7 +342,8 @@ def fm_bounds_decompress(cbounds, bounds: Bounds, dev_status, stream=None):
 
 
 def fm_debug_wait_test(kernel, limit_cycles):
-    """Test hook: the next forward (kernel=0) or backward (kernel=1) launch runs
+    """Test hook: the next forward (kernel=0), backward (kernel=1) or paged
+    attention launch (KERNEL_NAMES' index of "paged_decode" or "paged_chunk") runs
     with every device-side wait bounded by limit_cycles and its first CTA
     withholds one tile load, so it must end with FM_ERR_TIMEOUT in dev_status."""
     _check(_lib.fm_debug_wait_test(int(kernel), int(limit_cycles)), "fm_debug_wait_test")
