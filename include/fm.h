@@ -366,7 +366,9 @@ FM_API fm_status fm_attn_fwd_fp8(const uint8_t *q8, const uint8_t *k8, const uin
  * fm_attn_paged: q bf16 [rows, Hq, d] (strides of tokens and heads in elements, the
  *   last dimension contiguous), o [rows, Hq, d] and lse fp32 [rows, Hq] contiguous,
  *   with rows at least cu_q[requests] (else FM_ERR_LENGTHS in dev_status and nothing
- *   is written); rows at or behind cu_q[requests] are left as they were.  `step` has to be the plan's (else FM_ERR_PLAN_MISMATCH in dev_status),
+ *   is written); rows at or behind cu_q[requests] are left as they were, so that what a
+ *   fresh allocation held there (NaN too) is still there, as in all rows after a plan that
+ *   failed.  `step` has to be the plan's (else FM_ERR_PLAN_MISMATCH in dev_status),
  *   block_table the one it was built from.  Pages that no row of their request
  *   attends are not read, so their table entries may be stale (behind a window),
  *   and what a page holds behind the request's last token may be NaN.  The
@@ -376,19 +378,22 @@ FM_API fm_status fm_attn_fwd_fp8(const uint8_t *q8, const uint8_t *k8, const uin
  *   Scores, maxima, sums and products are fp32 (fp32 accumulation).  P enters the
  *   second product with 24 bits (o fp32, at most 32 rows of new tokens times Hq / Hkv per
  *   request), 16 bits (otherwise where o is fp32 or the rows are as few) or 8 bits
- *   (bf16 o, more rows); over an e4m3 cache with 22 or 11 bits, but in steps of 2^-31 of the
- *   row's largest weight at the finest (a weight is off by at most 2^-32 of the largest), and Q, where the
- *   rows are more, as two e4m3 terms (exact for elements of 2^-9 of the row's largest or
- *   more, off by at most 2^-17 of it for smaller ones).  o is rounded once.
- *   The plan holds the workspace as well: calls that share a plan (any number of layers
- *   per step) have to follow one another on the GPU, and so have replays of graphs
- *   that share one.  After a status other than 0, plan again.
+ *   (bf16 o, more rows); over an e4m3 cache with 22 (o fp32, or at most 8 rows) or 11 bits, but in
+ *   steps of 2^-31 of the row's largest weight at the finest (a weight is off by at most
+ *   2^-32 of the largest), and Q, where the rows are more, as two e4m3 terms (exact for
+ *   elements of 2^-9 of the row's largest or more, off by at most 2^-17 of it for smaller
+ *   ones).  o is rounded once.
+ *   The plan holds the workspace as well, whatever the number of requests: 5 MB (d = 128),
+ *   and 40 MB more where a request may have more than 32 rows (half of both for d = 64).
+ *   Calls that share a plan (any number of layers per step) have to follow one another on
+ *   the GPU, and so have replays of graphs that share one.  After a status other than 0,
+ *   plan again.
  *
  * Sizes: d = 64 or 128; page_size a multiple of 16, 65536 at most; Hq / Hkv whole and at
  * most 32, Hq at most 4096; at most 8192 requests and 2^24 rows; max_pages * page_size
- * below 2^31 - 2^17; without a window a sink changes nothing.  Caches: page (p, h, t) of k begins at element p * k_page
- * + h * k_head + t * k_tok, its d elements contiguous; strides and pointers are
- * multiples of 16 bytes.  Values are code * descale for e4m3 (device float each,
+ * below 2^31 - 2^17; without a window a sink changes nothing.  Caches: token (p, h, t) of k
+ * begins at element p * k_page + h * k_head + t * k_tok, its d elements contiguous; strides and
+ * pointers are multiples of 16 bytes.  Values are code * descale for e4m3 (device float each,
  * positive; ignored for bf16).
  */
 typedef struct {

@@ -347,8 +347,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) paged_plan_kernel(const PlanA
 
 // ---- append -----------------------------------------------------------------------
 // cache[slot] = x, one piece of 16 bytes of the cache of K and of V per thread: bound by
-// the bytes (13,000 tokens of 8 heads: bf16 9.1 us, e4m3 12.1; two or four pieces
-// in flight per thread: 9.1 to 10.4 and, then with plain divisions, 15.1 to 16.7 for 14.4).
+// the bytes (10,111 tokens of 8 heads: bf16 9.4 us on what L2 holds, 16.4 a call on what it does not;
+// 11,112 to e4m3 13.3 and 18.4; two or four pieces in flight per thread were slower, bf16 9.1 to 10.4 and,
+// then with plain divisions, e4m3 15.1 to 16.7 for 14.4).
 // e4m3: code = e4m3(x / descale), the quotient in fp32, nearest even, saturating:
 // the quantizer's rule.
 constexpr int kAppendThreads = 256;

@@ -25,7 +25,9 @@
 // ones are off by at most 2^-17 of it.  V becomes fp16, exactly, because P needs
 // more bits than e4m3 has.
 // P: bf16 caches one bf16 term for 16-bit outputs, two (hi + lo) for fp32
-// outputs; e4m3 caches fp16 terms likewise, lifted by 2^kLift.
+// outputs; e4m3 caches fp16 terms likewise, lifted by 2^kLift.  A second term doubles
+// the second product and the softmax's packing: 4,178 tokens over up to 16K keys 0.59 ms with one,
+// 1.03 with two, for 2.3e-3 of relative error in place of the bf16 output's own 1.7e-3.
 //
 // The mask is arithmetic: a row at position p attends keys j <= p, j > p -
 // window or j < sink, so a tile is either free of it or compared element by
@@ -518,8 +520,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, FP8>::kThreads, 1)
         for (int k = 0; run; ++k) {
             if (!read_unit(k, u)) break;
             if (!warp_wait(&bars[B_QR], nq & 1, abort, a.status, lim)) break;
-            // Four steps' rows at a time: their chains of loads, maxima and roundings overlap
-            // (one by one they took 7,000 cycles of a unit's start).
+            // Two steps' rows at a time: their chains of loads, maxima and roundings overlap.
             constexpr int QB = 2;
             for (int i0 = mate * QB; i0 < 128 / RPI; i0 += 4 * QB) {
                 uint4 x[QB];

@@ -26,8 +26,8 @@
 // order of keys as long as P and V do, and the order of output columns altogether, so K
 // and V fragments are read with 16-byte shared loads in an order that meets no bank
 // conflict under TMA's swizzle, and V is transposed by byte permutes of two keys'
-// registers.  e4m3 caches halve the bytes but not the products: 64 requests of two tokens
-// 0.122 ms, 5.9 TB/s, where the loads alone take 0.117 and the products alone 0.123.  A
+// registers.  e4m3 caches halve the bytes but not the products: 64 requests of one or two
+// tokens 0.123 ms, 5.9 TB/s, where the loads alone take 0.117 and the products alone 0.123.  A
 // unit's end is what stands between the two (the ring of loads fills up meanwhile): it is
 // one exchange between the warps, with the next unit's Q on its way (0.138 before).
 // For 8 rows, Q K in e4m3 instructions (half the products) was no faster, for more rows
@@ -497,7 +497,7 @@ __device__ __forceinline__ void walk_share(const CUtensorMap &tk, const CUtensor
     // them: every warp leaves its maxima, sums and output in shared memory, eight pieces
     // of the output at a time, and then adds one piece up.  (5 us a unit when it took an
     // exchange more for the maxima, twice the passes, and a fence and an atomic for a split
-    // unit in the middle of the walk: 64 requests of two tokens over e4m3 0.138 ms, 0.132 so.)
+    // unit in the middle of the walk: 64 requests of one or two tokens over e4m3 0.138 ms, 0.132 so.)
     constexpr int ZP = 4 * NR * (NR == 1 ? NP : 1);         // pieces of a pass
     static_assert(ZP <= C::kPieces && ZP <= kWarps, "pieces of a pass");
     auto end_unit = [&]() {
@@ -1034,8 +1034,8 @@ fm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &
 }
 
 // By the rows that a request of the step can have at most: a kernel with fewer ways in it is
-// faster where they are enough (8 rows alone 295 us, beside the others 301; 32 rows alone 252,
-// now 258).
+// faster where they are enough (when they were separated: 8 rows
+// alone 295 us, beside the others 301; 32 rows alone 252, beside the others 258; today 241).
 template <int D, bool FP8>
 fm_status launch_rows(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int box_keys, cudaStream_t stream)
 {

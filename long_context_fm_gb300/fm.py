@@ -761,7 +761,9 @@ class MaskedAttention:
 class PagedAttention:
     """A batch of requests over a paged cache: the step's sizes, plan, slot map and
     status word.  Per step one plan() (lengths and block table on the device), then
-    per layer an append() and an attend() with that layer's cache."""
+    per layer an append() and an attend() with that layer's cache.  The plan's buffer
+    takes 45 MB at d = 128 (23 at 64), 5 and 3 if no request can have more than
+    32 rows (max_q * Hq / Hkv)."""
 
     def __init__(self, requests, Hq, Hkv, d, page_size, num_pages, max_pages, max_tokens, max_q, window=0, sink=0,
                  device="cuda"):
@@ -793,6 +795,8 @@ class PagedAttention:
 
     def attend(self, q, k_cache, v_cache, block_table, scale=None, o_dtype=torch.bfloat16, k_descale=None,
                v_descale=None):
+        """(o, lse) of q's rows, newly allocated.  Rows at or behind cu_q[requests] (a padded
+        batch), and all of them after a plan that failed, hold what that memory held before."""
         scale = 1.0 / self.step.d ** 0.5 if scale is None else scale
         if o_dtype is torch.bfloat16 or o_dtype is torch.float32:
             r = _call.attend(ctypes.addressof(self.step), q, k_cache, v_cache, block_table, self.plan_buffer, scale,
