@@ -1,4 +1,4 @@
-"""Two plans of the same step at work at once, on two streams: chunks, split chunks and single tokens, each with the bits it has alone."""
+"""Two plans at work at once, on two streams: chunks, split chunks and single tokens, each with the bits it has alone."""
 import pytest
 import torch
 
@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_two_calls_at_once(e4m3):
     from long_context_fm_gb300 import fm
-    jobs = [base.Batch(fm, [3000, 40, 700, 9], new, 8, 2, 128, 32, e4m3=e4m3, seed=seed, q_max=100)
+    jobs = [base.Batch(fm, [3000, 40, 700, 9], new, 8, 2, 128, 32, e4m3=e4m3, seed=seed)
             for seed, new in ((1, [30, 1, 100, 2]), (2, [1, 60, 3, 0]))]
     alone = [[x.clone() for x in b.run(torch.float32, rows_behind=0)] for b in jobs]
     streams = [torch.cuda.Stream() for _ in jobs]
