@@ -60,7 +60,8 @@ typedef enum {
     FM_ERR_TIMEOUT = 8,          /* a bounded device-side wait ran out (kernel returned) */
     FM_ERR_DEBUG_CHECK = 9,      /* a device-side check of an FM_DEBUG build failed      */
     FM_ERR_LENGTHS = 10,         /* request lengths outside the sizes of the step        */
-    FM_ERR_PAGES = 11            /* too few free pages, or a page or slot out of range   */
+    FM_ERR_PAGES = 11,           /* too few free pages, or a page or slot out of range   */
+    FM_ERR_PROBS = 12            /* a drafted token or a row of probabilities that cannot be used */
 } fm_status;
 
 enum { FM_TILE_SKIP = 0, FM_TILE_FULL = 1, FM_TILE_PARTIAL = 2 };
@@ -424,6 +425,136 @@ FM_API fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t
                                float *lse, int32_t *dev_status, fm_stream_t stream);
 
 /*
+ * Rotary positions — DEVICE, async (fm_rotary_table: HOST).
+ * Element pairs (a, b) of a head turn by an angle that grows with the row's position p:
+ *     a' = m (a cos p theta_i - b sin p theta_i),   b' = m (b cos p theta_i + a sin p theta_i),
+ * so that the product of a query and a key depends on their distance.  The first `rot`
+ * elements of the head are turned, the others are copied; pair i is (x_i, x_(i + rot/2)), or
+ * (x_2i, x_(2i+1)) if `interleaved`.
+ *
+ * fm_rotary_table: the frequencies, as 64-bit fractions of a turn per position (so that an
+ *   angle is off by less than 2^-30 turns at any position below 2^24; int32 positions
+ *   all work), into host turns[rot / 2], and m.  theta_i = base^(-2 i / rot), and for contexts `factor` s >= 1 times
+ *   as long as those that the model was trained on:
+ *     FM_ROPE_LINEAR: theta_i / s;
+ *     FM_ROPE_NTK:    base s^(rot / (rot - 2)) in place of base (rot > 2);
+ *     FM_ROPE_YARN:   theta_i (g + (1 - g) / s), g = clamp((original theta_i / 2 pi - slow) /
+ *                     (fast - slow), 0, 1): pairs that turn more than `fast` times within the
+ *                     `original` positions are left, those that turn less than `slow` times are
+ *                     stretched; m = 0.1 ln s + 1.
+ *   m = 1 otherwise.  rot even, 2 to 128; base > 1; 0 <= slow < fast and original > 0 for YARN; all finite (else
+ *   FM_ERR_INVALID_ARG).
+ * fm_rope: y = the turned x.  x of x_dtype, y of y_dtype (bf16 or fp32): element (b, h, n, c) at b * batch +
+ *   h * head + n * tok + c (strides in elements, multiples of 16 bytes); positions int32, of row (b, n) at b *
+ *   pos_batch + n.  inverse != 0 turns back, with the same m: the gradient with respect
+ *   to x from the one with respect to y (the transposed map).  Rows whose position is
+ *   negative are left as they were in y.  y may be x (same strides and type), and may not
+ *   overlap it otherwise.  Sine and cosine are fp32, from an angle reduced in 64-bit
+ *   integers; products are fp32; y is rounded once.
+ * rotary: `turns` (device, 16-byte aligned) holds fm_rotary_table's values; rot a multiple of 8, at most
+ *   d (else FM_ERR_UNSUPPORTED); d = 64 or 128.
+ */
+enum { FM_ROPE_PLAIN = 0, FM_ROPE_LINEAR = 1, FM_ROPE_NTK = 2, FM_ROPE_YARN = 3 };
+typedef struct {
+    int32_t rot, scaling;
+    double base, factor, original, slow, fast;
+} fm_rotary_spec;
+typedef struct {
+    const uint64_t *turns;          /* device [rot / 2] */
+    int32_t rot, interleaved;
+    float magnitude;                /* m */
+} fm_rotary;
+typedef struct {
+    int64_t batch, head, tok;       /* strides, elements */
+} fm_strides;
+FM_API fm_status fm_rotary_table(const fm_rotary_spec *spec, uint64_t *turns, float *magnitude);
+FM_API fm_status fm_rope(const void *x, int x_dtype, fm_strides xs, const int32_t *positions, int64_t pos_batch,
+                         int B, int H, int N, int d, const fm_rotary *rotary, int inverse, void *y, int y_dtype,
+                         fm_strides ys, fm_stream_t stream);
+
+/*
+ * Long conversations over a paged cache — DEVICE, async: what a program does around
+ * fm_attn_paged once per layer (fm_paged_append_rope, fm_paged_weights, fm_paged_evict) or once
+ * per step (fm_verify_drafts, fm_paged_release).
+ *
+ * fm_paged_append_rope: fm_rope of a step's rows and fm_paged_append in one: q_out row t =
+ *   q row t turned by positions[t] (bf16 [T, Hq, d], strides of tokens and heads as q's own; q_out may be q);
+ *   k row t turned and v row t as it is go to the cache's slot slots[t].  K is rounded once, from the turned fp32
+ *   value (bf16, or e4m3 of value / descale).  Where positions[t] is negative nothing of row t
+ *   is written; a slot is treated as fm_paged_append treats it, and does not
+ *   concern q.  Positions are the caller's: after an eviction they run ahead of the
+ *   plan's, which count cached tokens.
+ * fm_paged_weights: the attention weight that every cached key of a step's requests receives,
+ *     weights[page, h, offset] (+)= sum over rows t and query heads g of KV head h that attend the key
+ *                                   of exp(scale q[t, g] . k - lse[t, g]),
+ *   fp32 [num_pages, Hkv, page_size], contiguous.  Keys that the step brought (position >= ctx_lens[r]) begin
+ *   from zero, the others are added to; keys that no row attends (behind a window) are left as they were.  Same step,
+ *   plan, q, cache (its k alone is read), block table and scale as fm_attn_paged, after it, with its lse; `rows` as there.
+ *   Scores and sums are fp32; beside an e4m3 cache the q of requests of at most 32 rows enters as two
+ *   e4m3 terms, as in fm_attn_paged.  A key's sum is added up in a fixed order, except that several
+ *   requests that hold one page add to it in any order.  A page number outside [0, num_pages) among the attended
+ *   gives FM_ERR_PAGES and its keys are left out.
+ * fm_paged_evict: cuts requests of more than `budget` cached tokens down to `budget` in one layer: per KV head the first
+ *   `sink` tokens stay, the last `recent` ones, and of those between the budget - sink - recent
+ *   with the largest weights (equal ones: the earlier; NaN counts as the largest), in their order, at
+ *   places 0 .. budget - 1 of the request: keys, values and weights are moved, in place.  Different heads may keep
+ *   different tokens.  lens: int32 [requests] cached tokens; new_lens[r] = min(lens[r], budget) (another array than
+ *   lens: every layer of the model reads the same lens); kept: int32 [requests, Hkv, budget], the
+ *   places kept, -1 for requests that are not cut.  What lies behind the new length is left as it is.
+ *   A request whose length is out of range (FM_ERR_LENGTHS) or that holds a page outside [0, num_pages) among those of its
+ *   tokens (FM_ERR_PAGES) is not cut, and new_lens[r] = lens[r].
+ *   Pages of a request that is cut may be held by no other request, and none twice.  weights as above; their page and
+ *   head sizes are the cache's.  1 <= budget, 0 <= sink, 0 <= recent, sink + recent <= budget.
+ * fm_paged_release: gives the pages behind the requests' new lengths back to the free list that fm_paged_plan
+ *   takes from: pages ceil(lens[r] / page_size) .. ceil(held[r] / page_size) - 1 of every request, in the order of
+ *   the requests and of their places, to free_pages[*free_head - n .. *free_head - 1], and *free_next = *free_head - n;
+ *   seq_lens[r] = lens[r].  0 <= lens[r] <= held[r]; lens[r] = 0 ends a request.  The table keeps the
+ *   entries (nothing reads behind a length).  seq_lens may be held or lens, and free_next may be
+ *   free_head.  Without a free list (free_pages NULL; free_head, free_next unused) only seq_lens is written.
+ *   Lengths out of range give FM_ERR_LENGTHS; a page outside [0, num_pages), or more pages than
+ *   were taken from the list (n > *free_head, or *free_head outside [0, n_free]), FM_ERR_PAGES: then nothing is given back and
+ *   seq_lens[r] = held[r], *free_next = *free_head.
+ *   Pages that several requests hold (a common prefix) would be given back several times: only
+ *   the last holder's call may include them.
+ * fm_verify_drafts: which of the drafted tokens of a step are kept, and the token behind them, so that
+ *   they are distributed as the target's own.  Rows of request r: [cu_q[r], cu_q[r + 1]) (the plan's cu_q); row i fed
+ *   tokens[i], whose first is the last known token and the others the drafted ones; target row
+ *   i: p = the target's probabilities of the token behind it; draft row i: q = those that token i + 1 was drawn
+ *   from, or draft NULL: it was taken with certainty (q is 1 there).  Draft t = tokens[i + 1] is kept if
+ *   u_accept[i] q(t) < p(t), up to the first that is not, at row a of the request (or its last row, all
+ *   kept); then the token is drawn that u_sample[r] in [0, 1) points at, the smallest x with
+ *       sum_(y <= x) w(y) > u_sample[r] sum w,   w = max(p - q, 0) of row a where a draft was refused and
+ *                                                that is not all zero, else w = max(p, 0).
+ *   Sums are held in about 48 bits.  out[row]: the kept drafts, the drawn token, -1 behind (int32 [rows]; rows of
+ *   no request are left as they were); n_out[r]: kept drafts + 1 (0 for a request without rows);
+ *   new_lens[r] = seq_lens[r] - rows of the request + n_out[r] (may be seq_lens): the tokens whose keys stay in the cache.
+ *   target, draft: [rows, V] of dtype (bf16 or fp32), row strides in elements, any alignment of a whole
+ *   element.  1 <= V <= 2^24.  A drafted token outside [0, V) is refused, with FM_ERR_PROBS; so is the draw where the
+ *   sum of w is zero, infinite or NaN: the token is then -1.  cu_q outside [0, rows] or
+ *   decreasing: FM_ERR_LENGTHS, and the request has no rows.
+ */
+FM_API fm_status fm_paged_append_rope(const void *q, int64_t q_tok, int64_t q_head, int Hq, const void *k, int64_t k_tok,
+                                      int64_t k_head, const void *v, int64_t v_tok, int64_t v_head, const int64_t *slots,
+                                      const int32_t *positions, int T, const fm_rotary *rotary,
+                                      const fm_paged_cache *cache, void *q_out, int64_t qo_tok, int64_t qo_head,
+                                      int32_t *dev_status, fm_stream_t stream);
+FM_API fm_status fm_paged_weights(const fm_paged_step *step, const void *q, int64_t q_tok, int64_t q_head, int rows,
+                                  const fm_paged_cache *cache, const int32_t *block_table, void *plan, size_t plan_bytes,
+                                  float scale, const float *lse, float *weights, int32_t *dev_status,
+                                  fm_stream_t stream);
+FM_API fm_status fm_paged_evict(const fm_paged_cache *cache, int requests, int max_pages, const int32_t *lens,
+                                const int32_t *block_table, float *weights, int budget, int recent, int sink,
+                                int32_t *kept, int32_t *new_lens, int32_t *dev_status, fm_stream_t stream);
+FM_API fm_status fm_paged_release(int requests, int max_pages, int num_pages, int page_size, const int32_t *held,
+                                  const int32_t *lens, const int32_t *block_table, int32_t *free_pages, int n_free,
+                                  const int32_t *free_head, int32_t *free_next, int32_t *seq_lens,
+                                  int32_t *dev_status, fm_stream_t stream);
+FM_API fm_status fm_verify_drafts(const void *target, int64_t target_row, const void *draft, int64_t draft_row, int dtype,
+                                  int V, int rows, const int32_t *tokens, const float *u_accept, const float *u_sample,
+                                  const int32_t *cu_q, const int32_t *seq_lens, int requests, int32_t *out,
+                                  int32_t *n_out, int32_t *new_lens, int32_t *dev_status, fm_stream_t stream);
+
+/*
  * Step graphs — create / destroy HOST, synchronous; launch DEVICE, async.
  * One step of the path (fm_tile_classify, fm_attn_fwd and, when dO is given,
  * fm_attn_bwd; 128 x 128 tiles) captured once into a CUDA graph for a fixed
@@ -473,7 +604,8 @@ FM_API fm_status fm_step_graph_destroy(fm_step_graph graph);
 enum { FM_K_CLASSIFY_MINMAX = 0, FM_K_CLASSIFY_LISTS = 1, FM_K_FWD = 2, FM_K_BWD_PRE = 3,
        FM_K_BWD = 4, FM_K_BWD_POST = 5, FM_K_CLASSIFY_ORDER = 6, FM_K_FP8_AMAX = 7,
        FM_K_FP8_CONVERT = 8, FM_K_PAGED_PLAN = 9, FM_K_PAGED_APPEND = 10, FM_K_PAGED_DECODE = 11,
-       FM_K_PAGED_CHUNK = 12, FM_K_COUNT = 13 };
+       FM_K_PAGED_CHUNK = 12, FM_K_ROPE = 13, FM_K_PAGED_APPEND_ROPE = 14, FM_K_PAGED_WEIGH_FEW = 15,
+       FM_K_PAGED_WEIGH_MANY = 16, FM_K_PAGED_EVICT = 17, FM_K_PAGED_RELEASE = 18, FM_K_VERIFY = 19, FM_K_COUNT = 20 };
 typedef struct {
     int32_t kernel;
     float ms;

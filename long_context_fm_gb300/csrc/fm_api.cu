@@ -284,6 +284,7 @@ const char *fm_status_string(fm_status st)
     case FM_ERR_DEBUG_CHECK: return "device-side check of a debug build failed";
     case FM_ERR_LENGTHS: return "request lengths outside the sizes of the step";
     case FM_ERR_PAGES: return "too few free pages, or a page or slot out of range";
+    case FM_ERR_PROBS: return "a drafted token or a row of probabilities that cannot be used";
     }
     return "unknown status";
 }

@@ -186,6 +186,13 @@ enum KernelId {
     kKPagedAppend = FM_K_PAGED_APPEND,
     kKPagedDecode = FM_K_PAGED_DECODE,
     kKPagedChunk = FM_K_PAGED_CHUNK,
+    kKRope = FM_K_ROPE,
+    kKPagedAppendRope = FM_K_PAGED_APPEND_ROPE,
+    kKPagedWeighFew = FM_K_PAGED_WEIGH_FEW,
+    kKPagedWeighMany = FM_K_PAGED_WEIGH_MANY,
+    kKPagedEvict = FM_K_PAGED_EVICT,
+    kKPagedRelease = FM_K_PAGED_RELEASE,
+    kKVerify = FM_K_VERIFY,
 };
 
 // Devices a process may use (per-device caches of kernel attributes).

@@ -91,19 +91,6 @@ __device__ __forceinline__ void block_scan(const PlanSums &mine, PlanSums *befor
     __syncthreads();
 }
 
-// Index of the last of n non-decreasing values that is <= x (a[0] = 0 <= x).
-template <class T>
-__device__ __forceinline__ int last_at_most(const T *a, int n, T x)
-{
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // Pieces per many-rows unit (called by a full warp): the number whose pieces are done
 // first, at a cost of `tiles` plus about eight tiles each (the pipeline's start, the
 // epilogue and the partial sums, measured): in one round when they fit on the
@@ -368,32 +355,6 @@ struct AppendArgs {
     int32_t *status;
 };
 
-// Correctly rounded quotients by one divisor, from its correctly rounded
-// reciprocal and one correction (Markstein, "Computation of elementary functions on the
-// IBM RISC System/6000 processor", 1990: q = x r, q + (x - q d) r): three instructions
-// each.  A divisor outside [2^-80, 2^80], where the remainder could underflow,
-// divides.
-struct Divisor {
-    float d, r;
-    bool plain;
-    __device__ __forceinline__ explicit Divisor(float x) : d(x), r(1.f / x), plain(!(x >= 8.271806e-25f && x <= 1.2089258e24f)) {}
-    __device__ __forceinline__ float operator()(float x) const
-    {
-        if (plain) return x / d;
-        const float q = x * r, c = fmaf(fmaf(-q, d, x), r, q);
-        return fabsf(q) == INFINITY ? q : copysignf(c, q);      // (the correction loses the sign of a zero)
-    }
-};
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, const Divisor &ds)
-{
-    return pack_e4m3x2(ds(__uint_as_float(w << 16)), ds(__uint_as_float(w & 0xffff0000u)));
-}
-__device__ __forceinline__ uint4 e4m3_piece(const uint4 &x, const uint4 &y, const Divisor &ds)
-{
-    return make_uint4(e4m3_pair(x.x, ds) | e4m3_pair(x.y, ds) << 16, e4m3_pair(x.z, ds) | e4m3_pair(x.w, ds) << 16,
-                      e4m3_pair(y.x, ds) | e4m3_pair(y.y, ds) << 16, e4m3_pair(y.z, ds) | e4m3_pair(y.w, ds) << 16);
-}
-
 template <bool FP8>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a)
 {
@@ -423,14 +384,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
 
 }  // namespace fm
 
-using namespace fm;
+namespace fm {
 
-namespace {
-
-bool aligned16(const void *p) { return p && ((uintptr_t)p & 15u) == 0; }
-bool aligned4(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
-
-// Sizes of a step; *out gets them in the library's own form.
 fm_status check_step(const fm_paged_step *p, PagedShape *out)
 {
     if (!p) return FM_ERR_INVALID_ARG;
@@ -450,7 +405,6 @@ fm_status check_step(const fm_paged_step *p, PagedShape *out)
     return FM_OK;
 }
 
-// Pages, strides and descales of a cache; alignment of 16 bytes everywhere.
 fm_status check_cache(const fm_paged_cache *c)
 {
     if (!c || !aligned16(c->k) || !aligned16(c->v)) return FM_ERR_INVALID_ARG;
@@ -468,7 +422,6 @@ fm_status check_cache(const fm_paged_cache *c)
     return FM_OK;
 }
 
-// Rows of bf16 read 16 bytes at a time: token and head strides in elements.
 bool rows_ok(const void *p, int64_t tok, int64_t head)
 {
     return aligned16(p) && tok > 0 && head > 0 && tok % 8 == 0 && head % 8 == 0 && tok <= ((int64_t)1 << 38) &&
@@ -495,7 +448,9 @@ fm_status device_ok()
     return k == 1 ? FM_OK : FM_ERR_UNSUPPORTED;
 }
 
-}  // namespace
+}  // namespace fm
+
+using namespace fm;
 
 extern "C" {
 

@@ -7,6 +7,9 @@
 #include <cmath>
 
 #include "fm_internal.h"
+#if defined(__CUDACC__)
+#include "fm_ptx.cuh"
+#endif
 
 namespace fm {
 
@@ -145,6 +148,45 @@ __device__ __forceinline__ float row_factor(float amax, int top)
 // output).  Sums are of the lifted P, and the maxima that belong to them are less kLift.
 constexpr float kLift = 7.f;
 
+// Index of the last of n non-decreasing values that is <= x (a[0] = 0 <= x).
+template <class T>
+__device__ __forceinline__ int last_at_most(const T *a, int n, T x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Correctly rounded quotients by one divisor, from its correctly rounded
+// reciprocal and one correction (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990: q = x r, q + (x - q d) r): three instructions
+// each.  A divisor outside [2^-80, 2^80], where the remainder could underflow,
+// divides.
+struct Divisor {
+    float d, r;
+    bool plain;
+    __device__ __forceinline__ explicit Divisor(float x) : d(x), r(1.f / x), plain(!(x >= 8.271806e-25f && x <= 1.2089258e24f)) {}
+    __device__ __forceinline__ float operator()(float x) const
+    {
+        if (plain) return x / d;
+        const float q = x * r, c = fmaf(fmaf(-q, d, x), r, q);
+        return fabsf(q) == INFINITY ? q : copysignf(c, q);      // (the correction loses the sign of a zero)
+    }
+};
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, const Divisor &ds)
+{
+    return pack_e4m3x2(ds(__uint_as_float(w << 16)), ds(__uint_as_float(w & 0xffff0000u)));
+}
+__device__ __forceinline__ uint4 e4m3_piece(const uint4 &x, const uint4 &y, const Divisor &ds)
+{
+    return make_uint4(e4m3_pair(x.x, ds) | e4m3_pair(x.y, ds) << 16, e4m3_pair(x.z, ds) | e4m3_pair(x.w, ds) << 16,
+                      e4m3_pair(y.x, ds) | e4m3_pair(y.y, ds) << 16, e4m3_pair(y.z, ds) | e4m3_pair(y.w, ds) << 16);
+}
+
 // Natural log-sum-exp of a row from its maximum (base 2) and sum.
 __device__ __forceinline__ float row_lse(float mx, float sum)
 {
@@ -171,6 +213,16 @@ struct PagedArgs {
     long long wait_limit;           // cycles after which a wait gives up
     int withhold;                   // wait test, 0 or 1: the first CTA leaves its second tile out (few rows), K's loads never end (many rows)
 };
+
+// Host checks of the paged calls (fm_paged.cu).  Sizes of a step, which *out gets in the library's own form;
+// pages, strides and descales of a cache, with alignment of 16 bytes everywhere; rows of bf16 read 16 bytes at a
+// time (token and head strides in elements); whether the current device is one the kernels are for.
+inline bool aligned16(const void *p) { return p && ((uintptr_t)p & 15u) == 0; }
+inline bool aligned4(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
+fm_status check_step(const fm_paged_step *p, PagedShape *out);
+fm_status check_cache(const fm_paged_cache *c);
+bool rows_ok(const void *p, int64_t tok, int64_t head);
+fm_status device_ok();
 
 // Tensor map of bf16 or 8-bit data with any strides (bytes, of dimensions 1 and
 // up), zero fill outside, swizzle of 128, 64 or 0 bytes (fm_api.cu).

@@ -27,13 +27,15 @@ _lib = ctypes.CDLL(_LIB_PATH)
 
 FM_OK, FM_ERR_INVALID_ARG, FM_ERR_UNSUPPORTED, FM_ERR_UNREPRESENTABLE = 0, 1, 2, 3
 FM_ERR_BAD_BOUNDS, FM_ERR_PLAN_MISMATCH, FM_ERR_WORKSPACE, FM_ERR_CUDA, FM_ERR_TIMEOUT = 4, 5, 6, 7, 8
-FM_ERR_DEBUG_CHECK, FM_ERR_LENGTHS, FM_ERR_PAGES = 9, 10, 11
+FM_ERR_DEBUG_CHECK, FM_ERR_LENGTHS, FM_ERR_PAGES, FM_ERR_PROBS = 9, 10, 11, 12
 FM_TILE_SKIP, FM_TILE_FULL, FM_TILE_PARTIAL = 0, 1, 2
 FM_DT_BF16, FM_DT_F32, FM_DT_E4M3 = 0, 1, 2
 FM_FLAG_PRECISE = 1
 KERNEL_NAMES = ["classify_minmax", "classify_lists", "fwd", "bwd_pre", "bwd", "bwd_post",
                 "classify_order", "fp8_amax", "fp8_convert", "paged_plan", "paged_append", "paged_decode",
-                "paged_chunk"]
+                "paged_chunk", "rope", "paged_append_rope", "paged_weigh_few", "paged_weigh_many", "paged_evict", "paged_release",
+                "verify"]
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 EXPORTED = ["fm_status_string", "fm_abi_version", "fm_mask_from_rows", "fm_mask_from_row_intervals",
             "fm_plan_bytes", "fm_tile_classify", "fm_fwd_workspace_bytes", "fm_attn_fwd", "fm_bwd_workspace_bytes",
@@ -42,7 +44,8 @@ EXPORTED = ["fm_status_string", "fm_abi_version", "fm_mask_from_rows", "fm_mask_
             "fm_plan_bytes_rows", "fm_tile_classify_rows", "fm_attn_fwd_rows", "fm_attn_bwd_rows",
             "fm_quantize_fp8", "fm_attn_fwd_fp8", "fm_debug_wait_test", "fm_bounds_compressed_bytes",
             "fm_bounds_compress", "fm_bounds_decompress", "fm_paged_plan_bytes", "fm_paged_plan", "fm_paged_append",
-            "fm_attn_paged"]
+            "fm_attn_paged", "fm_rotary_table", "fm_rope", "fm_paged_append_rope", "fm_paged_weights", "fm_paged_evict",
+            "fm_paged_release", "fm_verify_drafts"]
 # Size of the library's built-in backward workspace (FM_NOALLOC_SCRATCH_BYTES in fm.h).
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
@@ -92,6 +95,22 @@ class PagedCache(ctypes.Structure):
                 [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "Hkv", "d", "dtype")])
 
 
+class RotarySpec(ctypes.Structure):
+    """fm_rotary_spec of include/fm.h."""
+    _fields_ = [("rot", ctypes.c_int32), ("scaling", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "original", "slow", "fast")]
+
+
+class RotaryTable(ctypes.Structure):
+    """fm_rotary of include/fm.h."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+class Strides(ctypes.Structure):
+    """fm_strides of include/fm.h."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "head", "tok")]
+
+
 class KernelTime(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("ms", ctypes.c_float)]
 
@@ -139,6 +158,15 @@ _lib.fm_paged_append.argtypes = [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.
                                  ctypes.POINTER(PagedCache), _P, _P]
 _lib.fm_attn_paged.argtypes = [ctypes.POINTER(PagedStep), _P, ctypes.c_int64, ctypes.c_int64, _I,
                                ctypes.POINTER(PagedCache), _P, _P, _SZ, _F, _P, _I, _P, _P, _P]
+_L = ctypes.c_int64
+_lib.fm_rotary_table.argtypes = [ctypes.POINTER(RotarySpec), _P, _P]
+_lib.fm_rope.argtypes = [_P, _I, Strides, _P, _L, _I, _I, _I, _I, ctypes.POINTER(RotaryTable), _I, _P, _I, Strides, _P]
+_lib.fm_paged_append_rope.argtypes = [_P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _P, _P, _I, ctypes.POINTER(RotaryTable),
+                                      ctypes.POINTER(PagedCache), _P, _L, _L, _P, _P]
+_lib.fm_paged_weights.argtypes = [ctypes.POINTER(PagedStep), _P, _L, _L, _I, ctypes.POINTER(PagedCache), _P, _P, _SZ, _F, _P, _P, _P, _P]
+_lib.fm_paged_evict.argtypes = [ctypes.POINTER(PagedCache), _I, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]
+_lib.fm_paged_release.argtypes = [_I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P]
+_lib.fm_verify_drafts.argtypes = [_P, _L, _P, _L, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P]
 _lib.fm_step_graph_create.argtypes = [ctypes.POINTER(StepArgs), ctypes.POINTER(ctypes.c_void_p)]
 _lib.fm_step_graph_launch.argtypes = [_P, _P]
 _lib.fm_step_graph_destroy.argtypes = [_P]
@@ -649,6 +677,242 @@ def _attn_paged(step, q, k_cache, v_cache, block_table, plan, scale, o, lse, dev
         raise FmError(code, "fm_attn_paged")
 
 
+class Rotary:
+    """Rotary positions of a head's first `rot` dimensions (a multiple of 8): the frequency table on a
+    device.  interleaved: pairs are neighbours (2i, 2i + 1), else (i, i + rot / 2).  scaling: "none", or for
+    contexts `factor` times as long as the trained ones "linear", "ntk" or "yarn" (which goes by the `original`
+    trained length and leaves pairs that turn more than `fast` times within it); see fm.h.  magnitude:
+    factor on sine and cosine, by default what the scaling says."""
+
+    def __init__(self, rot, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=4096, slow=1.0, fast=32.0,
+                 magnitude=None, device="cuda"):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}")
+        if not 0 < rot <= 128 or rot % 8:
+            raise ValueError("rot must be a multiple of 8, 128 at most")
+        turns, m = fm_rotary_table(RotarySpec(rot, ROPE_SCALINGS[scaling], base, factor, original, slow, fast))
+        if magnitude is not None:
+            m = float(magnitude)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.table = RotaryTable(self.turns.data_ptr(), rot, int(bool(interleaved)), m)
+        self.rot, self.interleaved, self.magnitude = rot, bool(interleaved), m
+
+
+def fm_rotary_table(spec: RotarySpec):
+    """Frequencies (numpy uint64 [rot / 2], 2^-64 turns per position) and the factor on sine and cosine; host."""
+    turns = np.zeros(max(1, min(spec.rot, 128) // 2), np.uint64)
+    m = ctypes.c_float()
+    _check(_lib.fm_rotary_table(spec, turns.ctypes.data, ctypes.byref(m)), "fm_rotary_table")
+    return turns, m.value
+
+
+def _turning(rotary, dev):
+    if not isinstance(rotary, Rotary) or rotary.turns.get_device() != dev:
+        raise TypeError(f"rotary must be a Rotary on cuda:{dev}")
+    return rotary.table
+
+
+def _batch(t, dev, name, shape=None):
+    """[B, H, N, d], or rows [T, H, d] as one batch: (B, H, N, d, strides)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {list(shape)}, got {list(t.shape)}")
+    if t.dim() == 4:
+        (B, H, N, d), (sb, sh, st, se) = t.shape, t.stride()
+    elif t.dim() == 3:
+        (N, H, d), (st, sh, se) = t.shape, t.stride()
+        B, sb = 1, 0
+    else:
+        raise ValueError(f"{name} must be [B, H, N, d] or [T, H, d]")
+    if se != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # the stride of a dimension of size one is never used
+    return B, H, N, d, Strides(sb if B > 1 else 0, sh if H > 1 else 0, st if N > 1 else 0)
+
+
+def fm_rope(x, positions, rotary: Rotary, out=None, out_dtype=None, inverse=False, stream=None):
+    """x [B, H, N, d] (positions int32 [N] or [B, N]) or rows [T, H, d] (positions [T]) with every row turned by its
+    position; inverse turns back: the gradient of x from that of the result.  bf16 or fp32 in and out; out (which
+    may be x) is allocated if None, of out_dtype or x's type.  Rows with a negative position are not written."""
+    dev = _on(x, "x")
+    B, H, N, d, xs = _batch(x, dev, "x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    elif out_dtype is not None and out.dtype is not out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    *_, ys = _batch(out, dev, "out", x.shape)
+    table = _turning(rotary, dev)
+    if not isinstance(positions, torch.Tensor) or positions.shape not in ((N,), (B, N) if x.dim() == 4 else (N,)):
+        raise ValueError(f"positions must be int32 [{N}]" + (f" or [{B}, {N}]" if x.dim() == 4 else ""))
+    pos = _flat(positions, torch.int32, dev, "positions")
+    if x.numel() == 0:
+        return out
+    code = _lib.fm_rope(x.data_ptr(), _dt(x), xs, pos, N if positions.dim() == 2 else 0, B, H, N, d, table, int(bool(inverse)),
+                        out.data_ptr(), _dt(out), ys, _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_rope")
+    return out
+
+
+def fm_paged_append_rope(q, k, v, slots, positions, rotary: Rotary, k_cache, v_cache, dev_status, q_out=None, k_descale=None,
+                         v_descale=None, stream=None):
+    """q's rows (bf16 [T, Hq, d]) turned by their positions (int32 [T] at least), and k's, turned, and v's (bf16 [T, Hkv, d])
+    to the cache's slots (int64, T of them at least); returns the turned q (q_out, which may be q; allocated if
+    None).  Rows with a negative position are not written, of k and v neither those with a negative slot."""
+    cache = paged_cache(k_cache, v_cache, k_descale, v_descale)
+    dev = k_cache.get_device()
+    T, Hq, qt, qh = _rows(q, dev, "q", cache.d)
+    Tk, H, kt, kh = _rows(k, dev, "k", cache.d)
+    Tv, Hv, vt, vh = _rows(v, dev, "v", cache.d)
+    if not T == Tk == Tv or not H == Hv == cache.Hkv:
+        raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d] of the cache")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError(f"q_out must have the shape {list(q.shape)}, got {list(q_out.shape)}")
+    _, _, ot, oh = _rows(q_out, dev, "q_out", cache.d)
+    table = _turning(rotary, dev)
+    if slots.dim() != 1 or slots.shape[0] < T or positions.dim() != 1 or positions.shape[0] < T:
+        raise ValueError("slots (int64) and positions (int32) must have an entry for every row of q")
+    at, pos = _flat(slots, torch.int64, dev, "slots"), _flat(positions, torch.int32, dev, "positions")
+    status = _flat(dev_status, torch.int32, dev, "dev_status", (1,))
+    if T == 0:
+        return q_out
+    code = _lib.fm_paged_append_rope(q.data_ptr(), qt, qh, Hq, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, at, pos, T, table, cache,
+                                     q_out.data_ptr(), ot, oh, status, _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_paged_append_rope")
+    return q_out
+
+
+def _key_cache(k_cache, k_descale):
+    """fm_paged_cache for a call that reads keys alone."""
+    return paged_cache(k_cache, k_cache, k_descale, k_descale)
+
+
+def _weight_pool(weights, cache, dev):
+    return _flat(weights, torch.float32, dev, "weights", (cache.num_pages, cache.Hkv, cache.page_size))
+
+
+def fm_paged_weights(step: PagedStep, q, lse, k_cache, block_table, plan, scale, weights, dev_status, k_descale=None, stream=None):
+    """Adds the attention weight that each cached key received from the step's rows to weights (fp32 [num_pages, Hkv,
+    page_size]); q and lse (fp32 [rows, Hq]) as fm_attn_paged took and gave them, over the same plan."""
+    cache = _key_cache(k_cache, k_descale)
+    dev = k_cache.get_device()
+    T, H, qt, qh = _rows(q, dev, "q", step.d)
+    if H != step.Hq:
+        raise ValueError("q must be [rows, Hq, d] of the step")
+    z = _flat(lse, torch.float32, dev, "lse", (T, H))
+    pool = _weight_pool(weights, cache, dev)
+    table = _flat(block_table, torch.int32, dev, "block_table", (step.requests, step.max_pages))
+    buf, status = _flat(plan, torch.uint8, dev, "plan"), _flat(dev_status, torch.int32, dev, "dev_status", (1,))
+    if T == 0:
+        return
+    code = _lib.fm_paged_weights(step, q.data_ptr(), qt, qh, T, cache, table, buf, plan.numel(), scale, z, pool, status,
+                                 _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_paged_weights")
+
+
+def fm_paged_evict(lens, block_table, k_cache, v_cache, weights, budget, dev_status, recent=0, sink=0, kept=None, new_lens=None, stream=None):
+    """Cuts every request of more than `budget` cached tokens (lens: int32 [requests]) down to the first `sink`, the last
+    `recent` and, per KV head, the heaviest others, in one layer's caches and weights, in place.  Returns the new lengths
+    (new_lens, not lens itself); kept (int32 [requests, Hkv, budget], allocated if None) gets the places kept."""
+    cache = paged_cache(k_cache, v_cache, *([weights.view(-1)[:1]] * 2 if k_cache.dtype is not torch.bfloat16 else ()))
+    dev = k_cache.get_device()
+    R = lens.shape[0]
+    at = _flat(lens, torch.int32, dev, "lens", (R,))
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be int32 [requests, max_pages]")
+    table, pool = _flat(block_table, torch.int32, dev, "block_table"), _weight_pool(weights, cache, dev)
+    for name, x in (("budget", budget), ("recent", recent), ("sink", sink)):
+        if not -1 << 31 <= x < 1 << 31:
+            raise ValueError(f"{name} = {x} does not fit 32 bits")
+    if kept is None:
+        kept = torch.empty(R, cache.Hkv, max(budget, 0), dtype=torch.int32, device=lens.device)
+    if new_lens is None:
+        new_lens = torch.empty(R, dtype=torch.int32, device=lens.device)
+    places, after = _flat(kept, torch.int32, dev, "kept", (R, cache.Hkv, budget)), _flat(new_lens, torch.int32, dev, "new_lens", (R,))
+    code = _lib.fm_paged_evict(cache, R, block_table.shape[1], at, table, pool, budget, recent, sink, places, after,
+                               _flat(dev_status, torch.int32, dev, "dev_status", (1,)), _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_paged_evict")
+    return new_lens
+
+
+def fm_paged_release(held, lens, block_table, page_size, num_pages, free_pages, free_head, dev_status, free_next=None, seq_lens=None,
+                     stream=None):
+    """Gives the pages behind lens, of those that held tokens took (both int32 [requests]), back in front of the
+    free list's head.  Returns (seq_lens, free_next): the lengths now and the head now, allocated if None;
+    they may be held and free_head.  With free_pages None only seq_lens is written, and free_next is None."""
+    dev, i32 = _on(held, "held"), torch.int32
+    R = held.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be int32 [requests, max_pages]")
+    seq_lens = torch.empty_like(held) if seq_lens is None else seq_lens
+    free = head = after = None
+    n_free = 0
+    if free_pages is not None:
+        if free_head is None:
+            raise ValueError("free_pages comes with free_head")
+        free_next = torch.empty_like(free_head) if free_next is None else free_next
+        n_free = free_pages.numel()
+        if n_free >= 1 << 31:
+            raise ValueError("free_pages has 2^31 - 1 entries at most")
+        free = _flat(free_pages, i32, dev, "free_pages", (n_free,))
+        head = _flat(free_head, i32, dev, "free_head", (1,))
+        after = _flat(free_next, i32, dev, "free_next", (1,))
+        free = free or head         # an empty tensor has no address, but an empty list is not "no list"
+    else:
+        free_next = None
+    code = _lib.fm_paged_release(R, block_table.shape[1], num_pages, page_size, _flat(held, i32, dev, "held", (R,)),
+                                 _flat(lens, i32, dev, "lens", (R,)), _flat(block_table, i32, dev, "block_table"), free, n_free, head, after,
+                                 _flat(seq_lens, i32, dev, "seq_lens", (R,)), _flat(dev_status, i32, dev, "dev_status", (1,)),
+                                 _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_paged_release")
+    return seq_lens, free_next
+
+
+def _probs(t, dev, name):
+    """[rows, V] probabilities with any row stride: (rows, V, row stride)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise TypeError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, V], the last dimension contiguous")
+    return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def fm_verify_drafts(target, draft, tokens, u_accept, u_sample, cu_q, seq_lens, dev_status, out=None, n_out=None, new_lens=None, stream=None):
+    """Which drafted tokens of a step are kept, and the token drawn behind them: (out, n_out, new_lens).  target, draft
+    (None: the drafts were taken with certainty): probabilities [rows, V], bf16 or fp32; tokens: int32 [rows], what each row
+    fed; u_accept: fp32 [rows] and u_sample: fp32 [requests], uniform in [0, 1); cu_q, seq_lens: the plan's.  out: int32
+    [rows], per request the kept drafts, the drawn token, -1 behind; n_out: how many tokens; new_lens: the cached
+    tokens that stay (may be seq_lens).  All are allocated if None; rows of out that no request owns are not written."""
+    dev, i32 = _on(target, "target"), torch.int32
+    T, V, tr = _probs(target, dev, "target")
+    dr, dp = V, None
+    if draft is not None:
+        Td, Vd, dr = _probs(draft, dev, "draft")
+        if (Td, Vd) != (T, V) or draft.dtype is not target.dtype:
+            raise ValueError("draft must have target's shape and type")
+        dp = draft.data_ptr()
+    R = seq_lens.shape[0]
+    out = torch.empty(T, dtype=i32, device=target.device) if out is None else out
+    n_out = torch.empty(R, dtype=i32, device=target.device) if n_out is None else n_out
+    new_lens = torch.empty(R, dtype=i32, device=target.device) if new_lens is None else new_lens
+    args = (_flat(tokens, i32, dev, "tokens", (T,)), _flat(u_accept, torch.float32, dev, "u_accept", (T,)),
+            _flat(u_sample, torch.float32, dev, "u_sample", (R,)), _flat(cu_q, i32, dev, "cu_q", (R + 1,)),
+            _flat(seq_lens, i32, dev, "seq_lens", (R,)), R, _flat(out, i32, dev, "out", (T,)), _flat(n_out, i32, dev, "n_out", (R,)),
+            _flat(new_lens, i32, dev, "new_lens", (R,)), _flat(dev_status, i32, dev, "dev_status", (1,)))
+    code = _lib.fm_verify_drafts(target.data_ptr(), tr, dp, dr, _dt(target), V, T, *args,
+                                 _raw_stream(dev) if stream is None else _stream(stream))
+    if code:
+        raise FmError(code, "fm_verify_drafts")
+    return out, n_out, new_lens
+
+
 def fm_step_graph_create(q, k, v, dO, bounds: Bounds, plan, scale, o, lse, dev_status, dq=None, dk=None,
                          dv=None, ws=None, flags=0):
     """Capture classify + forward (+ backward when dO is given) for these
@@ -811,6 +1075,34 @@ class PagedAttention:
         _attn_paged(self.step, q, k_cache, v_cache, block_table, self.plan_buffer, scale, o, lse, self.status, k_descale,
                     v_descale, None)
         return o, lse
+
+    def append_rope(self, q, k, v, rotary, k_cache, v_cache, positions=None, q_out=None, k_descale=None, v_descale=None):
+        """append() with the rows of q and k turned by their positions (the plan's, unless others are given: those
+        of a request of which tokens were evicted run ahead); returns the turned q."""
+        return fm_paged_append_rope(q, k, v, self.slots, self.positions if positions is None else positions, rotary, k_cache, v_cache,
+                                    self.status, q_out, k_descale, v_descale)
+
+    def weigh(self, q, lse, k_cache, block_table, weights, scale=None, k_descale=None):
+        """Adds what the cached keys received in the attend() of q that gave lse to weights (fp32 [num_pages, Hkv, page_size])."""
+        scale = 1.0 / self.step.d ** 0.5 if scale is None else scale
+        fm_paged_weights(self.step, q, lse, k_cache, block_table, self.plan_buffer, scale, weights, self.status, k_descale)
+
+    def evict(self, lens, block_table, k_cache, v_cache, weights, budget, recent=0, sink=0, kept=None, new_lens=None):
+        """Cuts longer requests down to `budget` tokens in one layer; the new lengths, for release() once all layers are cut."""
+        return fm_paged_evict(lens, block_table, k_cache, v_cache, weights, budget, self.status, recent, sink, kept, new_lens)
+
+    def verify(self, target, draft, tokens, u_accept, u_sample, seq_lens=None, new_lens=None):
+        """(out, n_out, new_lens) of the step's drafted tokens.  seq_lens: the lengths with the drafts, the plan's own if
+        None (after a plan in place they are in the caller's array)."""
+        return fm_verify_drafts(target, draft, tokens, u_accept, u_sample, self.cu_q, self.seq_lens if seq_lens is None else seq_lens,
+                                self.status, new_lens=new_lens)
+
+    def release(self, held, lens, block_table, free_pages=None, free_head=None, in_place=False):
+        """Gives the pages behind lens back to the free list; with in_place held and free_head become what
+        they are now, else (seq_lens, free_next) are returned."""
+        s = self.step
+        return fm_paged_release(held, lens, block_table, s.page_size, s.num_pages, free_pages, free_head, self.status,
+                                free_head if in_place else None, held if in_place else None)
 
     def check_status(self):
         code = int(self.status.item())
