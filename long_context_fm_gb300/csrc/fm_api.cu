@@ -586,7 +586,8 @@ int fm_profile_end(fm_kernel_time *out, int max_entries)
 
 fm_status fm_debug_wait_test(int kernel, long long limit_cycles)
 {
-    const bool known = kernel == 0 || kernel == 1 || kernel == FM_K_PAGED_DECODE || kernel == FM_K_PAGED_CHUNK;
+    const bool known = kernel == 0 || kernel == 1 || kernel == FM_K_PAGED_DECODE || kernel == FM_K_PAGED_CHUNK ||
+                       kernel == FM_K_PAGED_WEIGH_FEW || kernel == FM_K_PAGED_WEIGH_MANY;
     if ((!known && kernel != -1) || (known && (limit_cycles < 100000 || limit_cycles > kWaitLimitCycles))) return FM_ERR_INVALID_ARG;
     g_dbg_limit.store(limit_cycles, std::memory_order_release);
     g_dbg_kernel.store(kernel, std::memory_order_release);

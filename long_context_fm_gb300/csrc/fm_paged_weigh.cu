@@ -1,9 +1,30 @@
 // Attention weight that the cached keys of a step's requests receive:
 //
-//   weights[key] (+)= sum over rows and query heads that attend the key of exp(scale q.k - lse)
+//   weights[key] (+)= sum over rows and query heads that attend the key of exp2(scale log2(e) q.k - log2(e) lse)
 //
-// The plain form: a block of 128 keys of a (request, KV head), thread = key, K as fp32 in shared memory, the rows that
-// attend them one after the other.  Bound by shared-memory reads (one per product).
+// The scores are computed with the keys as the rows of the product: S = K Q^T, so that a TMEM lane, and with it a thread,
+// holds one key and all its columns are summed in the thread: no exchange, no atomics among threads, one fixed
+// order.  Two kernels, as the attention has: requests of at most kFewRows rows (new tokens x query heads per KV
+// head), where K is read once and little is computed, and those with more, which are matrix work.
+//
+// Few rows: bound by HBM (K once).  Key tiles (128 keys) of all (request, KV head) units lie end to end and are cut into
+// equal shares, as the plan has them for the attention.  Rows are 16 or 32 columns of the product.
+//   warp 0      walks the share, looks pages up (a batch of tiles at a time), TMA of K (ring of 128 to 160 KB)
+//   warp 1      TMEM; one thread issues K Q^T
+//   warps 2-5   thread = key: exponentials, sum, one add or store to the key's weight
+//   warps 6-9   Q and lse of the next units to shared memory (e4m3 caches: Q as two e4m3 terms, so that K is used as it is)
+//
+// Many rows: a unit is one key tile of a (request, KV head), whose K stays in shared memory while the row tiles (128
+// rows: the query heads of the KV head times as many tokens as fit) that attend it stream through.  Per row tile 512
+// cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both about even, and in two
+// pipelines: four score buffers, two warpgroups on alternate row tiles.
+//   warp 0      claims units (longest first), TMA of K
+//   warp 1      TMEM; one thread issues K Q^T
+//   warps 2-5   even row tiles, thread = key;  warps 6-9  odd ones
+//   warp 10     TMA of Q
+//   warp 11     lse of the row tiles
+//   warps 12-15 e4m3 caches only: K to bf16, exactly, once per unit
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -15,90 +36,865 @@
 namespace fm {
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 struct WeighArgs {
     PagedArgs p;
-    const uint8_t *k;
-    int64_t k_page, k_head, k_tok;      // bytes
-    float *weights;
-    const float *lse;
+    float *weights;                 // [num_pages, Hkv, page_size]
+    const float *lse;               // [rows, Hq]
+    int box_keys;
+};
+
+// Place of key j of request r in the pool of weights (head 0), or -1 where no page of the pool holds it.
+__device__ __forceinline__ int64_t weight_place(const PagedArgs &a, int r, int j)
+{
+    const PagedShape &s = a.s;
+    const int b = a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size, in = j - b * s.page_size;
+    const int page = __ldg(a.table + (int64_t)r * s.max_pages + b);
+    return (unsigned)page < (unsigned)s.num_pages ? (int64_t)page * s.Hkv * s.page_size + in : -1;
+}
+
+// A key's sum to its weight: added, or the first one of a key that this step brought.
+__device__ __forceinline__ void put(float *at, float sum, bool fresh)
+{
+    if (fresh) *at = sum;
+    else red_add_f32(at, sum);
+}
+
+// ---- few rows ------------------------------------------------------------------------
+
+template <int D, bool FP8>
+struct FewCfg {
+    static constexpr int kThreads = 320;
+    static constexpr int kTile = 128 * D * (FP8 ? 1 : 2);
+    static constexpr int kSt = kTile == 32768 ? 5 : kTile == 16384 ? 8 : 16;    // 160 or 128 KB in flight
+    static constexpr int kSBuf = 4, kQSlots = 3, kRing = 8;
+    static constexpr int kQBox = kFewRows * 128;                  // 32 rows of 128 bytes
+    static constexpr int kQTerm = kFewRows * D;                   // e4m3: from the first term to the second
+    static constexpr int kQBytes = kFewRows * D * 2;
+    static constexpr int kQ = kSt * kTile;
+    static constexpr int kCol = kQ + kQSlots * kQBytes;           // float [kQSlots][2][32]: score factor and -log2(e) lse of the rows
+    static constexpr int kUnit = kCol + kQSlots * 2 * kFewRows * 4;   // int [kRing][8]
+    static constexpr int kBar = kUnit + kRing * 8 * 4;
+    enum { B_KF = 0, B_KE = B_KF + kSt, B_SF = B_KE + kSt, B_SE = B_SF + kSBuf, B_QF = B_SE + kSBuf, B_QE = B_QF + kQSlots,
+           B_UF = B_QE + kQSlots, B_UE = B_UF + kRing, B_DRAIN = B_UE + kRing, B_COUNT };
+    static constexpr int kMisc = kBar + B_COUNT * 8;
+    static constexpr int kBytes = kMisc + 64;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+// A stretch of a (request, KV head)'s tiles.
+struct FewUnit {
+    int n;                  // tiles; -1: no more
+    int r, h, tok0, ntok, ctx;
+    int x0;                 // its first tile in the request's range
 };
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(128) fm_paged_weigh_kernel(const WeighArgs w)
+__global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
+    fm_paged_weigh_few_kernel(const __grid_constant__ CUtensorMap tk, const WeighArgs w)
 {
-    extern __shared__ float sh[];       // [128][D + 1] keys, [D] a query
-    float *s_q = sh + 128 * (D + 1);
+    using C = FewCfg<D, FP8>;
+    constexpr int NBOX = FP8 ? 1 : D / 64;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *sCol = reinterpret_cast<float *>(smem + C::kCol);
+    volatile int *sUnit = reinterpret_cast<volatile int *>(smem + C::kUnit);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBar);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMisc);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
     const PagedArgs &a = w.p;
     const PagedShape &s = a.s;
     const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
-    if (!paged_plan_fits(hd, s) || hd->rows > a.rows) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, !paged_plan_fits(hd, s) ? FM_ERR_PLAN_MISMATCH : FM_ERR_LENGTHS);
+    const int warp = warp_id(), lane = lane_id();
+    if (!paged_plan_fits(hd, s) || hd->rows > a.rows || (smem_u32(smem) & 1023u) != 0) {
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            set_status(a.status, !paged_plan_fits(hd, s) ? FM_ERR_PLAN_MISMATCH : hd->rows > a.rows ? FM_ERR_LENGTHS : FM_ERR_UNSUPPORTED);
         return;
     }
-    const int G = s.Hq / s.Hkv, tid = threadIdx.x;
-    const float kd = FP8 ? *a.k_descale : 1.f;
-    int64_t base = 0;
-    for (int list = 0; list < 2; ++list) {
-        const PagedEntry *entries = reinterpret_cast<const PagedEntry *>(a.plan + (list ? a.L.off_many : a.L.off_few));
-        for (int e = 0; e < (list ? hd->n_many : hd->n_few); ++e) {
-            const PagedEntry en = entries[e];
-            const KeyRange kr = key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink);
-            const int64_t units = (int64_t)kr.n * s.Hkv;
-            for (int64_t u = (blockIdx.x + gridDim.x - base % gridDim.x) % gridDim.x; u < units; u += gridDim.x) {
-                const int h = (int)(u / kr.n), j = kr.tile((int)(u - (int64_t)h * kr.n)) * kKeyTile + tid;
-                const int b = j / s.page_size, in = j - b * s.page_size;
-                const bool any = j < en.ctx + en.n && (s.window == 0 || j > en.ctx - s.window || j < s.sink);
-                int page = any ? a.table[(int64_t)en.r * s.max_pages + b] : -1;
-                if (any && (unsigned)page >= (unsigned)s.num_pages) {
-                    set_status(a.status, FM_ERR_PAGES);
-                    page = -1;
-                }
-                __syncthreads();
-                if (page >= 0) {
-                    const uint8_t *row = w.k + page * w.k_page + h * w.k_head + in * w.k_tok;
-                    for (int c = 0; c < D; ++c) {
-                        float x, y;
-                        if (FP8) unpack_f16x2(f16x2_of_e4m3(row[c]), x, y);
-                        else x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(row)[c] << 16);
-                        sh[tid * (D + 1) + c] = x * kd;
-                    }
-                }
-                float sum = 0.f;
-                for (int i = 0; i < en.n * G; ++i) {
-                    const int t = i / G, hq = h * G + i % G;
-                    __syncthreads();
-                    for (int c = tid; c < D; c += 128)
-                        s_q[c] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(a.q + (en.tok0 + t) * a.q_tok + hq * a.q_head)[c] << 16);
-                    __syncthreads();
-                    const int p = en.ctx + t;
-                    if (page < 0 || j > p || !(s.window == 0 || j > p - s.window || j < s.sink)) continue;
-                    float x = 0.f;
-                    for (int c = 0; c < D; ++c) x += s_q[c] * sh[tid * (D + 1) + c];
-                    sum += exp2f(x * a.scale_log2 - w.lse[(int64_t)(en.tok0 + t) * s.Hq + hq] * 1.4426950408889634f);
-                }
-                if (page < 0) continue;
-                float *at = w.weights + ((int64_t)page * s.Hkv + h) * s.page_size + in;
-                if (j < en.ctx) red_add_f32(at, sum);
-                else *at = sum;
-            }
-            base += units;
+    if ((int)blockIdx.x >= hd->ctas_few) return;
+    if (warp == 0 && lane == 0) {
+        *abort = 0;
+        for (int i = 0; i < C::kSt; ++i) {
+            mbar_init(&bars[C::B_KF + i], 1);
+            mbar_init(&bars[C::B_KE + i], 1);
         }
+        for (int i = 0; i < C::kSBuf; ++i) {
+            mbar_init(&bars[C::B_SF + i], 1);
+            mbar_init(&bars[C::B_SE + i], 4);
+        }
+        for (int i = 0; i < C::kQSlots; ++i) {
+            mbar_init(&bars[C::B_QF + i], 4);
+            mbar_init(&bars[C::B_QE + i], 5);
+        }
+        for (int i = 0; i < C::kRing; ++i) {
+            mbar_init(&bars[C::B_UF + i], 1);
+            mbar_init(&bars[C::B_UE + i], 9);
+        }
+        mbar_init(&bars[C::B_DRAIN], 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, 128);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const int G = s.Hq / s.Hkv;
+    // a.wait_limit is for the thread that waits for K and for the drains; the other warps leave by the flag.
+    constexpr long long lim = kWaitLimitCycles;
+    auto read_unit = [&](int k) -> FewUnit {
+        const int slot = k % C::kRing;
+        FewUnit u{-1};
+        if (!warp_wait(&bars[C::B_UF + slot], (k / C::kRing) & 1, abort, a.status, lim)) return u;
+        const volatile int *p = sUnit + slot * 8;
+        u = FewUnit{p[0], p[1], p[2], p[3], p[4], p[5], p[6]};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::B_UE + slot]);
+        return u;
+    };
+    auto range_of = [&](int ctx, int n) { return key_range(ctx, ctx + n - 1, s.window, s.sink); };
+
+    if (warp == 0) {
+        // -------------------------------------------- the share's units; K
+        const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_few);
+        const PagedStart st0 = reinterpret_cast<const PagedStart *>(a.plan + a.L.off_start)[blockIdx.x];
+        int left = st0.count, e = st0.e, h = st0.h, x = st0.x;
+        PagedEntry en = st0.ent, en_next = list[min(e + 1, hd->n_few - 1)];
+        // Cuts the next unit off the share.
+        auto next_unit = [&]() -> FewUnit {
+            if (left <= 0) return FewUnit{-1};
+            const int n = min(left, range_of(en.ctx, en.n).n - x);
+            const FewUnit u{n, en.r, h, en.tok0, en.n, en.ctx, x};
+            left -= n;
+            x = 0;
+            if (++h == s.Hkv) {
+                h = 0;
+                ++e;
+                en = en_next;
+                en_next = list[min(e + 1, hd->n_few - 1)];
+            }
+            return u;
+        };
+        const int nb = kKeyTile / w.box_keys, batch = 32 / nb;     // boxes of a tile; tiles whose pages one look finds
+        const int my_tile = lane / nb, my_box = lane - my_tile * nb;
+        // Page and place in it of the lane's box of the unit's tile t0 + my_tile.
+        struct Box {
+            int page, in;
+        };
+        auto look_up = [&](const FewUnit &u, int t0) -> Box {
+            const int t = t0 + my_tile;
+            if (t >= u.n) return Box{s.num_pages, 0};
+            const KeyRange kr = range_of(u.ctx, u.ntok);
+            const int j = kr.tile(u.x0 + t) * kKeyTile + my_box * w.box_keys;
+            const int b = a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size, b0 = b * s.page_size;
+            Box box{s.num_pages, j - b0};               // a page that no row needs arrives as zeros
+            if (j < kr.hi && (b0 + s.page_size > kr.lo || b0 < s.sink)) {
+                const int page = __ldg(a.table + (int64_t)u.r * s.max_pages + b);
+                if ((unsigned)page < (unsigned)s.num_pages) box.page = page;
+                else set_status(a.status, FM_ERR_PAGES);
+            }
+            return box;
+        };
+        int g = 0;
+        bool run = true;
+        FewUnit u = next_unit();
+        Box box = look_up(u, 0);
+        for (int k = 0; run; ++k) {
+            const FewUnit un = next_unit();
+            const Box box_next = look_up(un, 0);
+            const int slot = k % C::kRing;
+            if (k >= C::kRing && !warp_wait(&bars[C::B_UE + slot], ((k / C::kRing) - 1) & 1, abort, a.status, lim)) break;
+            if (lane == 0) {
+                const int f[7] = {u.n, u.r, u.h, u.tok0, u.ntok, u.ctx, u.x0};
+#pragma unroll
+                for (int i = 0; i < 7; ++i) sUnit[slot * 8 + i] = f[i];
+                mbar_arrive(&bars[C::B_UF + slot]);
+            }
+            __syncwarp();
+            if (u.n < 0) break;
+            for (int t0 = 0; run && t0 < u.n; t0 += batch) {
+                const Box now = box;
+                if (t0 + batch < u.n) box = look_up(u, t0 + batch);
+                for (int t = t0; t < min(t0 + batch, u.n); ++t, ++g) {
+                    const int st = g % C::kSt;
+                    if (g >= C::kSt && !warp_wait(&bars[C::B_KE + st], ((g / C::kSt) - 1) & 1, abort, a.status, lim)) {
+                        run = false;
+                        break;
+                    }
+                    uint64_t *bar = &bars[C::B_KF + st];
+                    // Wait test: one byte more than comes.
+                    if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile + (a.withhold && blockIdx.x == 0 && g == 1 ? 1 : 0));
+                    __syncwarp();
+                    if (t - t0 == my_tile) {
+                        uint8_t *tile = smem + st * C::kTile;
+#pragma unroll
+                        for (int half = 0; half < NBOX; ++half)
+                            tma_load_4d(tile + half * (128 * 128) + my_box * w.box_keys * (FP8 ? D : 128), &tk, bar, half * 64, now.in, u.h, now.page);
+                    }
+                    __syncwarp();
+                }
+            }
+            u = un;
+            box = box_next;
+        }
+        // After an abort: copies in flight end before the CTA leaves.
+        if (lane == 0 && *abort)
+            for (int i = (g > C::kSt ? g - C::kSt : 0); i < g; ++i)
+                mbar_wait_drain(&bars[C::B_KF + i % C::kSt], (i / C::kSt) & 1, a.status, a.wait_limit);
+    } else if (warp == 1) {
+        // -------------------------------------------- K Q^T
+        auto desc = [&](uint8_t *p) {             // K-major rows of 128 bytes, or of 64 (e4m3, d = 64)
+            return FP8 && D == 64 ? sdesc_sw64(smem_u32(p), 16, 512) : sdesc_sw128(smem_u32(p), 16, 1024);
+        };
+        int g = 0;
+        bool run = true;
+        for (int k = 0; run; ++k) {
+            const FewUnit u = read_unit(k);
+            if (u.n < 0) break;
+            if (lane == 0) {
+                const int cols = u.ntok * G <= 16 ? 16 : 32, qs = k % C::kQSlots;
+                const uint32_t id = FP8 ? idesc_e4m3(128, cols) : idesc_bf16(128, cols, false, false);
+                run = mbar_wait(&bars[C::B_QF + qs], (k / C::kQSlots) & 1, abort, a.status, lim);
+                const uint64_t dQ = desc(smem + C::kQ + qs * C::kQBytes);
+                for (int t = 0; run && t < u.n; ++t, ++g) {
+                    const int st = g % C::kSt, sb = g % C::kSBuf;
+                    if (!mbar_wait(&bars[C::B_KF + st], (g / C::kSt) & 1, abort, a.status, a.wait_limit) ||
+                        (g >= C::kSBuf && !mbar_wait(&bars[C::B_SE + sb], ((g / C::kSBuf) - 1) & 1, abort, a.status, lim))) {
+                        run = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t dK = desc(smem + st * C::kTile);
+                    if (FP8) {
+#pragma unroll
+                        for (int term = 0; term < 2; ++term)
+#pragma unroll
+                            for (int kk = 0; kk < D / 32; ++kk)
+                                mma_ss_e4m3(tmem + sb * 32, sdesc_add(dK, kk * 32), sdesc_add(dQ, term * C::kQTerm + kk * 32), id, term + kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_ss(tmem + sb * 32, sdesc_add(dK, (kk >> 2) * (128 * 128) + (kk & 3) * 32),
+                                   sdesc_add(dQ, (kk >> 2) * C::kQBox + (kk & 3) * 32), id, kk > 0);
+                    }
+                    tc_commit(&bars[C::B_SF + sb]);
+                    tc_commit(&bars[C::B_KE + st]);
+                }
+                if (run) tc_commit(&bars[C::B_QE + qs]);
+            }
+            run = __shfl_sync(0xffffffffu, run, 0);
+        }
+        if (lane == 0) {
+            tc_commit(&bars[C::B_DRAIN]);
+            mbar_wait_drain(&bars[C::B_DRAIN], 0, a.status, a.wait_limit);
+        }
+    } else if (warp < 6) {
+        // -------------------------------------------- exponentials and sums
+        const int key = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        int g = 0;
+        bool run = true;
+        for (int k = 0; run; ++k) {
+            const FewUnit u = read_unit(k);
+            if (u.n < 0) break;
+            const int qs = k % C::kQSlots, rows = u.ntok * G;
+            if (!warp_wait(&bars[C::B_QF + qs], (k / C::kQSlots) & 1, abort, a.status, lim)) break;
+            const float *fac = sCol + qs * 2 * kFewRows, *off = fac + kFewRows;
+            const KeyRange kr = range_of(u.ctx, u.ntok);
+            for (int t = 0; t < u.n; ++t, ++g) {
+                const int sb = g % C::kSBuf;
+                const int j = kr.tile(u.x0 + t) * kKeyTile + key;
+                // Rows that attend the key: tokens at its place or behind it, within the window.
+                const int first = max(0, j - u.ctx), last = s.window > 0 && j >= s.sink ? min(u.ntok, j - u.ctx + s.window) : u.ntok;
+                const uint32_t mask = first < last ? row_bits32(first * G, last * G) : 0u;
+                const int64_t at = mask ? weight_place(a, u.r, j) : -1;      // on its way while the product is
+                if (!warp_wait(&bars[C::B_SF + sb], (g / C::kSBuf) & 1, abort, a.status, lim)) {
+                    run = false;
+                    break;
+                }
+                tc_fence_after();
+                float sum = 0.f;
+                auto add = [&](const uint32_t *v, int c0, int n) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        if (c >= n) break;
+                        const float p = ex2(fmaf(__uint_as_float(v[c]), FP8 ? fac[c0 + c] : a.scale_log2, off[c0 + c]));
+                        sum += mask >> (c0 + c) & 1 ? p : 0.f;
+                    }
+                };
+                const uint32_t tS = tmem + sb * 32 + lane_off;
+                if (rows <= 8) {
+                    uint32_t v[8];
+                    tmem_ld8(tS, v);
+                    tmem_ld_wait();
+                    tmem_reg_fence(v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
+                    add(v, 0, 8);
+                } else if (rows <= 16) {
+                    uint32_t v[16];
+                    tmem_ld16(tS, v);
+                    tmem_ld_wait();
+                    tmem_reg_fence(v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
+                    add(v, 0, 16);
+                } else {
+                    uint32_t v[32];
+                    tmem_ld32(tS, v);
+                    tmem_ld_wait();
+                    tmem_reg_fence(v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
+                    add(v, 0, 32);
+                }
+                if (at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum, j >= u.ctx);
+            }
+            __syncwarp();
+            if (run && lane == 0) mbar_arrive(&bars[C::B_QE + qs]);
+        }
+    } else {
+        // -------------------------------------------- Q and lse
+        constexpr int LPR = D / 8, RPI = 32 / LPR, STEPS = kFewRows / RPI / 4;      // lanes per row, rows per step of a warp, its steps
+        const int mate = warp - 6, l = lane % LPR, r_in = lane / LPR;
+        const float scale = a.scale_log2 * (FP8 ? *a.k_descale : 1.f);
+        for (int k = 0;; ++k) {
+            const FewUnit u = read_unit(k);
+            if (u.n < 0) break;
+            const int qs = k % C::kQSlots, rows = u.ntok * G;
+            uint4 x[STEPS];
+            float z[STEPS];
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const int row = (mate * STEPS + i) * RPI + r_in, t = row / G, hq = u.h * G + row - t * G;
+                x[i] = make_uint4(0, 0, 0, 0);
+                z[i] = 0.f;
+                if (row < rows) {
+                    x[i] = *reinterpret_cast<const uint4 *>(a.q + (int64_t)(u.tok0 + t) * a.q_tok + (int64_t)hq * a.q_head + l * 16);
+                    if (l == 0) z[i] = w.lse[(int64_t)(u.tok0 + t) * s.Hq + hq];
+                }
+            }
+            if (k >= C::kQSlots && !warp_wait(&bars[C::B_QE + qs], ((k / C::kQSlots) - 1) & 1, abort, a.status, lim)) break;
+            uint8_t *q = smem + C::kQ + qs * C::kQBytes;
+            float *fac = sCol + qs * 2 * kFewRows, *off = fac + kFewRows;
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+                const int row = (mate * STEPS + i) * RPI + r_in;
+                float f = 1.f;
+                if (FP8) {
+                    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    float amax = 0.f;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) amax = fmax3(amax, fabsf(__uint_as_float(v[y] << 16)), fabsf(__uint_as_float(v[y] & 0xffff0000u)));
+#pragma unroll
+                    for (int y = 1; y < LPR; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
+                    // An infinite element makes the row NaN (it would saturate).
+                    f = amax == INFINITY ? __uint_as_float(0x7fc00000u) : row_factor(amax, 7);
+                    uint32_t hi[2] = {0u, 0u}, lw[2] = {0u, 0u};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float q0 = __uint_as_float(v[y] << 16) * f, q1 = __uint_as_float(v[y] & 0xffff0000u) * f;
+                        const uint32_t h = pack_e4m3x2(q0, q1);
+                        float h0, h1;
+                        unpack_f16x2(f16x2_of_e4m3(h), h0, h1);
+                        hi[y >> 1] |= h << (16 * (y & 1));
+                        lw[y >> 1] |= pack_e4m3x2(q0 - h0, q1 - h1) << (16 * (y & 1));
+                    }
+                    const uint32_t at = D == 128 ? row * 128 + (((l >> 1) ^ (row & 7)) << 4) : row * 64 + (((l >> 1) ^ ((row >> 1) & 3)) << 4);
+                    uint8_t *p = q + at + (l & 1) * 8;
+                    *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(p + C::kQTerm) = make_uint2(lw[0], lw[1]);
+                } else {
+                    st_shared_v4(q + (l >> 3) * C::kQBox + row * 128 + (((l & 7) ^ (row & 7)) << 4), x[i]);
+                }
+                if (l == 0) {
+                    fac[row] = scale / f;
+                    off[row] = -z[i] * kLog2e;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[C::B_QF + qs]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
     }
 }
 
+// ---- many rows ------------------------------------------------------------------------
+
 template <int D, bool FP8>
-fm_status launch(const WeighArgs &w, cudaStream_t stream)
+struct ManyCfg {
+    static constexpr int kThreads = FP8 ? 512 : 384;
+    static constexpr int kBox = 128 * 128, kTile = 128 * D * 2, kRaw = 128 * D;
+    static constexpr int kQSt = FP8 ? 3 : 4, kSBuf = 4, kLSt = 4, kRing = 4;
+    static constexpr int kK = 0;                                  // two tiles of K
+    static constexpr int kQ = kK + 2 * kTile;
+    static constexpr int kRawK = kQ + kQSt * kTile;               // e4m3: two tiles as they come
+    static constexpr int kLse = kRawK + (FP8 ? 2 * kRaw : 0);     // float [kLSt][128]
+    static constexpr int kSum = kLse + kLSt * 128 * 4;            // float [2][128]
+    static constexpr int kUnit = kSum + 2 * 128 * 4;              // int [kRing][8]
+    static constexpr int kFlag = kUnit + kRing * 8 * 4;           // int [2][8]
+    static constexpr int kBar = kFlag + 16 * 4;
+    enum { B_KF = 0, B_KE = B_KF + 2, B_RF = B_KE + 2, B_RE = B_RF + 2, B_QF = B_RE + 2, B_QE = B_QF + kQSt, B_SF = B_QE + kQSt,
+           B_SE = B_SF + kSBuf, B_LF = B_SE + kSBuf, B_LE = B_LF + kLSt, B_UF = B_LE + kLSt, B_UE = B_UF + kRing,
+           B_DRAIN = B_UE + kRing, B_COUNT };
+    static constexpr int kMisc = kBar + B_COUNT * 8;
+    // Over 114 KB, so that one CTA with all of TMEM is resident per SM.
+    static constexpr int kBytes = kMisc + 64 > 120 * 1024 ? kMisc + 64 : 120 * 1024;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    static constexpr int kReaders = 11 + (FP8 ? 4 : 0);
+};
+
+// A key tile and the row tiles that attend it.
+struct ManyUnit {
+    int n;                  // row tiles; -1: no more
+    int r, h, tok0, ntok, ctx;
+    int kb, t0;             // first key, first row tile
+};
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
+    fm_paged_weigh_many_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const WeighArgs w)
 {
-    constexpr int kBytes = (128 * (D + 1) + D) * 4;
-    static std::atomic<uint8_t> done[kMaxDevices];
+    using C = ManyCfg<D, FP8>;
+    constexpr int NBOX = D / 64;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *sLse = reinterpret_cast<float *>(smem + C::kLse);
+    float *sSum = reinterpret_cast<float *>(smem + C::kSum);
+    volatile int *sUnit = reinterpret_cast<volatile int *>(smem + C::kUnit);
+    volatile int *sFlag = reinterpret_cast<volatile int *>(smem + C::kFlag);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBar);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMisc);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
+    const PagedArgs &a = w.p;
+    const PagedShape &s = a.s;
+    const PagedHeader *hd = reinterpret_cast<const PagedHeader *>(a.plan);
+    const int warp = warp_id(), lane = lane_id();
+    // The same verdict in every CTA: none claims a unit of a plan that does not fit.
+    if (!paged_plan_fits(hd, s) || hd->rows > a.rows || (smem_u32(smem) & 1023u) != 0) {
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            set_status(a.status, !paged_plan_fits(hd, s) ? FM_ERR_PLAN_MISMATCH : hd->rows > a.rows ? FM_ERR_LENGTHS : FM_ERR_UNSUPPORTED);
+        return;
+    }
+    if (hd->n_many == 0) return;
+    const int G = s.Hq / s.Hkv, tpt = 128 / G;      // tokens of a row tile
+    if (warp == 0 && lane == 0) {
+        *abort = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[C::B_KF + i], FP8 ? 4 : 1);
+            mbar_init(&bars[C::B_KE + i], 1);
+            mbar_init(&bars[C::B_RF + i], 1);
+            mbar_init(&bars[C::B_RE + i], 4);
+        }
+        for (int i = 0; i < C::kQSt; ++i) {
+            mbar_init(&bars[C::B_QF + i], 1);
+            mbar_init(&bars[C::B_QE + i], 1);
+        }
+        for (int i = 0; i < C::kSBuf; ++i) {
+            mbar_init(&bars[C::B_SF + i], 1);
+            mbar_init(&bars[C::B_SE + i], 4);
+        }
+        for (int i = 0; i < C::kLSt; ++i) {
+            mbar_init(&bars[C::B_LF + i], 1);
+            mbar_init(&bars[C::B_LE + i], 4);
+        }
+        for (int i = 0; i < C::kRing; ++i) {
+            mbar_init(&bars[C::B_UF + i], 1);
+            mbar_init(&bars[C::B_UE + i], C::kReaders);
+        }
+        mbar_init(&bars[C::B_DRAIN], 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    // Rows of a row tile that no token fills (128 is no multiple of G) are zeros for good: TMA writes the others alone.
+    const int filled = G * tpt;
+    for (int i = threadIdx.x; i < C::kQSt * NBOX * (128 - filled) * 8; i += C::kThreads) {
+        const int ch = i & 7, row = (i >> 3) % (128 - filled), box = (i >> 3) / (128 - filled);
+        st_shared_v4(smem + C::kQ + box * C::kBox + (filled + row) * 128 + ch * 16, make_uint4(0, 0, 0, 0));
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    constexpr long long lim = kWaitLimitCycles;
+    auto read_unit = [&](int k) -> ManyUnit {
+        const int slot = k % C::kRing;
+        ManyUnit u{-1};
+        if (!warp_wait(&bars[C::B_UF + slot], (k / C::kRing) & 1, abort, a.status, lim)) return u;
+        const volatile int *p = sUnit + slot * 8;
+        u = ManyUnit{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C::B_UE + slot]);
+        return u;
+    };
+
+    if (warp == 0) {
+        // -------------------------------------------- claims; K
+        const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_many);
+        unsigned *claim = reinterpret_cast<unsigned *>(a.plan + a.L.off_claim);
+        auto units_of = [&](const PagedEntry &en) { return (int64_t)key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink).n * s.Hkv; };
+        int64_t total = 0;
+        for (int i = lane; i < hd->n_many; i += 32) total += units_of(list[i]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const bool fits = total < (int64_t)1 << 31;
+        if (!fits && blockIdx.x == 0 && lane == 0) set_status(a.status, FM_ERR_LENGTHS);
+        const unsigned n_claims = fits ? (unsigned)total : 0u;
+        int e = 0;
+        int64_t cum = 0;            // units before entry e
+        PagedEntry en = list[0];
+        const int nb = kKeyTile / w.box_keys;
+        bool run = true;
+        int k = 0;
+        for (;; ++k) {
+            ManyUnit u{-1};
+            while (n_claims > 0) {
+                unsigned c = 0;
+                // Every CTA claims once past the end: the counter comes back to 0 by itself.
+                if (lane == 0) c = atomicInc(claim, n_claims + gridDim.x - 1);
+                c = __shfl_sync(0xffffffffu, c, 0);
+                if (c >= n_claims) break;
+                // Claims only grow, so the entry is at or behind the last one.
+                while ((int64_t)c >= cum + units_of(en)) {
+                    const int i = e + lane;
+                    const int64_t mine = i < hd->n_many ? units_of(list[i]) : 0;
+                    int64_t upto = mine;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                        if (lane >= o) upto += y;
+                    }
+                    const int past = __popc(__ballot_sync(0xffffffffu, cum + upto <= (int64_t)c));     // entries that end before the claim
+                    const int64_t gone = __shfl_sync(0xffffffffu, upto, max(past - 1, 0));
+                    if (past > 0) cum += gone;
+                    e += past;
+                    en = list[min(e, hd->n_many - 1)];
+                }
+                const int local = (int)((int64_t)c - cum), x = local / s.Hkv;
+                const KeyRange kr = key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink);
+                u = ManyUnit{0, en.r, local - x * s.Hkv, en.tok0, en.n, en.ctx, kr.tile(x) * kKeyTile, 0};
+                u.t0 = max(0, u.kb - en.ctx) / tpt;
+                int t1 = (en.n + tpt - 1) / tpt;
+                if (s.window > 0 && u.kb >= s.sink) t1 = min(t1, max(u.kb - en.ctx + kKeyTile - 2 + s.window + tpt, 0) / tpt);
+                u.n = t1 - u.t0;
+                if (u.n > 0) break;
+                u.n = -1;
+            }
+            // The tile's pages, looked up before the waits.
+            int page = s.num_pages, in = 0;
+            if (u.n > 0 && lane < nb) {
+                const KeyRange kr = key_range(u.ctx, u.ctx + u.ntok - 1, s.window, s.sink);
+                const int j = u.kb + lane * w.box_keys;
+                const int b = a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size, b0 = b * s.page_size;
+                in = j - b0;
+                if (j < kr.hi && (b0 + s.page_size > kr.lo || b0 < s.sink)) {
+                    const int p = __ldg(a.table + (int64_t)u.r * s.max_pages + b);
+                    if ((unsigned)p < (unsigned)s.num_pages) page = p;
+                    else set_status(a.status, FM_ERR_PAGES);
+                }
+            }
+            const int slot = k % C::kRing, ks = k & 1;
+            if (k >= C::kRing && !warp_wait(&bars[C::B_UE + slot], ((k / C::kRing) - 1) & 1, abort, a.status, lim)) run = false;
+            if (!run) break;
+            if (lane == 0) {
+                const int f[8] = {u.n, u.r, u.h, u.tok0, u.ntok, u.ctx, u.kb, u.t0};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sUnit[slot * 8 + i] = f[i];
+                mbar_arrive(&bars[C::B_UF + slot]);
+            }
+            __syncwarp();
+            if (u.n < 0) break;
+            if (k >= 2 && !warp_wait(&bars[(FP8 ? C::B_RE : C::B_KE) + ks], ((k >> 1) - 1) & 1, abort, a.status, lim)) break;
+            uint64_t *bar = &bars[(FP8 ? C::B_RF : C::B_KF) + ks];
+            // Wait test: one byte more than comes.
+            if (lane == 0) mbar_arrive_expect_tx(bar, (FP8 ? C::kRaw : C::kTile) + a.withhold);
+            __syncwarp();
+            if (lane < nb) {
+                if (FP8) {
+                    tma_load_4d(smem + C::kRawK + ks * C::kRaw + lane * w.box_keys * D, &tk, bar, 0, in, u.h, page);
+                } else {
+#pragma unroll
+                    for (int half = 0; half < NBOX; ++half)
+                        tma_load_4d(smem + C::kK + ks * C::kTile + half * C::kBox + lane * w.box_keys * 128, &tk, bar, half * 64, in, u.h, page);
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0 && *abort)
+            for (int i = max(k - 2, 0); i <= k; ++i)        // (the last may not have been started: its wait ends at once or runs out)
+                mbar_wait_drain(&bars[(FP8 ? C::B_RF : C::B_KF) + (i & 1)], (i >> 1) & 1, a.status, a.wait_limit);
+    } else if (warp == 1) {
+        // -------------------------------------------- K Q^T
+        constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+        int g = 0;
+        bool run = true;
+        for (int k = 0; run; ++k) {
+            const ManyUnit u = read_unit(k);
+            if (u.n < 0) break;
+            if (lane == 0) {
+                const int ks = k & 1;
+                run = mbar_wait(&bars[C::B_KF + ks], (k >> 1) & 1, abort, a.status, a.wait_limit);
+                const uint64_t dK = sdesc_sw128(smem_u32(smem + C::kK + ks * C::kTile), 16, 1024);
+                for (int t = 0; run && t < u.n; ++t, ++g) {
+                    const int st = g % C::kQSt, sb = g % C::kSBuf;
+                    if (!mbar_wait(&bars[C::B_QF + st], (g / C::kQSt) & 1, abort, a.status, a.wait_limit) ||
+                        (g >= C::kSBuf && !mbar_wait(&bars[C::B_SE + sb], ((g / C::kSBuf) - 1) & 1, abort, a.status, a.wait_limit))) {
+                        run = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t dQ = sdesc_sw128(smem_u32(smem + C::kQ + st * C::kTile), 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * C::kBox + (kk & 3) * 32;
+                        mma_ss(tmem + sb * 128, sdesc_add(dK, off), sdesc_add(dQ, off), id, kk > 0);
+                    }
+                    tc_commit(&bars[C::B_SF + sb]);
+                    tc_commit(&bars[C::B_QE + st]);
+                }
+                if (run) tc_commit(&bars[C::B_KE + ks]);
+            }
+            run = __shfl_sync(0xffffffffu, run, 0);
+        }
+        if (lane == 0) {
+            tc_commit(&bars[C::B_DRAIN]);
+            mbar_wait_drain(&bars[C::B_DRAIN], 0, a.status, a.wait_limit);
+        }
+    } else if (warp < 10) {
+        // -------------------------------------------- exponentials and sums
+        const int wg = warp < 6 ? 0 : 1;                  // the tiles g with g & 1 == wg
+        const int key = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const float scale = a.scale_log2 * (FP8 ? *a.k_descale : 1.f);
+        const uint64_t sc2 = f2_pack(scale, scale);
+        // False for the whole warp once a wait gave up: it still reaches every named barrier, so that the other
+        // warpgroup is never left waiting.
+        bool live = true;
+        int g0 = 0;
+        for (int k = 0;; ++k) {
+            const ManyUnit u = read_unit(k);
+            if (lane == 0) sFlag[(k & 1) * 8 + (warp - 2)] = u.n >= 0 ? 1 : 0;
+            named_bar_sync(1, 256);
+            int all = sFlag[(k & 1) * 8];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) all &= sFlag[(k & 1) * 8 + q];
+            if (!all) break;
+            const int j = u.kb + key, seq = u.ctx + u.ntok;
+            const bool some = j < seq && (s.window == 0 || j > u.ctx - s.window || j < s.sink);     // attended by some row
+            int64_t at = -1;
+            if (wg == 0 && some) at = weight_place(a, u.r, j);
+            float sum = 0.f;
+            for (int t = (wg - g0) & 1; t < u.n; t += 2) {
+                const int g = g0 + t, sb = g % C::kSBuf, ls = g % C::kLSt;
+                const int tok = (u.t0 + t) * tpt, pos = u.ctx + tok, ntok = min(tpt, u.ntok - tok);
+                // Free of the mask: every row behind every key, within every window.
+                const bool full = u.kb + kKeyTile - 1 <= pos && ntok == tpt &&
+                                  (s.window == 0 || u.kb > pos + tpt - 1 - s.window || u.kb + kKeyTile <= s.sink);
+                live = live && warp_wait(&bars[C::B_LF + ls], (g / C::kLSt) & 1, abort, a.status, lim);
+                live = live && warp_wait(&bars[C::B_SF + sb], (g / C::kSBuf) & 1, abort, a.status, lim);
+                if (!live) continue;
+                tc_fence_after();
+                uint32_t keep[4];
+                if (!full) {
+                    const int lo = min(max(j - pos, 0), 128) * G, hi = (s.window > 0 && j >= s.sink ? min(max(j - pos + s.window, 0), ntok) : ntok) * G;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) keep[c] = row_bits32(lo - 32 * c, hi - 32 * c);
+                }
+                const uint32_t tS = tmem + sb * 128 + lane_off;
+                const float4 *z = reinterpret_cast<const float4 *>(sLse + ls * 128);
+                uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                uint32_t v[2][32];
+                tmem_ld32(tS, v[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait();
+                    tmem_reg_fence(v[c & 1]);
+                    if (c < 3) {
+                        tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
+                    }
+                    uint32_t (&x)[32] = v[c & 1];
+                    if (!full) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = (keep[c] >> i) & 1 ? x[i] : 0xff800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 o = z[c * 8 + i];
+                        float e0, e1, e2, e3;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), sc2, f2_pack(o.x, o.y)), e0, e1);
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), sc2, f2_pack(o.z, o.w)), e2, e3);
+                        sum2[0] = f2_add(sum2[0], f2_pack(ex2(e0), ex2(e1)));
+                        sum2[1] = f2_add(sum2[1], f2_pack(ex2(e2), ex2(e3)));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[C::B_LE + ls]);
+                float s0, s1;
+                f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
+                sum += s0 + s1;
+            }
+            g0 += u.n;
+            if (wg == 1) sSum[(k & 1) * 128 + key] = sum;
+            named_bar_sync(1, 256);
+            if (wg == 0 && live && at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum + sSum[(k & 1) * 128 + key], j >= u.ctx);
+        }
+    } else if (warp == 10) {
+        // -------------------------------------------- Q
+        int g = 0;
+        bool run = true;
+        for (int k = 0; run; ++k) {
+            const ManyUnit u = read_unit(k);
+            if (u.n < 0) break;
+            for (int t = 0; t < u.n; ++t, ++g) {
+                const int st = g % C::kQSt;
+                if (g >= C::kQSt && !warp_wait(&bars[C::B_QE + st], ((g / C::kQSt) - 1) & 1, abort, a.status, lim)) {
+                    run = false;
+                    break;
+                }
+                if (lane == 0) {
+                    uint64_t *bar = &bars[C::B_QF + st];
+                    mbar_arrive_expect_tx(bar, (uint32_t)(filled * D * 2));
+#pragma unroll
+                    for (int x = 0; x < NBOX; ++x)
+                        tma_load_3d(smem + C::kQ + st * C::kTile + x * C::kBox, &tq, bar, x * 64, u.h * G, u.tok0 + (u.t0 + t) * tpt);
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0 && *abort)
+            for (int i = (g > C::kQSt ? g - C::kQSt : 0); i < g; ++i)
+                mbar_wait_drain(&bars[C::B_QF + i % C::kQSt], (i / C::kQSt) & 1, a.status, a.wait_limit);
+    } else if (warp == 11) {
+        // -------------------------------------------- lse of the rows
+        int tk[4], at[4];                   // token of a row tile's row, and its place from the tile's first
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = lane + 32 * i;
+            tk[i] = c < filled ? c / G : 1 << 20;
+            at[i] = c < filled ? tk[i] * s.Hq + c % G : 0;
+        }
+        int g = 0;
+        bool run = true;
+        for (int k = 0; run; ++k) {
+            const ManyUnit u = read_unit(k);
+            if (u.n < 0) break;
+            float z[4];
+            auto fetch = [&](int t) {
+                const int tok = (u.t0 + t) * tpt;
+                const float *p = w.lse + (int64_t)(u.tok0 + tok) * s.Hq + u.h * G;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = tok + tk[i] < u.ntok ? __ldg(p + at[i]) : INFINITY;
+            };
+            fetch(0);
+            for (int t = 0; t < u.n; ++t, ++g) {
+                const int ls = g % C::kLSt;
+                float now[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now[i] = -z[i] * kLog2e;
+                if (t + 1 < u.n) fetch(t + 1);
+                if (g >= C::kLSt && !warp_wait(&bars[C::B_LE + ls], ((g / C::kLSt) - 1) & 1, abort, a.status, lim)) {
+                    run = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sLse[ls * 128 + lane + 32 * i] = now[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[C::B_LF + ls]);
+            }
+        }
+    } else if (FP8) {
+        // -------------------------------------------- K to bf16
+        const int mate = warp & 3;
+        constexpr int LPR = D / 8, RPI = 32 / LPR;        // lanes per row, rows per step of a warp
+        const int l = lane % LPR, r_in = lane / LPR;
+        auto bf16x2 = [](uint32_t x) {
+            float lo, hi;
+            unpack_f16x2(f16x2_of_e4m3(x), lo, hi);
+            return pack_bf16x2(lo, hi);
+        };
+        for (int k = 0;; ++k) {
+            const ManyUnit u = read_unit(k);
+            if (u.n < 0) break;
+            const int ks = k & 1;
+            if (!warp_wait(&bars[C::B_RF + ks], (k >> 1) & 1, abort, a.status, lim)) break;
+            if (k >= 2 && !warp_wait(&bars[C::B_KE + ks], ((k >> 1) - 1) & 1, abort, a.status, lim)) break;
+            const uint8_t *raw = smem + C::kRawK + ks * C::kRaw;
+            uint8_t *tile = smem + C::kK + ks * C::kTile;
+#pragma unroll 4
+            for (int i = mate; i < 128 / RPI; i += 4) {
+                const int row = i * RPI + r_in;
+                const uint2 x = *reinterpret_cast<const uint2 *>(raw + row * D + l * 8);
+                st_shared_v4(tile + (l >> 3) * C::kBox + row * 128 + (((l & 7) ^ (row & 7)) << 4),
+                             make_uint4(bf16x2(x.x), bf16x2(x.x >> 16), bf16x2(x.y), bf16x2(x.y >> 16)));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[C::B_KF + ks]);
+                mbar_arrive(&bars[C::B_RE + ks]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Opts a kernel into its shared memory, once per device.
+template <class K>
+fm_status ready(K kernel, int bytes, std::atomic<uint8_t> *done)
+{
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FM_ERR_CUDA;
     if (!done[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(fm_paged_weigh_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess) return FM_ERR_CUDA;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return FM_ERR_CUDA;
         done[dev].store(1, std::memory_order_release);
     }
+    return FM_OK;
+}
+
+template <int D, bool FP8>
+fm_status launch_few(const CUtensorMap &tk, const WeighArgs &w, cudaStream_t stream)
+{
+    using C = FewCfg<D, FP8>;
+    static std::atomic<uint8_t> done[kMaxDevices];
+    const fm_status st = ready(fm_paged_weigh_few_kernel<D, FP8>, C::kBytes, done);
+    if (st != FM_OK) return st;
     ProfScope ps(kKPagedWeighFew, stream);
-    fm_paged_weigh_kernel<D, FP8><<<kPagedCtas * 3, 128, kBytes, stream>>>(w);
+    fm_paged_weigh_few_kernel<D, FP8><<<kPagedCtas, C::kThreads, C::kBytes, stream>>>(tk, w);
+    return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+}
+
+template <int D, bool FP8>
+fm_status launch_many(const CUtensorMap &tq, const CUtensorMap &tk, const WeighArgs &w, cudaStream_t stream)
+{
+    using C = ManyCfg<D, FP8>;
+    static std::atomic<uint8_t> done[kMaxDevices];
+    const fm_status st = ready(fm_paged_weigh_many_kernel<D, FP8>, C::kBytes, done);
+    if (st != FM_OK) return st;
+    ProfScope ps(kKPagedWeighMany, stream);
+    fm_paged_weigh_many_kernel<D, FP8><<<kPagedCtas, C::kThreads, C::kBytes, stream>>>(tq, tk, w);
     return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
@@ -133,13 +929,36 @@ extern "C" fm_status fm_paged_weights(const fm_paged_step *step, const void *q, 
     a.q_head = q_head * 2;
     a.k_descale = cache->k_descale;
     a.status = dev_status;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale * kLog2e;
     a.rows = rows;
+    a.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (a.s.page_size == 1 << i) a.page_shift = i;
     w.lse = lse;
     w.weights = weights;
-    w.k = (const uint8_t *)cache->k;
-    w.k_page = cache->k_page * esz, w.k_head = cache->k_head * esz, w.k_tok = cache->k_tok * esz;
+    // Boxes of consecutive keys of one page, a power of two of them.
+    w.box_keys = kPageGranule;
+    while (w.box_keys < kKeyTile && a.s.page_size % (2 * w.box_keys) == 0) w.box_keys *= 2;
+    const int G = a.s.Hq / a.s.Hkv;
+    const bool d128 = a.s.d == 128;
+    const uint64_t cd[4] = {(uint64_t)a.s.d, (uint64_t)a.s.page_size, (uint64_t)a.s.Hkv, (uint64_t)a.s.num_pages};
+    const uint64_t ks[3] = {(uint64_t)(cache->k_tok * esz), (uint64_t)(cache->k_head * esz), (uint64_t)(cache->k_page * esz)};
+    const uint32_t cb[4] = {fp8 ? (uint32_t)a.s.d : 64u, (uint32_t)w.box_keys, 1, 1};
     cudaStream_t cs = (cudaStream_t)stream;
-    if (a.s.d == 128) return fp8 ? launch<128, true>(w, cs) : launch<128, false>(w, cs);
-    return fp8 ? launch<64, true>(w, cs) : launch<64, false>(w, cs);
+    CUtensorMap tq, tk;
+    if ((int64_t)a.s.max_q * G > kFewRows) {            // some request may have many rows
+        const uint64_t qd[3] = {(uint64_t)a.s.d, (uint64_t)a.s.Hq, (uint64_t)(rows > 0 ? rows : 1)};
+        const uint64_t qs[2] = {(uint64_t)a.q_head, (uint64_t)a.q_tok};
+        const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)(128 / G)};
+        if (!make_tmap_strided(&tq, q, false, 3, qd, qs, qb, 128) || !make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, fp8 ? 0 : 128))
+            return FM_ERR_CUDA;
+        wait_test_args(kKPagedWeighMany, &a.wait_limit, &a.withhold);
+        if (d128) st = fp8 ? launch_many<128, true>(tq, tk, w, cs) : launch_many<128, false>(tq, tk, w, cs);
+        else st = fp8 ? launch_many<64, true>(tq, tk, w, cs) : launch_many<64, false>(tq, tk, w, cs);
+        if (st != FM_OK) return st;
+    }
+    if (!make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, fp8 ? a.s.d : 128)) return FM_ERR_CUDA;
+    wait_test_args(kKPagedWeighFew, &a.wait_limit, &a.withhold);
+    if (d128) return fp8 ? launch_few<128, true>(tk, w, cs) : launch_few<128, false>(tk, w, cs);
+    return fp8 ? launch_few<64, true>(tk, w, cs) : launch_few<64, false>(tk, w, cs);
 }
