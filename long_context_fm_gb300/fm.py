@@ -485,7 +485,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", lambda: -1)
 
 class _NoCall:
     """In _call's place where the extension was not built, or against another torch: the functions here then do it all."""
-    plan = append = attend = staticmethod(lambda *args: None)
+    plan = append = attend = rope = append_rope = weigh = evict = release = verify = staticmethod(lambda *args: None)
 
 
 def _load_call():
@@ -498,7 +498,9 @@ def _load_call():
         spec.loader.exec_module(call)
     except ImportError:
         return _NoCall
-    call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (_lib.fm_paged_plan, _lib.fm_paged_append, _lib.fm_attn_paged)])
+    call.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+        _lib.fm_paged_plan, _lib.fm_paged_append, _lib.fm_attn_paged, _lib.fm_rope, _lib.fm_paged_append_rope, _lib.fm_paged_weights,
+        _lib.fm_paged_evict, _lib.fm_paged_release, _lib.fm_verify_drafts)])
     return call
 
 
@@ -695,6 +697,7 @@ class Rotary:
             m = float(magnitude)
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         self.table = RotaryTable(self.turns.data_ptr(), rot, int(bool(interleaved)), m)
+        self.address = ctypes.addressof(self.table)
         self.rot, self.interleaved, self.magnitude = rot, bool(interleaved), m
 
 
@@ -735,6 +738,12 @@ def fm_rope(x, positions, rotary: Rotary, out=None, out_dtype=None, inverse=Fals
     """x [B, H, N, d] (positions int32 [N] or [B, N]) or rows [T, H, d] (positions [T]) with every row turned by its
     position; inverse turns back: the gradient of x from that of the result.  bf16 or fp32 in and out; out (which
     may be x) is allocated if None, of out_dtype or x's type.  Rows with a negative position are not written."""
+    if stream is None and type(rotary) is Rotary and (out_dtype is None or out_dtype is torch.bfloat16 or out_dtype is torch.float32):
+        r = _call.rope(x, positions, rotary.address, rotary.turns, out, None if out_dtype is None else out_dtype is torch.float32, bool(inverse))
+        if type(r) is int:
+            raise FmError(r, "fm_rope")
+        if r is not None:
+            return r
     dev = _on(x, "x")
     B, H, N, d, xs = _batch(x, dev, "x")
     if out is None:
@@ -760,6 +769,12 @@ def fm_paged_append_rope(q, k, v, slots, positions, rotary: Rotary, k_cache, v_c
     """q's rows (bf16 [T, Hq, d]) turned by their positions (int32 [T] at least), and k's, turned, and v's (bf16 [T, Hkv, d])
     to the cache's slots (int64, T of them at least); returns the turned q (q_out, which may be q; allocated if
     None).  Rows with a negative position are not written, of k and v neither those with a negative slot."""
+    if stream is None and type(rotary) is Rotary:
+        r = _call.append_rope(q, k, v, slots, positions, rotary.address, rotary.turns, k_cache, v_cache, dev_status, q_out, k_descale, v_descale)
+        if type(r) is int:
+            raise FmError(r, "fm_paged_append_rope")
+        if r is not None:
+            return r
     cache = paged_cache(k_cache, v_cache, k_descale, v_descale)
     dev = k_cache.get_device()
     T, Hq, qt, qh = _rows(q, dev, "q", cache.d)
@@ -798,6 +813,12 @@ def _weight_pool(weights, cache, dev):
 def fm_paged_weights(step: PagedStep, q, lse, k_cache, block_table, plan, scale, weights, dev_status, k_descale=None, stream=None):
     """Adds the attention weight that each cached key received from the step's rows to weights (fp32 [num_pages, Hkv,
     page_size]); q and lse (fp32 [rows, Hq]) as fm_attn_paged took and gave them, over the same plan."""
+    if stream is None:
+        code = _call.weigh(ctypes.addressof(step), q, lse, k_cache, block_table, plan, scale, weights, dev_status, k_descale)
+        if code == 0:
+            return
+        if code is not None:
+            raise FmError(code, "fm_paged_weights")
     cache = _key_cache(k_cache, k_descale)
     dev = k_cache.get_device()
     T, H, qt, qh = _rows(q, dev, "q", step.d)
@@ -819,6 +840,12 @@ def fm_paged_evict(lens, block_table, k_cache, v_cache, weights, budget, dev_sta
     """Cuts every request of more than `budget` cached tokens (lens: int32 [requests]) down to the first `sink`, the last
     `recent` and, per KV head, the heaviest others, in one layer's caches and weights, in place.  Returns the new lengths
     (new_lens, not lens itself); kept (int32 [requests, Hkv, budget], allocated if None) gets the places kept."""
+    if stream is None:
+        r = _call.evict(lens, block_table, k_cache, v_cache, weights, budget, dev_status, recent, sink, kept, new_lens)
+        if type(r) is int:
+            raise FmError(r, "fm_paged_evict")
+        if r is not None:
+            return r
     cache = paged_cache(k_cache, v_cache, *([weights.view(-1)[:1]] * 2 if k_cache.dtype is not torch.bfloat16 else ()))
     dev = k_cache.get_device()
     R = lens.shape[0]
@@ -846,6 +873,12 @@ def fm_paged_release(held, lens, block_table, page_size, num_pages, free_pages, 
     """Gives the pages behind lens, of those that held tokens took (both int32 [requests]), back in front of the
     free list's head.  Returns (seq_lens, free_next): the lengths now and the head now, allocated if None;
     they may be held and free_head.  With free_pages None only seq_lens is written, and free_next is None."""
+    if stream is None:
+        r = _call.release(held, lens, block_table, page_size, num_pages, free_pages, free_head, dev_status, free_next, seq_lens)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            raise FmError(r, "fm_paged_release")
     dev, i32 = _on(held, "held"), torch.int32
     R = held.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] != R:
@@ -890,6 +923,12 @@ def fm_verify_drafts(target, draft, tokens, u_accept, u_sample, cu_q, seq_lens, 
     fed; u_accept: fp32 [rows] and u_sample: fp32 [requests], uniform in [0, 1); cu_q, seq_lens: the plan's.  out: int32
     [rows], per request the kept drafts, the drawn token, -1 behind; n_out: how many tokens; new_lens: the cached
     tokens that stay (may be seq_lens).  All are allocated if None; rows of out that no request owns are not written."""
+    if stream is None:
+        r = _call.verify(target, draft, tokens, u_accept, u_sample, cu_q, seq_lens, dev_status, out, n_out, new_lens)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            raise FmError(r, "fm_verify_drafts")
     dev, i32 = _on(target, "target"), torch.int32
     T, V, tr = _probs(target, dev, "target")
     dr, dp = V, None
