@@ -6,19 +6,22 @@
 //   1. each weight becomes a 32-bit key that orders as the weights do; three rounds of a histogram (11, 11, 10
 //      bits from the top; every CTA adds the cluster's histograms up through shared memory of the
 //      others) find the key of the m-th largest and how many equal ones are kept;
-//   2. each CTA counts its keys above and at that key, learns the counts before its slice from the others,
+//   2. each warp counts its keys above and at that key, learns the counts before its own from the others,
 //      and writes its kept places in order;
-//   3. keys, values and weights move down in windows: every CTA reads its tokens of the
-//      window into registers, the cluster meets, every CTA writes.  A token never moves up, so a
+//   3. keys, values and weights move down in windows: every CTA has its tokens of the window copied to shared
+//      memory, two windows ahead, the cluster meets, every CTA writes.  A token never moves up, so a
 //      write hits only places whose tokens this window or an earlier one has read.
-// Bound by HBM where there are many requests: the weights are read once (slices stay in shared memory), every moved
-// token read and written once; by the trips to memory (about eight in a row, then two a window) where there are few.
+// Bound by HBM where there are many requests: the weights are read once (they stay in shared memory), every moved
+// token read and written once; by the trips to memory and the meetings (about ten in a row, then one a window) where
+// there are few.  Steps, of 32 requests of up to 12,000 tokens cut to 4,096 and of one of 128K cut to 16K in e4m3: windows
+// of registers without copies ahead, histograms read one count at a time 427 and 122 us; copies ahead, 16 bytes of a histogram at
+// a time 213 and 90; places by warps instead of block-wide scans, weights 16 bytes at a time, and a meeting that waits for no
+// stores (each thread's would have to reach L2 first) 154 and 73.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
-
-#include <cmath>
+#include <type_traits>
 
 #include "fm_paged.h"
 #include "fm_ptx.cuh"
@@ -30,10 +33,13 @@ namespace {
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictCluster = 8;        // portable cluster size
 constexpr int kBins = 2048;
-constexpr int kHeld = 12288;            // keys of a slice that stay in shared memory (48 KB); longer slices are read again
-constexpr int kMoves = 8;               // pieces of 16 bytes of a thread per window
+constexpr int kHeld = 16384;            // keys of a CTA that stay in shared memory (64 KB); more are read again
+constexpr int kLoads = 4;               // groups of four weights of a thread in flight
+constexpr int kMoves = 3, kStages = 3;  // pieces of 16 bytes of a thread per window; windows in shared memory
+constexpr int kStageBytes = kMoves * kEvictThreads * 16;
+constexpr int kEvictBytes = 3 * kBins * 4 + kHeld * 4;
+static_assert(kStages * (kStageBytes + kMoves * (kEvictThreads / 8) * 4) <= kEvictBytes, "the windows fit where the keys were");   // 8 pieces a token at least
 
 struct EvictArgs {
     uint8_t *kv[2];
@@ -45,6 +51,7 @@ struct EvictArgs {
     int32_t max_pages, num_pages, page_size, Hkv;
     int32_t pieces;                     // of 16 bytes in a row
     int32_t piece_shift;                // log2 of the pieces of a token's key and value
+    int32_t page_shift;                 // log2 of the page size, -1 if it is no power of two
     int32_t budget, recent, sink;
 };
 
@@ -80,22 +87,72 @@ __device__ __forceinline__ int block_before(int x, int *total, int *sh)
     return before + y - x;
 }
 
+// Finds, among the counts of keys by digit of all C CTAs, the digit of the need-th largest key; *need becomes its rank
+// among the keys of that digit.  Thread t looks at the t-th PER digits from the top.
+template <int C, int BINS>
+__device__ __forceinline__ int digit_of(const cg::cluster_group &cl, const int *hist, int *need, int *s_warp, int *s_found)
+{
+    constexpr int PER = BINS / kEvictThreads;
+    static_assert(PER == 4 || PER == 2, "digits of a thread");
+    using V = typename std::conditional<PER == 4, int4, int2>::type;
+    const int at = BINS / PER - 1 - threadIdx.x;
+    int count[PER] = {};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const V v = reinterpret_cast<const V *>(C > 1 ? cl.map_shared_rank(hist, c) : hist)[at];
+        count[0] += v.x;
+        count[1] += v.y;
+        if constexpr (PER == 4) {
+            count[2] += v.z;
+            count[3] += v.w;
+        }
+    }
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += count[i];
+    int total, before = block_before(sum, &total, s_warp);
+    if (before < *need && before + sum >= *need) {
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {
+            if (before < *need && before + count[i] >= *need) {
+                s_found[0] = at * PER + i;
+                s_found[1] = *need - before;
+            }
+            before += count[i];
+        }
+    }
+    __syncthreads();
+    *need = s_found[1];
+    const int digit = s_found[0];
+    __syncthreads();
+    return digit;
+}
+
+template <int C>
 __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const EvictArgs a)
 {
-    extern __shared__ __align__(16) uint32_t s_key[];       // [kHeld]
-    __shared__ int s_hist[3][kBins];
+    // The histograms and the keys, later the tokens on their way.
+    extern __shared__ __align__(16) uint8_t smem[];
+    int (*s_hist)[kBins] = reinterpret_cast<int (*)[kBins]>(smem);
+    uint4 *s_key = reinterpret_cast<uint4 *>(smem + 3 * kBins * 4);             // [kHeld / 4]
+    float *s_moved = reinterpret_cast<float *>(smem + kStages * kStageBytes);    // [kStages][kMoves][tokens of a step]
     __shared__ int s_warp[kEvictWarps];
-    __shared__ int s_bad, s_bin, s_need, s_count[2];
-    cg::cluster_group cl = cg::this_cluster();
-    const int ctas = (int)cl.num_blocks(), cta = (int)cl.block_rank(), tid = threadIdx.x;
-    const int64_t unit = blockIdx.x / (unsigned)ctas;
+    __shared__ int s_bad, s_found[2];
+    __shared__ int2 s_count[kEvictWarps];
+    const cg::cluster_group cl = cg::this_cluster();
+    auto meet = [&]() {
+        if (C > 1) cl.sync();
+        else __syncthreads();
+    };
+    const int cta = C > 1 ? (int)cl.block_rank() : 0, tid = threadIdx.x;
+    const int64_t unit = blockIdx.x / (unsigned)C;
     const int r = (int)(unit / a.Hkv), h = (int)(unit - (int64_t)r * a.Hkv);
     const int len = a.lens[r];
     const bool in_range = len >= 0 && len <= a.max_tokens;
     int32_t *kept = a.kept + unit * a.budget;
     const int32_t *table = a.table + (int64_t)r * a.max_pages;
     auto leave = [&](int32_t code) {
-        for (int i = cta * kEvictThreads + tid; i < a.budget; i += ctas * kEvictThreads) kept[i] = -1;
+        for (int i = cta * kEvictThreads + tid; i < a.budget; i += C * kEvictThreads) kept[i] = -1;
         if (cta == 0 && tid == 0) {
             if (code != FM_OK) set_status(a.status, code);
             if (h == 0) a.new_lens[r] = len;
@@ -105,161 +162,216 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
         leave(in_range ? FM_OK : FM_ERR_LENGTHS);
         return;
     }
-    const int n = len - a.recent - a.sink, m = a.budget - a.recent - a.sink;        // m of n; m < n
-    const int slice = (n + ctas - 1) / ctas;
-    const int first = min(cta * slice, n), mine = min(slice, n - first);            // places sink + first ..
-    const float *weights = a.weights + (int64_t)h * a.page_size;
-    const int64_t page_weights = (int64_t)a.Hkv * a.page_size;
-    auto weight_at = [&](int i) {
-        const int p = a.sink + first + i, b = p / a.page_size;
-        const int page = __ldg(table + b);
-        return (unsigned)page < (unsigned)a.num_pages ? weights + page * page_weights + (p - b * a.page_size) : nullptr;
+    const int lo = a.sink, hi = len - a.recent, m = a.budget - a.recent - a.sink;    // m of the places [lo, hi)
+    // The places in groups of four that share a page and 16 bytes of weights; each warp of the cluster has
+    // consecutive ones, and its lanes next to one another.
+    const int g_lo = lo >> 2, groups = m > 0 ? ((hi + 3) >> 2) - g_lo : 0;
+    const int per_warp = ((groups + C * kEvictWarps - 1) / (C * kEvictWarps) + 31) & ~31, per_cta = per_warp * kEvictWarps;
+    const int warp = tid >> 5, lane = lane_id();
+    const int own = warp * per_warp;                                                // the warp's first group of the CTA
+    const int64_t head_weights = (int64_t)h * a.page_size, page_weights = (int64_t)a.Hkv * a.page_size;
+    auto page_of = [&](int p) { return a.page_shift >= 0 ? p >> a.page_shift : p / a.page_size; };
+    // Keys of the CTA's groups i, i + 32, ..: their loads are in flight together.  A place that is none of [lo, hi) has
+    // key 0, which no weight has; so has a page outside the pool, whose request is then left alone.
+    auto keys_of = [&](int i, uint4 (&key)[kLoads]) {
+        int page[kLoads], in[kLoads];
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const int64_t g = (int64_t)g_lo + (int64_t)cta * per_cta + i + 32 * q;
+            page[q] = -1;
+            if (4 * g >= hi) continue;
+            const int p = (int)(4 * g), b = page_of(p);
+            in[q] = p - b * a.page_size;
+            page[q] = __ldg(table + b);
+        }
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            key[q] = make_uint4(0u, 0u, 0u, 0u);
+            if ((unsigned)page[q] >= (unsigned)a.num_pages) continue;
+            const float4 w = *reinterpret_cast<const float4 *>(a.weights + page[q] * page_weights + head_weights + in[q]);
+            const int p = (int)(4 * ((int64_t)g_lo + (int64_t)cta * per_cta + i + 32 * q));
+            if (p >= lo) key[q].x = order_of(w.x);
+            if (p + 1 >= lo && p + 1 < hi) key[q].y = order_of(w.y);
+            if (p + 2 >= lo && p + 2 < hi) key[q].z = order_of(w.z);
+            if (p + 3 >= lo && p + 3 < hi) key[q].w = order_of(w.w);
+        }
     };
-    auto key_of = [&](int i) -> uint32_t {
-        if (i < kHeld) return s_key[i];
-        const float *w = weight_at(i);
-        return w ? order_of(*w) : 0u;
+    // f(group, its keys) of the warp's groups, all lanes together.
+    auto each = [&](auto f) {
+        for (int i0 = 0; i0 < per_warp; i0 += 32 * kLoads) {
+            uint4 key[kLoads];
+            if (per_cta > kHeld / 4) {
+                keys_of(own + i0 + lane, key);
+            } else {
+#pragma unroll
+                for (int q = 0; q < kLoads; ++q) key[q] = i0 + 32 * q < per_warp ? s_key[own + i0 + 32 * q + lane] : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q)
+                if (i0 + 32 * q < per_warp) f(own + i0 + 32 * q + lane, key[q]);
+        }
     };
 
-    for (int i = tid; i < 3 * kBins; i += kEvictThreads) s_hist[0][i] = 0;
+    if (m > 0)
+        for (int i = tid; i < 3 * kBins / 4; i += kEvictThreads) reinterpret_cast<int4 *>(s_hist)[i] = make_int4(0, 0, 0, 0);
     if (tid == 0) s_bad = 0;
     __syncthreads();
     // Every page of the request is one of the pool's, or the request is left alone.
-    const int pages = (int)(((int64_t)len + a.page_size - 1) / a.page_size);
-    for (int b = cta * kEvictThreads + tid; b < pages; b += ctas * kEvictThreads)
+    const int pages = page_of(len - 1) + 1;
+    for (int b = cta * kEvictThreads + tid; b < pages; b += C * kEvictThreads)
         if ((unsigned)__ldg(table + b) >= (unsigned)a.num_pages) s_bad = 1;
-    if (m > 0) {
-        for (int i = tid; i < mine; i += kEvictThreads) {
-            const float *w = weight_at(i);
-            const uint32_t key = w ? order_of(*w) : 0u;
-            if (i < kHeld) s_key[i] = key;
-            atomicAdd(&s_hist[0][key >> 21], 1);
+    for (int i0 = 0; m > 0 && i0 < per_warp; i0 += 32 * kLoads) {
+        uint4 key[kLoads];
+        keys_of(own + i0 + lane, key);
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            if (i0 + 32 * q >= per_warp) break;
+            if (per_cta <= kHeld / 4) s_key[own + i0 + 32 * q + lane] = key[q];
+            const uint32_t k[4] = {key[q].x, key[q].y, key[q].z, key[q].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k[j]) atomicAdd(&s_hist[0][k[j] >> 21], 1);
         }
     }
-    cl.sync();
+    meet();
     bool bad = false;
-    for (int c = 0; c < ctas; ++c) bad |= *cl.map_shared_rank(&s_bad, c) != 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) bad |= *(C > 1 ? cl.map_shared_rank(&s_bad, c) : &s_bad) != 0;
     if (bad) {
-        cl.sync();                                  // the others have read this CTA's flag
+        meet();                                     // the others have read this CTA's flag
         leave(FM_ERR_PAGES);
         return;
     }
 
     // The key of the m-th largest, from the top bits down: `prefix` its bits so far, `need` the keys
     // with that prefix that are kept.
-    uint32_t prefix = 0;
-    int need = m;
     if (m > 0) {
-#pragma unroll 1
-        for (int round = 0; round < 3; ++round) {
-            const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bins = round == 2 ? 1024 : kBins;
-            if (round > 0) {
-                const int above = round == 1 ? 21 : 10;
-                for (int i = tid; i < mine; i += kEvictThreads) {
-                    const uint32_t key = key_of(i);
-                    if (key >> above == prefix) atomicAdd(&s_hist[round][(key >> shift) & (bins - 1)], 1);
-                }
-                cl.sync();
-            }
-            // Thread t's bins are the t-th group from the top.
-            const int per = bins / kEvictThreads;
-            int sum = 0;
-            for (int c = 0; c < ctas; ++c) {
-                const int *hist = cl.map_shared_rank(&s_hist[round][0], c);
-                for (int j = 0; j < per; ++j) sum += hist[bins - 1 - (tid * per + j)];
-            }
-            int total;
-            int before = block_before(sum, &total, s_warp);
-            if (before < need && before + sum >= need) {
-                for (int j = 0; j < per; ++j) {
-                    const int bin = bins - 1 - (tid * per + j);
-                    int x = 0;
-                    for (int c = 0; c < ctas; ++c) x += cl.map_shared_rank(&s_hist[round][0], c)[bin];
-                    if (before + x >= need) {
-                        s_bin = bin;
-                        s_need = need - before;
-                        break;
-                    }
-                    before += x;
-                }
-            }
-            __syncthreads();
-            prefix = prefix << (round == 2 ? 10 : 11) | (uint32_t)s_bin;
-            need = s_need;
-            __syncthreads();
-        }
-        // How many of the slice lie above the key and at it.
+        int need = m;
+        uint32_t prefix = (uint32_t)digit_of<C, kBins>(cl, s_hist[0], &need, s_warp, s_found);
+        each([&](int, const uint4 &key) {
+            const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k[j] >> 21 == prefix && k[j]) atomicAdd(&s_hist[1][(k[j] >> 10) & 2047], 1);
+        });
+        meet();
+        prefix = prefix << 11 | (uint32_t)digit_of<C, kBins>(cl, s_hist[1], &need, s_warp, s_found);
+        each([&](int, const uint4 &key) {
+            const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k[j] >> 10 == prefix && k[j]) atomicAdd(&s_hist[2][k[j] & 1023], 1);
+        });
+        meet();
+        prefix = prefix << 10 | (uint32_t)digit_of<C, 1024>(cl, s_hist[2], &need, s_warp, s_found);
+        // How many of the warp's keys lie above that key and at it, and how many of the warps and CTAs before.
         int above = 0, at = 0;
-        for (int i = tid; i < mine; i += kEvictThreads) {
-            const uint32_t key = key_of(i);
-            above += key > prefix;
-            at += key == prefix;
+        each([&](int, const uint4 &key) {
+            above += (key.x > prefix) + (key.y > prefix) + (key.z > prefix) + (key.w > prefix);
+            at += (key.x == prefix) + (key.y == prefix) + (key.z == prefix) + (key.w == prefix);
+        });
+        above = __reduce_add_sync(0xffffffffu, above);
+        at = __reduce_add_sync(0xffffffffu, at);
+        if (lane == 0) s_count[warp] = make_int2(above, at);
+        meet();
+        above = at = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {               // lane w: warp w of CTA c
+            int2 v = make_int2(0, 0);
+            if (lane < kEvictWarps && (c < cta || (c == cta && lane < warp))) v = (C > 1 ? cl.map_shared_rank(&s_count[0], c) : s_count)[lane];
+            above += v.x;
+            at += v.y;
         }
-        int total_above, total_at;
-        block_before(above, &total_above, s_warp);
-        block_before(at, &total_at, s_warp);
-        if (tid == 0) {
-            s_count[0] = total_above;
-            s_count[1] = total_at;
-        }
-        cl.sync();
-        int run_above = 0, run_at = 0;
-        for (int c = 0; c < cta; ++c) {
-            run_above += cl.map_shared_rank(&s_count[0], c)[0];
-            run_at += cl.map_shared_rank(&s_count[0], c)[1];
-        }
-        for (int i0 = 0; i0 < mine; i0 += kEvictThreads) {
-            const int i = i0 + tid;
-            const uint32_t key = i < mine ? key_of(i) : 0u;
-            const bool up = i < mine && key > prefix, eq = i < mine && key == prefix;
-            int total;
-            const int before = block_before((up ? 1 : 0) | (eq ? 1 << 16 : 0), &total, s_warp);    // at most 512 of each
-            const int ups = run_above + (before & 0xffff), eqs = run_at + (before >> 16);
-            if (up || (eq && eqs < need)) kept[a.sink + ups + min(eqs, need)] = a.sink + first + i;
+        int run_above = __reduce_add_sync(0xffffffffu, above), run_at = __reduce_add_sync(0xffffffffu, at);
+        each([&](int i, const uint4 &key) {
+            const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+            int count = 0;                          // above | at << 16: 128 of a step at most
+#pragma unroll
+            for (int j = 0; j < 4; ++j) count += (k[j] > prefix ? 1 : 0) + (k[j] == prefix ? 1 << 16 : 0);
+            int upto = count;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            int ups = run_above + ((upto - count) & 0xffff), eqs = run_at + ((upto - count) >> 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (k[j] > prefix || (k[j] == prefix && eqs < need))
+                    kept[a.sink + ups + min(eqs, need)] = (int)(4 * ((int64_t)g_lo + (int64_t)cta * per_cta + i)) + j;
+                ups += k[j] > prefix;
+                eqs += k[j] == prefix;
+            }
+            const int total = __shfl_sync(0xffffffffu, upto, 31);
             run_above += total & 0xffff;
             run_at += total >> 16;
-        }
+        });
     }
-    for (int i = cta * kEvictThreads + tid; i < a.sink; i += ctas * kEvictThreads) kept[i] = i;
-    for (int i = cta * kEvictThreads + tid; i < a.recent; i += ctas * kEvictThreads) kept[a.budget - a.recent + i] = len - a.recent + i;
+    for (int i = cta * kEvictThreads + tid; i < a.sink; i += C * kEvictThreads) kept[i] = i;
+    for (int i = cta * kEvictThreads + tid; i < a.recent; i += C * kEvictThreads) kept[a.budget - a.recent + i] = len - a.recent + i;
     if (cta == 0 && tid == 0 && h == 0) a.new_lens[r] = a.budget;
-    cl.sync();                                      // the kept places are visible to the cluster
+    meet();                                          // the kept places are visible to the cluster
 
-    // Windows of kMoves pieces a thread.
-    const int per_token = 1 << a.piece_shift, tokens = kEvictThreads >> a.piece_shift;      // tokens of a step of the CTA
+    // Windows of kMoves pieces a thread, kStages - 1 of them on their way to shared memory while one is written.
+    const int per_token = 1 << a.piece_shift, tokens = kEvictThreads >> a.piece_shift, mate = tid >> a.piece_shift;    // tokens of a step of the CTA
     const int piece = tid & (per_token - 1), which = piece >= a.pieces ? 1 : 0;
     const int64_t col = (int64_t)h * a.head[which] + (int64_t)(piece - which * a.pieces) * 16;
-    const int window = tokens * kMoves * ctas;
-    for (int w0 = a.sink; w0 < a.budget; w0 += window) {
-        const int j0 = w0 + cta * tokens * kMoves + (tid >> a.piece_shift);
-        uint4 x[kMoves];
-        float w[kMoves];
-        int from[kMoves];
+    const int64_t st_page = a.page[which], st_tok = a.tok[which];
+    uint8_t *kv = a.kv[which];
+    const int window = tokens * kMoves * C, j0 = a.sink + cta * tokens * kMoves + mate;
+    const int windows = (a.budget - a.sink + window - 1) / window;
+    auto sources = [&](int w, int (&from)[kMoves]) {
 #pragma unroll
         for (int i = 0; i < kMoves; ++i) {
-            const int j = j0 + i * tokens;
-            from[i] = j < a.budget ? __ldcg(kept + j) : j;
+            const int64_t j = (int64_t)w * window + j0 + i * tokens;
+            from[i] = w < windows && j < a.budget ? __ldcg(kept + j) : -1;
         }
+    };
+    // Starts the loads of window w; a bit for each piece that moves.
+    auto start = [&](int w, const int (&from)[kMoves]) {
+        unsigned moves = 0;
+        uint8_t *stage = smem + (w % kStages) * kStageBytes;
 #pragma unroll
         for (int i = 0; i < kMoves; ++i) {
-            const int j = j0 + i * tokens;
-            if (j >= a.budget || from[i] == j) continue;
-            const int b = from[i] / a.page_size;
-            const int64_t page = __ldg(table + b), in = from[i] - b * a.page_size;
-            x[i] = __ldcg(reinterpret_cast<const uint4 *>(a.kv[which] + page * a.page[which] + in * a.tok[which] + col));
-            if (piece == 0) w[i] = __ldcg(weights + page * page_weights + in);
+            if (from[i] < 0 || from[i] == w * window + j0 + i * tokens) continue;
+            moves |= 1u << i;
+            const int b = page_of(from[i]), in = from[i] - b * a.page_size;
+            const int64_t page = __ldg(table + b);
+            copy_async16(stage + (i * kEvictThreads + tid) * 16, kv + page * st_page + in * st_tok + col);
+            if (piece == 0) copy_async4(s_moved + ((w % kStages) * kMoves + i) * tokens + mate, a.weights + page * page_weights + head_weights + in);
         }
-        cl.sync();
+        copy_async_commit();
+        return moves;
+    };
+    unsigned moves[kStages] = {};
+    int from[kMoves];
 #pragma unroll
-        for (int i = 0; i < kMoves; ++i) {
-            const int j = j0 + i * tokens;
-            if (j >= a.budget || from[i] == j) continue;
-            const int b = j / a.page_size;
-            const int64_t page = __ldg(table + b), in = j - b * a.page_size;
-            *reinterpret_cast<uint4 *>(a.kv[which] + page * a.page[which] + in * a.tok[which] + col) = x[i];
-            if (piece == 0) a.weights[(int64_t)h * a.page_size + page * page_weights + in] = w[i];
-        }
+    for (int w = 0; w < kStages - 1; ++w) {
+        sources(w, from);
+        moves[w] = start(w, from);
     }
+    sources(kStages - 1, from);
+    for (int w = 0; w < windows; ++w) {
+        copy_async_wait<kStages - 2>();
+        if (C > 1) cluster_arrive_relaxed();               // this thread has read its sources of the window
+        moves[kStages - 1] = start(w + kStages - 1, from);
+        sources(w + kStages, from);
+        if (C > 1) cluster_wait();                   // and every other
+        else __syncthreads();
+        const uint8_t *stage = smem + (w % kStages) * kStageBytes;
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i) {
+            if (!(moves[0] >> i & 1u)) continue;
+            const int j = w * window + j0 + i * tokens;
+            const int b = page_of(j), in = j - b * a.page_size;
+            const int64_t page = __ldg(table + b);
+            *reinterpret_cast<uint4 *>(kv + page * st_page + in * st_tok + col) = *reinterpret_cast<const uint4 *>(stage + (i * kEvictThreads + tid) * 16);
+            if (piece == 0) a.weights[page * page_weights + head_weights + in] = s_moved[((w % kStages) * kMoves + i) * tokens + mate];
+        }
+#pragma unroll
+        for (int i = 0; i + 1 < kStages; ++i) moves[i] = moves[i + 1];
+    }
+    copy_async_wait<0>();
 }
 
 // ---- release ---------------------------------------------------------------------------
@@ -328,6 +440,30 @@ __global__ void __launch_bounds__(kReleaseThreads) fm_paged_release_kernel(const
     }
 }
 
+template <int C>
+fm_status launch_evict(const EvictArgs &a, int64_t units, cudaStream_t stream)
+{
+    static std::atomic<uint8_t> done[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FM_ERR_CUDA;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(fm_paged_evict_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictBytes) != cudaSuccess) return FM_ERR_CUDA;
+        done[dev].store(1, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(units * C));
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = kEvictBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fm_paged_evict_kernel<C>, a) == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace fm
 
@@ -342,7 +478,7 @@ fm_status fm_paged_evict(const fm_paged_cache *cache, int requests, int max_page
     fm_status st = check_cache(cache);
     if (st != FM_OK) return st;
     if (requests <= 0 || max_pages <= 0 || budget <= 0 || recent < 0 || sink < 0 || (int64_t)recent + sink > budget) return FM_ERR_INVALID_ARG;
-    if (!aligned4(lens) || !aligned4(block_table) || !aligned4(weights) || !aligned4(kept) || !aligned4(new_lens) || !aligned4(dev_status) ||
+    if (!aligned4(lens) || !aligned4(block_table) || !aligned16(weights) || !aligned4(kept) || !aligned4(new_lens) || !aligned4(dev_status) ||
         lens == new_lens)
         return FM_ERR_INVALID_ARG;
     if (requests > kMaxRequests || (int64_t)max_pages * cache->page_size > (int64_t)0x7fffffff - 2 * kMaxPage) return FM_ERR_UNSUPPORTED;
@@ -369,26 +505,18 @@ fm_status fm_paged_evict(const fm_paged_cache *cache, int requests, int max_page
     a.budget = budget;
     a.recent = recent;
     a.sink = sink;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((int64_t)requests * cache->Hkv * kEvictCluster));
-    cfg.blockDim = dim3(kEvictThreads);
-    cfg.dynamicSmemBytes = kHeld * 4;
-    cfg.stream = (cudaStream_t)stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kEvictCluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    static std::atomic<uint8_t> done[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FM_ERR_CUDA;
-    if (!done[dev].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(fm_paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4) != cudaSuccess) return FM_ERR_CUDA;
-        done[dev].store(1, std::memory_order_release);
-    }
+    a.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (a.page_size == 1 << i) a.page_shift = i;
+    const int64_t units = (int64_t)requests * cache->Hkv;
+    cudaStream_t cs = (cudaStream_t)stream;
     ProfScope ps(kKPagedEvict, stream);
-    return cudaLaunchKernelEx(&cfg, fm_paged_evict_kernel, a) == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+    // As many CTAs per unit as one round of the device holds (two of them a SM; a cluster within a part of the
+    // device): 8 units of 12,000 tokens to 4,096 with 1, 2, 4 and 8 CTAs 128, 80, 48 and 35 us; 32 of 1,500 to 500 25, 21, 20 and 31;
+    // 256 of up to 12,000 to 4,096 216, 154, 166 and 219; 512 of up to 2,000 to 1,000 39, 53, 70 and 146.
+    if (units <= 16) return launch_evict<8>(a, units, cs);
+    if (units <= 64) return launch_evict<4>(a, units, cs);
+    return units <= 304 ? launch_evict<2>(a, units, cs) : launch_evict<1>(a, units, cs);
 }
 
 fm_status fm_paged_release(int requests, int max_pages, int num_pages, int page_size, const int32_t *held, const int32_t *lens,

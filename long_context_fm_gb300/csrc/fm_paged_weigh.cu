@@ -914,7 +914,7 @@ extern "C" fm_status fm_paged_weights(const fm_paged_step *step, const void *q, 
     if ((st = check_cache(cache)) != FM_OK) return st;
     if (cache->num_pages != a.s.num_pages || cache->page_size != a.s.page_size || cache->Hkv != a.s.Hkv || cache->d != a.s.d)
         return FM_ERR_INVALID_ARG;
-    if (rows < 0 || !rows_ok(q, q_tok, q_head) || !aligned4(lse) || !aligned4(weights) || !aligned4(block_table) || !aligned4(dev_status))
+    if (rows < 0 || !rows_ok(q, q_tok, q_head) || !aligned4(lse) || !aligned16(weights) || !aligned4(block_table) || !aligned4(dev_status))
         return FM_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) return FM_ERR_INVALID_ARG;
     a.L = paged_layout(a.s);

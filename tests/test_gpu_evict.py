@@ -100,6 +100,14 @@ def test_weights_that_are_equal_or_odd(fm, values, lens, budget, recent, sink):
     Pool(lens, 2, 64, 32, values=values, seed=8).check(fm, budget, recent, sink)
 
 
+@pytest.mark.parametrize("values", ["spread", "ties"])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("R", [8, 9, 32, 33, 152, 153])
+def test_many_requests(fm, R, e4m3, values):
+    """More and more (request, head) pairs: fewer and fewer blocks share one."""
+    Pool([(37 * r) % 400 for r in range(R)], 2, 64, 16, e4m3, seed=R, values=values).check(fm, 90, 11, 3)
+
+
 @pytest.mark.parametrize("layout", ["tokens", "pairs"])
 @pytest.mark.parametrize("page", [16, 48, 128])
 def test_strides_and_pages(fm, layout, page):
