@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "fm_paged.h"
 #include "fm_ptx.cuh"
@@ -219,51 +220,47 @@ __global__ void __launch_bounds__(kRopeThreads) fm_paged_append_rope_kernel(cons
     const int lo = turned && !INTER ? 4 * u : 8 * u, hi = turned && !INTER ? 4 * (a.units + u) : 8 * u + 4;
     Turn ang;
     if (turned && r0 < a.Hq + a.Hkv) ang = turn_of(a.turns, u, pos, a.m, false);
-    for (int r = r0; r < r1; r += kInFlight) {
-        Bf8 x[kInFlight];
-        int kind[kInFlight];                     // 0: q, 1: k, 2: v, 3: nothing
+    // Heads [h0, h1) of q (kind 0), k (1) or v (2).
+    auto heads = [&](auto kind_of, int h0, int h1) {
+        constexpr int K = decltype(kind_of)::value;
+        const bool tu = turned && K < 2;
+        if (h0 >= h1 || (K > 0 && !inside) || (K == 0 && !turned && a.q_in_place)) return;
+        const int l = K == 2 ? 8 * u : lo, g = K == 2 ? 8 * u + 4 : hi;
+        const Divisor ds(K > 0 && FP8 ? __ldg(a.descale[K > 0 ? K - 1 : 0]) : 1.f);
+        const int64_t step_in = a.head[K], step_out = a.out_head[K];
+        const uint8_t *x = a.in[K] + t * a.tok[K] + h0 * step_in;
+        uint8_t *y = a.out[K] + (K == 0 ? t * a.q_tok : at[K > 0 ? K - 1 : 0]) + h0 * step_out;
+        for (int h = h0; h < h1; h += kInFlight) {
+            Bf8 r[kInFlight];
 #pragma unroll
-        for (int i = 0; i < kInFlight; ++i) {
-            const int row = r + i;
-            kind[i] = row >= r1 ? 3 : row < a.Hq ? 0 : row < a.Hq + a.Hkv ? 1 : 2;
-            if ((kind[i] == 0 && !turned && a.q_in_place) || (kind[i] > 0 && !inside)) kind[i] = 3;
-            if (kind[i] == 3) continue;
-            const int k = kind[i], h = k == 0 ? row : k == 1 ? row - a.Hq : row - a.Hq - a.Hkv;
-            const uint8_t *p = a.in[k] + t * a.tok[k] + h * a.head[k];
-            x[i] = k == 2 ? load8<uint16_t>(p, 8 * u, 8 * u + 4) : load8<uint16_t>(p, lo, hi);
-        }
+            for (int i = 0; i < kInFlight; ++i)
+                if (h + i < h1) r[i] = load8<uint16_t>(x + i * step_in, l, g);
 #pragma unroll
-        for (int i = 0; i < kInFlight; ++i) {
-            const int row = r + i, k = kind[i];
-            if (k == 3) continue;
-            const int h = k == 0 ? row : k == 1 ? row - a.Hq : row - a.Hq - a.Hkv;
-            const bool tu = turned && k < 2;
-            const int l = k == 2 ? 8 * u : lo, g = k == 2 ? 8 * u + 4 : hi;
-            if (k == 0 || !FP8) {
-                Bf8 w = x[i];
-                if (tu) {
-                    float v[8];
-                    values(x[i], v);
-                    turn8<INTER>(ang, v);
-                    of_values(v, w);
-                }
-                uint8_t *p = a.out[k] + (k == 0 ? t * a.q_tok : at[k - 1]) + h * a.out_head[k];
-                store8<uint16_t>(p, l, g, w);
-            } else {
+            for (int i = 0; i < kInFlight; ++i) {
+                if (h + i >= h1) break;
                 float v[8];
-                values(x[i], v);
+                values(r[i], v);
                 if (tu) turn8<INTER>(ang, v);
-                const Divisor ds(__ldg(a.descale[k - 1]));
-                uint32_t w[2];
+                if constexpr (K > 0 && FP8) {
+                    uint32_t w[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    w[j] = pack_e4m3x2(ds(v[4 * j]), ds(v[4 * j + 1])) | pack_e4m3x2(ds(v[4 * j + 2]), ds(v[4 * j + 3])) << 16;
-                uint8_t *p = a.out[k] + at[k - 1] + h * a.out_head[k];
-                *reinterpret_cast<uint32_t *>(p + l) = w[0];
-                *reinterpret_cast<uint32_t *>(p + g) = w[1];
+                    for (int j = 0; j < 2; ++j)
+                        w[j] = pack_e4m3x2(ds(v[4 * j]), ds(v[4 * j + 1])) | pack_e4m3x2(ds(v[4 * j + 2]), ds(v[4 * j + 3])) << 16;
+                    *reinterpret_cast<uint32_t *>(y + i * step_out + l) = w[0];
+                    *reinterpret_cast<uint32_t *>(y + i * step_out + g) = w[1];
+                } else {
+                    Bf8 w = r[i];               // the same bits where nothing turns
+                    if (tu) of_values(v, w);
+                    store8<uint16_t>(y + i * step_out, l, g, w);
+                }
             }
+            x += kInFlight * step_in;
+            y += kInFlight * step_out;
         }
-    }
+    };
+    heads(std::integral_constant<int, 0>{}, r0, min(r1, a.Hq));
+    heads(std::integral_constant<int, 1>{}, max(r0 - a.Hq, 0), min(r1 - a.Hq, a.Hkv));
+    heads(std::integral_constant<int, 2>{}, max(r0 - a.Hq - a.Hkv, 0), r1 - a.Hq - a.Hkv);
 }
 
 bool rotary_ok(const fm_rotary *r) { return r && aligned16(r->turns) && r->rot > 0 && std::isfinite(r->magnitude); }

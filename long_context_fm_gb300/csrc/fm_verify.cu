@@ -6,9 +6,10 @@
 // One row of p and one of q are read per request, by a cluster of CTAs that share the vocabulary in contiguous
 // slices, so that a few requests are spread over the SMs: bound by HBM at large batches, by
 // latency below.  A token at a border has to come out the same however the sums are added up, which 24 bits do not
-// give over 100,000 terms, and GB300's 64-bit units would take longer than the memory (two results a cycle
-// and SM): each thread adds in pairs of floats (the exact error of a sum and of a difference in six and two
-// more operations: Knuth's two-sum, Dekker's), about 48 bits, and only the sums of segments meet in 64 bits.
+// give over 100,000 terms, and 64-bit units take far too long here (two results a cycle and SM: with them in the search
+// alone, 64 requests over 131,072 tokens took 51 us for 17, two over 32,000 21 for 7): every sum is held in a pair of
+// floats, with the exact error of each addition and difference (Knuth's two-sum, Dekker's fast one for a larger minus a
+// smaller), about 48 bits.  Every CTA of 512 is resident at once (64 registers, 4 a SM).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -26,7 +27,8 @@ constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCluster = 8;
 constexpr int kSegments = 256;          // of a CTA's slice at most
-constexpr int kSegment = 1024;          // tokens of a segment at least: 32 lanes, 4 loads of 8
+constexpr int kLoads = 2;               // loads of 8 tokens of a lane in flight, of p and of q
+constexpr int kSegment = 512;           // tokens of a segment at least: 32 lanes and as many loads
 
 struct VerifyArgs {
     const uint8_t *target, *draft;      // bytes; draft may be null
@@ -78,6 +80,26 @@ struct Pair {
         lo += ((hi - (s - b)) + (x - b)) + more;
         hi = s;
     }
+    __device__ __forceinline__ void add(const Pair &o) { add(o.hi, o.lo); }
+    // lo below half a step of hi, so that pairs compare.
+    __device__ __forceinline__ Pair whole() const
+    {
+        const float s = hi + lo;
+        return Pair{s, lo - (s - hi)};
+    }
+    __device__ __forceinline__ bool above(const Pair &o) const { return (hi - o.hi) + (lo - o.lo) > 0.f; }      // (both whole; exact where they are near)
+    __device__ __forceinline__ Pair from(int lane) const { return Pair{__shfl_sync(0xffffffffu, hi, lane), __shfl_sync(0xffffffffu, lo, lane)}; }
+    // Sum over the lanes up to this one.
+    __device__ __forceinline__ Pair upto() const
+    {
+        Pair s = *this;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Pair y{__shfl_up_sync(0xffffffffu, s.hi, o), __shfl_up_sync(0xffffffffu, s.lo, o)};
+            if (lane_id() >= o) s.add(y);
+        }
+        return s;
+    }
 };
 
 // The weights of a request's draw.
@@ -86,12 +108,23 @@ struct Row {
     int hot;                    // the token whose weight is zero (drafts taken with certainty), or -1
 };
 
+// Weight of a token: x in two floats, exactly.
+__device__ __forceinline__ Pair weight_of(const Row &w, float p, float q, int64_t i)
+{
+    Pair x{p, 0.f};
+    if (w.q) {
+        x.hi = p - q;
+        x.lo = (p - x.hi) - q;                  // exact where p > q
+    }
+    if (i == w.hot || (!(x.hi > 0.f) && x.hi == x.hi)) x = Pair{0.f, 0.f};
+    return x;
+}
+
 // Sum of a segment's weights, the same in every lane.
 template <class T>
-__device__ __forceinline__ double segment_sum(const Row &w, int64_t begin, int64_t end, bool wide)
+__device__ __forceinline__ Pair segment_sum(const Row &w, int64_t begin, int64_t end, bool wide)
 {
     Pair s[2] = {{0.f, 0.f}, {0.f, 0.f}};
-    constexpr int kLoads = 4;
     for (int64_t i0 = begin + lane_id() * 8; i0 < end; i0 += 32 * 8 * kLoads) {
         float p[kLoads][8], q[kLoads][8];
 #pragma unroll
@@ -103,29 +136,19 @@ __device__ __forceinline__ double segment_sum(const Row &w, int64_t begin, int64
 #pragma unroll
         for (int l = 0; l < kLoads; ++l)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float x = p[l][j], more = 0.f;
-                if (w.q) {
-                    const float d = x - q[l][j];
-                    more = (x - d) - q[l][j];           // exact where d > 0: x is the larger
-                    x = d;
-                }
-                if (i0 + l * 256 + j == w.hot) x = 0.f;
-                if (!(x > 0.f) && x == x) x = more = 0.f;
-                s[j & 1].add(x, more);
-            }
+            for (int j = 0; j < 8; ++j) s[j & 1].add(weight_of(w, p[l][j], q[l][j], i0 + l * 256 + j));
     }
-    double t = ((double)s[0].hi + (double)s[1].hi) + ((double)s[0].lo + (double)s[1].lo);
+    s[0].add(s[1]);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
+    for (int o = 1; o < 32; o <<= 1) s[0].add(Pair{__shfl_xor_sync(0xffffffffu, s[0].hi, o), __shfl_xor_sync(0xffffffffu, s[0].lo, o)});
+    return s[0].whole();
 }
 
 template <class T>
-__global__ void __launch_bounds__(kVerifyThreads) fm_verify_kernel(const VerifyArgs a)
+__global__ void __launch_bounds__(kVerifyThreads, 4) fm_verify_kernel(const VerifyArgs a)
 {
-    __shared__ double s_seg[kSegments];
-    __shared__ double s_total[2];           // of the weights, of p alone (where they are zero)
+    __shared__ Pair s_seg[kSegments];
+    __shared__ Pair s_total[2];             // of the weights, of p alone (where they are zero)
     __shared__ int s_row;
     cg::cluster_group cl = cg::this_cluster();
     const int ctas = (int)cl.num_blocks(), cta = (int)cl.block_rank(), tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
@@ -179,49 +202,42 @@ __global__ void __launch_bounds__(kVerifyThreads) fm_verify_kernel(const VerifyA
     }
     const int64_t v0 = min((int64_t)cta * a.slice, (int64_t)a.V), v1 = min(v0 + a.slice, (int64_t)a.V);
     const int segments = (int)((v1 - v0 + a.segment - 1) / a.segment);
-    double total = 0.0, before = 0.0, want = 0.0;
+    Pair total{0.f, 0.f}, before{0.f, 0.f}, want{0.f, 0.f};
     int owner = -1;                         // the CTA whose slice holds the border
     // Once, and a second time with p alone where the weights are all zero.
     for (int go = 0; go < 2; ++go) {
         for (int x = warp; x < segments; x += kVerifyWarps) {
             const int64_t b = v0 + (int64_t)x * a.segment;
-            const double t = segment_sum<T>(w, b, min(b + a.segment, v1), a.wide);
+            const Pair t = segment_sum<T>(w, b, min(b + a.segment, v1), a.wide);
             if (lane == 0) s_seg[x] = t;
         }
         __syncthreads();
         if (warp == 0) {
-            double t = 0.0;
-            for (int x = lane; x < segments; x += 32) t += s_seg[x];
+            Pair t{0.f, 0.f};
+            for (int x = lane; x < segments; x += 32) t.add(s_seg[x]);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            if (lane == 0) s_total[go] = t;
+            for (int o = 1; o < 32; o <<= 1) t.add(Pair{__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o)});
+            if (lane == 0) s_total[go] = t.whole();
         }
         cl.sync();
-        double part[kVerifyCluster];
-#pragma unroll
-        for (int c = 0; c < kVerifyCluster; ++c) part[c] = c < ctas ? *cl.map_shared_rank(&s_total[go], c) : 0.0;
-        total = 0.0;
-#pragma unroll
-        for (int c = 0; c < kVerifyCluster; ++c) total += part[c];
-        want = (double)a.u_sample[r] * total;
-        // (The last one with any weight, if rounding or a number outside [0, 1) leaves the border behind all.)
-        double run = 0.0;
-        bool found = false;
-        owner = -1;
-#pragma unroll
-        for (int c = 0; c < kVerifyCluster; ++c) {
-            if (!found && part[c] > 0.0) {
-                owner = c;
-                before = run;
-                found = run + part[c] > want;
-            }
-            run += part[c];
-        }
-        if (total != 0.0 || (!w.q && w.hot < 0)) break;
+        // Lane c: the slice of CTA c.  (The last one with any weight, if rounding or a number outside [0, 1) leaves the
+        // border behind all.)
+        Pair part{0.f, 0.f};
+        if (lane < ctas) part = *cl.map_shared_rank(&s_total[go], lane);
+        const Pair upto = part.upto();
+        total = upto.whole().from(31);
+        const float u = __ldg(a.u_sample + r);
+        want.hi = u * total.hi;
+        want.lo = fmaf(u, total.hi, -want.hi) + u * total.lo;
+        want = want.whole();
+        const unsigned past = __ballot_sync(0xffffffffu, part.hi > 0.f && upto.whole().above(want)), any = __ballot_sync(0xffffffffu, part.hi > 0.f);
+        owner = past ? __ffs(past) - 1 : any ? 31 - __clz(any) : -1;
+        before = owner > 0 ? upto.from(max(owner - 1, 0)) : Pair{0.f, 0.f};
+        if (total.hi != 0.f || (!w.q && w.hot < 0)) break;
         w.q = nullptr;
         w.hot = -1;
     }
-    const bool usable = total > 0.0 && total < INFINITY && owner >= 0;
+    const bool usable = total.hi > 0.f && total.hi < INFINITY && owner >= 0;
     if (cta == 0) {
         for (int i = tid; i < n; i += kVerifyThreads)
             if (i != kept) a.out[begin + i] = i < kept ? a.tokens[begin + i + 1] : -1;
@@ -236,25 +252,22 @@ __global__ void __launch_bounds__(kVerifyThreads) fm_verify_kernel(const VerifyA
     }
     if (usable && cta == owner && warp == 0) {
         // The segment that holds the border, then the token, a warp's width at a time.
-        double run = before;
+        Pair run = before;
         int seg = 0;
         bool found = false;
         for (int x0 = 0; x0 < segments && !found; x0 += 32) {
-            const double mine = x0 + lane < segments ? s_seg[x0 + lane] : 0.0;
-            double sum = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += y;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, mine > 0.0 && run + sum > want), any = __ballot_sync(0xffffffffu, mine > 0.0);
+            const Pair mine = x0 + lane < segments ? s_seg[x0 + lane] : Pair{0.f, 0.f};
+            Pair upto = mine.upto();
+            upto.add(run);
+            const unsigned past = __ballot_sync(0xffffffffu, mine.hi > 0.f && upto.whole().above(want)), any = __ballot_sync(0xffffffffu, mine.hi > 0.f);
             const int at = past ? __ffs(past) - 1 : any ? 31 - __clz(any) : -1;
             found = past != 0;
             if (at >= 0) {
                 seg = x0 + at;
-                before = run + __shfl_sync(0xffffffffu, sum - mine, at);
+                const Pair b = upto.from(max(at - 1, 0));
+                before = at > 0 ? b : run;
             }
-            run += __shfl_sync(0xffffffffu, sum, 31);
+            run = upto.from(31);
         }
         const int64_t b = v0 + (int64_t)seg * a.segment, e = min(b + a.segment, v1);
         int64_t token = b;
@@ -265,27 +278,23 @@ __global__ void __launch_bounds__(kVerifyThreads) fm_verify_kernel(const VerifyA
             float p[8], q[8];
             probs8<T>(w.p, i, e, a.wide, p);
             if (w.q) probs8<T>(w.q, i, e, a.wide, q);
-            double x[8], sum = 0.0;
+            Pair x[8], sum{0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                x[j] = i + j == w.hot ? 0.0 : w.q ? (double)p[j] - (double)q[j] : (double)p[j];
-                x[j] = x[j] > 0.0 ? x[j] : 0.0;
-                sum += x[j];
+                x[j] = weight_of(w, p[j], q[j], i + j);
+                sum.add(x[j]);
             }
-            double upto = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
-            double here = run + (upto - sum);
+            const Pair upto = sum.upto();
+            Pair here{__shfl_up_sync(0xffffffffu, upto.hi, 1), __shfl_up_sync(0xffffffffu, upto.lo, 1)};
+            if (lane == 0) here = Pair{0.f, 0.f};
+            here.add(run);
             int first = -1, last = -1;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                here += x[j];
-                if (x[j] > 0.0) {
+                here.add(x[j]);
+                if (x[j].hi > 0.f) {
                     last = j;
-                    if (first < 0 && here > want) first = j;
+                    if (first < 0 && here.whole().above(want)) first = j;
                 }
             }
             const unsigned past = __ballot_sync(0xffffffffu, first >= 0), any = __ballot_sync(0xffffffffu, last >= 0);
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(kVerifyThreads) fm_verify_kernel(const VerifyA
                 const int at = past ? __ffs(past) - 1 : 31 - __clz(any);
                 token = i0 + at * 8 + __shfl_sync(0xffffffffu, past ? first : last, at);
             }
-            run += __shfl_sync(0xffffffffu, upto, 31);
+            run.add(upto.from(31));
         }
         if (lane == 0) a.out[row] = (int)token;
     }
