@@ -198,7 +198,7 @@ struct AppendRopeArgs {
 
 // Rows of a token in one line: its query heads, its key heads, its value heads.
 template <bool FP8, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) fm_paged_append_rope_kernel(const AppendRopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, 4) fm_paged_append_rope_kernel(const AppendRopeArgs a)
 {
     const int u = threadIdx.x & ((1 << a.shift) - 1);
     const int64_t t = (int64_t)blockIdx.x * (kRopeThreads >> a.shift) + (threadIdx.x >> a.shift);
@@ -423,7 +423,7 @@ fm_status fm_paged_append_rope(const void *q, int64_t q_tok, int64_t q_head, int
     a.status = dev_status;
     const int per = kRopeThreads >> a.shift, rows = Hq + 2 * cache->Hkv;
     const int64_t tiles = (T + per - 1) / per;
-    a.rows = rows_per_thread(tiles, rows, 16);
+    a.rows = rows_per_thread(tiles, rows, 8);
     const dim3 grid((unsigned)tiles, (unsigned)((rows + a.rows - 1) / a.rows));
     ProfScope ps(kKPagedAppendRope, stream);
     const bool inter = rotary->interleaved != 0;
