@@ -10,19 +10,18 @@
 // Few rows: bound by HBM (K once).  Key tiles (128 keys) of all (request, KV head) units lie end to end and are cut into
 // equal shares, as the plan has them for the attention.  Rows are 16 or 32 columns of the product.
 //   warp 0      walks the share, looks pages up (a batch of tiles at a time), TMA of K (ring of 128 to 160 KB)
-//   warp 1      TMEM; one thread issues K Q^T
-//   warps 2-5   thread = key: exponentials, sum, one add or store to the key's weight
-//   warps 6-9   Q and lse of the next units to shared memory (e4m3 caches: Q as two e4m3 terms, so that K is used as it is)
+//   warps 1, 10 one thread each issues K Q^T of every second tile (1: TMEM)
+//   warps 2-5   even tiles, thread = key: exponentials, sum, one add or store to the key's weight;  warps 6-9  odd ones
+//   warps 12-15 Q and lse of the next units to shared memory (e4m3 caches: Q as two e4m3 terms, so that K is used as it is)
 //
 // Many rows: a unit is one key tile of a (request, KV head), whose K stays in shared memory while the row tiles (128
 // rows: the query heads of the KV head times as many tokens as fit) that attend it stream through.  Per row tile 512
 // cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both about even, and in two
 // pipelines: four score buffers, two warpgroups on alternate row tiles.
 //   warp 0      claims units (longest first), TMA of K
-//   warp 1      TMEM; one thread issues K Q^T
+//   warps 1, 11 one thread each issues K Q^T of every second row tile (1: TMEM)
 //   warps 2-5   even row tiles, thread = key;  warps 6-9  odd ones
-//   warp 10     TMA of Q
-//   warp 11     lse of the row tiles
+//   warp 10     TMA of Q, lse of the row tiles
 //   warps 12-15 e4m3 caches only: K to bf16, exactly, once per unit
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -65,10 +64,13 @@ __device__ __forceinline__ void put(float *at, float sum, bool fresh)
 
 template <int D, bool FP8>
 struct FewCfg {
-    static constexpr int kThreads = 320;
+    static constexpr int kThreads = 512;
     static constexpr int kTile = 128 * D * (FP8 ? 1 : 2);
-    static constexpr int kSt = kTile == 32768 ? 5 : kTile == 16384 ? 8 : 16;    // 160 or 128 KB in flight
+    static constexpr int kSt = kTile == 32768 ? 6 : kTile == 16384 ? 8 : 16;    // 192 or 128 KB in flight
     static constexpr int kSBuf = 4, kQSlots = 3, kRing = 8;
+    // Who takes every second tile meets a stage in every phase or in none: with an odd number it would see a phase that another
+    // one was to wait for, and take the parity of the one before it for its own.
+    static_assert(kSt % 2 == 0 && kSBuf % 2 == 0, "stages that alternate");
     static constexpr int kQBox = kFewRows * 128;                  // 32 rows of 128 bytes
     static constexpr int kQTerm = kFewRows * D;                   // e4m3: from the first term to the second
     static constexpr int kQBytes = kFewRows * D * 2;
@@ -124,13 +126,13 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
         }
         for (int i = 0; i < C::kQSlots; ++i) {
             mbar_init(&bars[C::B_QF + i], 4);
-            mbar_init(&bars[C::B_QE + i], 5);
+            mbar_init(&bars[C::B_QE + i], 10);
         }
         for (int i = 0; i < C::kRing; ++i) {
             mbar_init(&bars[C::B_UF + i], 1);
-            mbar_init(&bars[C::B_UE + i], 9);
+            mbar_init(&bars[C::B_UE + i], 14);
         }
-        mbar_init(&bars[C::B_DRAIN], 1);
+        mbar_init(&bars[C::B_DRAIN], 2);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -243,8 +245,9 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
         if (lane == 0 && *abort)
             for (int i = (g > C::kSt ? g - C::kSt : 0); i < g; ++i)
                 mbar_wait_drain(&bars[C::B_KF + i % C::kSt], (i / C::kSt) & 1, a.status, a.wait_limit);
-    } else if (warp == 1) {
-        // -------------------------------------------- K Q^T
+    } else if (warp == 1 || warp == 10) {
+        // -------------------------------------------- K Q^T, every second tile
+        const int mine = warp == 1 ? 0 : 1;
         auto desc = [&](uint8_t *p) {             // K-major rows of 128 bytes, or of 64 (e4m3, d = 64)
             return FP8 && D == 64 ? sdesc_sw64(smem_u32(p), 16, 512) : sdesc_sw128(smem_u32(p), 16, 1024);
         };
@@ -259,6 +262,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
                 run = mbar_wait(&bars[C::B_QF + qs], (k / C::kQSlots) & 1, abort, a.status, lim);
                 const uint64_t dQ = desc(smem + C::kQ + qs * C::kQBytes);
                 for (int t = 0; run && t < u.n; ++t, ++g) {
+                    if ((g & 1) != mine) continue;
                     const int st = g % C::kSt, sb = g % C::kSBuf;
                     if (!mbar_wait(&bars[C::B_KF + st], (g / C::kSt) & 1, abort, a.status, a.wait_limit) ||
                         (g >= C::kSBuf && !mbar_wait(&bars[C::B_SE + sb], ((g / C::kSBuf) - 1) & 1, abort, a.status, lim))) {
@@ -290,8 +294,9 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
             tc_commit(&bars[C::B_DRAIN]);
             mbar_wait_drain(&bars[C::B_DRAIN], 0, a.status, a.wait_limit);
         }
-    } else if (warp < 6) {
-        // -------------------------------------------- exponentials and sums
+    } else if (warp < 10) {
+        // -------------------------------------------- exponentials and sums, every second tile
+        const int mine = warp < 6 ? 0 : 1;
         const int key = (warp & 3) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         int g = 0;
@@ -304,6 +309,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
             const float *fac = sCol + qs * 2 * kFewRows, *off = fac + kFewRows;
             const KeyRange kr = range_of(u.ctx, u.ntok);
             for (int t = 0; t < u.n; ++t, ++g) {
+                if ((g & 1) != mine) continue;
                 const int sb = g % C::kSBuf;
                 const int j = kr.tile(u.x0 + t) * kKeyTile + key;
                 // Rows that attend the key: tokens at its place or behind it, within the window.
@@ -358,10 +364,10 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
             __syncwarp();
             if (run && lane == 0) mbar_arrive(&bars[C::B_QE + qs]);
         }
-    } else {
+    } else if (warp >= 12) {
         // -------------------------------------------- Q and lse
         constexpr int LPR = D / 8, RPI = 32 / LPR, STEPS = kFewRows / RPI / 4;      // lanes per row, rows per step of a warp, its steps
-        const int mate = warp - 6, l = lane % LPR, r_in = lane / LPR;
+        const int mate = warp - 12, l = lane % LPR, r_in = lane / LPR;
         const float scale = a.scale_log2 * (FP8 ? *a.k_descale : 1.f);
         for (int k = 0;; ++k) {
             const FewUnit u = read_unit(k);
@@ -436,16 +442,17 @@ template <int D, bool FP8>
 struct ManyCfg {
     static constexpr int kThreads = FP8 ? 512 : 384;
     static constexpr int kBox = 128 * 128, kTile = 128 * D * 2, kRaw = 128 * D;
-    static constexpr int kQSt = FP8 ? 3 : 4, kSBuf = 4, kLSt = 4, kRing = 4;
+    static constexpr int kQSt = 4, kSBuf = 4, kLSt = 8, kRing = 4;    // (a place for lse beyond those of Q, so that its loads never wait for the sums)
+    static_assert(kQSt % 2 == 0 && kSBuf % 2 == 0 && kLSt % 2 == 0, "stages that alternate");
     static constexpr int kK = 0;                                  // two tiles of K
     static constexpr int kQ = kK + 2 * kTile;
-    static constexpr int kRawK = kQ + kQSt * kTile;               // e4m3: two tiles as they come
-    static constexpr int kLse = kRawK + (FP8 ? 2 * kRaw : 0);     // float [kLSt][128]
+    static constexpr int kRawK = kQ + kQSt * kTile;               // e4m3: a tile as it comes
+    static constexpr int kLse = kRawK + (FP8 ? kRaw : 0);         // float [kLSt][128]
     static constexpr int kSum = kLse + kLSt * 128 * 4;            // float [2][128]
     static constexpr int kUnit = kSum + 2 * 128 * 4;              // int [kRing][8]
     static constexpr int kFlag = kUnit + kRing * 8 * 4;           // int [2][8]
     static constexpr int kBar = kFlag + 16 * 4;
-    enum { B_KF = 0, B_KE = B_KF + 2, B_RF = B_KE + 2, B_RE = B_RF + 2, B_QF = B_RE + 2, B_QE = B_QF + kQSt, B_SF = B_QE + kQSt,
+    enum { B_KF = 0, B_KE = B_KF + 2, B_RF = B_KE + 2, B_RE, B_QF, B_QE = B_QF + kQSt, B_SF = B_QE + kQSt,
            B_SE = B_SF + kSBuf, B_LF = B_SE + kSBuf, B_LE = B_LF + kLSt, B_UF = B_LE + kLSt, B_UE = B_UF + kRing,
            B_DRAIN = B_UE + kRing, B_COUNT };
     static constexpr int kMisc = kBar + B_COUNT * 8;
@@ -492,10 +499,10 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         *abort = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars[C::B_KF + i], FP8 ? 4 : 1);
-            mbar_init(&bars[C::B_KE + i], 1);
-            mbar_init(&bars[C::B_RF + i], 1);
-            mbar_init(&bars[C::B_RE + i], 4);
+            mbar_init(&bars[C::B_KE + i], 2);
         }
+        mbar_init(&bars[C::B_RF], 1);
+        mbar_init(&bars[C::B_RE], 4);
         for (int i = 0; i < C::kQSt; ++i) {
             mbar_init(&bars[C::B_QF + i], 1);
             mbar_init(&bars[C::B_QE + i], 1);
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             mbar_init(&bars[C::B_UF + i], 1);
             mbar_init(&bars[C::B_UE + i], C::kReaders);
         }
-        mbar_init(&bars[C::B_DRAIN], 1);
+        mbar_init(&bars[C::B_DRAIN], 2);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -559,8 +566,8 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         PagedEntry en = list[0];
         const int nb = kKeyTile / w.box_keys;
         bool run = true;
-        int k = 0;
-        for (;; ++k) {
+        int started = 0;            // loads of K
+        for (int k = 0;; ++k) {
             ManyUnit u{-1};
             while (n_claims > 0) {
                 unsigned c = 0;
@@ -618,14 +625,18 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             }
             __syncwarp();
             if (u.n < 0) break;
-            if (k >= 2 && !warp_wait(&bars[(FP8 ? C::B_RE : C::B_KE) + ks], ((k >> 1) - 1) & 1, abort, a.status, lim)) break;
-            uint64_t *bar = &bars[(FP8 ? C::B_RF : C::B_KF) + ks];
+            // The tile's place: of two for K, one for codes on their way to the conversion.
+            if (FP8 ? k >= 1 && !warp_wait(&bars[C::B_RE], (k - 1) & 1, abort, a.status, lim)
+                    : k >= 2 && !warp_wait(&bars[C::B_KE + ks], ((k >> 1) - 1) & 1, abort, a.status, lim))
+                break;
+            uint64_t *bar = &bars[FP8 ? C::B_RF : C::B_KF + ks];
             // Wait test: one byte more than comes.
             if (lane == 0) mbar_arrive_expect_tx(bar, (FP8 ? C::kRaw : C::kTile) + a.withhold);
+            ++started;
             __syncwarp();
             if (lane < nb) {
                 if (FP8) {
-                    tma_load_4d(smem + C::kRawK + ks * C::kRaw + lane * w.box_keys * D, &tk, bar, 0, in, u.h, page);
+                    tma_load_4d(smem + C::kRawK + lane * w.box_keys * D, &tk, bar, 0, in, u.h, page);
                 } else {
 #pragma unroll
                     for (int half = 0; half < NBOX; ++half)
@@ -634,11 +645,13 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             }
             __syncwarp();
         }
-        if (lane == 0 && *abort)
-            for (int i = max(k - 2, 0); i <= k; ++i)        // (the last may not have been started: its wait ends at once or runs out)
-                mbar_wait_drain(&bars[(FP8 ? C::B_RF : C::B_KF) + (i & 1)], (i >> 1) & 1, a.status, a.wait_limit);
-    } else if (warp == 1) {
-        // -------------------------------------------- K Q^T
+        if (lane == 0 && *abort) {
+            if (FP8 && started > 0) mbar_wait_drain(&bars[C::B_RF], (started - 1) & 1, a.status, a.wait_limit);
+            for (int i = max(started - 2, 0); !FP8 && i < started; ++i) mbar_wait_drain(&bars[C::B_KF + (i & 1)], (i >> 1) & 1, a.status, a.wait_limit);
+        }
+    } else if (warp == 1 || warp == 11) {
+        // -------------------------------------------- K Q^T, every second row tile
+        const int mine = warp == 1 ? 0 : 1;
         constexpr uint32_t id = idesc_bf16(128, 128, false, false);
         int g = 0;
         bool run = true;
@@ -650,6 +663,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 run = mbar_wait(&bars[C::B_KF + ks], (k >> 1) & 1, abort, a.status, a.wait_limit);
                 const uint64_t dK = sdesc_sw128(smem_u32(smem + C::kK + ks * C::kTile), 16, 1024);
                 for (int t = 0; run && t < u.n; ++t, ++g) {
+                    if ((g & 1) != mine) continue;
                     const int st = g % C::kQSt, sb = g % C::kSBuf;
                     if (!mbar_wait(&bars[C::B_QF + st], (g / C::kQSt) & 1, abort, a.status, a.wait_limit) ||
                         (g >= C::kSBuf && !mbar_wait(&bars[C::B_SE + sb], ((g / C::kSBuf) - 1) & 1, abort, a.status, a.wait_limit))) {
@@ -704,8 +718,8 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 // Free of the mask: every row behind every key, within every window.
                 const bool full = u.kb + kKeyTile - 1 <= pos && ntok == tpt &&
                                   (s.window == 0 || u.kb > pos + tpt - 1 - s.window || u.kb + kKeyTile <= s.sink);
-                live = live && warp_wait(&bars[C::B_LF + ls], (g / C::kLSt) & 1, abort, a.status, lim);
                 live = live && warp_wait(&bars[C::B_SF + sb], (g / C::kSBuf) & 1, abort, a.status, lim);
+                live = live && warp_wait(&bars[C::B_LF + ls], (g / C::kLSt) & 1, abort, a.status, lim);
                 if (!live) continue;
                 tc_fence_after();
                 uint32_t keep[4];
@@ -757,33 +771,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             if (wg == 0 && live && at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum + sSum[(k & 1) * 128 + key], j >= u.ctx);
         }
     } else if (warp == 10) {
-        // -------------------------------------------- Q
-        int g = 0;
-        bool run = true;
-        for (int k = 0; run; ++k) {
-            const ManyUnit u = read_unit(k);
-            if (u.n < 0) break;
-            for (int t = 0; t < u.n; ++t, ++g) {
-                const int st = g % C::kQSt;
-                if (g >= C::kQSt && !warp_wait(&bars[C::B_QE + st], ((g / C::kQSt) - 1) & 1, abort, a.status, lim)) {
-                    run = false;
-                    break;
-                }
-                if (lane == 0) {
-                    uint64_t *bar = &bars[C::B_QF + st];
-                    mbar_arrive_expect_tx(bar, (uint32_t)(filled * D * 2));
-#pragma unroll
-                    for (int x = 0; x < NBOX; ++x)
-                        tma_load_3d(smem + C::kQ + st * C::kTile + x * C::kBox, &tq, bar, x * 64, u.h * G, u.tok0 + (u.t0 + t) * tpt);
-                }
-                __syncwarp();
-            }
-        }
-        if (lane == 0 && *abort)
-            for (int i = (g > C::kQSt ? g - C::kQSt : 0); i < g; ++i)
-                mbar_wait_drain(&bars[C::B_QF + i % C::kQSt], (i / C::kQSt) & 1, a.status, a.wait_limit);
-    } else if (warp == 11) {
-        // -------------------------------------------- lse of the rows
+        // -------------------------------------------- Q and lse of the row tiles
         int tk[4], at[4];                   // token of a row tile's row, and its place from the tile's first
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -805,12 +793,25 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             };
             fetch(0);
             for (int t = 0; t < u.n; ++t, ++g) {
-                const int ls = g % C::kLSt;
+                const int st = g % C::kQSt, ls = g % C::kLSt;
+                if (g >= C::kQSt && !warp_wait(&bars[C::B_QE + st], ((g / C::kQSt) - 1) & 1, abort, a.status, lim)) {
+                    run = false;
+                    break;
+                }
+                if (lane == 0) {
+                    uint64_t *bar = &bars[C::B_QF + st];
+                    mbar_arrive_expect_tx(bar, (uint32_t)(filled * D * 2));
+#pragma unroll
+                    for (int x = 0; x < NBOX; ++x)
+                        tma_load_3d(smem + C::kQ + st * C::kTile + x * C::kBox, &tq, bar, x * 64, u.h * G, u.tok0 + (u.t0 + t) * tpt);
+                }
+                __syncwarp();
                 float now[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) now[i] = -z[i] * kLog2e;
                 if (t + 1 < u.n) fetch(t + 1);
                 if (g >= C::kLSt && !warp_wait(&bars[C::B_LE + ls], ((g / C::kLSt) - 1) & 1, abort, a.status, lim)) {
+                    ++g;
                     run = false;
                     break;
                 }
@@ -820,6 +821,9 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&bars[C::B_LF + ls]);
             }
         }
+        if (lane == 0 && *abort)
+            for (int i = (g > C::kQSt ? g - C::kQSt : 0); i < g; ++i)
+                mbar_wait_drain(&bars[C::B_QF + i % C::kQSt], (i / C::kQSt) & 1, a.status, a.wait_limit);
     } else if (FP8) {
         // -------------------------------------------- K to bf16
         const int mate = warp & 3;
@@ -834,9 +838,9 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             const ManyUnit u = read_unit(k);
             if (u.n < 0) break;
             const int ks = k & 1;
-            if (!warp_wait(&bars[C::B_RF + ks], (k >> 1) & 1, abort, a.status, lim)) break;
+            if (!warp_wait(&bars[C::B_RF], k & 1, abort, a.status, lim)) break;
             if (k >= 2 && !warp_wait(&bars[C::B_KE + ks], ((k >> 1) - 1) & 1, abort, a.status, lim)) break;
-            const uint8_t *raw = smem + C::kRawK + ks * C::kRaw;
+            const uint8_t *raw = smem + C::kRawK;
             uint8_t *tile = smem + C::kK + ks * C::kTile;
 #pragma unroll 4
             for (int i = mate; i < 128 / RPI; i += 4) {
@@ -849,7 +853,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&bars[C::B_KF + ks]);
-                mbar_arrive(&bars[C::B_RE + ks]);
+                mbar_arrive(&bars[C::B_RE]);
             }
         }
     }

@@ -72,6 +72,13 @@ def test_windows(fm, new, window, sink, e4m3):
     check(fm, base.Batch(fm, [700, 333, 64], new, 8, 2, 128, 16, window=window, sink=sink, e4m3=e4m3, seed=window))
 
 
+@pytest.mark.parametrize("d,e4m3", [(128, False), (64, False), (128, True), (64, True)])
+@pytest.mark.parametrize("new", [[1, 2, 1], [60, 1, 200]])
+def test_long_walks(fm, new, d, e4m3):
+    """Dozens of tiles for every block: every stage comes round many times."""
+    check(fm, base.Batch(fm, [20000, 9000, 14001], new, 16, 8, d, 64, e4m3=e4m3, seed=12))
+
+
 @pytest.mark.parametrize("layout", ["tokens", "pairs"])
 @pytest.mark.parametrize("new", [[2, 1], [90, 1]])
 def test_strides(fm, layout, new):
