@@ -9,18 +9,18 @@
 //
 // Few rows: bound by HBM (K once).  Key tiles (128 keys) of all (request, KV head) units lie end to end and are cut into
 // equal shares, as the plan has them for the attention.  Rows are 16 or 32 columns of the product.
-//   warp 0      walks the share, looks pages up (a batch of tiles at a time), TMA of K (ring of 128 to 160 KB)
+//   warps 0, 11 walk the share, look pages up (a batch of tiles at a time), TMA of K, alternate tiles (ring of 128 to 192 KB)
 //   warps 1, 10 one thread each issues K Q^T of every second tile (1: TMEM)
 //   warps 2-5   even tiles, thread = key: exponentials, sum, one add or store to the key's weight;  warps 6-9  odd ones
 //   warps 12-15 Q and lse of the next units to shared memory (e4m3 caches: Q as two e4m3 terms, so that K is used as it is)
 //
-// Many rows: a unit is one key tile of a (request, KV head), whose K stays in shared memory while the row tiles (128
-// rows: the query heads of the KV head times as many tokens as fit) that attend it stream through.  Per row tile 512
-// cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both about even, and in two
-// pipelines: four score buffers, two warpgroups on alternate row tiles.
+// Many rows: a unit is two key tiles of a (request, KV head), whose K stays in shared memory while the row tiles (128
+// rows: the query heads of the KV head times as many tokens as fit) that attend them stream through, each multiplied by
+// both.  Per pair of tiles 512 cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both
+// about even, and each tile has its own issuing thread, two score buffers and a warpgroup.
 //   warp 0      claims units (longest first), TMA of K
-//   warps 1, 11 one thread each issues K Q^T of every second row tile (1: TMEM)
-//   warps 2-5   even row tiles, thread = key;  warps 6-9  odd ones
+//   warps 1, 11 one thread each issues K Q^T of one of the key tiles (1: TMEM)
+//   warps 2-5   first key tile, thread = key;  warps 6-9  second one
 //   warp 10     TMA of Q, lse of the row tiles
 //   warps 12-15 e4m3 caches only: K to bf16, exactly, once per unit
 #include <cuda.h>
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
         }
         for (int i = 0; i < C::kRing; ++i) {
             mbar_init(&bars[C::B_UF + i], 1);
-            mbar_init(&bars[C::B_UE + i], 14);
+            mbar_init(&bars[C::B_UE + i], 15);
         }
         mbar_init(&bars[C::B_DRAIN], 2);
         fence_barrier_init();
@@ -158,27 +158,44 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
     };
     auto range_of = [&](int ctx, int n) { return key_range(ctx, ctx + n - 1, s.window, s.sink); };
 
-    if (warp == 0) {
-        // -------------------------------------------- the share's units; K
+    if (warp == 0 || warp == 11) {
+        // -------------------------------------------- the share's units (warp 0); K, every second tile each
+        const int mine = warp == 0 ? 0 : 1;
         const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_few);
         const PagedStart st0 = reinterpret_cast<const PagedStart *>(a.plan + a.L.off_start)[blockIdx.x];
         int left = st0.count, e = st0.e, h = st0.h, x = st0.x;
         PagedEntry en = st0.ent, en_next = list[min(e + 1, hd->n_few - 1)];
-        // Cuts the next unit off the share.
-        auto next_unit = [&]() -> FewUnit {
-            if (left <= 0) return FewUnit{-1};
-            const int n = min(left, range_of(en.ctx, en.n).n - x);
-            const FewUnit u{n, en.r, h, en.tok0, en.n, en.ctx, x};
-            left -= n;
-            x = 0;
-            if (++h == s.Hkv) {
-                h = 0;
-                ++e;
-                en = en_next;
-                en_next = list[min(e + 1, hd->n_few - 1)];
+        bool run = true;
+        // Cuts unit k off the share, and tells the others.
+        auto next_unit = [&](int k) -> FewUnit {
+            FewUnit u{-1};
+            if (left > 0) {
+                const int n = min(left, range_of(en.ctx, en.n).n - x);
+                u = FewUnit{n, en.r, h, en.tok0, en.n, en.ctx, x};
+                left -= n;
+                x = 0;
+                if (++h == s.Hkv) {
+                    h = 0;
+                    ++e;
+                    en = en_next;
+                    en_next = list[min(e + 1, hd->n_few - 1)];
+                }
             }
+            const int slot = k % C::kRing;
+            if (k >= C::kRing && !warp_wait(&bars[C::B_UE + slot], ((k / C::kRing) - 1) & 1, abort, a.status, lim)) {
+                run = false;
+                return FewUnit{-1};
+            }
+            if (lane == 0) {
+                const int f[7] = {u.n, u.r, u.h, u.tok0, u.ntok, u.ctx, u.x0};
+#pragma unroll
+                for (int i = 0; i < 7; ++i) sUnit[slot * 8 + i] = f[i];
+                mbar_arrive(&bars[C::B_UF + slot]);
+            }
+            __syncwarp();
             return u;
         };
+        auto unit = [&](int k) { return mine == 0 ? next_unit(k) : read_unit(k); };
         const int nb = kKeyTile / w.box_keys, batch = 32 / nb;     // boxes of a tile; tiles whose pages one look finds
         const int my_tile = lane / nb, my_box = lane - my_tile * nb;
         // Page and place in it of the lane's box of the unit's tile t0 + my_tile.
@@ -200,26 +217,18 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
             return box;
         };
         int g = 0;
-        bool run = true;
-        FewUnit u = next_unit();
+        unsigned loaded = 0;            // stages that this warp has loaded
+        FewUnit u = unit(0);
         Box box = look_up(u, 0);
-        for (int k = 0; run; ++k) {
-            const FewUnit un = next_unit();
+        // A unit ahead: the pages of its first tiles are on their way while this one's tiles are loaded.
+        for (int k = 0; run && u.n >= 0; ++k) {
+            const FewUnit un = unit(k + 1);
             const Box box_next = look_up(un, 0);
-            const int slot = k % C::kRing;
-            if (k >= C::kRing && !warp_wait(&bars[C::B_UE + slot], ((k / C::kRing) - 1) & 1, abort, a.status, lim)) break;
-            if (lane == 0) {
-                const int f[7] = {u.n, u.r, u.h, u.tok0, u.ntok, u.ctx, u.x0};
-#pragma unroll
-                for (int i = 0; i < 7; ++i) sUnit[slot * 8 + i] = f[i];
-                mbar_arrive(&bars[C::B_UF + slot]);
-            }
-            __syncwarp();
-            if (u.n < 0) break;
             for (int t0 = 0; run && t0 < u.n; t0 += batch) {
                 const Box now = box;
                 if (t0 + batch < u.n) box = look_up(u, t0 + batch);
                 for (int t = t0; t < min(t0 + batch, u.n); ++t, ++g) {
+                    if ((g & 1) != mine) continue;
                     const int st = g % C::kSt;
                     if (g >= C::kSt && !warp_wait(&bars[C::B_KE + st], ((g / C::kSt) - 1) & 1, abort, a.status, lim)) {
                         run = false;
@@ -228,6 +237,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
                     uint64_t *bar = &bars[C::B_KF + st];
                     // Wait test: one byte more than comes.
                     if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile + (a.withhold && blockIdx.x == 0 && g == 1 ? 1 : 0));
+                    loaded |= 1u << st;
                     __syncwarp();
                     if (t - t0 == my_tile) {
                         uint8_t *tile = smem + st * C::kTile;
@@ -241,10 +251,13 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
             u = un;
             box = box_next;
         }
-        // After an abort: copies in flight end before the CTA leaves.
+        // After an abort: copies in flight end before the CTA leaves (the last load of a stage is that of its last tile before g).
         if (lane == 0 && *abort)
-            for (int i = (g > C::kSt ? g - C::kSt : 0); i < g; ++i)
-                mbar_wait_drain(&bars[C::B_KF + i % C::kSt], (i / C::kSt) & 1, a.status, a.wait_limit);
+            for (int st = 0; st < C::kSt; ++st)
+                if (loaded >> st & 1) {
+                    const int last = g - 1 - ((g - 1 - st) % C::kSt + C::kSt) % C::kSt;
+                    mbar_wait_drain(&bars[C::B_KF + st], (last / C::kSt) & 1, a.status, a.wait_limit);
+                }
     } else if (warp == 1 || warp == 10) {
         // -------------------------------------------- K Q^T, every second tile
         const int mine = warp == 1 ? 0 : 1;
@@ -442,31 +455,30 @@ template <int D, bool FP8>
 struct ManyCfg {
     static constexpr int kThreads = FP8 ? 512 : 384;
     static constexpr int kBox = 128 * 128, kTile = 128 * D * 2, kRaw = 128 * D;
-    static constexpr int kQSt = 4, kSBuf = 4, kLSt = 8, kRing = 4;    // (a place for lse beyond those of Q, so that its loads never wait for the sums)
-    static_assert(kQSt % 2 == 0 && kSBuf % 2 == 0 && kLSt % 2 == 0, "stages that alternate");
-    static constexpr int kK = 0;                                  // two tiles of K
-    static constexpr int kQ = kK + 2 * kTile;
-    static constexpr int kRawK = kQ + kQSt * kTile;               // e4m3: a tile as it comes
-    static constexpr int kLse = kRawK + (FP8 ? kRaw : 0);         // float [kLSt][128]
-    static constexpr int kSum = kLse + kLSt * 128 * 4;            // float [2][128]
-    static constexpr int kUnit = kSum + 2 * 128 * 4;              // int [kRing][8]
-    static constexpr int kFlag = kUnit + kRing * 8 * 4;           // int [2][8]
-    static constexpr int kBar = kFlag + 16 * 4;
-    enum { B_KF = 0, B_KE = B_KF + 2, B_RF = B_KE + 2, B_RE, B_QF, B_QE = B_QF + kQSt, B_SF = B_QE + kQSt,
-           B_SE = B_SF + kSBuf, B_LF = B_SE + kSBuf, B_LE = B_LF + kLSt, B_UF = B_LE + kLSt, B_UE = B_UF + kRing,
-           B_DRAIN = B_UE + kRing, B_COUNT };
+    // bf16: K of two units. e4m3: K of one unit, and of the next as it comes.
+    static constexpr int kKBuf = FP8 ? 1 : 2, kQSt = D == 64 ? 6 : FP8 ? 4 : 3, kLSt = 4, kRing = 4;
+    static constexpr int kK = 0;                                  // [kKBuf][2 key tiles]
+    static constexpr int kQ = kK + kKBuf * 2 * kTile;
+    static constexpr int kRawK = kQ + kQSt * kTile;               // e4m3: [2 key tiles]
+    static constexpr int kLse = kRawK + (FP8 ? 2 * kRaw : 0);     // float [kLSt][128]
+    static constexpr int kUnit = kLse + kLSt * 128 * 4;           // int [kRing][kInts]
+    static constexpr int kInts = 12;
+    static constexpr int kBar = kUnit + kRing * kInts * 4;
+    enum { B_KF = 0, B_KE = B_KF + kKBuf, B_RF = B_KE + kKBuf, B_RE, B_QF, B_QE = B_QF + kQSt, B_SF = B_QE + kQSt, B_SE = B_SF + 4,
+           B_LF = B_SE + 4, B_LE = B_LF + kLSt, B_UF = B_LE + kLSt, B_UE = B_UF + kRing, B_DRAIN = B_UE + kRing, B_COUNT };
     static constexpr int kMisc = kBar + B_COUNT * 8;
     // Over 114 KB, so that one CTA with all of TMEM is resident per SM.
     static constexpr int kBytes = kMisc + 64 > 120 * 1024 ? kMisc + 64 : 120 * 1024;
-    static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(kBytes <= 227 * 1024 && kBar % 8 == 0, "shared memory");
     static constexpr int kReaders = 11 + (FP8 ? 4 : 0);
 };
 
-// A key tile and the row tiles that attend it.
+// Two key tiles and the row tiles that attend one of them.
 struct ManyUnit {
     int n;                  // row tiles; -1: no more
     int r, h, tok0, ntok, ctx;
-    int kb, t0;             // first key, first row tile
+    int t0;                 // first row tile
+    int kb[2];              // first key of either tile (the second one may lie behind the request: no row attends it)
 };
 
 template <int D, bool FP8>
@@ -477,9 +489,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
     constexpr int NBOX = D / 64;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *sLse = reinterpret_cast<float *>(smem + C::kLse);
-    float *sSum = reinterpret_cast<float *>(smem + C::kSum);
     volatile int *sUnit = reinterpret_cast<volatile int *>(smem + C::kUnit);
-    volatile int *sFlag = reinterpret_cast<volatile int *>(smem + C::kFlag);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kBar);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kMisc + 4);
@@ -497,7 +507,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
     const int G = s.Hq / s.Hkv, tpt = 128 / G;      // tokens of a row tile
     if (warp == 0 && lane == 0) {
         *abort = 0;
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kKBuf; ++i) {
             mbar_init(&bars[C::B_KF + i], FP8 ? 4 : 1);
             mbar_init(&bars[C::B_KE + i], 2);
         }
@@ -505,15 +515,15 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         mbar_init(&bars[C::B_RE], 4);
         for (int i = 0; i < C::kQSt; ++i) {
             mbar_init(&bars[C::B_QF + i], 1);
-            mbar_init(&bars[C::B_QE + i], 1);
+            mbar_init(&bars[C::B_QE + i], 2);
         }
-        for (int i = 0; i < C::kSBuf; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&bars[C::B_SF + i], 1);
             mbar_init(&bars[C::B_SE + i], 4);
         }
         for (int i = 0; i < C::kLSt; ++i) {
             mbar_init(&bars[C::B_LF + i], 1);
-            mbar_init(&bars[C::B_LE + i], 4);
+            mbar_init(&bars[C::B_LE + i], 8);
         }
         for (int i = 0; i < C::kRing; ++i) {
             mbar_init(&bars[C::B_UF + i], 1);
@@ -542,8 +552,8 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         const int slot = k % C::kRing;
         ManyUnit u{-1};
         if (!warp_wait(&bars[C::B_UF + slot], (k / C::kRing) & 1, abort, a.status, lim)) return u;
-        const volatile int *p = sUnit + slot * 8;
-        u = ManyUnit{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+        const volatile int *p = sUnit + slot * C::kInts;
+        u = ManyUnit{p[0], p[1], p[2], p[3], p[4], p[5], p[6], {p[7], p[8]}};
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[C::B_UE + slot]);
         return u;
@@ -553,7 +563,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         // -------------------------------------------- claims; K
         const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_many);
         unsigned *claim = reinterpret_cast<unsigned *>(a.plan + a.L.off_claim);
-        auto units_of = [&](const PagedEntry &en) { return (int64_t)key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink).n * s.Hkv; };
+        auto units_of = [&](const PagedEntry &en) { return (int64_t)((key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink).n + 1) / 2) * s.Hkv; };
         int64_t total = 0;
         for (int i = lane; i < hd->n_many; i += 32) total += units_of(list[i]);
 #pragma unroll
@@ -593,19 +603,29 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 }
                 const int local = (int)((int64_t)c - cum), x = local / s.Hkv;
                 const KeyRange kr = key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink);
-                u = ManyUnit{0, en.r, local - x * s.Hkv, en.tok0, en.n, en.ctx, kr.tile(x) * kKeyTile, 0};
-                u.t0 = max(0, u.kb - en.ctx) / tpt;
-                int t1 = (en.n + tpt - 1) / tpt;
-                if (s.window > 0 && u.kb >= s.sink) t1 = min(t1, max(u.kb - en.ctx + kKeyTile - 2 + s.window + tpt, 0) / tpt);
+                u = ManyUnit{0, en.r, local - x * s.Hkv, en.tok0, en.n, en.ctx, 0, {0, 0}};
+                // Row tiles [t0, t1) attend the unit: from the first token at its first key's place on, until the last within a
+                // window of its last key.
+                int t1 = 0;
+                u.t0 = INT32_MAX;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    u.kb[y] = 2 * x + y < kr.n ? kr.tile(2 * x + y) * kKeyTile : (kr.hi + kKeyTile - 1) / kKeyTile * kKeyTile;
+                    if (2 * x + y >= kr.n) continue;
+                    u.t0 = min(u.t0, max(0, u.kb[y] - en.ctx) / tpt);
+                    int last = (en.n + tpt - 1) / tpt;
+                    if (s.window > 0 && u.kb[y] >= s.sink) last = min(last, max(u.kb[y] - en.ctx + kKeyTile - 2 + s.window + tpt, 0) / tpt);
+                    t1 = max(t1, last);
+                }
                 u.n = t1 - u.t0;
                 if (u.n > 0) break;
                 u.n = -1;
             }
-            // The tile's pages, looked up before the waits.
+            // The tiles' pages, looked up before the waits: lane i the box i of the two tiles.
             int page = s.num_pages, in = 0;
-            if (u.n > 0 && lane < nb) {
+            if (u.n > 0 && lane < 2 * nb) {
                 const KeyRange kr = key_range(u.ctx, u.ctx + u.ntok - 1, s.window, s.sink);
-                const int j = u.kb + lane * w.box_keys;
+                const int j = (lane < nb ? u.kb[0] + lane * w.box_keys : u.kb[1] + (lane - nb) * w.box_keys);
                 const int b = a.page_shift >= 0 ? j >> a.page_shift : j / s.page_size, b0 = b * s.page_size;
                 in = j - b0;
                 if (j < kr.hi && (b0 + s.page_size > kr.lo || b0 < s.sink)) {
@@ -614,59 +634,60 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                     else set_status(a.status, FM_ERR_PAGES);
                 }
             }
-            const int slot = k % C::kRing, ks = k & 1;
+            const int slot = k % C::kRing, ks = k % C::kKBuf;
             if (k >= C::kRing && !warp_wait(&bars[C::B_UE + slot], ((k / C::kRing) - 1) & 1, abort, a.status, lim)) run = false;
             if (!run) break;
             if (lane == 0) {
-                const int f[8] = {u.n, u.r, u.h, u.tok0, u.ntok, u.ctx, u.kb, u.t0};
+                const int f[9] = {u.n, u.r, u.h, u.tok0, u.ntok, u.ctx, u.t0, u.kb[0], u.kb[1]};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sUnit[slot * 8 + i] = f[i];
+                for (int i = 0; i < 9; ++i) sUnit[slot * C::kInts + i] = f[i];
                 mbar_arrive(&bars[C::B_UF + slot]);
             }
             __syncwarp();
             if (u.n < 0) break;
-            // The tile's place: of two for K, one for codes on their way to the conversion.
+            // Where the tiles go is free again: the codes converted, or K multiplied.
             if (FP8 ? k >= 1 && !warp_wait(&bars[C::B_RE], (k - 1) & 1, abort, a.status, lim)
-                    : k >= 2 && !warp_wait(&bars[C::B_KE + ks], ((k >> 1) - 1) & 1, abort, a.status, lim))
+                    : k >= C::kKBuf && !warp_wait(&bars[C::B_KE + ks], (k / C::kKBuf - 1) & 1, abort, a.status, lim))
                 break;
             uint64_t *bar = &bars[FP8 ? C::B_RF : C::B_KF + ks];
             // Wait test: one byte more than comes.
-            if (lane == 0) mbar_arrive_expect_tx(bar, (FP8 ? C::kRaw : C::kTile) + a.withhold);
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * (FP8 ? C::kRaw : C::kTile) + a.withhold);
             ++started;
             __syncwarp();
-            if (lane < nb) {
+            if (lane < 2 * nb) {
+                const int y = lane < nb ? 0 : 1, box = lane - y * nb;
                 if (FP8) {
-                    tma_load_4d(smem + C::kRawK + lane * w.box_keys * D, &tk, bar, 0, in, u.h, page);
+                    tma_load_4d(smem + C::kRawK + y * C::kRaw + box * w.box_keys * D, &tk, bar, 0, in, u.h, page);
                 } else {
 #pragma unroll
                     for (int half = 0; half < NBOX; ++half)
-                        tma_load_4d(smem + C::kK + ks * C::kTile + half * C::kBox + lane * w.box_keys * 128, &tk, bar, half * 64, in, u.h, page);
+                        tma_load_4d(smem + C::kK + (ks * 2 + y) * C::kTile + half * C::kBox + box * w.box_keys * 128, &tk, bar, half * 64, in, u.h, page);
                 }
             }
             __syncwarp();
         }
         if (lane == 0 && *abort) {
             if (FP8 && started > 0) mbar_wait_drain(&bars[C::B_RF], (started - 1) & 1, a.status, a.wait_limit);
-            for (int i = max(started - 2, 0); !FP8 && i < started; ++i) mbar_wait_drain(&bars[C::B_KF + (i & 1)], (i >> 1) & 1, a.status, a.wait_limit);
+            for (int i = max(started - C::kKBuf, 0); !FP8 && i < started; ++i)
+                mbar_wait_drain(&bars[C::B_KF + i % C::kKBuf], (i / C::kKBuf) & 1, a.status, a.wait_limit);
         }
     } else if (warp == 1 || warp == 11) {
-        // -------------------------------------------- K Q^T, every second row tile
-        const int mine = warp == 1 ? 0 : 1;
+        // -------------------------------------------- K Q^T of one of the key tiles
         constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+        const int mine = warp == 1 ? 0 : 1;
         int g = 0;
         bool run = true;
         for (int k = 0; run; ++k) {
             const ManyUnit u = read_unit(k);
             if (u.n < 0) break;
             if (lane == 0) {
-                const int ks = k & 1;
-                run = mbar_wait(&bars[C::B_KF + ks], (k >> 1) & 1, abort, a.status, a.wait_limit);
-                const uint64_t dK = sdesc_sw128(smem_u32(smem + C::kK + ks * C::kTile), 16, 1024);
+                const int ks = k % C::kKBuf;
+                run = mbar_wait(&bars[C::B_KF + ks], (k / C::kKBuf) & 1, abort, a.status, a.wait_limit);
+                const uint64_t dK = sdesc_sw128(smem_u32(smem + C::kK + (ks * 2 + mine) * C::kTile), 16, 1024);
                 for (int t = 0; run && t < u.n; ++t, ++g) {
-                    if ((g & 1) != mine) continue;
-                    const int st = g % C::kQSt, sb = g % C::kSBuf;
+                    const int st = g % C::kQSt, sb = 2 * mine + (g & 1);
                     if (!mbar_wait(&bars[C::B_QF + st], (g / C::kQSt) & 1, abort, a.status, a.wait_limit) ||
-                        (g >= C::kSBuf && !mbar_wait(&bars[C::B_SE + sb], ((g / C::kSBuf) - 1) & 1, abort, a.status, a.wait_limit))) {
+                        (g >= 2 && !mbar_wait(&bars[C::B_SE + sb], ((g >> 1) - 1) & 1, abort, a.status, a.wait_limit))) {
                         run = false;
                         break;
                     }
@@ -689,65 +710,61 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             mbar_wait_drain(&bars[C::B_DRAIN], 0, a.status, a.wait_limit);
         }
     } else if (warp < 10) {
-        // -------------------------------------------- exponentials and sums
-        const int wg = warp < 6 ? 0 : 1;                  // the tiles g with g & 1 == wg
+        // -------------------------------------------- exponentials and sums of one of the key tiles
+        const int mine = warp < 6 ? 0 : 1;
         const int key = (warp & 3) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const float scale = a.scale_log2 * (FP8 ? *a.k_descale : 1.f);
         const uint64_t sc2 = f2_pack(scale, scale);
-        // False for the whole warp once a wait gave up: it still reaches every named barrier, so that the other
-        // warpgroup is never left waiting.
-        bool live = true;
-        int g0 = 0;
-        for (int k = 0;; ++k) {
+        int g = 0;
+        bool run = true;
+        for (int k = 0; run; ++k) {
             const ManyUnit u = read_unit(k);
-            if (lane == 0) sFlag[(k & 1) * 8 + (warp - 2)] = u.n >= 0 ? 1 : 0;
-            named_bar_sync(1, 256);
-            int all = sFlag[(k & 1) * 8];
-#pragma unroll
-            for (int q = 1; q < 8; ++q) all &= sFlag[(k & 1) * 8 + q];
-            if (!all) break;
-            const int j = u.kb + key, seq = u.ctx + u.ntok;
+            if (u.n < 0) break;
+            const int kb = mine ? u.kb[1] : u.kb[0], j = kb + key, seq = u.ctx + u.ntok;
             const bool some = j < seq && (s.window == 0 || j > u.ctx - s.window || j < s.sink);     // attended by some row
-            int64_t at = -1;
-            if (wg == 0 && some) at = weight_place(a, u.r, j);
+            const int64_t at = some ? weight_place(a, u.r, j) : -1;
             float sum = 0.f;
-            for (int t = (wg - g0) & 1; t < u.n; t += 2) {
-                const int g = g0 + t, sb = g % C::kSBuf, ls = g % C::kLSt;
+            for (int t = 0; t < u.n; ++t, ++g) {
+                const int sb = 2 * mine + (g & 1), ls = g % C::kLSt;
                 const int tok = (u.t0 + t) * tpt, pos = u.ctx + tok, ntok = min(tpt, u.ntok - tok);
                 // Free of the mask: every row behind every key, within every window.
-                const bool full = u.kb + kKeyTile - 1 <= pos && ntok == tpt &&
-                                  (s.window == 0 || u.kb > pos + tpt - 1 - s.window || u.kb + kKeyTile <= s.sink);
-                live = live && warp_wait(&bars[C::B_SF + sb], (g / C::kSBuf) & 1, abort, a.status, lim);
-                live = live && warp_wait(&bars[C::B_LF + ls], (g / C::kLSt) & 1, abort, a.status, lim);
-                if (!live) continue;
+                const bool full = kb + kKeyTile - 1 <= pos && ntok == tpt && (s.window == 0 || kb > pos + tpt - 1 - s.window || kb + kKeyTile <= s.sink);
+                if (!warp_wait(&bars[C::B_LF + ls], (g / C::kLSt) & 1, abort, a.status, lim) ||
+                    !warp_wait(&bars[C::B_SF + sb], (g >> 1) & 1, abort, a.status, lim)) {
+                    run = false;
+                    break;
+                }
                 tc_fence_after();
                 uint32_t keep[4];
+                bool any = true;
                 if (!full) {
-                    const int lo = min(max(j - pos, 0), 128) * G, hi = (s.window > 0 && j >= s.sink ? min(max(j - pos + s.window, 0), ntok) : ntok) * G;
+                    const int lo = some ? min(max(j - pos, 0), 128) * G : 128;
+                    const int hi = (s.window > 0 && j >= s.sink ? min(max(j - pos + s.window, 0), ntok) : ntok) * G;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) keep[c] = row_bits32(lo - 32 * c, hi - 32 * c);
+                    any = __any_sync(0xffffffffu, lo < hi);
                 }
                 const uint32_t tS = tmem + sb * 128 + lane_off;
                 const float4 *z = reinterpret_cast<const float4 *>(sLse + ls * 128);
                 uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
                 uint32_t v[2][32];
-                tmem_ld32(tS, v[0]);
+                if (any) tmem_ld32(tS, v[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
+                    if (!any) break;
                     tmem_ld_wait();
                     tmem_reg_fence(v[c & 1]);
-                    if (c < 3) {
-                        tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
-                    }
+                    if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
                     uint32_t (&x)[32] = v[c & 1];
                     if (!full) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = (keep[c] >> i) & 1 ? x[i] : 0xff800000u;
+                    }
+                    if (c == 3) {                   // every score is in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -760,15 +777,15 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[C::B_LE + ls]);
+                if (lane == 0) {
+                    if (!any) mbar_arrive(&bars[C::B_SE + sb]);
+                    mbar_arrive(&bars[C::B_LE + ls]);
+                }
                 float s0, s1;
                 f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
                 sum += s0 + s1;
             }
-            g0 += u.n;
-            if (wg == 1) sSum[(k & 1) * 128 + key] = sum;
-            named_bar_sync(1, 256);
-            if (wg == 0 && live && at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum + sSum[(k & 1) * 128 + key], j >= u.ctx);
+            if (run && at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum, j >= u.ctx);
         }
     } else if (warp == 10) {
         // -------------------------------------------- Q and lse of the row tiles
@@ -837,22 +854,21 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         for (int k = 0;; ++k) {
             const ManyUnit u = read_unit(k);
             if (u.n < 0) break;
-            const int ks = k & 1;
             if (!warp_wait(&bars[C::B_RF], k & 1, abort, a.status, lim)) break;
-            if (k >= 2 && !warp_wait(&bars[C::B_KE + ks], ((k >> 1) - 1) & 1, abort, a.status, lim)) break;
+            if (k >= 1 && !warp_wait(&bars[C::B_KE], (k - 1) & 1, abort, a.status, lim)) break;
             const uint8_t *raw = smem + C::kRawK;
-            uint8_t *tile = smem + C::kK + ks * C::kTile;
 #pragma unroll 4
-            for (int i = mate; i < 128 / RPI; i += 4) {
-                const int row = i * RPI + r_in;
-                const uint2 x = *reinterpret_cast<const uint2 *>(raw + row * D + l * 8);
+            for (int i = mate; i < 256 / RPI; i += 4) {
+                const int line = i * RPI + r_in, row = line & 127;
+                const uint2 x = *reinterpret_cast<const uint2 *>(raw + line * D + l * 8);
+                uint8_t *tile = smem + C::kK + (line >> 7) * C::kTile;
                 st_shared_v4(tile + (l >> 3) * C::kBox + row * 128 + (((l & 7) ^ (row & 7)) << 4),
                              make_uint4(bf16x2(x.x), bf16x2(x.x >> 16), bf16x2(x.y), bf16x2(x.y >> 16)));
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bars[C::B_KF + ks]);
+                mbar_arrive(&bars[C::B_KF]);
                 mbar_arrive(&bars[C::B_RE]);
             }
         }
