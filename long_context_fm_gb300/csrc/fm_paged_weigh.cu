@@ -17,12 +17,12 @@
 // Many rows: a unit is two key tiles of a (request, KV head), whose K stays in shared memory while the row tiles (128
 // rows: the query heads of the KV head times as many tokens as fit) that attend them stream through, each multiplied by
 // both.  Per pair of tiles 512 cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both
-// about even, and each tile has its own issuing thread, two score buffers and a warpgroup.
+// about even, and each tile has its own issuing thread, two score buffers and a warpgroup for each of them.
 //   warp 0      claims units (longest first), TMA of K
-//   warps 1, 11 one thread each issues K Q^T of one of the key tiles (1: TMEM)
-//   warps 2-5   first key tile, thread = key;  warps 6-9  second one
-//   warp 10     TMA of Q, lse of the row tiles
-//   warps 12-15 e4m3 caches only: K to bf16, exactly, once per unit
+//   warps 1, 19 one thread each issues K Q^T of one of the key tiles (1: TMEM)
+//   warps 2-5, 6-9    first key tile, even and odd row tiles, thread = key;  warps 10-13, 14-17  second one
+//   warp 18     TMA of Q, lse of the row tiles
+//   warps 20-23 e4m3 caches only: K to bf16, exactly, once per unit
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
 
 template <int D, bool FP8>
 struct ManyCfg {
-    static constexpr int kThreads = FP8 ? 512 : 384;
+    static constexpr int kThreads = FP8 ? 768 : 640;
     static constexpr int kBox = 128 * 128, kTile = 128 * D * 2, kRaw = 128 * D;
     // bf16: K of two units. e4m3: K of one unit, and of the next as it comes.
     static constexpr int kKBuf = FP8 ? 1 : 2, kQSt = D == 64 ? 6 : FP8 ? 4 : 3, kLSt = 4, kRing = 4;
@@ -465,12 +465,13 @@ struct ManyCfg {
     static constexpr int kInts = 12;
     static constexpr int kBar = kUnit + kRing * kInts * 4;
     enum { B_KF = 0, B_KE = B_KF + kKBuf, B_RF = B_KE + kKBuf, B_RE, B_QF, B_QE = B_QF + kQSt, B_SF = B_QE + kQSt, B_SE = B_SF + 4,
-           B_LF = B_SE + 4, B_LE = B_LF + kLSt, B_UF = B_LE + kLSt, B_UE = B_UF + kRing, B_DRAIN = B_UE + kRing, B_COUNT };
+           B_LF = B_SE + 4, B_LE = B_LF + kLSt, B_XF = B_LE + kLSt, B_XE = B_XF + 4, B_UF = B_XE + 4, B_UE = B_UF + kRing, B_DRAIN = B_UE + kRing, B_COUNT };
     static constexpr int kMisc = kBar + B_COUNT * 8;
     // Over 114 KB, so that one CTA with all of TMEM is resident per SM.
     static constexpr int kBytes = kMisc + 64 > 120 * 1024 ? kMisc + 64 : 120 * 1024;
     static_assert(kBytes <= 227 * 1024 && kBar % 8 == 0, "shared memory");
-    static constexpr int kReaders = 11 + (FP8 ? 4 : 0);
+    static constexpr int kReaders = 19 + (FP8 ? 4 : 0);
+    static_assert(kLSt % 2 == 0, "alternate row tiles meet alternate places");
 };
 
 // Two key tiles and the row tiles that attend one of them.
@@ -520,6 +521,8 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars[C::B_SF + i], 1);
             mbar_init(&bars[C::B_SE + i], 4);
+            mbar_init(&bars[C::B_XF + i], 4);
+            mbar_init(&bars[C::B_XE + i], 4);
         }
         for (int i = 0; i < C::kLSt; ++i) {
             mbar_init(&bars[C::B_LF + i], 1);
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             for (int i = max(started - C::kKBuf, 0); !FP8 && i < started; ++i)
                 mbar_wait_drain(&bars[C::B_KF + i % C::kKBuf], (i / C::kKBuf) & 1, a.status, a.wait_limit);
         }
-    } else if (warp == 1 || warp == 11) {
+    } else if (warp == 1 || warp == 19) {
         // -------------------------------------------- K Q^T of one of the key tiles
         constexpr uint32_t id = idesc_bf16(128, 128, false, false);
         const int mine = warp == 1 ? 0 : 1;
@@ -709,13 +712,16 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             tc_commit(&bars[C::B_DRAIN]);
             mbar_wait_drain(&bars[C::B_DRAIN], 0, a.status, a.wait_limit);
         }
-    } else if (warp < 10) {
-        // -------------------------------------------- exponentials and sums of one of the key tiles
-        const int mine = warp < 6 ? 0 : 1;
-        const int key = (warp & 3) * 32 + lane;
-        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    } else if (warp < 18) {
+        // -------------------------------------------- exponentials and sums: of one of the key tiles, alternate row tiles
+        const int mine = warp < 10 ? 0 : 1, turn = (warp - 2) >> 2 & 1;
+        const int key = (warp & 3) * 32 + lane, sb = 2 * mine + turn;
+        const uint32_t tS = tmem + sb * 128 + ((uint32_t)((warp & 3) * 32) << 16);
         const float scale = a.scale_log2 * (FP8 ? *a.k_descale : 1.f);
         const uint64_t sc2 = f2_pack(scale, scale);
+        // Where the odd row tiles' sums go to those of the even ones: in the plan's workspace, for shared memory is full; by unit and
+        // key tile in turn.
+        float *part = reinterpret_cast<float *>(a.plan + a.L.off_many_o) + ((int64_t)blockIdx.x * 4 + mine) * 128 + key;
         int g = 0;
         bool run = true;
         for (int k = 0; run; ++k) {
@@ -723,10 +729,12 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             if (u.n < 0) break;
             const int kb = mine ? u.kb[1] : u.kb[0], j = kb + key, seq = u.ctx + u.ntok;
             const bool some = j < seq && (s.window == 0 || j > u.ctx - s.window || j < s.sink);     // attended by some row
-            const int64_t at = some ? weight_place(a, u.r, j) : -1;
+            int64_t at = -1;
+            if (turn == 0 && some) at = weight_place(a, u.r, j);
             float sum = 0.f;
             for (int t = 0; t < u.n; ++t, ++g) {
-                const int sb = 2 * mine + (g & 1), ls = g % C::kLSt;
+                if ((g & 1) != turn) continue;
+                const int ls = g % C::kLSt;
                 const int tok = (u.t0 + t) * tpt, pos = u.ctx + tok, ntok = min(tpt, u.ntok - tok);
                 // Free of the mask: every row behind every key, within every window.
                 const bool full = kb + kKeyTile - 1 <= pos && ntok == tpt && (s.window == 0 || kb > pos + tpt - 1 - s.window || kb + kKeyTile <= s.sink);
@@ -736,35 +744,31 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                uint32_t keep[4];
+                int lo = 0, hi = 128;               // the row tile's columns that attend the key
                 bool any = true;
                 if (!full) {
-                    const int lo = some ? min(max(j - pos, 0), 128) * G : 128;
-                    const int hi = (s.window > 0 && j >= s.sink ? min(max(j - pos + s.window, 0), ntok) : ntok) * G;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) keep[c] = row_bits32(lo - 32 * c, hi - 32 * c);
+                    lo = some ? min(max(j - pos, 0), 128) * G : 128;
+                    hi = (s.window > 0 && j >= s.sink ? min(max(j - pos + s.window, 0), ntok) : ntok) * G;
                     any = __any_sync(0xffffffffu, lo < hi);
                 }
-                const uint32_t tS = tmem + sb * 128 + lane_off;
                 const float4 *z = reinterpret_cast<const float4 *>(sLse + ls * 128);
                 uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                uint32_t v[2][32];
-                if (any) tmem_ld32(tS, v[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (!any) break;
+                    uint32_t x[32];
+                    tmem_ld32(tS + 32 * c, x);
                     tmem_ld_wait();
-                    tmem_reg_fence(v[c & 1]);
-                    if (c < 3) tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-                    uint32_t (&x)[32] = v[c & 1];
-                    if (!full) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = (keep[c] >> i) & 1 ? x[i] : 0xff800000u;
-                    }
+                    tmem_reg_fence(x);
                     if (c == 3) {                   // every score is in registers
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
+                    }
+                    if (!full) {
+                        const uint32_t keep = row_bits32(lo - 32 * c, hi - 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = (keep >> i) & 1 ? x[i] : 0xff800000u;
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -785,9 +789,23 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
                 sum += s0 + s1;
             }
-            if (run && at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum, j >= u.ctx);
+            if (!run) break;
+            const int x = 2 * mine + (k & 1);
+            float *to = part + (k & 1) * 256;
+            if (turn == 1) {
+                if (k >= 2 && !warp_wait(&bars[C::B_XE + x], ((k >> 1) - 1) & 1, abort, a.status, lim)) break;
+                __stcg(to, sum);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[C::B_XF + x]);
+            } else {
+                if (!warp_wait(&bars[C::B_XF + x], (k >> 1) & 1, abort, a.status, lim)) break;
+                sum += ld_cg(to);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[C::B_XE + x]);
+                if (at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum, j >= u.ctx);
+            }
         }
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // -------------------------------------------- Q and lse of the row tiles
         int tk[4], at[4];                   // token of a row tile's row, and its place from the tile's first
 #pragma unroll
