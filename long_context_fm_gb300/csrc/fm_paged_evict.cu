@@ -9,14 +9,15 @@
 //   2. each warp counts its keys above and at that key, learns the counts before its own from the others,
 //      and writes its kept places in order;
 //   3. keys, values and weights move down in windows: every CTA has its tokens of the window copied to shared
-//      memory, two windows ahead, the cluster meets, every CTA writes.  A token never moves up, so a
+//      memory, a window ahead, the cluster meets, every CTA writes.  A token never moves up, so a
 //      write hits only places whose tokens this window or an earlier one has read.
 // Bound by HBM where there are many requests: the weights are read once (they stay in shared memory), every moved
 // token read and written once; by the trips to memory and the meetings (about ten in a row, then one a window) where
 // there are few.  Steps, of 32 requests of up to 12,000 tokens cut to 4,096 and of one of 128K cut to 16K in e4m3: windows
 // of registers without copies ahead, histograms read one count at a time 427 and 122 us; copies ahead, 16 bytes of a histogram at
 // a time 213 and 90; places by warps instead of block-wide scans, weights 16 bytes at a time, and a meeting that waits for no
-// stores (each thread's would have to reach L2 first) 154 and 73.
+// stores (each thread's would have to reach L2 first) 156 and 82; key and value of a token by the same threads 124 and 65. (Bulk
+// copies of a row each instead, a thread per token: 258 and 148.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -36,10 +37,10 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kHeld = 16384;            // keys of a CTA that stay in shared memory (64 KB); more are read again
 constexpr int kLoads = 4;               // groups of four weights of a thread in flight
-constexpr int kMoves = 3, kStages = 3;  // pieces of 16 bytes of a thread per window; windows in shared memory
-constexpr int kStageBytes = kMoves * kEvictThreads * 16;
+constexpr int kMoves = 2, kStages = 2;  // tokens of a thread per window; windows in shared memory
+constexpr int kStageBytes = kMoves * kEvictThreads * 32;
 constexpr int kEvictBytes = 3 * kBins * 4 + kHeld * 4;
-static_assert(kStages * (kStageBytes + kMoves * (kEvictThreads / 8) * 4) <= kEvictBytes, "the windows fit where the keys were");   // 8 pieces a token at least
+static_assert(kStages * (kStageBytes + kMoves * (kEvictThreads / 4) * 4) <= kEvictBytes, "the windows fit where the keys were");   // 4 pieces a row at least
 
 struct EvictArgs {
     uint8_t *kv[2];
@@ -50,7 +51,7 @@ struct EvictArgs {
     int64_t max_tokens;                 // of a request
     int32_t max_pages, num_pages, page_size, Hkv;
     int32_t pieces;                     // of 16 bytes in a row
-    int32_t piece_shift;                // log2 of the pieces of a token's key and value
+    int32_t piece_shift;                // log2 of them
     int32_t page_shift;                 // log2 of the page size, -1 if it is no power of two
     int32_t budget, recent, sink;
 };
@@ -312,12 +313,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
     if (cta == 0 && tid == 0 && h == 0) a.new_lens[r] = a.budget;
     meet();                                          // the kept places are visible to the cluster
 
-    // Windows of kMoves pieces a thread, kStages - 1 of them on their way to shared memory while one is written.
-    const int per_token = 1 << a.piece_shift, tokens = kEvictThreads >> a.piece_shift, mate = tid >> a.piece_shift;    // tokens of a step of the CTA
-    const int piece = tid & (per_token - 1), which = piece >= a.pieces ? 1 : 0;
-    const int64_t col = (int64_t)h * a.head[which] + (int64_t)(piece - which * a.pieces) * 16;
-    const int64_t st_page = a.page[which], st_tok = a.tok[which];
-    uint8_t *kv = a.kv[which];
+    // Windows of kMoves tokens a thread, of each of which it moves 16 bytes of the key and of the value, kStages - 1 of them on
+    // their way to shared memory while one is written.
+    const int tokens = kEvictThreads >> a.piece_shift, mate = tid >> a.piece_shift;      // tokens of a step of the CTA
+    const int piece = tid & (a.pieces - 1);
+    const int64_t col_k = (int64_t)h * a.head[0] + piece * 16, col_v = (int64_t)h * a.head[1] + piece * 16;
     const int window = tokens * kMoves * C, j0 = a.sink + cta * tokens * kMoves + mate;
     const int windows = (a.budget - a.sink + window - 1) / window;
     auto sources = [&](int w, int (&from)[kMoves]) {
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
             from[i] = w < windows && j < a.budget ? __ldcg(kept + j) : -1;
         }
     };
-    // Starts the loads of window w; a bit for each piece that moves.
+    // Starts the loads of window w; a bit for each token that moves.
     auto start = [&](int w, const int (&from)[kMoves]) {
         unsigned moves = 0;
         uint8_t *stage = smem + (w % kStages) * kStageBytes;
@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
             moves |= 1u << i;
             const int b = page_of(from[i]), in = from[i] - b * a.page_size;
             const int64_t page = __ldg(table + b);
-            copy_async16(stage + (i * kEvictThreads + tid) * 16, kv + page * st_page + in * st_tok + col);
+            copy_async16(stage + (i * 2 * kEvictThreads + tid) * 16, a.kv[0] + page * a.page[0] + in * a.tok[0] + col_k);
+            copy_async16(stage + ((i * 2 + 1) * kEvictThreads + tid) * 16, a.kv[1] + page * a.page[1] + in * a.tok[1] + col_v);
             if (piece == 0) copy_async4(s_moved + ((w % kStages) * kMoves + i) * tokens + mate, a.weights + page * page_weights + head_weights + in);
         }
         copy_async_commit();
@@ -365,7 +366,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
             const int j = w * window + j0 + i * tokens;
             const int b = page_of(j), in = j - b * a.page_size;
             const int64_t page = __ldg(table + b);
-            *reinterpret_cast<uint4 *>(kv + page * st_page + in * st_tok + col) = *reinterpret_cast<const uint4 *>(stage + (i * kEvictThreads + tid) * 16);
+            *reinterpret_cast<uint4 *>(a.kv[0] + page * a.page[0] + in * a.tok[0] + col_k) = *reinterpret_cast<const uint4 *>(stage + (i * 2 * kEvictThreads + tid) * 16);
+            *reinterpret_cast<uint4 *>(a.kv[1] + page * a.page[1] + in * a.tok[1] + col_v) = *reinterpret_cast<const uint4 *>(stage + ((i * 2 + 1) * kEvictThreads + tid) * 16);
             if (piece == 0) a.weights[page * page_weights + head_weights + in] = s_moved[((w % kStages) * kMoves + i) * tokens + mate];
         }
 #pragma unroll
@@ -501,7 +503,7 @@ fm_status fm_paged_evict(const fm_paged_cache *cache, int requests, int max_page
     a.page_size = cache->page_size;
     a.Hkv = cache->Hkv;
     a.pieces = (int)(cache->d * esz / 16);
-    for (a.piece_shift = 0; 1 << a.piece_shift < 2 * a.pieces; ++a.piece_shift) {}
+    for (a.piece_shift = 0; 1 << a.piece_shift < a.pieces; ++a.piece_shift) {}
     a.budget = budget;
     a.recent = recent;
     a.sink = sink;
