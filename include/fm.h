@@ -503,7 +503,8 @@ FM_API fm_status fm_rope(const void *x, int x_dtype, fm_strides xs, const int32_
  *   places kept, -1 for requests that are not cut.  What lies behind the new length is left as it is.
  *   A request whose length is out of range (FM_ERR_LENGTHS) or that holds a page outside [0, num_pages) among those of its
  *   tokens (FM_ERR_PAGES) is not cut, and new_lens[r] = lens[r].
- *   Pages of a request that is cut may be held by no other request, and none twice.  weights as above; their page and
+ *   Places, and with them positions of the next plan and windows, count the tokens that are left; rotary positions are the
+ *   caller's to keep.  Pages of a request that is cut may be held by no other request, and none twice.  weights as above; their page and
  *   head sizes are the cache's.  1 <= budget, 0 <= sink, 0 <= recent, sink + recent <= budget.
  * fm_paged_release: gives the pages behind the requests' new lengths back to the free list that fm_paged_plan
  *   takes from: pages ceil(lens[r] / page_size) .. ceil(held[r] / page_size) - 1 of every request, in the order of
@@ -531,7 +532,8 @@ FM_API fm_status fm_rope(const void *x, int x_dtype, fm_strides xs, const int32_
  *   target, draft: [rows, V] of dtype (bf16 or fp32), row strides in elements, any alignment of a whole
  *   element.  1 <= V <= 2^24.  A drafted token outside [0, V) is refused, with FM_ERR_PROBS; so is the draw where the
  *   sum of w is zero, infinite or NaN: the token is then -1.  cu_q outside [0, rows] or
- *   decreasing: FM_ERR_LENGTHS, and the request has no rows.
+ *   decreasing: FM_ERR_LENGTHS, and the request has no rows.  rows = 0 (target, draft, tokens, u_accept and out unused) is a
+ *   step without any.  No other two arrays may overlap.
  */
 FM_API fm_status fm_paged_append_rope(const void *q, int64_t q_tok, int64_t q_head, int Hq, const void *k, int64_t k_tok,
                                       int64_t k_head, const void *v, int64_t v_tok, int64_t v_head, const int64_t *slots,

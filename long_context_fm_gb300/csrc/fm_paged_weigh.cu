@@ -7,8 +7,11 @@
 // order.  Two kernels, as the attention has: requests of at most kFewRows rows (new tokens x query heads per KV
 // head), where K is read once and little is computed, and those with more, which are matrix work.
 //
-// Few rows: bound by HBM (K once).  Key tiles (128 keys) of all (request, KV head) units lie end to end and are cut into
-// equal shares, as the plan has them for the attention.  Rows are 16 or 32 columns of the product.
+// Few rows: bound by HBM (K once): 96 requests of one token over up to 16,000 keys, 32 / 8 heads, 159 us (6.4 TB/s), 64 of up
+// to three over e4m3 77 us (5.0 TB/s).  Key tiles (128 keys) of all (request, KV head) units lie end to end and are cut into
+// equal shares, as the plan has them for the attention.  Rows are 16 or 32 columns of the product.  A tile of codes takes
+// as little as 700 cycles of HBM, so each step that one thread or warp does for every tile (loads, products, sums) is done by
+// two on alternate tiles: with one of each the e4m3 batch took 92 us, with the products and sums alone doubled 91.
 //   warps 0, 11 walk the share, look pages up (a batch of tiles at a time), TMA of K, alternate tiles (ring of 128 to 192 KB)
 //   warps 1, 10 one thread each issues K Q^T of every second tile (1: TMEM)
 //   warps 2-5   even tiles, thread = key: exponentials, sum, one add or store to the key's weight;  warps 6-9  odd ones
@@ -17,7 +20,13 @@
 // Many rows: a unit is two key tiles of a (request, KV head), whose K stays in shared memory while the row tiles (128
 // rows: the query heads of the KV head times as many tokens as fit) that attend them stream through, each multiplied by
 // both.  Per pair of tiles 512 cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both
-// about even, and each tile has its own issuing thread, two score buffers and a warpgroup for each of them.
+// about even, and each key tile has its own issuing thread, two score buffers and a warpgroup for each of them.  4,178 tokens
+// over up to 16K keys: 345 to 365 us (1,300 to 1,370 TFLOP/s); while an SM has work the tensor pipe and the exponentials are
+// busy two thirds of the time each, and the SMs have work 86 % of it (504 units of up to 128 row tiles for 152 CTAs).
+// One key tile a unit, one issuing thread and two warpgroups took 455 us (a row tile's products waited for their own
+// barriers), two issuing threads 457 (Q's arrival), two key tiles a unit 439 (the sums' latency), four warpgroups 350.  Not
+// kept: four issuing threads (375), K as the TMEM operand with three score buffers (375: the buffers come free too late), two
+// warpgroups that hold all 128 scores of a row tile (380).
 //   warp 0      claims units (longest first), TMA of K
 //   warps 1, 19 one thread each issues K Q^T of one of the key tiles (1: TMEM)
 //   warps 2-5, 6-9    first key tile, even and odd row tiles, thread = key;  warps 10-13, 14-17  second one

@@ -322,10 +322,11 @@ extern "C" fm_status fm_verify_drafts(const void *target, int64_t target_row, co
 {
     if (dtype != FM_DT_BF16 && dtype != FM_DT_F32) return FM_ERR_INVALID_ARG;
     const int64_t esz = dtype == FM_DT_F32 ? 4 : 2;
-    if (requests <= 0 || rows <= 0 || V <= 0 || !target || (uintptr_t)target % esz || (uintptr_t)draft % esz) return FM_ERR_INVALID_ARG;
+    if (requests <= 0 || rows < 0 || V <= 0 || (uintptr_t)target % esz || (uintptr_t)draft % esz) return FM_ERR_INVALID_ARG;
     if (target_row < V || (draft && draft_row < V) || target_row > ((int64_t)1 << 38) || draft_row > ((int64_t)1 << 38)) return FM_ERR_INVALID_ARG;
-    if (!aligned4(tokens) || !aligned4(u_accept) || !aligned4(u_sample) || !aligned4(cu_q) || !aligned4(seq_lens) || !aligned4(out) ||
-        !aligned4(n_out) || !aligned4(new_lens) || !aligned4(dev_status))
+    // (A step without rows has no place for them.)
+    if (rows > 0 && (!target || !aligned4(tokens) || !aligned4(u_accept) || !aligned4(out))) return FM_ERR_INVALID_ARG;
+    if (!aligned4(u_sample) || !aligned4(cu_q) || !aligned4(seq_lens) || !aligned4(n_out) || !aligned4(new_lens) || !aligned4(dev_status))
         return FM_ERR_INVALID_ARG;
     if (requests > kMaxRequests || rows > (1 << 24) || V > (1 << 24)) return FM_ERR_UNSUPPORTED;
     const fm_status st = device_ok();

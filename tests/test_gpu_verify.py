@@ -168,3 +168,21 @@ def test_tokens_come_out_as_the_targets(fm):
         freq += torch.bincount(out[::2].long().cpu(), minlength=5).float()
     assert int(status.item()) == 0
     assert ((freq / n - p).abs() <= 6 * (p * (1 - p) / n).sqrt()).all()
+
+
+def test_a_step_without_rows(fm):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    p = torch.empty(0, 50, device="cuda")
+    for draft in (None, p):
+        out, n_out, lens = fm.fm_verify_drafts(p, draft, none, none.float(), torch.zeros(2, device="cuda"), i32([0, 0, 0]), i32([5, 0]), status)
+        assert out.shape == (0,) and n_out.tolist() == [0, 0] and lens.tolist() == [5, 0] and int(status.item()) == 0
+
+
+def test_lengths_in_place(fm):
+    p, q, tokens, u, s, cu = rows_of([3, 1], 40, torch.float32, False, 5)
+    status, seq = torch.zeros(1, dtype=torch.int32, device="cuda"), i32([30, 20])
+    args = (p.cuda(), q.cuda(), tokens.cuda(), u.cuda(), s.cuda(), i32(cu), seq, status)
+    want = fm.fm_verify_drafts(*args)[2].tolist()
+    got = fm.fm_verify_drafts(*args, new_lens=seq)[2]
+    assert got.data_ptr() == seq.data_ptr() and seq.tolist() == want

@@ -160,7 +160,7 @@ def test_release_arguments_that_are_refused(fm, change, code):
 
 
 @pytest.mark.parametrize("change,code", [
-    (dict(target=None), 1), (dict(target=A + 2), 1), (dict(tr=99), 1), (dict(draft=A + 3), 1), (dict(dr=99), 1), (dict(dtype=2), 1), (dict(V=0), 1), (dict(rows=0), 1),
+    (dict(target=None), 1), (dict(target=A + 2), 1), (dict(tr=99), 1), (dict(draft=A + 3), 1), (dict(dr=99), 1), (dict(dtype=2), 1), (dict(V=0), 1), (dict(rows=-1), 1),
     (dict(V=(1 << 24) + 1, tr=1 << 25, dr=1 << 25), 2), (dict(rows=(1 << 24) + 1), 2), (dict(tr=1 << 39), 1), (dict(tokens=None), 1), (dict(ua=A + 2), 1), (dict(us=None), 1),
     (dict(cu=None), 1), (dict(seq=None), 1), (dict(R=0), 1), (dict(R=8193), 2), (dict(out=None), 1), (dict(n_out=None), 1), (dict(new=A + 1), 1), (dict(status=None), 1)])
 def test_verify_arguments_that_are_refused(fm, change, code):
