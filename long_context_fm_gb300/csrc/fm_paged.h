@@ -38,7 +38,8 @@ struct PagedHeader {
     int32_t n_many;       // entries of the many-rows list
     int32_t units_many;   // its units (request, KV head, query tile)
     int32_t splits_many;  // pieces per unit along the keys (1: whole units)
-    int32_t pad[44];
+    int32_t weigh_len;    // row tiles of a piece where the weights' units were cut, 0 where none was (left by that kernel for the next)
+    int32_t pad[43];
 };
 static_assert(sizeof(PagedHeader) == 256, "plan header size");
 

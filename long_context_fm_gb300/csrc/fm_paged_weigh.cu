@@ -21,8 +21,8 @@
 // rows: the query heads of the KV head times as many tokens as fit) that attend them stream through, each multiplied by
 // both.  Per pair of tiles 512 cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both
 // about even, and each key tile has its own issuing thread, two score buffers and a warpgroup for each of them.  4,178 tokens
-// over up to 16K keys: 345 to 365 us (1,300 to 1,370 TFLOP/s); while an SM has work the tensor pipe and the exponentials are
-// busy two thirds of the time each, and the SMs have work 86 % of it (504 units of up to 128 row tiles for 152 CTAs).
+// over up to 16K keys: 327 us (1,450 TFLOP/s); while an SM has work the tensor pipe and the exponentials are busy
+// two thirds of the time each (a warp's waits and loads from TMEM are what is between).
 // One key tile a unit, one issuing thread and two warpgroups took 455 us (a row tile's products waited for their own
 // barriers), two issuing threads 457 (Q's arrival), two key tiles a unit 439 (the sums' latency), four warpgroups 350.  Not
 // kept: four issuing threads (375), K as the TMEM operand with three score buffers (375: the buffers come free too late), two
@@ -67,6 +67,66 @@ __device__ __forceinline__ void put(float *at, float sum, bool fresh)
 {
     if (fresh) *at = sum;
     else red_add_f32(at, sum);
+}
+
+// ---- pieces of the many rows ------------------------------------------------------------
+// A unit (two key tiles of a request's KV head) whose row tiles are many is cut into pieces along them, so that the CTAs
+// end together: pieces of about an eighth of a CTA's share, four row tiles at least.  Their sums go to the plan's workspace and
+// the kernel of the few rows, which follows, adds them up in their order.  (504 units of up to 128 row tiles: whole
+// 350 us, in thirds 327; one KV head of 2,000 tokens over 4,000 keys, 16 units, 115 and 29.)
+struct ManyPieces {
+    int len;                // row tiles of a piece
+    int tpt;                // tokens of a row tile
+    int64_t units, pieces;  // of all entries
+    __device__ __forceinline__ int64_t units_of(const PagedShape &s, const PagedEntry &en) const
+    {
+        return (int64_t)((key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink).n + 1) / 2) * s.Hkv;
+    }
+    __device__ __forceinline__ int tiles_of(const PagedEntry &en) const { return (en.n + tpt - 1) / tpt; }
+    __device__ __forceinline__ int parts_of(const PagedEntry &en) const { return (tiles_of(en) + len - 1) / len; }
+};
+
+// Room for the pieces' sums behind that of the exchange within a CTA (floats of the workspace).
+constexpr int64_t kExchange = (int64_t)kPagedCtas * 4 * 128;
+
+// Called by a full warp; the same in every CTA.
+__device__ __forceinline__ ManyPieces many_pieces(const PagedArgs &a, const PagedHeader *hd, int tpt)
+{
+    const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_many);
+    const PagedShape &s = a.s;
+    auto sum = [](int64_t x) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    };
+    const int n = hd->n_many, lane = lane_id();
+    ManyPieces m{1, tpt, 0, 0};
+    // The lane's first entry is all that it has, most often: once read.
+    const PagedEntry first = list[min(lane, n - 1)];
+    const int64_t u0 = lane < n ? m.units_of(s, first) : 0;
+    const int t0 = m.tiles_of(first);
+    int64_t tiles = u0 * t0;
+    m.units = u0;
+    for (int i = lane + 32; i < n; i += 32) {
+        const int64_t u = m.units_of(s, list[i]);
+        m.units += u;
+        tiles += u * m.tiles_of(list[i]);
+    }
+    tiles = sum(tiles);
+    m.units = sum(m.units);
+    m.len = (int)min(max(tiles / (8 * kPagedCtas), (int64_t)4), (int64_t)1 << 24);
+    if (!__any_sync(0xffffffffu, lane < n && t0 > m.len) && n <= 32) {
+        m.pieces = m.units;                         // nothing to cut
+        return m;
+    }
+    for (int go = 0; go < 2; ++go) {
+        m.pieces = u0 * ((t0 + m.len - 1) / m.len);
+        for (int i = lane + 32; i < n; i += 32) m.pieces += m.units_of(s, list[i]) * m.parts_of(list[i]);
+        m.pieces = sum(m.pieces);
+        if ((m.pieces + 1) * 256 + kExchange <= (int64_t)kMaxPieces * 128 * s.d) break;
+        m.len = 1 << 24;                            // no room: whole units
+    }
+    return m;
 }
 
 // ---- few rows ------------------------------------------------------------------------
@@ -121,6 +181,45 @@ __global__ void __launch_bounds__(FewCfg<D, FP8>::kThreads, 1)
         if (blockIdx.x == 0 && threadIdx.x == 0)
             set_status(a.status, !paged_plan_fits(hd, s) ? FM_ERR_PLAN_MISMATCH : hd->rows > a.rows ? FM_ERR_LENGTHS : FM_ERR_UNSUPPORTED);
         return;
+    }
+    if (hd->n_many > 0 && hd->weigh_len > 0) {
+        // The pieces of the many rows' units, whose kernel is over: a thread per key.
+        const ManyPieces mp{hd->weigh_len, 128 / (s.Hq / s.Hkv), 0, 0};
+        const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_many);
+        const float *ws = reinterpret_cast<const float *>(a.plan + a.L.off_many_o) + kExchange;
+        int64_t cum = 0;
+        for (int e0 = 0; e0 < hd->n_many; e0 += 32) {
+            const int i = e0 + lane;
+            const int64_t mine = i < hd->n_many ? mp.units_of(s, list[i]) * mp.parts_of(list[i]) : 0;
+            int64_t upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            unsigned cut = __ballot_sync(0xffffffffu, i < hd->n_many && mp.parts_of(list[min(i, hd->n_many - 1)]) > 1);
+            while (cut) {
+                const int l = __ffs(cut) - 1;
+                cut &= cut - 1;
+                const PagedEntry en = list[e0 + l];
+                const int64_t first = cum + __shfl_sync(0xffffffffu, upto - mine, l);
+                const int parts = mp.parts_of(en);
+                const int64_t units = mp.units_of(s, en);
+                const KeyRange kr = key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink);
+                for (int64_t u = blockIdx.x * 2 + (threadIdx.x >> 8); u < units; u += gridDim.x * 2) {
+                    const int x = 2 * (int)(u / s.Hkv) + (threadIdx.x >> 7 & 1);
+                    if (x >= kr.n) continue;
+                    const int j = kr.tile(x) * kKeyTile + (threadIdx.x & 127);
+                    if (j >= en.ctx + en.n || !(s.window == 0 || j > en.ctx - s.window || j < s.sink)) continue;
+                    const float *from = ws + (first + u * parts) * 256 + (threadIdx.x & 255);
+                    float sum = 0.f;
+                    for (int p = 0; p < parts; ++p) sum += ld_cg(from + (int64_t)p * 256);
+                    const int64_t at = weight_place(a, en.r, j);
+                    if (at >= 0) put(w.weights + at + (u % s.Hkv) * s.page_size, sum, j >= en.ctx);
+                }
+            }
+            cum += __shfl_sync(0xffffffffu, upto, 31);
+        }
     }
     if ((int)blockIdx.x >= hd->ctas_few) return;
     if (warp == 0 && lane == 0) {
@@ -489,6 +588,7 @@ struct ManyUnit {
     int r, h, tok0, ntok, ctx;
     int t0;                 // first row tile
     int kb[2];              // first key of either tile (the second one may lie behind the request: no row attends it)
+    int piece;              // where the sums go in the workspace; -1: to the weights
 };
 
 template <int D, bool FP8>
@@ -565,7 +665,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         ManyUnit u{-1};
         if (!warp_wait(&bars[C::B_UF + slot], (k / C::kRing) & 1, abort, a.status, lim)) return u;
         const volatile int *p = sUnit + slot * C::kInts;
-        u = ManyUnit{p[0], p[1], p[2], p[3], p[4], p[5], p[6], {p[7], p[8]}};
+        u = ManyUnit{p[0], p[1], p[2], p[3], p[4], p[5], p[6], {p[7], p[8]}, p[9]};
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[C::B_UE + slot]);
         return u;
@@ -575,17 +675,16 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         // -------------------------------------------- claims; K
         const PagedEntry *list = reinterpret_cast<const PagedEntry *>(a.plan + a.L.off_many);
         unsigned *claim = reinterpret_cast<unsigned *>(a.plan + a.L.off_claim);
-        auto units_of = [&](const PagedEntry &en) { return (int64_t)((key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink).n + 1) / 2) * s.Hkv; };
-        int64_t total = 0;
-        for (int i = lane; i < hd->n_many; i += 32) total += units_of(list[i]);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        const bool fits = total < (int64_t)1 << 31;
+        const ManyPieces mp = many_pieces(a, hd, tpt);
+        if (blockIdx.x == 0 && lane == 0) reinterpret_cast<PagedHeader *>(a.plan)->weigh_len = mp.pieces > mp.units ? mp.len : 0;
+        const bool fits = mp.pieces < (int64_t)1 << 31;
         if (!fits && blockIdx.x == 0 && lane == 0) set_status(a.status, FM_ERR_LENGTHS);
-        const unsigned n_claims = fits ? (unsigned)total : 0u;
+        const unsigned n_claims = fits ? (unsigned)mp.pieces : 0u;
         int e = 0;
-        int64_t cum = 0;            // units before entry e
+        int64_t cum = 0;            // pieces before entry e
         PagedEntry en = list[0];
+        int64_t units = mp.units_of(s, en);
+        int parts = mp.parts_of(en);
         const int nb = kKeyTile / w.box_keys;
         bool run = true;
         int started = 0;            // loads of K
@@ -598,9 +697,9 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 c = __shfl_sync(0xffffffffu, c, 0);
                 if (c >= n_claims) break;
                 // Claims only grow, so the entry is at or behind the last one.
-                while ((int64_t)c >= cum + units_of(en)) {
+                while ((int64_t)c >= cum + units * parts) {
                     const int i = e + lane;
-                    const int64_t mine = i < hd->n_many ? units_of(list[i]) : 0;
+                    const int64_t mine = i < hd->n_many ? mp.units_of(s, list[i]) * mp.parts_of(list[i]) : 0;
                     int64_t upto = mine;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -612,10 +711,12 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                     if (past > 0) cum += gone;
                     e += past;
                     en = list[min(e, hd->n_many - 1)];
+                    units = mp.units_of(s, en);
+                    parts = mp.parts_of(en);
                 }
-                const int local = (int)((int64_t)c - cum), x = local / s.Hkv;
+                const int local = (int)((int64_t)c - cum), part = local % parts, unit = local / parts, x = unit / s.Hkv;
                 const KeyRange kr = key_range(en.ctx, en.ctx + en.n - 1, s.window, s.sink);
-                u = ManyUnit{0, en.r, local - x * s.Hkv, en.tok0, en.n, en.ctx, 0, {0, 0}};
+                u = ManyUnit{0, en.r, unit - x * s.Hkv, en.tok0, en.n, en.ctx, 0, {0, 0}, parts > 1 ? (int)c : -1};
                 // Row tiles [t0, t1) attend the unit: from the first token at its first key's place on, until the last within a
                 // window of its last key.
                 int t1 = 0;
@@ -629,9 +730,11 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                     if (s.window > 0 && u.kb[y] >= s.sink) last = min(last, max(u.kb[y] - en.ctx + kKeyTile - 2 + s.window + tpt, 0) / tpt);
                     t1 = max(t1, last);
                 }
-                u.n = t1 - u.t0;
-                if (u.n > 0) break;
-                u.n = -1;
+                // The piece's share of them, which may be empty (its sums are then zeros).
+                const int n = max(t1 - u.t0, 0), t_first = (int)((int64_t)n * part / parts);
+                u.n = (int)((int64_t)n * (part + 1) / parts) - t_first;
+                u.t0 += t_first;
+                break;
             }
             // The tiles' pages, looked up before the waits: lane i the box i of the two tiles.
             int page = s.num_pages, in = 0;
@@ -650,9 +753,9 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
             if (k >= C::kRing && !warp_wait(&bars[C::B_UE + slot], ((k / C::kRing) - 1) & 1, abort, a.status, lim)) run = false;
             if (!run) break;
             if (lane == 0) {
-                const int f[9] = {u.n, u.r, u.h, u.tok0, u.ntok, u.ctx, u.t0, u.kb[0], u.kb[1]};
+                const int f[10] = {u.n, u.r, u.h, u.tok0, u.ntok, u.ctx, u.t0, u.kb[0], u.kb[1], u.piece};
 #pragma unroll
-                for (int i = 0; i < 9; ++i) sUnit[slot * C::kInts + i] = f[i];
+                for (int i = 0; i < 10; ++i) sUnit[slot * C::kInts + i] = f[i];
                 mbar_arrive(&bars[C::B_UF + slot]);
             }
             __syncwarp();
@@ -731,6 +834,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         // Where the odd row tiles' sums go to those of the even ones: in the plan's workspace, for shared memory is full; by unit and
         // key tile in turn.
         float *part = reinterpret_cast<float *>(a.plan + a.L.off_many_o) + ((int64_t)blockIdx.x * 4 + mine) * 128 + key;
+        float *ws = reinterpret_cast<float *>(a.plan + a.L.off_many_o) + kExchange + mine * 128 + key;     // of pieces
         int g = 0;
         bool run = true;
         for (int k = 0; run; ++k) {
@@ -811,7 +915,8 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 sum += ld_cg(to);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C::B_XE + x]);
-                if (at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum, j >= u.ctx);
+                if (u.piece >= 0) __stcg(ws + (int64_t)u.piece * 256, sum);
+                else if (at >= 0) put(w.weights + at + (int64_t)u.h * s.page_size, sum, j >= u.ctx);
             }
         }
     } else if (warp == 18) {

@@ -79,6 +79,18 @@ def test_long_walks(fm, new, d, e4m3):
     check(fm, base.Batch(fm, [20000, 9000, 14001], new, 16, 8, d, 64, e4m3=e4m3, seed=12))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window,sink", [(0, 0), (300, 5), (40, 0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_heads_of_many_rows(fm, d, window, sink, e4m3):
+    """Few pairs of key tiles against dozens of row tiles: cut along the rows, and added up again; next to requests that are not."""
+    check(fm, base.Batch(fm, [100, 700, 64], [1500, 40, 2], 8, 1, d, 32, window=window, sink=sink, e4m3=e4m3, seed=7))
+
+
+def test_more_requests_of_many_rows_than_a_warp(fm):
+    check(fm, base.Batch(fm, [60 * (r % 7) for r in range(45)], [33 + 9 * (r % 40) for r in range(45)], 2, 2, 64, 16, seed=8))
+
+
 @pytest.mark.parametrize("layout", ["tokens", "pairs"])
 @pytest.mark.parametrize("new", [[2, 1], [90, 1]])
 def test_strides(fm, layout, new):
