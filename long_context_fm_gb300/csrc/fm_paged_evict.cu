@@ -88,24 +88,36 @@ __device__ __forceinline__ int block_before(int x, int *total, int *sh)
     return before + y - x;
 }
 
-// Finds, among the counts of keys by digit of all C CTAs, the digit of the need-th largest key; *need becomes its rank
+// Adds a CTA's counts of keys by digit to those of the cluster, of which each CTA holds its share of the digits.  (Every CTA reading
+// the counts of all the others instead takes 2 us a round for 1, with eight of them.)
+template <int C, int BINS>
+__device__ __forceinline__ void share_counts(const cg::cluster_group &cl, const int *hist, int *shared)
+{
+    if (C == 1) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < BINS; i += kEvictThreads) {
+        const int x = hist[i];
+        if (x) atomicAdd(cl.map_shared_rank(shared + i % (BINS / C), i / (BINS / C)), x);
+    }
+}
+
+// Finds, among the cluster's counts, the digit of the need-th largest key; *need becomes its rank
 // among the keys of that digit.  Thread t looks at the t-th PER digits from the top.
 template <int C, int BINS>
-__device__ __forceinline__ int digit_of(const cg::cluster_group &cl, const int *hist, int *need, int *s_warp, int *s_found)
+__device__ __forceinline__ int digit_of(const cg::cluster_group &cl, int *hist, int *shared, int *need, int *s_warp, int *s_found)
 {
     constexpr int PER = BINS / kEvictThreads;
-    static_assert(PER == 4 || PER == 2, "digits of a thread");
+    static_assert((PER == 4 || PER == 2) && BINS / C % PER == 0, "digits of a thread");
     using V = typename std::conditional<PER == 4, int4, int2>::type;
-    const int at = BINS / PER - 1 - threadIdx.x;
+    const int at = BINS / PER - 1 - threadIdx.x, owner = at * PER / (BINS / C);
     int count[PER] = {};
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const V v = reinterpret_cast<const V *>(C > 1 ? cl.map_shared_rank(hist, c) : hist)[at];
-        count[0] += v.x;
-        count[1] += v.y;
+    {
+        const V v = *reinterpret_cast<const V *>(C > 1 ? cl.map_shared_rank(shared + at * PER - owner * (BINS / C), owner) : hist + at * PER);
+        count[0] = v.x;
+        count[1] = v.y;
         if constexpr (PER == 4) {
-            count[2] += v.z;
-            count[3] += v.w;
+            count[2] = v.z;
+            count[3] = v.w;
         }
     }
     int sum = 0;
@@ -140,6 +152,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
     __shared__ int s_warp[kEvictWarps];
     __shared__ int s_bad, s_found[2];
     __shared__ int2 s_count[kEvictWarps];
+    __shared__ __align__(16) int s_shared[3][C > 1 ? kBins / C : 4];
     const cg::cluster_group cl = cg::this_cluster();
     auto meet = [&]() {
         if (C > 1) cl.sync();
@@ -215,8 +228,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
 
     if (m > 0)
         for (int i = tid; i < 3 * kBins / 4; i += kEvictThreads) reinterpret_cast<int4 *>(s_hist)[i] = make_int4(0, 0, 0, 0);
+    if (C > 1 && m > 0)
+        for (int i = tid; i < 3 * kBins / C; i += kEvictThreads) s_shared[0][i] = 0;
     if (tid == 0) s_bad = 0;
-    __syncthreads();
+    meet();                                         // every CTA's counts are zero
     // Every page of the request is one of the pool's, or the request is left alone.
     const int pages = page_of(len - 1) + 1;
     for (int b = cta * kEvictThreads + tid; b < pages; b += C * kEvictThreads)
@@ -234,6 +249,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
                 if (k[j]) atomicAdd(&s_hist[0][k[j] >> 21], 1);
         }
     }
+    if (m > 0) share_counts<C, kBins>(cl, s_hist[0], s_shared[0]);
     meet();
     bool bad = false;
 #pragma unroll
@@ -248,23 +264,25 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
     // with that prefix that are kept.
     if (m > 0) {
         int need = m;
-        uint32_t prefix = (uint32_t)digit_of<C, kBins>(cl, s_hist[0], &need, s_warp, s_found);
+        uint32_t prefix = (uint32_t)digit_of<C, kBins>(cl, s_hist[0], s_shared[0], &need, s_warp, s_found);
         each([&](int, const uint4 &key) {
             const uint32_t k[4] = {key.x, key.y, key.z, key.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (k[j] >> 21 == prefix && k[j]) atomicAdd(&s_hist[1][(k[j] >> 10) & 2047], 1);
         });
+        share_counts<C, kBins>(cl, s_hist[1], s_shared[1]);
         meet();
-        prefix = prefix << 11 | (uint32_t)digit_of<C, kBins>(cl, s_hist[1], &need, s_warp, s_found);
+        prefix = prefix << 11 | (uint32_t)digit_of<C, kBins>(cl, s_hist[1], s_shared[1], &need, s_warp, s_found);
         each([&](int, const uint4 &key) {
             const uint32_t k[4] = {key.x, key.y, key.z, key.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (k[j] >> 10 == prefix && k[j]) atomicAdd(&s_hist[2][k[j] & 1023], 1);
         });
+        share_counts<C, 1024>(cl, s_hist[2], s_shared[2]);
         meet();
-        prefix = prefix << 10 | (uint32_t)digit_of<C, 1024>(cl, s_hist[2], &need, s_warp, s_found);
+        prefix = prefix << 10 | (uint32_t)digit_of<C, 1024>(cl, s_hist[2], s_shared[2], &need, s_warp, s_found);
         // How many of the warp's keys lie above that key and at it, and how many of the warps and CTAs before.
         int above = 0, at = 0;
         each([&](int, const uint4 &key) {
