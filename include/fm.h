@@ -492,7 +492,8 @@ FM_API fm_status fm_rope(const void *x, int x_dtype, fm_strides xs, const int32_
  *   plan, q, cache (its k alone is read), block table and scale as fm_attn_paged, after it, with its lse; `rows` as there.
  *   Scores and sums are fp32; beside an e4m3 cache the q of requests of at most 32 rows enters as two
  *   e4m3 terms, as in fm_attn_paged.  A key's sum is added up in a fixed order, except that several
- *   requests that hold one page add to it in any order.  A page number outside [0, num_pages) among the attended
+ *   requests that hold one page add to it in any order.  A row gives nothing to keys that it does not attend, whatever its
+ *   lse.  A page number outside [0, num_pages) among the attended
  *   gives FM_ERR_PAGES and its keys are left out.
  * fm_paged_evict: cuts requests of more than `budget` cached tokens down to `budget` in one layer: per KV head the first
  *   `sink` tokens stay, the last `recent` ones, and of those between the budget - sink - recent
@@ -620,8 +621,8 @@ FM_API int fm_profile_end(fm_kernel_time *out, int max_entries);
  * Failure detection is tested on the real kernels without faulting the GPU:
  * after this call, the next fm_attn_fwd / fm_attn_fwd_rows launch
  * (kernel = 0), fm_attn_bwd / fm_attn_bwd_rows launch (kernel = 1) or launch of
- * fm_attn_paged's few-rows or many-rows kernel (FM_K_PAGED_DECODE,
- * FM_K_PAGED_CHUNK) made by the process bounds every device-side wait by
+ * the few-rows or many-rows kernel of fm_attn_paged (FM_K_PAGED_DECODE,
+ * FM_K_PAGED_CHUNK) or fm_paged_weights (FM_K_PAGED_WEIGH_FEW, _MANY) made by the process bounds every device-side wait by
  * limit_cycles SM cycles (100,000 .. the default bound of about 3e9) instead of
  * the default, and its first CTA withholds the load of its second K tile (forward),
  * of its second Q/dO half (backward) or of its second tile (few rows; many rows:

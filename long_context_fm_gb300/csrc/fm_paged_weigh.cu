@@ -37,6 +37,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "fm_paged.h"
 #include "fm_ptx.cuh"
@@ -866,6 +867,22 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 }
                 const float4 *z = reinterpret_cast<const float4 *>(sLse + ls * 128);
                 uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                // (The mask is put over the exponents: a row that does not attend the key gives it nothing, whatever its lse.)
+                auto add = [&](const uint32_t (&x)[32], const float4 *off, uint32_t keep, auto masked) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 o = off[i];
+                        float e[4];
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), sc2, f2_pack(o.x, o.y)), e[0], e[1]);
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), sc2, f2_pack(o.z, o.w)), e[2], e[3]);
+                        if constexpr (decltype(masked)::value) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) e[y] = keep >> (4 * i + y) & 1 ? e[y] : -INFINITY;
+                        }
+                        sum2[0] = f2_add(sum2[0], f2_pack(ex2(e[0]), ex2(e[1])));
+                        sum2[1] = f2_add(sum2[1], f2_pack(ex2(e[2]), ex2(e[3])));
+                    }
+                };
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (!any) break;
@@ -878,20 +895,9 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
                     }
-                    if (!full) {
-                        const uint32_t keep = row_bits32(lo - 32 * c, hi - 32 * c);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = (keep >> i) & 1 ? x[i] : 0xff800000u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 o = z[c * 8 + i];
-                        float e0, e1, e2, e3;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), sc2, f2_pack(o.x, o.y)), e0, e1);
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), sc2, f2_pack(o.z, o.w)), e2, e3);
-                        sum2[0] = f2_add(sum2[0], f2_pack(ex2(e0), ex2(e1)));
-                        sum2[1] = f2_add(sum2[1], f2_pack(ex2(e2), ex2(e3)));
-                    }
+                    const uint32_t keep = full ? 0xffffffffu : row_bits32(lo - 32 * c, hi - 32 * c);
+                    if (full) add(x, z + c * 8, keep, std::false_type{});
+                    else add(x, z + c * 8, keep, std::true_type{});
                 }
                 __syncwarp();
                 if (lane == 0) {

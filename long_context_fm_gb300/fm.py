@@ -371,7 +371,7 @@ def fm_bounds_decompress(cbounds, bounds: Bounds, dev_status, stream=None):
 
 def fm_debug_wait_test(kernel, limit_cycles):
     """Test hook: the next forward (kernel=0), backward (kernel=1) or paged
-    attention launch (KERNEL_NAMES' index of "paged_decode" or "paged_chunk") runs
+    attention or weight launch (KERNEL_NAMES' index of "paged_decode", "paged_chunk", "paged_weigh_few" or "paged_weigh_many") runs
     with every device-side wait bounded by limit_cycles and its first CTA
     withholds one tile load, so it must end with FM_ERR_TIMEOUT in dev_status."""
     _check(_lib.fm_debug_wait_test(int(kernel), int(limit_cycles)), "fm_debug_wait_test")
@@ -709,6 +709,17 @@ def fm_rotary_table(spec: RotarySpec):
     return turns, m.value
 
 
+def _made(stream, shape, dtype, device):
+    """A new tensor that a kernel on `stream` (None: the current one) writes, of that stream's memory: the allocator hands what
+    was freed on a stream to whoever asks on it next."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _turning(rotary, dev):
     if not isinstance(rotary, Rotary) or rotary.turns.get_device() != dev:
         raise TypeError(f"rotary must be a Rotary on cuda:{dev}")
@@ -747,7 +758,7 @@ def fm_rope(x, positions, rotary: Rotary, out=None, out_dtype=None, inverse=Fals
     dev = _on(x, "x")
     B, H, N, d, xs = _batch(x, dev, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        out = _made(stream, x.shape, x.dtype if out_dtype is None else out_dtype, x.device)
     elif out_dtype is not None and out.dtype is not out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
     *_, ys = _batch(out, dev, "out", x.shape)
@@ -783,7 +794,7 @@ def fm_paged_append_rope(q, k, v, slots, positions, rotary: Rotary, k_cache, v_c
     if not T == Tk == Tv or not H == Hv == cache.Hkv:
         raise ValueError("q must be [T, Hq, d], k and v [T, Hkv, d] of the cache")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _made(stream, q.shape, q.dtype, q.device)
     elif q_out.shape != q.shape:
         raise ValueError(f"q_out must have the shape {list(q.shape)}, got {list(q_out.shape)}")
     _, _, ot, oh = _rows(q_out, dev, "q_out", cache.d)
@@ -857,9 +868,9 @@ def fm_paged_evict(lens, block_table, k_cache, v_cache, weights, budget, dev_sta
         if not -1 << 31 <= x < 1 << 31:
             raise ValueError(f"{name} = {x} does not fit 32 bits")
     if kept is None:
-        kept = torch.empty(R, cache.Hkv, max(budget, 0), dtype=torch.int32, device=lens.device)
+        kept = _made(stream, (R, cache.Hkv, max(budget, 0)), torch.int32, lens.device)
     if new_lens is None:
-        new_lens = torch.empty(R, dtype=torch.int32, device=lens.device)
+        new_lens = _made(stream, (R,), torch.int32, lens.device)
     places, after = _flat(kept, torch.int32, dev, "kept", (R, cache.Hkv, budget)), _flat(new_lens, torch.int32, dev, "new_lens", (R,))
     code = _lib.fm_paged_evict(cache, R, block_table.shape[1], at, table, pool, budget, recent, sink, places, after,
                                _flat(dev_status, torch.int32, dev, "dev_status", (1,)), _raw_stream(dev) if stream is None else _stream(stream))
@@ -883,13 +894,13 @@ def fm_paged_release(held, lens, block_table, page_size, num_pages, free_pages, 
     R = held.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("block_table must be int32 [requests, max_pages]")
-    seq_lens = torch.empty_like(held) if seq_lens is None else seq_lens
+    seq_lens = _made(stream, (R,), i32, held.device) if seq_lens is None else seq_lens
     free = head = after = None
     n_free = 0
     if free_pages is not None:
         if free_head is None:
             raise ValueError("free_pages comes with free_head")
-        free_next = torch.empty_like(free_head) if free_next is None else free_next
+        free_next = _made(stream, (1,), i32, held.device) if free_next is None else free_next
         n_free = free_pages.numel()
         if n_free >= 1 << 31:
             raise ValueError("free_pages has 2^31 - 1 entries at most")
@@ -938,9 +949,9 @@ def fm_verify_drafts(target, draft, tokens, u_accept, u_sample, cu_q, seq_lens, 
             raise ValueError("draft must have target's shape and type")
         dp = draft.data_ptr()
     R = seq_lens.shape[0]
-    out = torch.empty(T, dtype=i32, device=target.device) if out is None else out
-    n_out = torch.empty(R, dtype=i32, device=target.device) if n_out is None else n_out
-    new_lens = torch.empty(R, dtype=i32, device=target.device) if new_lens is None else new_lens
+    out = _made(stream, (T,), i32, target.device) if out is None else out
+    n_out = _made(stream, (R,), i32, target.device) if n_out is None else n_out
+    new_lens = _made(stream, (R,), i32, target.device) if new_lens is None else new_lens
     args = (_flat(tokens, i32, dev, "tokens", (T,)), _flat(u_accept, torch.float32, dev, "u_accept", (T,)),
             _flat(u_sample, torch.float32, dev, "u_sample", (R,)), _flat(cu_q, i32, dev, "cu_q", (R + 1,)),
             _flat(seq_lens, i32, dev, "seq_lens", (R,)), R, _flat(out, i32, dev, "out", (T,)), _flat(n_out, i32, dev, "n_out", (R,)),

@@ -241,3 +241,30 @@ def test_a_cache_past_32_bits(fm):
         places = long_ref.kept_places(heavy[h].tolist(), new, 150, 20, 4)
         assert torch.equal(line(kc)[h, :150], keys[h, places]) and torch.equal(line(vc)[h, :150], values[h, places])
         assert torch.equal(line(weights)[h, :150].cpu(), heavy[h, places])
+
+
+def test_results_of_a_call_on_a_given_stream(fm):
+    """They are of that stream's memory: what the current stream frees and asks for is never theirs."""
+    side = torch.cuda.Stream()
+    rot = fm.Rotary(64)
+    lens, new, table = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([40], [20], [[0, 1, 2]]))
+    k = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    pool, status, x = torch.zeros(3, 2, 16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(20, 2, 64, dtype=torch.bfloat16, device="cuda")
+    places, slots, v = torch.arange(20, dtype=torch.int32, device="cuda"), torch.arange(20, device="cuda"), torch.zeros_like(k)
+    p, u = torch.full((2, 100), 0.01, device="cuda"), torch.full((2,), 0.5, device="cuda")
+    tokens, cu = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    calls = [lambda s: fm.fm_rope(x, places, rot, stream=s),
+             lambda s: fm.fm_paged_append_rope(x, x, x, slots, places, rot, k, v, status, stream=s),
+             lambda s: fm.fm_paged_evict(lens, table, k, v, pool, 30, status, stream=s),
+             lambda s: fm.fm_paged_release(lens, new, table, 16, 3, None, None, status, stream=s)[0],
+             lambda s: fm.fm_verify_drafts(p, None, tokens, u, u[:1], cu, lens, status, stream=s)[0]]
+    for call in calls:
+        for stream in (side, side.cuda_stream):
+            got = call(stream)
+            torch.cuda.synchronize()
+            at, like = got.data_ptr(), (got.shape, got.dtype)
+            del got
+            mine = [torch.empty(like[0], dtype=like[1], device="cuda") for _ in range(50)]
+            assert all(m.data_ptr() != at for m in mine)
+    assert int(status) == 0

@@ -126,6 +126,32 @@ def test_a_call_repeats_itself(fm):
     assert torch.equal(pools[0], pools[1]) and torch.equal(pools[0], pools[2])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("new,row", [([3, 1], 1), ([100, 2], 40), ([300, 1], 130)])
+def test_a_row_that_is_no_number(fm, new, row, window, e4m3):
+    """Its weights reach the keys that it attends and no others: neither those behind it nor those behind its window."""
+    b = base.Batch(fm, [200, 30], new, 8, 2, 128, 16, window=window, e4m3=e4m3, seed=9, poison=False)
+    _, lse = b.run(torch.float32)
+
+    def weigh(z):
+        pool = torch.zeros(b.k.shape[:3], device="cuda")
+        b.att.weigh(b.q, z, b.k, b.dev_table, pool, b.scale, b.kd)
+        b.att.check_status()
+        return [torch.stack([pool[b.table[r][j // 16], :, j % 16] for j in range(c + n)]) for r, (c, n) in enumerate(zip(b.ctx, b.new))]
+
+    want, at = weigh(lse), b.ctx[0] + row
+    j = torch.arange(b.ctx[0] + new[0], device="cuda")
+    attended = (j <= at) & (j > at - window if window else j >= 0)
+    for value in (float("nan"), float("-inf"), float("inf")):
+        z = lse.clone()
+        z[row] = value
+        got = weigh(z)
+        assert torch.equal(got[1], want[1]) and torch.equal(got[0][~attended], want[0][~attended])
+        if value != value:
+            assert got[0][attended].isnan().all()
+
+
 @pytest.mark.parametrize("new", [[1, 2], [100, 1]])
 def test_pages_outside_the_pool(fm, new):
     b = base.Batch(fm, [300, 20], new, 8, 2, 64, 16)
