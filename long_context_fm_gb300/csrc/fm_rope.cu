@@ -36,10 +36,12 @@ __device__ __forceinline__ Turn turn_of(const uint64_t *turns, int u, int pos, f
     Turn t;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int32_t a = (int32_t)((f[i] * (uint64_t)(uint32_t)pos) >> 32);     // 2^-32 turns, [-1/2, 1/2)
-        sincospif((float)a * 0x1p-31f, &t.s[i], &t.c[i]);
-        t.c[i] *= m;
-        t.s[i] *= inverse ? -m : m;
+        // In 2^-32 turns: the nearest quarter, taken off as an integer, and what is left, which 24 bits hold to 2^-28 turns.
+        const uint32_t a = (uint32_t)((f[i] * (uint64_t)(uint32_t)pos) >> 32), quarter = (a + (1u << 29)) >> 30;
+        float s, c;
+        sincospif((float)(int32_t)(a - (quarter << 30)) * 0x1p-31f, &s, &c);
+        t.c[i] = (quarter & 1 ? s : c) * ((quarter + 1) & 2 ? -m : m);
+        t.s[i] = (quarter & 1 ? c : s) * (((quarter & 2) != 0) != inverse ? -m : m);
     }
     return t;
 }
