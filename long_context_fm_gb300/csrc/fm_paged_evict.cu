@@ -16,8 +16,8 @@
 // there are few.  Steps, of 32 requests of up to 12,000 tokens cut to 4,096 and of one of 128K cut to 16K in e4m3: windows
 // of registers without copies ahead, histograms read one count at a time 427 and 122 us; copies ahead, 16 bytes of a histogram at
 // a time 213 and 90; places by warps instead of block-wide scans, weights 16 bytes at a time, and a meeting that waits for no
-// stores (each thread's would have to reach L2 first) 156 and 82; key and value of a token by the same threads 124 and 65. (Bulk
-// copies of a row each instead, a thread per token: 258 and 148.)
+// stores (each thread's would have to reach L2 first) 156 and 82; key and value of a token by the same threads 124 and 65; pages
+// looked up a window before they are used 113 and 52. (Bulk copies of a row each instead, a thread per token: 258 and 148.)
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -345,16 +345,30 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
             from[i] = w < windows && j < a.budget ? __ldcg(kept + j) : -1;
         }
     };
+    // Pages of places (those that are none: -1), and of the window's own tokens: looked up a window before they are used.
+    auto pages_of = [&](const int (&at)[kMoves], int (&page)[kMoves]) {
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i) page[i] = at[i] >= 0 ? __ldg(table + page_of(at[i])) : 0;
+    };
+    auto targets = [&](int w, int (&page)[kMoves]) {
+        int at[kMoves];
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i) {
+            const int64_t j = (int64_t)w * window + j0 + i * tokens;
+            at[i] = w < windows && j < a.budget ? (int)j : -1;
+        }
+        pages_of(at, page);
+    };
     // Starts the loads of window w; a bit for each token that moves.
-    auto start = [&](int w, const int (&from)[kMoves]) {
+    auto start = [&](int w, const int (&from)[kMoves], const int (&pages)[kMoves]) {
         unsigned moves = 0;
         uint8_t *stage = smem + (w % kStages) * kStageBytes;
 #pragma unroll
         for (int i = 0; i < kMoves; ++i) {
             if (from[i] < 0 || from[i] == w * window + j0 + i * tokens) continue;
             moves |= 1u << i;
-            const int b = page_of(from[i]), in = from[i] - b * a.page_size;
-            const int64_t page = __ldg(table + b);
+            const int in = from[i] - page_of(from[i]) * a.page_size;
+            const int64_t page = pages[i];
             copy_async16(stage + (i * 2 * kEvictThreads + tid) * 16, a.kv[0] + page * a.page[0] + in * a.tok[0] + col_k);
             copy_async16(stage + ((i * 2 + 1) * kEvictThreads + tid) * 16, a.kv[1] + page * a.page[1] + in * a.tok[1] + col_v);
             if (piece == 0) copy_async4(s_moved + ((w % kStages) * kMoves + i) * tokens + mate, a.weights + page * page_weights + head_weights + in);
@@ -363,18 +377,30 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
         return moves;
     };
     unsigned moves[kStages] = {};
-    int from[kMoves];
+    int from[kMoves], next[kMoves], from_page[kMoves], to_page[kMoves];
 #pragma unroll
     for (int w = 0; w < kStages - 1; ++w) {
         sources(w, from);
-        moves[w] = start(w, from);
+        pages_of(from, from_page);
+        moves[w] = start(w, from, from_page);
     }
     sources(kStages - 1, from);
+    sources(kStages, next);
+    pages_of(from, from_page);
+    targets(0, to_page);
     for (int w = 0; w < windows; ++w) {
         copy_async_wait<kStages - 2>();
         if (C > 1) cluster_arrive_relaxed();               // this thread has read its sources of the window
-        moves[kStages - 1] = start(w + kStages - 1, from);
-        sources(w + kStages, from);
+        moves[kStages - 1] = start(w + kStages - 1, from, from_page);
+        int page_now[kMoves];
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i) {
+            page_now[i] = to_page[i];
+            from[i] = next[i];
+        }
+        pages_of(from, from_page);
+        targets(w + 1, to_page);
+        sources(w + kStages + 1, next);
         if (C > 1) cluster_wait();                   // and every other
         else __syncthreads();
         const uint8_t *stage = smem + (w % kStages) * kStageBytes;
@@ -382,8 +408,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) fm_paged_evict_kernel(const 
         for (int i = 0; i < kMoves; ++i) {
             if (!(moves[0] >> i & 1u)) continue;
             const int j = w * window + j0 + i * tokens;
-            const int b = page_of(j), in = j - b * a.page_size;
-            const int64_t page = __ldg(table + b);
+            const int in = j - page_of(j) * a.page_size;
+            const int64_t page = page_now[i];
             *reinterpret_cast<uint4 *>(a.kv[0] + page * a.page[0] + in * a.tok[0] + col_k) = *reinterpret_cast<const uint4 *>(stage + (i * 2 * kEvictThreads + tid) * 16);
             *reinterpret_cast<uint4 *>(a.kv[1] + page * a.page[1] + in * a.tok[1] + col_v) = *reinterpret_cast<const uint4 *>(stage + ((i * 2 + 1) * kEvictThreads + tid) * 16);
             if (piece == 0) a.weights[page * page_weights + head_weights + in] = s_moved[((w % kStages) * kMoves + i) * tokens + mate];
