@@ -21,10 +21,11 @@
 // rows: the query heads of the KV head times as many tokens as fit) that attend them stream through, each multiplied by
 // both.  Per pair of tiles 512 cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both
 // about even, and each key tile has its own issuing thread, two score buffers and a warpgroup for each of them.  4,178 tokens
-// over up to 16K keys: 327 us (1,450 TFLOP/s); while an SM has work the tensor pipe and the exponentials are busy
+// over up to 16K keys: 318 us (1,490 TFLOP/s); while an SM has work the tensor pipe and the exponentials are busy
 // two thirds of the time each (a warp's waits and loads from TMEM are what is between).
 // One key tile a unit, one issuing thread and two warpgroups took 455 us (a row tile's products waited for their own
-// barriers), two issuing threads 457 (Q's arrival), two key tiles a unit 439 (the sums' latency), four warpgroups 350.  Not
+// barriers), two issuing threads 457 (Q's arrival), two key tiles a unit 439 (the sums' latency), four warpgroups 350, units cut
+// along the rows 327, the next scores on their way while some are summed and the masked case apart 318.  Not
 // kept: four issuing threads (375), K as the TMEM operand with three score buffers (375: the buffers come free too late), two
 // warpgroups that hold all 128 scores of a row tile (380).
 //   warp 0      claims units (longest first), TMA of K
@@ -883,21 +884,33 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                         sum2[1] = f2_add(sum2[1], f2_pack(ex2(e[2]), ex2(e[3])));
                     }
                 };
+                auto release = [&]() {              // every score is in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
+                };
+                if (full) {
+                    uint32_t x[2][32];              // the next ones on their way
+                    tmem_ld32(tS, x[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (!any) break;
-                    uint32_t x[32];
-                    tmem_ld32(tS + 32 * c, x);
-                    tmem_ld_wait();
-                    tmem_reg_fence(x);
-                    if (c == 3) {                   // every score is in registers
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars[C::B_SE + sb]);
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_wait();
+                        tmem_reg_fence(x[c & 1]);
+                        if (c < 3) tmem_ld32(tS + 32 * (c + 1), x[(c + 1) & 1]);
+                        else release();
+                        add(x[c & 1], z + c * 8, 0u, std::false_type{});
                     }
-                    const uint32_t keep = full ? 0xffffffffu : row_bits32(lo - 32 * c, hi - 32 * c);
-                    if (full) add(x, z + c * 8, keep, std::false_type{});
-                    else add(x, z + c * 8, keep, std::true_type{});
+                } else if (any) {
+                    // (Rolled up: unrolled beside the other one it costs 5 % of the whole, in registers and instruction fetches.)
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(tS + 32 * c, x);
+                        tmem_ld_wait();
+                        tmem_reg_fence(x);
+                        if (c == 3) release();
+                        add(x, z + c * 8, row_bits32(lo - 32 * c, hi - 32 * c), std::true_type{});
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) {
