@@ -1,8 +1,8 @@
 """Plain 64-bit references of the operators around the attention of long conversations, and the tolerances that their
 tests use.
 
-Rotary: an angle is held to 2^-32 turns and rounded to fp32 within [-1/2, 1/2) turns (2^-26 turns), so off by at
-most 2 pi (2^-32 + 2^-26) = 9.6e-8 rad; the frequency is a double after four roundings on either side: 2^-50 p theta rad
+Rotary: an angle is held to 2^-32 turns and rounded to fp32 within [-1/2, 1/2) turns (2^-26 turns; 2^-28 where the nearest
+quarter is taken off first), so off by at most 2 pi (2^-32 + 2^-26) = 9.6e-8 rad; the frequency is a double after four roundings on either side: 2^-50 p theta rad
 more; sine and cosine of it are within two units of the last place (2^-23), and times m rounded (2^-24): 2^-21 m in all.  Two
 products and a sum in fp32: 3 x 2^-24 m (|a| + |b|).  The result is rounded once.
   bound = m (|a| + |b|) (2^-21 + 2^-22 + 2^-50 p theta) + half a step of the result.
