@@ -940,11 +940,11 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
         }
     } else if (warp == 18) {
         // -------------------------------------------- Q and lse of the row tiles
-        int tk[4], at[4];                   // token of a row tile's row, and its place from the tile's first
+        int tk[4], at[4];                   // token of a row tile's row (past any step's rows where none fills it), and its place from the tile's first
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = lane + 32 * i;
-            tk[i] = c < filled ? c / G : 1 << 20;
+            tk[i] = c < filled ? c / G : 1 << 30;
             at[i] = c < filled ? tk[i] * s.Hq + c % G : 0;
         }
         int g = 0;
