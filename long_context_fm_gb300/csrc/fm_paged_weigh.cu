@@ -593,7 +593,12 @@ struct ManyUnit {
     int piece;              // where the sums go in the workspace; -1: to the weights
 };
 
-template <int D, bool FP8>
+// PAD: the last columns of a row tile that may be empty, 0, 8 or 24, where K may hold infinities (bf16).  Columns that no token fills (128
+// is no multiple of the query heads of a KV head) are rows of zeros, which have no score beside such a key; the tokens' rows may have
+// scored it at -infinity, a weight of nothing.  So these columns are masked, in a kernel of its own: chunks of 4,096 tokens of 28 / 4
+// heads 294 -> 297 us (with the last 32 305, the sum looked at and taken again 311), of 28 / 1, with 24 columns, 320 -> 338.
+// An e4m3 code is finite, or no number for every row.
+template <int D, bool FP8, int PAD>
 __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
     fm_paged_weigh_many_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const WeighArgs w)
 {
@@ -868,15 +873,16 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                 }
                 const float4 *z = reinterpret_cast<const float4 *>(sLse + ls * 128);
                 uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                // (The mask is put over the exponents: a row that does not attend the key gives it nothing, whatever its lse.)
-                auto add = [&](const uint32_t (&x)[32], const float4 *off, uint32_t keep, auto masked) {
+                // (The mask is put over the exponents: a row that does not attend the key gives it nothing, whatever its lse.)  `first`:
+                // the group of four columns from which on it is looked at.
+                auto add = [&](const uint32_t (&x)[32], const float4 *off, uint32_t keep, auto first) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float4 o = off[i];
                         float e[4];
                         f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), sc2, f2_pack(o.x, o.y)), e[0], e[1]);
                         f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), sc2, f2_pack(o.z, o.w)), e[2], e[3]);
-                        if constexpr (decltype(masked)::value) {
+                        if (i >= decltype(first)::value) {
 #pragma unroll
                             for (int y = 0; y < 4; ++y) e[y] = keep >> (4 * i + y) & 1 ? e[y] : -INFINITY;
                         }
@@ -898,7 +904,8 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                         tmem_reg_fence(x[c & 1]);
                         if (c < 3) tmem_ld32(tS + 32 * (c + 1), x[(c + 1) & 1]);
                         else release();
-                        add(x[c & 1], z + c * 8, 0u, std::false_type{});
+                        if (c < 3) add(x[c & 1], z + c * 8, 0u, std::integral_constant<int, 8>{});
+                        else add(x[c & 1], z + c * 8, row_bits32(0, filled - 96), std::integral_constant<int, 8 - PAD / 4>{});
                     }
                 } else if (any) {
                     // (Rolled up: unrolled beside the other one it costs 5 % of the whole, in registers and instruction fetches.)
@@ -909,7 +916,7 @@ __global__ void __launch_bounds__(ManyCfg<D, FP8>::kThreads, 1)
                         tmem_ld_wait();
                         tmem_reg_fence(x);
                         if (c == 3) release();
-                        add(x, z + c * 8, row_bits32(lo - 32 * c, hi - 32 * c), std::true_type{});
+                        add(x, z + c * 8, row_bits32(lo - 32 * c, hi - 32 * c), std::integral_constant<int, 0>{});
                     }
                 }
                 __syncwarp();
@@ -1057,15 +1064,15 @@ fm_status launch_few(const CUtensorMap &tk, const WeighArgs &w, cudaStream_t str
     return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int PAD>
 fm_status launch_many(const CUtensorMap &tq, const CUtensorMap &tk, const WeighArgs &w, cudaStream_t stream)
 {
     using C = ManyCfg<D, FP8>;
     static std::atomic<uint8_t> done[kMaxDevices];
-    const fm_status st = ready(fm_paged_weigh_many_kernel<D, FP8>, C::kBytes, done);
+    const fm_status st = ready(fm_paged_weigh_many_kernel<D, FP8, PAD>, C::kBytes, done);
     if (st != FM_OK) return st;
     ProfScope ps(kKPagedWeighMany, stream);
-    fm_paged_weigh_many_kernel<D, FP8><<<kPagedCtas, C::kThreads, C::kBytes, stream>>>(tq, tk, w);
+    fm_paged_weigh_many_kernel<D, FP8, PAD><<<kPagedCtas, C::kThreads, C::kBytes, stream>>>(tq, tk, w);
     return cudaPeekAtLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
@@ -1124,8 +1131,11 @@ extern "C" fm_status fm_paged_weights(const fm_paged_step *step, const void *q, 
         if (!make_tmap_strided(&tq, q, false, 3, qd, qs, qb, 128) || !make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, fp8 ? 0 : 128))
             return FM_ERR_CUDA;
         wait_test_args(kKPagedWeighMany, &a.wait_limit, &a.withhold);
-        if (d128) st = fp8 ? launch_many<128, true>(tq, tk, w, cs) : launch_many<128, false>(tq, tk, w, cs);
-        else st = fp8 ? launch_many<64, true>(tq, tk, w, cs) : launch_many<64, false>(tq, tk, w, cs);
+        const int empty = 128 % G;          // 24 at most, with 26 heads
+        if (fp8) st = d128 ? launch_many<128, true, 0>(tq, tk, w, cs) : launch_many<64, true, 0>(tq, tk, w, cs);
+        else if (empty == 0) st = d128 ? launch_many<128, false, 0>(tq, tk, w, cs) : launch_many<64, false, 0>(tq, tk, w, cs);
+        else if (empty <= 8) st = d128 ? launch_many<128, false, 8>(tq, tk, w, cs) : launch_many<64, false, 8>(tq, tk, w, cs);
+        else st = d128 ? launch_many<128, false, 24>(tq, tk, w, cs) : launch_many<64, false, 24>(tq, tk, w, cs);
         if (st != FM_OK) return st;
     }
     if (!make_tmap_strided(&tk, cache->k, fp8, 4, cd, ks, cb, fp8 ? a.s.d : 128)) return FM_ERR_CUDA;
