@@ -492,7 +492,10 @@ FM_API fm_status fm_rope(const void *x, int x_dtype, fm_strides xs, const int32_
  *   plan, q, cache (its k alone is read), block table and scale as fm_attn_paged, after it, with its lse; `rows` as there.
  *   Scores and sums are fp32; beside an e4m3 cache the q of requests of at most 32 rows enters as two
  *   e4m3 terms, as in fm_attn_paged.  A key's sum is added up in a fixed order, except that several
- *   requests that hold one page add to it in any order.  A step for which this is not called leaves the weights of its keys as
+ *   requests that hold one page add to it in any order.  Every row counts, those of drafted tokens that fm_verify_drafts
+ *   refuses among them, and what older keys have from them stays.  A row whose lse is +infinity gives nothing where its score is finite: a program that
+ *   wants the kept rows alone calls this after the verification, with the lse of the rows behind (out < 0) at +infinity.
+ *   A step for which this is not called leaves the weights of its keys as
  *   that memory was (a page given out again holds another request's).  A row gives nothing to keys that it does not attend, whatever its
  *   lse.  A page number outside [0, num_pages) among the attended
  *   gives FM_ERR_PAGES and its keys are left out.

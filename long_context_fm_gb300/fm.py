@@ -823,7 +823,8 @@ def _weight_pool(weights, cache, dev):
 
 def fm_paged_weights(step: PagedStep, q, lse, k_cache, block_table, plan, scale, weights, dev_status, k_descale=None, stream=None):
     """Adds the attention weight that each cached key received from the step's rows to weights (fp32 [num_pages, Hkv,
-    page_size]); q and lse (fp32 [rows, Hq]) as fm_attn_paged took and gave them, over the same plan."""
+    page_size]); q and lse (fp32 [rows, Hq]) as fm_attn_paged took and gave them, over the same plan.  A row whose lse is
+    +infinity gives nothing (that of a refused draft)."""
     if stream is None:
         code = _call.weigh(ctypes.addressof(step), q, lse, k_cache, block_table, plan, scale, weights, dev_status, k_descale)
         if code == 0:
@@ -1133,7 +1134,8 @@ class PagedAttention:
                                     self.status, q_out, k_descale, v_descale)
 
     def weigh(self, q, lse, k_cache, block_table, weights, scale=None, k_descale=None):
-        """Adds what the cached keys received in the attend() of q that gave lse to weights (fp32 [num_pages, Hkv, page_size])."""
+        """Adds what the cached keys received in the attend() of q that gave lse to weights (fp32 [num_pages, Hkv, page_size]).
+        Rows of drafts that verify() refused are left out by lse.masked_fill((out < 0)[:, None], math.inf)."""
         scale = 1.0 / self.step.d ** 0.5 if scale is None else scale
         fm_paged_weights(self.step, q, lse, k_cache, block_table, self.plan_buffer, scale, weights, self.status, k_descale)
 
