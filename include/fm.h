@@ -441,7 +441,9 @@ FM_API fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t
  *     FM_ROPE_YARN:   theta_i (g + (1 - g) / s), g = clamp((original theta_i / 2 pi - slow) /
  *                     (fast - slow), 0, 1): pairs that turn more than `fast` times within the
  *                     `original` positions are left, those that turn less than `slow` times are
- *                     stretched; m = 0.1 ln s + 1.
+ *                     stretched; m = 0.1 ln s + 1.  (The ramp g is linear in the turns, as in the method's formula.  Programs
+ *                     whose ramp is linear in the pair's index, between those that turn `fast` and `slow` times, have other
+ *                     frequencies in between, by up to a factor of 2.3 at s = 8: their models need a table of their own.)
  *   m = 1 otherwise.  rot even, 2 to 128; base > 1; 0 <= slow < fast and original > 0 for YARN; all finite (else
  *   FM_ERR_INVALID_ARG).
  * fm_rope: y = the turned x.  x of x_dtype, y of y_dtype (bf16 or fp32): element (b, h, n, c) at b * batch +
@@ -451,8 +453,8 @@ FM_API fm_status fm_attn_paged(const fm_paged_step *step, const void *q, int64_t
  *   negative are left as they were in y.  y may be x (same strides and type), and may not
  *   overlap it otherwise.  Sine and cosine are fp32, from an angle reduced in 64-bit
  *   integers; products are fp32; y is rounded once.
- * rotary: `turns` (device, 16-byte aligned) holds fm_rotary_table's values; rot a multiple of 8, at most
- *   d (else FM_ERR_UNSUPPORTED); d = 64 or 128.
+ * rotary: `turns` (device, 16-byte aligned) holds fm_rotary_table's values, or others: theta_i / 2 pi modulo 1,
+ *   times 2^64; rot a multiple of 8, at most d (else FM_ERR_UNSUPPORTED); d = 64 or 128.
  */
 enum { FM_ROPE_PLAIN = 0, FM_ROPE_LINEAR = 1, FM_ROPE_NTK = 2, FM_ROPE_YARN = 3 };
 typedef struct {

@@ -684,15 +684,25 @@ class Rotary:
     device.  interleaved: pairs are neighbours (2i, 2i + 1), else (i, i + rot / 2).  scaling: "none", or for
     contexts `factor` times as long as the trained ones "linear", "ntk" or "yarn" (which goes by the `original`
     trained length and leaves pairs that turn more than `fast` times within it); see fm.h.  magnitude:
-    factor on sine and cosine, by default what the scaling says."""
+    factor on sine and cosine, by default what the scaling says.  frequencies: rot / 2 of the caller's own in their
+    place, in radians per position, [0, 2 pi) (base and scaling are not used then, and magnitude is 1 by default): those
+    of a model that was stretched in another way, as by a "yarn" whose ramp goes by the pairs' index, not by their turns."""
 
     def __init__(self, rot, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=4096, slow=1.0, fast=32.0,
-                 magnitude=None, device="cuda"):
+                 magnitude=None, device="cuda", frequencies=None):
         if scaling not in ROPE_SCALINGS:
             raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}")
         if not 0 < rot <= 128 or rot % 8:
             raise ValueError("rot must be a multiple of 8, 128 at most")
-        turns, m = fm_rotary_table(RotarySpec(rot, ROPE_SCALINGS[scaling], base, factor, original, slow, fast))
+        if frequencies is None:
+            turns, m = fm_rotary_table(RotarySpec(rot, ROPE_SCALINGS[scaling], base, factor, original, slow, fast))
+        elif scaling != "none":
+            raise ValueError("frequencies come without a scaling")
+        else:
+            turn = torch.as_tensor(frequencies, dtype=torch.float64).cpu().numpy() / (2 * np.pi)
+            if turn.shape != (rot // 2,) or not ((turn >= 0) & (turn < 1)).all():
+                raise ValueError(f"frequencies must be {rot // 2} numbers in [0, 2 pi)")
+            turns, m = np.ldexp(turn, 64).astype(np.uint64), 1.0
         if magnitude is not None:
             m = float(magnitude)
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
