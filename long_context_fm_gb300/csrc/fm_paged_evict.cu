@@ -557,9 +557,14 @@ fm_status fm_paged_evict(const fm_paged_cache *cache, int requests, int max_page
     const int64_t units = (int64_t)requests * cache->Hkv;
     cudaStream_t cs = (cudaStream_t)stream;
     ProfScope ps(kKPagedEvict, stream);
-    // As many CTAs per unit as one round of the device holds (two of them a SM; a cluster within a part of the
-    // device): 8 units of 12,000 tokens to 4,096 with 1, 2, 4 and 8 CTAs 128, 80, 48 and 35 us; 32 of 1,500 to 500 25, 21, 20 and 31;
-    // 256 of up to 12,000 to 4,096 216, 154, 166 and 219; 512 of up to 2,000 to 1,000 39, 53, 70 and 146.
+    // CTAs per unit by the number of units, at measured crossovers: the lengths are on the device.  More CTAs shorten a unit's
+    // chain of loads, fewer leave room for more units at once (two CTAs a SM) and meet at less cost.  us with 1, 2, 4 and 8 a unit:
+    //   12,000 tokens each to 4,096: 16 units 109, 57, 37, 39; 64 109, 72, 68, 84; 65 109, 72, 70, 82; 76 111, 78, 98, 100;
+    //     304 254, 252, 268, 326; 305 303, 266, 268, 326; 512 395, 397, 424, 532
+    //   spread below 12,000 (what is not cut leaves at once): 16 units 109, 55, 37, 29; 17 109, 57, 37, 37; 64 109, 55, 55, 39; 65 109, 57, 57, 45;
+    //     160 109, 94, 74, 90; 256 180, 104, 117, 125; 384 176, 113, 123, 143; 512 182, 197, 182, 219
+    //   2,000 each to 1,000: 17 units 35, 27, 23, 23; 64 35, 29, 29, 45; 76 35, 31, 45, 57; 152 41, 45, 70, 96; 304 70, 84, 115, 174
+    // The rule is at the best of the four or within a fifth of it where all units are cut, and within 1.6 where few are.
     if (units <= 16) return launch_evict<8>(a, units, cs);
     if (units <= 64) return launch_evict<4>(a, units, cs);
     return units <= 304 ? launch_evict<2>(a, units, cs) : launch_evict<1>(a, units, cs);

@@ -8,7 +8,7 @@
 // head), where K is read once and little is computed, and those with more, which are matrix work.
 //
 // Few rows: bound by HBM (K once): 96 requests of one token over up to 16,000 keys, 32 / 8 heads, 159 us (6.4 TB/s), 64 of up
-// to three over e4m3 77 us (5.0 TB/s).  Key tiles (128 keys) of all (request, KV head) units lie end to end and are cut into
+// to three over e4m3 73 us (5.3 TB/s).  Key tiles (128 keys) of all (request, KV head) units lie end to end and are cut into
 // equal shares, as the plan has them for the attention.  Rows are 16 or 32 columns of the product.  A tile of codes takes
 // as little as 700 cycles of HBM, so each step that one thread or warp does for every tile (loads, products, sums) is done by
 // two on alternate tiles: with one of each the e4m3 batch took 92 us, with the products and sums alone doubled 91.
@@ -21,8 +21,8 @@
 // rows: the query heads of the KV head times as many tokens as fit) that attend them stream through, each multiplied by
 // both.  Per pair of tiles 512 cycles of products (128 x 128 x 128) beside 512 of exponentials (32 a cycle and SM): both
 // about even, and each key tile has its own issuing thread, two score buffers and a warpgroup for each of them.  4,178 tokens
-// over up to 16K keys: 318 us (1,490 TFLOP/s); while an SM has work the tensor pipe and the exponentials are busy
-// two thirds of the time each (a warp's waits and loads from TMEM are what is between).
+// over up to 16K keys: 316 to 336 us (1,410 to 1,500 TFLOP/s, by the clock that the power leaves); while an SM has work the tensor pipe
+// and the exponentials are busy 70 % of the time each (a warp's waits and loads from TMEM are what is between).
 // One key tile a unit, one issuing thread and two warpgroups took 455 us (a row tile's products waited for their own
 // barriers), two issuing threads 457 (Q's arrival), two key tiles a unit 439 (the sums' latency), four warpgroups 350, units cut
 // along the rows 327, the next scores on their way while some are summed and the masked case apart 318.  Not

@@ -4,12 +4,14 @@
 //   then the smallest x with sum_(y <= x) w(y) > u sum w,  w = max(p - q, 0), or p where all are kept.
 //
 // One row of p and one of q are read per request, by a cluster of CTAs that share the vocabulary in contiguous
-// slices, so that a few requests are spread over the SMs: bound by HBM at large batches, by
-// latency below.  A token at a border has to come out the same however the sums are added up, which 24 bits do not
-// give over 100,000 terms, and 64-bit units take far too long here (two results a cycle and SM: with them in the search
-// alone, 64 requests over 131,072 tokens took 51 us for 17, two over 32,000 21 for 7): every sum is held in a pair of
-// floats, with the exact error of each addition and difference (Knuth's two-sum, Dekker's fast one for a larger minus a
-// smaller), about 48 bits.  Every CTA of 512 is resident at once (64 registers, 4 a SM).
+// slices, so that a few requests are spread over the SMs.  Bound by a chain, not by bytes or terms: lengths, tokens,
+// their probabilities, a vote, the row's first load, its sums, a meeting, the search (64 requests of up to five rows over
+// 131,072 tokens, fp32 or bf16, with or without the drafts' probabilities: 10 to 2.5 us of bytes, 20 to 21 us each, the
+// release of the pages among them).  A token at a border has to come out the same however the sums are added up,
+// which 24 bits do not give over 100,000 terms, and 64-bit units take far too long here (two results a cycle and SM: with
+// them in the search alone, 64 requests over 131,072 tokens took 51 us for 17, two over 32,000 21 for 7): every sum is
+// held in a pair of floats, with the exact error of each addition and difference (Knuth's two-sum, Dekker's fast one for a
+// larger minus a smaller), about 48 bits.  Every CTA of 512 is resident at once (64 registers, 4 a SM).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -758,7 +758,8 @@ def _batch(t, dev, name, shape=None):
 def fm_rope(x, positions, rotary: Rotary, out=None, out_dtype=None, inverse=False, stream=None):
     """x [B, H, N, d] (positions int32 [N] or [B, N]) or rows [T, H, d] (positions [T]) with every row turned by its
     position; inverse turns back: the gradient of x from that of the result.  bf16 or fp32 in and out; out (which
-    may be x) is allocated if None, of out_dtype or x's type.  Rows with a negative position are not written."""
+    may be x) is allocated if None, of out_dtype or x's type.  Rows with a negative position are not written.  Like
+    every call here it is outside autograd: the result has no grad_fn, the inverse call is the backward pass."""
     if stream is None and type(rotary) is Rotary and (out_dtype is None or out_dtype is torch.bfloat16 or out_dtype is torch.float32):
         r = _call.rope(x, positions, rotary.address, rotary.turns, out, None if out_dtype is None else out_dtype is torch.float32, bool(inverse))
         if type(r) is int:
